@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Combi
     }
     float mb = m;
 #pragma unroll
-    for (int u = 0; u < kCombineBatch; ++u) mb = fmaxf(mb, w[u]);
+    for (int u = 0; u < kCombineBatch; ++u) mb = fmax_nan(mb, w[u]);  // a NaN split is not an empty one
     if (mb != -INFINITY) {
       const float c = ex2_approx((m - mb) * kLog2e);  // 0 while m is -inf
 #pragma unroll
@@ -662,12 +662,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Combi
   // Block merge: the common max, then every thread's state rescaled to it.
   float mx = m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 16; o > 0; o >>= 1) mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) s_max[warp] = mx;
   __syncthreads();
   mx = s_max[0];
 #pragma unroll
-  for (int w = 1; w < kCombineWarps; ++w) mx = fmaxf(mx, s_max[w]);
+  for (int w = 1; w < kCombineWarps; ++w) mx = fmax_nan(mx, s_max[w]);
   float4* out = reinterpret_cast<float4*>(a.o + (size_t)bh * D);
   if (mx == -INFINITY) {  // every split empty
     for (int i = threadIdx.x; i < D / 4; i += blockDim.x) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
