@@ -23,5 +23,10 @@ from .api import (  # noqa: F401
     quantize_fp8_varlen,
     prefill_fp8,
     prefill_fp8_varlen,
+    cache_write_fp8,
+    cache_read_fp8,
+    decode_fp8_splitkv,
+    decode_fp8,
+    decode_append_fp8,
 )
 from ._lib import AttnError, lib  # noqa: F401

@@ -18,6 +18,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "attn.h")
 c_int, c_float, c_void_p, c_uint64, c_char_p = (ctypes.c_int, ctypes.c_float, ctypes.c_void_p,
                                                  ctypes.c_uint64, ctypes.c_char_p)
 c_uint = ctypes.c_uint
+c_size_t, c_int64 = ctypes.c_size_t, ctypes.c_int64
 
 # name -> (restype, argtypes); pointers are passed as c_void_p (raw addresses).
 SIGNATURES = {
@@ -55,6 +56,15 @@ SIGNATURES = {
     "attn_check_device_status": (c_int, [c_void_p]),
     "attn_set_wait_timeout_ns": (c_uint64, [c_uint64]),
     "attn_selftest_bounded_wait": (c_int, [c_void_p]),
+    "attn_cache_write_fp8": (c_int, [c_void_p] * 2 + [c_int64] * 4 + [c_void_p] * 7 + [c_int] * 8
+                             + [c_void_p]),
+    "attn_cache_read_fp8": (c_int, [c_void_p] * 6 + [c_int64] * 4 + [c_void_p] * 3 + [c_int] * 8
+                            + [c_void_p]),
+    "attn_decode_fp8_splitkv": (c_int, [c_void_p] * 7 + [c_int] + [c_void_p] * 2 + [c_int] * 8
+                                + [c_float, c_int, c_float, c_void_p, c_void_p]),
+    "attn_decode_fp8_workspace_bytes": (c_size_t, [c_int] * 4),
+    "attn_decode_fp8": (c_int, [c_void_p] * 9 + [c_int, c_void_p, c_size_t] + [c_void_p] * 2
+                        + [c_int] * 8 + [c_float, c_int, c_float, c_void_p, c_void_p]),
     "attn_decode_noalloc": (c_int, [c_void_p] * 5 + [c_int] + [c_void_p] * 2 + [c_int] * 8
                             + [c_float, c_void_p]),
 }

@@ -7,12 +7,13 @@ here computes any part of attention.
 
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Optional
 
 import torch
 
-from ._lib import check, lib
+from ._lib import ATTN_MAX_SPLITS, check, lib
 
 _BF16 = torch.bfloat16
 
@@ -571,3 +572,327 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                                    num_blocks, int(max_kv_len), float(scale), _stream(stream))
     check("attn_decode_noalloc", st)
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# A key/value cache held in 8 bits (include/attn.h, "A key/value cache held in
+# 8 bits").
+# ---------------------------------------------------------------------------
+
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(t: torch.Tensor, stream):
+    """What a call runs under: t's device current, and `stream` as torch's
+    current stream, so that what the call allocates belongs to that stream
+    (a workspace freed on return may only be reused behind the kernels that
+    still use it)."""
+    dev = t.device
+    here = dev.index == torch.cuda.current_device()
+    if stream is None and here:
+        return _NO_SCOPE
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                      else torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _need_on(t: torch.Tensor, name: str, dtype, ndim: int, dev) -> None:
+    """_need, and on this device; one test where everything is right."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.device == dev
+            and t.is_contiguous()):
+        return
+    _need(t, name, dtype, ndim)
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _rows_stride(t: torch.Tensor, name: str, dev) -> None:
+    """A strided (heads, tokens, head_dim) bf16 tensor: values of a row
+    contiguous, rows 16-byte aligned."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got shape {tuple(t.shape)}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    st = t.stride()
+    if st[2] != 1 or st[0] % 8 or st[1] % 8:
+        raise ValueError(f"{name} must have contiguous rows and strides that are multiples of 8, "
+                         f"got strides {st}")
+
+
+def _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, num_seqs: int):
+    """Checks an 8-bit cache; returns (its four pointers and the block
+    table's, (block_size, max_blocks, num_blocks, capacity))."""
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        _need(k_cache, "k_cache", torch.uint8, 4)
+    dev = k_cache.device
+    _need_on(k_cache, "k_cache", torch.uint8, 4, dev)
+    _need_on(v_cache, "v_cache", torch.uint8, 4, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if block_table is not None:
+        _need_on(block_table, "block_table", torch.int32, 2, dev)
+        if block_table.shape[0] != num_seqs:
+            raise ValueError("block_table must have one row per sequence")
+        if block_size is not None and block_size != shape[1]:
+            raise ValueError(f"block_size {block_size} does not match the paged cache's {shape[1]}")
+        geom = (shape[1], block_table.shape[1], shape[0], shape[1] * block_table.shape[1])
+        want, bt = (shape[0], shape[2]), block_table.data_ptr()
+    else:
+        if shape[0] != num_seqs:
+            raise ValueError("a contiguous cache must be (num_seqs, L, n_kv, d)")
+        if block_size is None or block_size < 1:
+            raise ValueError("block_size (tokens that share a scale) is needed for a contiguous "
+                             "cache")
+        geom = (block_size, 0, 0, shape[1])
+        want, bt = (num_seqs, -(-shape[1] // block_size), shape[2]), None
+    _need_on(k_scales, "k_scales", torch.float32, len(want), dev)
+    _need_on(v_scales, "v_scales", torch.float32, len(want), dev)
+    if tuple(k_scales.shape) != want or tuple(v_scales.shape) != want:
+        raise ValueError(f"k_scales and v_scales must have shape {want}")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            bt), geom
+
+
+def cache_write_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                    kv_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                    block_table: Optional[torch.Tensor] = None,
+                    block_size: Optional[int] = None, stream=None) -> None:
+    """Quantises new keys and values into an 8-bit cache
+    (``attn_cache_write_fp8``), behind the kv_lens[s] tokens that each
+    sequence has there.
+
+    k_new, v_new: bf16, (n_kv, total, d) with sequence s on rows
+    [cu_seqlens[s], cu_seqlens[s + 1]) (the layout of :func:`prefill_varlen`),
+    or without cu_seqlens (B, n_kv, d), one token a sequence.  Their rows must
+    be contiguous, the other strides multiples of 8 (a view of a fused
+    projection, or (total, n_kv, d) seen through ``transpose(0, 1)``).
+    k_cache, v_cache: uint8 e4m3 codes, paged (num_blocks, block_size, n_kv, d)
+    with block_table (B, max_blocks) int32, or contiguous (B, L, n_kv, d) with
+    ``block_size`` tokens to a scale; k_scales, v_scales: fp32, (num_blocks,
+    n_kv) or (B, ceil(L / block_size), n_kv).  Caches and scales are written
+    in place; kv_lens is left to the caller to increment.
+    """
+    if not isinstance(k_new, torch.Tensor) or not isinstance(v_new, torch.Tensor):
+        raise TypeError("k_new and v_new must be torch.Tensors")
+    dev = k_new.device
+    _rows_stride(k_new, "k_new", dev)
+    _rows_stride(v_new, "v_new", dev)
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    _need_on(kv_lens, "kv_lens", torch.int32, 1, dev)
+    B = kv_lens.shape[0]
+    ptrs, geom = _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
+    ks, vs = k_new.stride(), v_new.stride()
+    if cu_seqlens is not None:
+        _need_on(cu_seqlens, "cu_seqlens", torch.int32, 1, dev)
+        if cu_seqlens.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must have one entry more than kv_lens")
+        n_kv, total, d = k_new.shape
+        strides, cu = (ks[1], ks[0], vs[1], vs[0]), cu_seqlens.data_ptr()
+    else:
+        total, n_kv, d = k_new.shape
+        if total != B:
+            raise ValueError("without cu_seqlens k_new and v_new must be (B, n_kv, d)")
+        strides, cu = (ks[0], ks[1], vs[0], vs[1]), None
+    if k_cache.shape[2] != n_kv or k_cache.shape[3] != d or k_cache.device != dev:
+        raise ValueError("the cache's heads, head_dim or device do not match k_new")
+    with _scope(k_new, stream):
+        st = lib().attn_cache_write_fp8(k_new.data_ptr(), v_new.data_ptr(), *strides, *ptrs, cu,
+                                        kv_lens.data_ptr(), B, total, n_kv, d, *geom, _stream(None))
+    check("attn_cache_write_fp8", st)
+
+
+def cache_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                   v_scales: torch.Tensor, cu_seqlens: torch.Tensor, total: int,
+                   block_table: Optional[torch.Tensor] = None,
+                   starts: Optional[torch.Tensor] = None, block_size: Optional[int] = None,
+                   k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Reads tokens of an 8-bit cache back as bf16 (``attn_cache_read_fp8``):
+    row cu_seqlens[s] + i is position starts[s] + i (starts None: i) of
+    sequence s.  The cache is that of :func:`cache_write_fp8`; ``total`` is
+    the number of rows.  Returns (K, V), (n_kv, total, d) bf16 each, written
+    into ``k_out`` / ``v_out`` when given (rows contiguous, other strides
+    multiples of 8); rows outside every sequence are left as they were.
+    """
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    dev, B = cu_seqlens.device, cu_seqlens.shape[0] - 1
+    ptrs, geom = _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
+    if k_cache.device != dev:
+        raise ValueError(f"the cache must be on {dev}, got {k_cache.device}")
+    if starts is not None:
+        _need_on(starts, "starts", torch.int32, 1, dev)
+        if starts.shape[0] != B:
+            raise ValueError("starts must have one entry per sequence")
+    n_kv, d, total = k_cache.shape[2], k_cache.shape[3], int(total)
+    with _scope(k_cache, stream):
+        if k_out is None:
+            k_out = torch.empty((n_kv, total, d), dtype=_BF16, device=dev)
+        if v_out is None:
+            v_out = torch.empty((n_kv, total, d), dtype=_BF16, device=dev)
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            _rows_stride(t, name, dev)
+            if tuple(t.shape) != (n_kv, total, d):
+                raise ValueError(f"{name} must have shape {(n_kv, total, d)}")
+        ks, vs = k_out.stride(), v_out.stride()
+        st = lib().attn_cache_read_fp8(*ptrs[:4], k_out.data_ptr(), v_out.data_ptr(), ks[1], ks[0],
+                                       vs[1], vs[0], ptrs[4], cu_seqlens.data_ptr(),
+                                       None if starts is None else starts.data_ptr(), B, total,
+                                       n_kv, d, *geom, _stream(None))
+    check("attn_cache_read_fp8", st)
+    return k_out, v_out
+
+
+def _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table, block_size,
+                     max_kv_len, scale, alibi_slopes):
+    """Checks shared by the decodes over an 8-bit cache; returns (cache and
+    block table pointers, sizes from batch to max_kv_len, scale, slopes)."""
+    _need(q, "q", _BF16, 3)
+    dev = q.device
+    B, n_q, d = q.shape
+    _need_on(kv_lens, "kv_lens", torch.int32, 1, dev)
+    if kv_lens.shape[0] != B:
+        raise ValueError("kv_lens must have one entry per sequence")
+    ptrs, geom = _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
+    if k_cache.shape[3] != d or k_cache.device != dev:
+        raise ValueError("the cache's head_dim or device does not match q")
+    capacity = geom[3]
+    if block_table is not None and max_kv_len is not None:
+        geom = (*geom[:3], int(max_kv_len))
+    elif max_kv_len is not None and max_kv_len > capacity:
+        raise ValueError("max_kv_len exceeds the contiguous cache's length")
+    al = None
+    if alibi_slopes is not None:
+        _need_on(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
+        if alibi_slopes.numel() != n_q:
+            raise ValueError("alibi_slopes must have one slope per query head")
+        al = alibi_slopes.data_ptr()
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    return ptrs, (B, n_q, k_cache.shape[2], d, *geom), scale, al
+
+
+def decode_fp8_splitkv(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scales: torch.Tensor, v_scales: torch.Tensor, kv_lens: torch.Tensor,
+                       block_table: Optional[torch.Tensor] = None, num_splits: int = 0,
+                       max_kv_len: Optional[int] = None, scale: Optional[float] = None,
+                       o_partial: Optional[torch.Tensor] = None,
+                       lse_partial: Optional[torch.Tensor] = None, stream=None,
+                       window_left: int = -1, softcap: float = 0.0,
+                       alibi_slopes: Optional[torch.Tensor] = None,
+                       block_size: Optional[int] = None):
+    """Split-KV single-token decode over an 8-bit cache
+    (``attn_decode_fp8_splitkv``): q (B, n_q, d) bf16, the cache that of
+    :func:`cache_write_fp8`, everything else as :func:`decode_splitkv`.
+    Returns (o_partial (S, B, n_q, d), lse_partial (S, B, n_q)), fp32, for
+    :func:`combine`."""
+    ptrs, sizes, scale, al = _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens,
+                                              block_table, block_size, max_kv_len, scale,
+                                              alibi_slopes)
+    B, n_q, n_kv, d = sizes[:4]
+    with _scope(q, stream):
+        if num_splits == 0:
+            num_splits = decode_num_splits(B, n_kv, sizes[7])
+        if o_partial is None:
+            o_partial = torch.empty((num_splits, B, n_q, d), dtype=torch.float32, device=q.device)
+        if lse_partial is None:
+            lse_partial = torch.empty((num_splits, B, n_q), dtype=torch.float32, device=q.device)
+        _need_on(o_partial, "o_partial", torch.float32, 4, q.device)
+        _need_on(lse_partial, "lse_partial", torch.float32, 3, q.device)
+        if (tuple(o_partial.shape) != (num_splits, B, n_q, d)
+                or tuple(lse_partial.shape) != (num_splits, B, n_q)):
+            raise ValueError("partial buffers must be (num_splits, B, n_q, d) and "
+                             "(num_splits, B, n_q)")
+        st = lib().attn_decode_fp8_splitkv(q.data_ptr(), *ptrs, kv_lens.data_ptr(), num_splits,
+                                           o_partial.data_ptr(), lse_partial.data_ptr(), *sizes,
+                                           scale, window_left, softcap, al, _stream(None))
+    check("attn_decode_fp8_splitkv", st)
+    return o_partial, lse_partial
+
+
+def _decode_fp8(name, q, new_kv, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
+                num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left, softcap,
+                alibi_slopes, block_size):
+    ptrs, sizes, scale, al = _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens,
+                                              block_table, block_size, max_kv_len, scale,
+                                              alibi_slopes)
+    B, n_q, n_kv, d = sizes[:4]
+    dev = q.device
+    kn = vn = None
+    if new_kv is not None:
+        for t, what in zip(new_kv, ("k_new", "v_new")):
+            _need_on(t, what, _BF16, 3, dev)
+            if tuple(t.shape) != (B, n_kv, d):
+                raise ValueError(f"{what} must be (batch, n_kv_heads, head_dim)")
+        kn, vn = new_kv[0].data_ptr(), new_kv[1].data_ptr()
+    with _scope(q, stream):
+        if num_splits == 0:
+            num_splits = decode_num_splits(B, n_kv, sizes[7])
+        if out is None:
+            out = torch.empty((B, n_q, d), dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty((B, n_q), dtype=torch.float32, device=dev)
+        _need_on(out, "out", torch.float32, 3, dev)
+        _need_on(lse, "lse", torch.float32, 2, dev)
+        if tuple(out.shape) != (B, n_q, d) or tuple(lse.shape) != (B, n_q):
+            raise ValueError("out and lse must be (B, n_q, d) and (B, n_q)")
+        if workspace is None:
+            # out of range counts are refused by the call
+            n = lib().attn_decode_fp8_workspace_bytes(num_splits, B, n_q, d) \
+                if 1 < num_splits <= ATTN_MAX_SPLITS else 0
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        else:
+            _need_on(workspace, "workspace", torch.uint8, 1, dev)
+        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        st = lib().attn_decode_fp8(q.data_ptr(), kn, vn, *ptrs, kv_lens.data_ptr(), num_splits, wp,
+                                   wn, out.data_ptr(), lse.data_ptr(), *sizes, scale, window_left,
+                                   softcap, al, _stream(None))
+    check(name, st)
+    return out, lse
+
+
+def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               k_scales: torch.Tensor, v_scales: torch.Tensor, kv_lens: torch.Tensor,
+               block_table: Optional[torch.Tensor] = None, num_splits: int = 0,
+               max_kv_len: Optional[int] = None, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None, window_left: int = -1,
+               softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+               block_size: Optional[int] = None):
+    """Decode over an 8-bit cache, split and combined in one call
+    (``attn_decode_fp8``): returns (O (B, n_q, d), LSE (B, n_q)), fp32.
+    Arguments as :func:`decode_fp8_splitkv`; ``workspace`` (uint8, allocated
+    when not given) holds the split partials."""
+    return _decode_fp8("attn_decode_fp8", q, None, k_cache, v_cache, k_scales, v_scales, kv_lens,
+                       block_table, num_splits, max_kv_len, scale, out, lse, workspace, stream,
+                       window_left, softcap, alibi_slopes, block_size)
+
+
+def decode_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                      k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                      v_scales: torch.Tensor, kv_lens: torch.Tensor,
+                      block_table: Optional[torch.Tensor] = None, num_splits: int = 0,
+                      max_kv_len: Optional[int] = None, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None,
+                      window_left: int = -1, softcap: float = 0.0,
+                      alibi_slopes: Optional[torch.Tensor] = None,
+                      block_size: Optional[int] = None):
+    """A decode step: each sequence's new key and value (k_new, v_new: (B,
+    n_kv, d) bf16) are quantised into the cache at position kv_lens[b], as
+    :func:`cache_write_fp8` does, and its query attends over kv_lens[b] + 1
+    tokens (``attn_decode_fp8``).  Returns (O, LSE) as :func:`decode_fp8`;
+    kv_lens is left to the caller to increment."""
+    return _decode_fp8("attn_decode_fp8", q, (k_new, v_new), k_cache, v_cache, k_scales, v_scales,
+                       kv_lens, block_table, num_splits, max_kv_len, scale, out, lse, workspace,
+                       stream, window_left, softcap, alibi_slopes, block_size)

@@ -158,7 +158,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_LAUNCH: return "ATTN_ERR_LAUNCH: a CUDA call or kernel launch failed";
     case ATTN_ERR_TIMEOUT: return "ATTN_ERR_TIMEOUT: a kernel-side bounded wait gave up";
     case ATTN_ERR_DEVICE: return "ATTN_ERR_DEVICE: a kernel saw a bad block-table entry or kv_len";
-    case ATTN_ERR_SCRATCH: return "ATTN_ERR_SCRATCH: the split partials exceed the fixed scratch buffer";
+    case ATTN_ERR_SCRATCH: return "ATTN_ERR_SCRATCH: the split partials exceed the scratch buffer";
     default: return "ATTN_ERR_UNKNOWN";
   }
 }
@@ -561,6 +561,208 @@ int attn_quantize_fp8_qkv(const attn_bf16* q, const attn_bf16* k, const attn_bf1
   attn::QuantArgs av{v, v_codes_t, v_scales, nullptr, planes_kv, rows, head_dim, 0, 1, inv};
   if (attn::launch_quantize_qkv(aq, ak, av, make_ctx(stream, ds)) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+namespace {
+
+// Checks of an 8-bit cache shared by its entry points.
+int validate_cache_fp8(const attn::CacheFp8& c) {
+  if (!c.k || !c.v || !c.k_scales || !c.v_scales) return ATTN_ERR_NULL;
+  if (c.n_kv_heads < 1 || c.n_kv_heads > 65535 || c.block_size < 1 || c.block_size > (1 << 20) ||
+      c.max_kv_len < 0 || c.max_kv_len > (1 << 30))
+    return ATTN_ERR_SHAPE;
+  if (c.block_table) {
+    if (c.max_blocks_per_seq < 1 || c.num_blocks < 1 ||
+        (long long)c.block_size * c.max_blocks_per_seq > (1LL << 30))
+      return ATTN_ERR_SHAPE;
+  } else if (c.max_kv_len < 1) {
+    return ATTN_ERR_SHAPE;
+  }
+  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return ATTN_ERR_HEADDIM;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scales, 4) ||
+      !aligned(c.v_scales, 4) || !aligned(c.block_table, 4))
+    return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+// Checks of a write or a read of packed rows.
+int validate_rows(const attn::CacheRowsArgs& a, bool read) {
+  if (!a.k || !a.v || (read ? !a.cu_seqlens : !a.starts)) return ATTN_ERR_NULL;
+  const int st = validate_cache_fp8(a.c);
+  if (st != ATTN_OK && st != ATTN_ERR_ALIGN) return st;
+  if (a.num_seqs < 1 || a.num_seqs > (1 << 20) || a.total_tokens < 1 ||
+      a.total_tokens > (1 << 24) || (!a.cu_seqlens && a.total_tokens != a.num_seqs))
+    return ATTN_ERR_SHAPE;
+  for (long long s : {a.k_token_stride, a.k_head_stride, a.v_token_stride, a.v_head_stride})
+    if (s < 0 || s % 8 != 0) return ATTN_ERR_SHAPE;
+  if (read) {  // rows that are written must not lie on one another
+    for (long long s : {a.k_token_stride, a.v_token_stride})
+      if (a.total_tokens > 1 && s < a.c.head_dim) return ATTN_ERR_SHAPE;
+    for (long long s : {a.k_head_stride, a.v_head_stride})
+      if (a.c.n_kv_heads > 1 && s < a.c.head_dim) return ATTN_ERR_SHAPE;
+  }
+  // units of work (at most total / block_size + 2 num_seqs blocks, K and V of
+  // every head) are counted in 32 bits, eight warps each at most
+  if (((long long)a.total_tokens / a.c.block_size + 2LL * a.num_seqs) * a.c.n_kv_heads * 2 >
+      0x7fffffffLL)
+    return ATTN_ERR_SHAPE;
+  if (st != ATTN_OK) return st;
+  if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.cu_seqlens, 4) ||
+      !aligned(a.starts, 4))
+    return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+int validate_decode_fp8(const attn::DecodeFp8Args& a) {
+  if (!a.q || !a.kv_lens) return ATTN_ERR_NULL;
+  const int st = validate_cache_fp8(a.c);
+  if (st == ATTN_ERR_NULL || st == ATTN_ERR_SHAPE) return st;
+  if (!valid_variant(a.window_left, a.softcap) || (a.alibi_slopes && a.softcap > 0.f) ||
+      a.batch < 1 || a.batch > 65535 || a.n_q_heads < 1 || !valid_scale(a.scale))
+    return ATTN_ERR_SHAPE;
+  if (st == ATTN_ERR_HEADDIM) return st;
+  if (a.n_q_heads % a.c.n_kv_heads != 0 || a.n_q_heads / a.c.n_kv_heads > 64) return ATTN_ERR_GQA;
+  if (a.num_splits < 0 || a.num_splits > ATTN_MAX_SPLITS) return ATTN_ERR_SPLITS;
+  if (st != ATTN_OK) return st;
+  if (!aligned(a.q, 16) || !aligned(a.kv_lens, 4) || !aligned(a.alibi_slopes, 4))
+    return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+attn::CacheFp8 cache_fp8(const uint8_t* k, const uint8_t* v, const float* ks, const float* vs,
+                         const int32_t* block_table, int n_kv_heads, int head_dim, int block_size,
+                         int max_blocks_per_seq, int num_blocks, int max_kv_len) {
+  return attn::CacheFp8{const_cast<uint8_t*>(k), const_cast<uint8_t*>(v), const_cast<float*>(ks),
+                        const_cast<float*>(vs), block_table, n_kv_heads, head_dim, block_size,
+                        block_table ? max_blocks_per_seq : 0, block_table ? num_blocks : 0,
+                        max_kv_len};
+}
+
+// Where the LSE partials begin in attn_decode_fp8's workspace (after the
+// output partials), and its size.
+size_t fp8_lse_offset(int num_splits, int batch, int n_q_heads, int head_dim) {
+  const size_t rows = (size_t)num_splits * (size_t)batch * (size_t)n_q_heads;
+  return (rows * (size_t)head_dim * sizeof(float) + 255) / 256 * 256;
+}
+
+}  // namespace
+
+int attn_cache_write_fp8(const attn_bf16* k, const attn_bf16* v, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                         const int32_t* block_table, const int32_t* cu_seqlens,
+                         const int32_t* kv_lens, int num_seqs, int total_tokens, int n_kv_heads,
+                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                         int max_kv_len, void* stream) {
+  attn::CacheRowsArgs a{cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, n_kv_heads,
+                                  head_dim, block_size, max_blocks_per_seq, num_blocks,
+                                  max_kv_len),
+                        const_cast<attn_bf16*>(k), const_cast<attn_bf16*>(v), k_token_stride,
+                        k_head_stride, v_token_stride, v_head_stride, cu_seqlens, kv_lens,
+                        num_seqs, total_tokens};
+  int st = validate_rows(a, false);
+  if (st != ATTN_OK) return st;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  if (attn::launch_cache_write_fp8(a, make_ctx(stream, ds)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+int attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+                        const float* v_scales, attn_bf16* k, attn_bf16* v, int64_t k_token_stride,
+                        int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                        const int32_t* block_table, const int32_t* cu_seqlens,
+                        const int32_t* starts, int num_seqs, int total_tokens, int n_kv_heads,
+                        int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                        int max_kv_len, void* stream) {
+  attn::CacheRowsArgs a{cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, n_kv_heads,
+                                  head_dim, block_size, max_blocks_per_seq, num_blocks,
+                                  max_kv_len),
+                        k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                        cu_seqlens, starts, num_seqs, total_tokens};
+  int st = validate_rows(a, true);
+  if (st != ATTN_OK) return st;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  if (attn::launch_cache_read_fp8(a, make_ctx(stream, ds)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+int attn_decode_fp8_splitkv(const attn_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                            const float* k_scales, const float* v_scales,
+                            const int32_t* block_table, const int32_t* kv_lens, int num_splits,
+                            float* o_partial, float* lse_partial, int batch, int n_q_heads,
+                            int n_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                            int num_blocks, int max_kv_len, float scale, int window_left,
+                            float softcap, const float* alibi_slopes, void* stream) {
+  attn::DecodeFp8Args a{cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, n_kv_heads,
+                                  head_dim, block_size, max_blocks_per_seq, num_blocks,
+                                  max_kv_len),
+                        q, kv_lens, num_splits, o_partial, lse_partial, batch, n_q_heads, scale,
+                        window_left, softcap, alibi_slopes, 0};
+  if (!o_partial || !lse_partial) return ATTN_ERR_NULL;
+  int st = validate_decode_fp8(a);
+  if (st != ATTN_OK) return st;
+  if (!aligned(o_partial, 16) || !aligned(lse_partial, 4)) return ATTN_ERR_ALIGN;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  if (num_splits == 0) a.num_splits = split_policy(batch, n_kv_heads, max_kv_len, ds->num_sms);
+  if (attn::launch_decode_fp8(a, make_ctx(stream, ds)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int head_dim) {
+  if (num_splits <= 1 || batch < 1 || n_q_heads < 1 || head_dim < 1) return 0;
+  return fp8_lse_offset(num_splits, batch, n_q_heads, head_dim) +
+         (size_t)num_splits * (size_t)batch * (size_t)n_q_heads * sizeof(float);
+}
+
+int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new,
+                    uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                    const int32_t* block_table, const int32_t* kv_lens, int num_splits,
+                    void* workspace, size_t workspace_bytes, float* o, float* lse, int batch,
+                    int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                    int max_blocks_per_seq, int num_blocks, int max_kv_len, float scale,
+                    int window_left, float softcap, const float* alibi_slopes, void* stream) {
+  if (!o || !lse || (k_new == nullptr) != (v_new == nullptr)) return ATTN_ERR_NULL;
+  const bool append = k_new != nullptr;
+  attn::DecodeFp8Args a{cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, n_kv_heads,
+                                  head_dim, block_size, max_blocks_per_seq, num_blocks,
+                                  max_kv_len),
+                        q, kv_lens, num_splits, o, lse, batch, n_q_heads, scale, window_left,
+                        softcap, alibi_slopes, append ? 1 : 0};
+  int st = validate_decode_fp8(a);
+  if (st != ATTN_OK) return st;
+  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+      !aligned(workspace, 16))
+    return ATTN_ERR_ALIGN;
+  const long long row = (long long)n_kv_heads * head_dim;
+  attn::CacheRowsArgs w{a.c, const_cast<attn_bf16*>(k_new), const_cast<attn_bf16*>(v_new), row,
+                        head_dim, row, head_dim, nullptr, kv_lens, batch, batch};
+  if (append) {
+    st = validate_rows(w, false);
+    if (st != ATTN_OK) return st;
+  }
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  if (a.num_splits == 0) a.num_splits = split_policy(batch, n_kv_heads, max_kv_len, ds->num_sms);
+  const int S = a.num_splits;
+  if (S > 1) {
+    if (workspace_bytes < attn_decode_fp8_workspace_bytes(S, batch, n_q_heads, head_dim))
+      return ATTN_ERR_SCRATCH;
+    if (!workspace) return ATTN_ERR_NULL;
+    a.o_partial = static_cast<float*>(workspace);
+    a.lse_partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                             fp8_lse_offset(S, batch, n_q_heads, head_dim));
+  }
+  const attn::LaunchCtx ctx = make_ctx(stream, ds);
+  if (append && attn::launch_cache_write_fp8(w, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  if (attn::launch_decode_fp8(a, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  if (S > 1) {  // one split's partial is the result
+    attn::CombineArgs c{a.o_partial, a.lse_partial, S, batch, n_q_heads, head_dim, o, lse};
+    if (attn::launch_combine(c, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  }
   return ATTN_OK;
 }
 

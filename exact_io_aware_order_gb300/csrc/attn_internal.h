@@ -113,6 +113,59 @@ struct QuantArgs {
   int tiles = 0;        // columns of the scale array: ceil(rows / 128) + num_seqs
 };
 
+// A cache held in 8 bits: e4m3 codes, paged (num_blocks, block_size,
+// n_kv_heads, head_dim) or contiguous (num_seqs, max_kv_len, n_kv_heads,
+// head_dim), and one fp32 scale for each block of block_size tokens and kv
+// head, (num_blocks, n_kv_heads) or (num_seqs, ceil(max_kv_len / block_size),
+// n_kv_heads).  A value is code * scale.
+struct CacheFp8 {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* block_table;  // null: contiguous
+  int n_kv_heads, head_dim;
+  int block_size, max_blocks_per_seq, num_blocks, max_kv_len;
+  // Tokens a sequence can hold.
+  __host__ __device__ long long capacity() const {
+    return block_table ? (long long)max_blocks_per_seq * block_size : (long long)max_kv_len;
+  }
+};
+
+// The scale's exponents: 2^k, k within these.  |k| <= 60 keeps a score's and a
+// weight's product with a scale, and the sum of exponentials taken against a
+// reference that includes V's scale, far inside fp32.
+constexpr int kScaleExpMin = -60;
+constexpr int kScaleExpMax = 60;
+
+// Rows moved between packed bf16 tensors and an 8-bit cache (write or read).
+// Row t of head h of k starts at k + t * k_token_stride + h * k_head_stride
+// (elements), its head_dim values contiguous; v likewise.
+struct CacheRowsArgs {
+  CacheFp8 c;
+  uint16_t* k;  // read: written; write: only read
+  uint16_t* v;
+  long long k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  const int32_t* cu_seqlens;  // (num_seqs + 1,); null (write): one row a sequence
+  const int32_t* starts;      // (num_seqs,) first cache position of each sequence; null (read): 0
+  int num_seqs, total_tokens;
+};
+
+struct DecodeFp8Args {
+  CacheFp8 c;
+  const uint16_t* q;
+  const int32_t* kv_lens;
+  int num_splits;
+  float* o_partial;
+  float* lse_partial;
+  int batch, n_q_heads;
+  float scale;
+  int window_left;
+  float softcap;
+  const float* alibi_slopes;
+  int append;  // 1: each sequence holds one token more than kv_lens says (just written)
+};
+
 // Each returns cudaSuccess or the launch error.  Arguments are already
 // validated by the caller.
 cudaError_t launch_prefill(const PrefillArgs& a, const LaunchCtx& ctx);
@@ -124,6 +177,10 @@ cudaError_t launch_quantize(const QuantArgs& a, const LaunchCtx& ctx);
 // transposed; the three share rows and head_dim.
 cudaError_t launch_quantize_qkv(const QuantArgs& q, const QuantArgs& k, const QuantArgs& v,
                                 const LaunchCtx& ctx);
+
+cudaError_t launch_cache_write_fp8(const CacheRowsArgs& a, const LaunchCtx& ctx);
+cudaError_t launch_cache_read_fp8(const CacheRowsArgs& a, const LaunchCtx& ctx);
+cudaError_t launch_decode_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 
 // Resolves the current device's launch context (architecture check, error
 // word, SM count) for a call on `stream`; returns an attn_status code.

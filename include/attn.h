@@ -38,6 +38,7 @@
 #ifndef ATTN_SM103_H
 #define ATTN_SM103_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -58,7 +59,7 @@ typedef enum attn_status {
   ATTN_ERR_LAUNCH = 8,   /* a CUDA runtime call or kernel launch failed          */
   ATTN_ERR_TIMEOUT = 9,  /* a kernel's bounded wait gave up (device error word)  */
   ATTN_ERR_DEVICE = 10,  /* bad block-table entry or kv_len seen by a kernel     */
-  ATTN_ERR_SCRATCH = 11  /* attn_decode_noalloc: partials exceed its fixed buffer */
+  ATTN_ERR_SCRATCH = 11  /* the split partials exceed the buffer (attn_decode_noalloc, _fp8) */
 } attn_status;
 
 /* Name of a status code; never NULL. */
@@ -567,6 +568,167 @@ int attn_decode_noalloc(const attn_bf16* q, const attn_bf16* k_cache, const attn
                         float* o, float* lse, int batch, int n_q_heads, int n_kv_heads,
                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
                         int max_kv_len, float scale, void* stream);
+
+/*
+ * A key/value cache held in 8 bits.
+ *
+ * The pages have no counterpart to the entry points from here to
+ * attn_decode_fp8: the page "FlashAttention for inference: tiled prefill and
+ * split-KV decoding", section "Decode: a different bottleneck", says that
+ * decode is bound by streaming the cache, and section "Interaction with
+ * post-trained models" that FP8 attention scales blocks; a cache in 8 bits
+ * with block scales halves what decode streams.
+ *
+ *   k_cache, v_cache  : e4m3 codes, uint8, 16-byte aligned;
+ *                paged (block_table != NULL): (num_blocks, block_size, n_kv_heads, head_dim)
+ *                contiguous (block_table == NULL): (num_seqs, max_kv_len, n_kv_heads, head_dim)
+ *   k_scales, v_scales: fp32, 4-byte aligned; one for each block of block_size
+ *                tokens and kv head:
+ *                paged: (num_blocks, n_kv_heads)
+ *                contiguous: (num_seqs, ceil(max_kv_len / block_size), n_kv_heads)
+ * A value is code * scale.  block_size is given for a contiguous cache too (the
+ * tokens that share a scale).  block_table, max_blocks_per_seq, num_blocks:
+ * as attn_decode_splitkv (max_blocks_per_seq and num_blocks are ignored
+ * without a block_table).  Nothing has to be initialised: a block's scale is
+ * set when its first slot is written, and what lies in slots that no sequence
+ * has reached is not looked at.
+ * Limits: head_dim in {64, 128, 256}; 1 <= block_size <= 2^20;
+ *   block_size * max_blocks_per_seq <= 2^30; max_kv_len <= 2^30 (and >= 1
+ *   without a block_table).
+ */
+
+/*
+ * attn_cache_write_fp8 -- quantises new keys and values into an 8-bit cache.
+ *
+ * Page: same, section "Minimal implementation" (new keys and values go into
+ * the cache in place; the caller increments the counts afterwards).
+ *
+ *   k, v       : bf16, 16-byte aligned.  Row t (0 <= t < total_tokens) of head
+ *                h starts at k + t * k_token_stride + h * k_head_stride
+ *                (elements; multiples of 8, >= 0), its head_dim values
+ *                contiguous; v likewise.
+ *   cu_seqlens : (num_seqs + 1,) int32, as attn_prefill_varlen: sequence s is
+ *                rows [cu[s], cu[s+1]); or NULL: one row a sequence
+ *                (total_tokens == num_seqs).  A list that breaks the rule is
+ *                clamped and flagged.
+ *   kv_lens    : (num_seqs,) int32 tokens already cached (read, not modified);
+ *                sequence s's rows go to positions kv_lens[s], kv_lens[s]+1, ...
+ *   k_cache, v_cache, k_scales, v_scales: WRITTEN as follows; nothing else changes.
+ * For each block that receives rows, K and V and each head apart: with amax
+ * the largest finite |x| of its new rows, the scale is 2^k with the smallest
+ * k in [-60, 60] for which amax <= 448 * 2^k.  Where the first written slot is
+ * not the block's slot 0, the scale is the larger of that and the block's
+ * present one, and if it grew the codes of the slots before the first written
+ * one become e4m3(code * old scale / new scale).  The new codes are
+ * e4m3(x / scale), to nearest, ties to even; values beyond 448 * scale
+ * (infinities, or |x| > 448 * 2^60) saturate to +-448, NaN stays NaN.  Every
+ * step but the rounding is exact, so the codes do not depend on how a
+ * sequence's rows are divided over calls as long as no block's scale grows.
+ * A sequence whose rows do not fit its capacity, or whose kv_lens is negative,
+ * is flagged and nothing of it is written; a block-table entry outside [0,
+ * num_blocks) is flagged and that block's rows are not written.  Two
+ * sequences must not write the same block, and the call must not overlap, on
+ * the device, another call that reads or writes the same blocks.
+ * Limits: 1 <= num_seqs <= 2^20; 1 <= total_tokens <= 2^24;
+ *   (total_tokens / block_size + 2 num_seqs) * 2 n_kv_heads < 2^31.
+ * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _ALIGN, _ARCH, _LAUNCH.
+ */
+int attn_cache_write_fp8(const attn_bf16* k, const attn_bf16* v, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                         const int32_t* block_table, const int32_t* cu_seqlens,
+                         const int32_t* kv_lens, int num_seqs, int total_tokens, int n_kv_heads,
+                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                         int max_kv_len, void* stream);
+
+/*
+ * attn_cache_read_fp8 -- reads tokens of an 8-bit cache back as bf16.
+ *
+ * Page: same, section "Decode: a different bottleneck" (paged caches).
+ *
+ *   k, v       : bf16 OUTPUTS, strides as attn_cache_write_fp8 but at least
+ *                head_dim wherever there is more than one token or head: row
+ *                cu[s] + i receives position starts[s] + i of sequence s, for
+ *                i < cu[s+1] - cu[s].  Rows outside every sequence are not
+ *                written.
+ *   cu_seqlens : (num_seqs + 1,) int32, as attn_prefill_varlen
+ *   starts     : (num_seqs,) int32 first position read of each sequence, or
+ *                NULL: 0
+ *   total_tokens: rows of k and v
+ * Each value is code * scale rounded to bf16: exact for scales that
+ * attn_cache_write_fp8 set.  A sequence whose positions leave its capacity is
+ * flagged and nothing of it is written; so is a bad block-table entry, for
+ * that block's rows.  Limits and errors as attn_cache_write_fp8.
+ */
+int attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+                        const float* v_scales, attn_bf16* k, attn_bf16* v, int64_t k_token_stride,
+                        int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                        const int32_t* block_table, const int32_t* cu_seqlens,
+                        const int32_t* starts, int num_seqs, int total_tokens, int n_kv_heads,
+                        int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                        int max_kv_len, void* stream);
+
+/*
+ * attn_decode_fp8_splitkv -- attn_decode_splitkv_ex over an 8-bit cache.
+ *
+ * Page: same, section "Decode: a different bottleneck" (split-KV, GQA-aware
+ * key/value sharing, paged caches).
+ *
+ *   q          : (batch, n_q_heads, head_dim) bf16, 16-byte aligned
+ *   k_cache, v_cache, k_scales, v_scales: the cache (num_seqs = batch).  Any
+ *                scales in [2^-60, 2^60] do, not only powers of two.
+ *   kv_lens, num_splits, o_partial, lse_partial, scale, window_left, softcap,
+ *   alibi_slopes: as attn_decode_splitkv_ex, with its split rule
+ * q, the codes and the scales are used as they are (q's bf16 values and the
+ * codes are exact as fp16 operands), the weights with 22 significant bits and
+ * every sum in fp32.  Keys and values of masked positions (past kv_lens, left
+ * of the window) may hold anything, NaN included.
+ * Limits: those of the cache; n_q_heads / n_kv_heads <= 64; batch and
+ *   n_kv_heads <= 65535.
+ * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _GQA, _SPLITS, _ALIGN, _ARCH, _LAUNCH.
+ */
+int attn_decode_fp8_splitkv(const attn_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                            const float* k_scales, const float* v_scales,
+                            const int32_t* block_table, const int32_t* kv_lens, int num_splits,
+                            float* o_partial, float* lse_partial, int batch, int n_q_heads,
+                            int n_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                            int num_blocks, int max_kv_len, float scale, int window_left,
+                            float softcap, const float* alibi_slopes, void* stream);
+
+/* Bytes of workspace that attn_decode_fp8 needs (0 for num_splits = 1, and for
+ * arguments out of range).  Pure host function. */
+size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int head_dim);
+
+/*
+ * attn_decode_fp8 -- a decode step over an 8-bit cache in one call: the new
+ * token's write (optional), the split-KV decode and the combine.
+ *
+ * Page: same, section "Minimal implementation" (append, attend, merge).
+ *
+ *   k_new, v_new: (batch, n_kv_heads, head_dim) bf16, 16-byte aligned: written
+ *                at position kv_lens[b] as attn_cache_write_fp8 does, then
+ *                attended as the last of kv_lens[b] + 1 tokens (what the cache
+ *                then holds of it); or both NULL: nothing is written (the
+ *                cache's pointers are then only read)
+ *   num_splits : >= 1, or 0 for attn_decode_num_splits(batch, n_kv_heads,
+ *                max_kv_len, 0)
+ *   workspace  : attn_decode_fp8_workspace_bytes(num_splits, ...) bytes, 16-byte
+ *                aligned (NULL where that is 0); overwritten.  Calls that may
+ *                overlap on the device need one each.
+ *   workspace_bytes: its size; less than needed is ATTN_ERR_SCRATCH
+ *   o, lse     : (batch, n_q_heads, head_dim) and (batch, n_q_heads) fp32
+ *                outputs, 16- and 4-byte aligned
+ * The results equal attn_cache_write_fp8, attn_decode_fp8_splitkv (over
+ * kv_lens + 1 tokens when appending) and attn_combine.  Other arguments,
+ * limits and errors as those.
+ */
+int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new,
+                    uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                    const int32_t* block_table, const int32_t* kv_lens, int num_splits,
+                    void* workspace, size_t workspace_bytes, float* o, float* lse, int batch,
+                    int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                    int max_blocks_per_seq, int num_blocks, int max_kv_len, float scale,
+                    int window_left, float softcap, const float* alibi_slopes, void* stream);
 
 /* Library version string, e.g. "0.1.0 sm_103a". */
 const char* attn_version(void);

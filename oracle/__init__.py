@@ -20,3 +20,4 @@ from .attention_ref import (  # noqa: F401
     prefill_varlen_rows,
 )
 from . import fp8_ref  # noqa: F401  (FP8 block quantisation and its attention)
+from . import cache_fp8_ref  # noqa: F401  (a key/value cache held in 8 bits)
