@@ -8,6 +8,7 @@ here computes any part of attention.
 from __future__ import annotations
 
 import contextlib
+import functools
 import math
 from typing import Optional
 
@@ -580,16 +581,19 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 # ---------------------------------------------------------------------------
 
 _NO_SCOPE = contextlib.nullcontext()
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
+# The current stream's handle without the Stream object around it, which costs
+# several microseconds a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _scope(t: torch.Tensor, stream):
-    """What a call runs under: t's device current, and `stream` as torch's
-    current stream, so that what the call allocates belongs to that stream
-    (a workspace freed on return may only be reused behind the kernels that
-    still use it)."""
-    dev = t.device
-    here = dev.index == torch.cuda.current_device()
-    if stream is None and here:
+def _scope(dev, stream):
+    """What a call runs under: `dev` current, and `stream` as torch's current
+    stream, so that what the call allocates belongs to that stream (a
+    workspace freed on return may only be reused behind the kernels that still
+    use it)."""
+    if stream is None and dev.index == torch.cuda.current_device():
         return _NO_SCOPE
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(dev))
@@ -603,13 +607,16 @@ def _scope(t: torch.Tensor, stream):
     return stack
 
 
-def _need_on(t: torch.Tensor, name: str, dtype, ndim: int, dev) -> None:
-    """_need, and on this device; one test where everything is right."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.device == dev
-            and t.is_contiguous()):
-        return
-    _need(t, name, dtype, ndim)
-    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _need_all(dev, *checks) -> None:
+    """Each of (tensor, name, dtype, shape): a contiguous tensor of that type
+    and shape on dev.  A call checks all of its tensors in one test and comes
+    here only if it fails, to say what is wrong."""
+    for t, name, dtype, shape in checks:
+        _need(t, name, dtype, len(shape))
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _rows_stride(t: torch.Tensor, name: str, dev) -> None:
@@ -627,39 +634,61 @@ def _rows_stride(t: torch.Tensor, name: str, dev) -> None:
                          f"got strides {st}")
 
 
-def _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, num_seqs: int):
+def _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_size, num_seqs: int):
     """Checks an 8-bit cache; returns (its four pointers and the block
     table's, (block_size, max_blocks, num_blocks, capacity))."""
-    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
-        _need(k_cache, "k_cache", torch.uint8, 4)
-    dev = k_cache.device
-    _need_on(k_cache, "k_cache", torch.uint8, 4, dev)
-    _need_on(v_cache, "v_cache", torch.uint8, 4, dev)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _need(k_cache, "k_cache", _U8, 4)
     shape = k_cache.shape
-    if v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
+    n, rows, n_kv = shape[:3]
     if block_table is not None:
-        _need_on(block_table, "block_table", torch.int32, 2, dev)
+        if (not isinstance(block_table, torch.Tensor) or block_table.dtype is not _I32
+                or block_table.dim() != 2 or not block_table.is_contiguous()
+                or block_table.device != dev):
+            _need_all(dev, (block_table, "block_table", _I32, (num_seqs, "max_blocks")))
         if block_table.shape[0] != num_seqs:
             raise ValueError("block_table must have one row per sequence")
-        if block_size is not None and block_size != shape[1]:
-            raise ValueError(f"block_size {block_size} does not match the paged cache's {shape[1]}")
-        geom = (shape[1], block_table.shape[1], shape[0], shape[1] * block_table.shape[1])
-        want, bt = (shape[0], shape[2]), block_table.data_ptr()
+        if block_size is not None and block_size != rows:
+            raise ValueError(f"block_size {block_size} does not match the paged cache's {rows}")
+        most = block_table.shape[1]
+        geom, want, bt = (rows, most, n, rows * most), (n, n_kv), block_table.data_ptr()
     else:
-        if shape[0] != num_seqs:
+        if n != num_seqs:
             raise ValueError("a contiguous cache must be (num_seqs, L, n_kv, d)")
         if block_size is None or block_size < 1:
             raise ValueError("block_size (tokens that share a scale) is needed for a contiguous "
                              "cache")
-        geom = (block_size, 0, 0, shape[1])
-        want, bt = (num_seqs, -(-shape[1] // block_size), shape[2]), None
-    _need_on(k_scales, "k_scales", torch.float32, len(want), dev)
-    _need_on(v_scales, "v_scales", torch.float32, len(want), dev)
-    if tuple(k_scales.shape) != want or tuple(v_scales.shape) != want:
-        raise ValueError(f"k_scales and v_scales must have shape {want}")
+        geom, want, bt = (block_size, 0, 0, rows), (n, -(-rows // block_size), n_kv), None
+    try:
+        fine = (k_cache.dtype is _U8 and v_cache.dtype is _U8 and k_scales.dtype is _F32
+                and v_scales.dtype is _F32 and v_cache.shape == shape and k_scales.shape == want
+                and v_scales.shape == want and k_cache.device == dev and v_cache.device == dev
+                and k_scales.device == dev and v_scales.device == dev and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _need_all(dev, (k_cache, "k_cache", _U8, shape), (v_cache, "v_cache", _U8, shape),
+                  (k_scales, "k_scales", _F32, want), (v_scales, "v_scales", _F32, want))
     return (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             bt), geom
+
+
+def _lens(t, name: str, n, dev) -> int:
+    """An int32 vector of n entries (None: any) on dev; its pointer."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 1
+            or t.device != dev or not t.is_contiguous()):
+        _need_all(dev, (t, name, _I32, (n,)))
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _splits(batch: int, n_kv_heads: int, max_kv_len: int, device: int) -> int:
+    """The split-count policy on a device (which has to be current)."""
+    return decode_num_splits(batch, n_kv_heads, max_kv_len)
 
 
 def cache_write_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -689,26 +718,23 @@ def cache_write_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Ten
     _rows_stride(v_new, "v_new", dev)
     if k_new.shape != v_new.shape:
         raise ValueError("k_new and v_new must have the same shape")
-    _need_on(kv_lens, "kv_lens", torch.int32, 1, dev)
+    lens = _lens(kv_lens, "kv_lens", None, dev)
     B = kv_lens.shape[0]
-    ptrs, geom = _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
+    ptrs, geom = _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
     ks, vs = k_new.stride(), v_new.stride()
     if cu_seqlens is not None:
-        _need_on(cu_seqlens, "cu_seqlens", torch.int32, 1, dev)
-        if cu_seqlens.shape[0] != B + 1:
-            raise ValueError("cu_seqlens must have one entry more than kv_lens")
         n_kv, total, d = k_new.shape
-        strides, cu = (ks[1], ks[0], vs[1], vs[0]), cu_seqlens.data_ptr()
+        strides, cu = (ks[1], ks[0], vs[1], vs[0]), _lens(cu_seqlens, "cu_seqlens", B + 1, dev)
     else:
         total, n_kv, d = k_new.shape
         if total != B:
             raise ValueError("without cu_seqlens k_new and v_new must be (B, n_kv, d)")
         strides, cu = (ks[0], ks[1], vs[0], vs[1]), None
-    if k_cache.shape[2] != n_kv or k_cache.shape[3] != d or k_cache.device != dev:
-        raise ValueError("the cache's heads, head_dim or device do not match k_new")
-    with _scope(k_new, stream):
+    if k_cache.shape[2] != n_kv or k_cache.shape[3] != d:
+        raise ValueError("the cache's heads or head_dim do not match k_new")
+    with _scope(dev, stream):
         st = lib().attn_cache_write_fp8(k_new.data_ptr(), v_new.data_ptr(), *strides, *ptrs, cu,
-                                        kv_lens.data_ptr(), B, total, n_kv, d, *geom, _stream(None))
+                                        lens, B, total, n_kv, d, *geom, _raw_stream(dev.index))
     check("attn_cache_write_fp8", st)
 
 
@@ -725,61 +751,57 @@ def cache_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch
     into ``k_out`` / ``v_out`` when given (rows contiguous, other strides
     multiples of 8); rows outside every sequence are left as they were.
     """
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    dev, B = cu_seqlens.device, cu_seqlens.shape[0] - 1
-    ptrs, geom = _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
-    if k_cache.device != dev:
-        raise ValueError(f"the cache must be on {dev}, got {k_cache.device}")
-    if starts is not None:
-        _need_on(starts, "starts", torch.int32, 1, dev)
-        if starts.shape[0] != B:
-            raise ValueError("starts must have one entry per sequence")
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        _need(k_cache, "k_cache", _U8, 4)
+    dev = k_cache.device
+    cu = _lens(cu_seqlens, "cu_seqlens", None, dev)
+    B = cu_seqlens.shape[0] - 1
+    ptrs, geom = _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
+    first = None if starts is None else _lens(starts, "starts", B, dev)
     n_kv, d, total = k_cache.shape[2], k_cache.shape[3], int(total)
-    with _scope(k_cache, stream):
+    with _scope(dev, stream):
         if k_out is None:
             k_out = torch.empty((n_kv, total, d), dtype=_BF16, device=dev)
         if v_out is None:
             v_out = torch.empty((n_kv, total, d), dtype=_BF16, device=dev)
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             _rows_stride(t, name, dev)
-            if tuple(t.shape) != (n_kv, total, d):
+            if t.shape != (n_kv, total, d):
                 raise ValueError(f"{name} must have shape {(n_kv, total, d)}")
         ks, vs = k_out.stride(), v_out.stride()
         st = lib().attn_cache_read_fp8(*ptrs[:4], k_out.data_ptr(), v_out.data_ptr(), ks[1], ks[0],
-                                       vs[1], vs[0], ptrs[4], cu_seqlens.data_ptr(),
-                                       None if starts is None else starts.data_ptr(), B, total,
-                                       n_kv, d, *geom, _stream(None))
+                                       vs[1], vs[0], ptrs[4], cu, first, B, total, n_kv, d, *geom,
+                                       _raw_stream(dev.index))
     check("attn_cache_read_fp8", st)
     return k_out, v_out
 
 
 def _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table, block_size,
                      max_kv_len, scale, alibi_slopes):
-    """Checks shared by the decodes over an 8-bit cache; returns (cache and
-    block table pointers, sizes from batch to max_kv_len, scale, slopes)."""
-    _need(q, "q", _BF16, 3)
+    """Checks shared by the decodes over an 8-bit cache; returns (cache, block
+    table and kv_lens pointers, sizes from batch to max_kv_len, scale, slopes)."""
+    if not isinstance(q, torch.Tensor) or q.dtype is not _BF16 or q.dim() != 3 or \
+            not q.is_cuda or not q.is_contiguous():
+        _need(q, "q", _BF16, 3)
     dev = q.device
     B, n_q, d = q.shape
-    _need_on(kv_lens, "kv_lens", torch.int32, 1, dev)
-    if kv_lens.shape[0] != B:
-        raise ValueError("kv_lens must have one entry per sequence")
-    ptrs, geom = _cache_fp8(k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
-    if k_cache.shape[3] != d or k_cache.device != dev:
-        raise ValueError("the cache's head_dim or device does not match q")
-    capacity = geom[3]
-    if block_table is not None and max_kv_len is not None:
-        geom = (*geom[:3], int(max_kv_len))
-    elif max_kv_len is not None and max_kv_len > capacity:
-        raise ValueError("max_kv_len exceeds the contiguous cache's length")
+    lens = _lens(kv_lens, "kv_lens", B, dev)
+    ptrs, geom = _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
+    n_kv, dk = k_cache.shape[2:]
+    if dk != d:
+        raise ValueError("the cache's head_dim does not match q")
+    if max_kv_len is not None:
+        if block_table is not None:
+            geom = (*geom[:3], int(max_kv_len))
+        elif max_kv_len > geom[3]:
+            raise ValueError("max_kv_len exceeds the contiguous cache's length")
     al = None
     if alibi_slopes is not None:
-        _need_on(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
-        if alibi_slopes.numel() != n_q:
-            raise ValueError("alibi_slopes must have one slope per query head")
+        _need_all(dev, (alibi_slopes, "alibi_slopes", _F32, (n_q,)))
         al = alibi_slopes.data_ptr()
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    return ptrs, (B, n_q, k_cache.shape[2], d, *geom), scale, al
+    return (*ptrs, lens), (B, n_q, n_kv, d, *geom), scale, al
 
 
 def decode_fp8_splitkv(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -800,27 +822,24 @@ def decode_fp8_splitkv(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                                               block_table, block_size, max_kv_len, scale,
                                               alibi_slopes)
     B, n_q, n_kv, d = sizes[:4]
-    with _scope(q, stream):
+    dev = q.device
+    with _scope(dev, stream):
         if num_splits == 0:
-            num_splits = decode_num_splits(B, n_kv, sizes[7])
+            num_splits = _splits(B, n_kv, sizes[7], dev.index)
         if o_partial is None:
-            o_partial = torch.empty((num_splits, B, n_q, d), dtype=torch.float32, device=q.device)
+            o_partial = torch.empty((num_splits, B, n_q, d), dtype=_F32, device=dev)
         if lse_partial is None:
-            lse_partial = torch.empty((num_splits, B, n_q), dtype=torch.float32, device=q.device)
-        _need_on(o_partial, "o_partial", torch.float32, 4, q.device)
-        _need_on(lse_partial, "lse_partial", torch.float32, 3, q.device)
-        if (tuple(o_partial.shape) != (num_splits, B, n_q, d)
-                or tuple(lse_partial.shape) != (num_splits, B, n_q)):
-            raise ValueError("partial buffers must be (num_splits, B, n_q, d) and "
-                             "(num_splits, B, n_q)")
-        st = lib().attn_decode_fp8_splitkv(q.data_ptr(), *ptrs, kv_lens.data_ptr(), num_splits,
-                                           o_partial.data_ptr(), lse_partial.data_ptr(), *sizes,
-                                           scale, window_left, softcap, al, _stream(None))
+            lse_partial = torch.empty((num_splits, B, n_q), dtype=_F32, device=dev)
+        _need_all(dev, (o_partial, "o_partial", _F32, (num_splits, B, n_q, d)),
+                  (lse_partial, "lse_partial", _F32, (num_splits, B, n_q)))
+        st = lib().attn_decode_fp8_splitkv(q.data_ptr(), *ptrs, num_splits, o_partial.data_ptr(),
+                                           lse_partial.data_ptr(), *sizes, scale, window_left,
+                                           softcap, al, _raw_stream(dev.index))
     check("attn_decode_fp8_splitkv", st)
     return o_partial, lse_partial
 
 
-def _decode_fp8(name, q, new_kv, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
+def _decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
                 num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left, softcap,
                 alibi_slopes, block_size):
     ptrs, sizes, scale, al = _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens,
@@ -829,35 +848,32 @@ def _decode_fp8(name, q, new_kv, k_cache, v_cache, k_scales, v_scales, kv_lens, 
     B, n_q, n_kv, d = sizes[:4]
     dev = q.device
     kn = vn = None
-    if new_kv is not None:
-        for t, what in zip(new_kv, ("k_new", "v_new")):
-            _need_on(t, what, _BF16, 3, dev)
-            if tuple(t.shape) != (B, n_kv, d):
-                raise ValueError(f"{what} must be (batch, n_kv_heads, head_dim)")
-        kn, vn = new_kv[0].data_ptr(), new_kv[1].data_ptr()
-    with _scope(q, stream):
+    if k_new is not None:
+        _need_all(dev, (k_new, "k_new", _BF16, (B, n_kv, d)), (v_new, "v_new", _BF16, (B, n_kv, d)))
+        kn, vn = k_new.data_ptr(), v_new.data_ptr()
+    with _scope(dev, stream):
         if num_splits == 0:
-            num_splits = decode_num_splits(B, n_kv, sizes[7])
+            num_splits = _splits(B, n_kv, sizes[7], dev.index)
         if out is None:
-            out = torch.empty((B, n_q, d), dtype=torch.float32, device=dev)
-        if lse is None:
-            lse = torch.empty((B, n_q), dtype=torch.float32, device=dev)
-        _need_on(out, "out", torch.float32, 3, dev)
-        _need_on(lse, "lse", torch.float32, 2, dev)
-        if tuple(out.shape) != (B, n_q, d) or tuple(lse.shape) != (B, n_q):
-            raise ValueError("out and lse must be (B, n_q, d) and (B, n_q)")
-        if workspace is None:
-            # out of range counts are refused by the call
-            n = lib().attn_decode_fp8_workspace_bytes(num_splits, B, n_q, d) \
-                if 1 < num_splits <= ATTN_MAX_SPLITS else 0
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            out = torch.empty((B, n_q, d), dtype=_F32, device=dev)
         else:
-            _need_on(workspace, "workspace", torch.uint8, 1, dev)
+            _need_all(dev, (out, "out", _F32, (B, n_q, d)))
+        if lse is None:
+            lse = torch.empty((B, n_q), dtype=_F32, device=dev)
+        else:
+            _need_all(dev, (lse, "lse", _F32, (B, n_q)))
+        if workspace is not None:
+            _need(workspace, "workspace", _U8, 1)
+            _need_all(dev, (workspace, "workspace", _U8, workspace.shape))
+        elif 1 < num_splits <= ATTN_MAX_SPLITS:  # other counts need none, or are refused below
+            rows = num_splits * B * n_q          # attn_decode_fp8_workspace_bytes
+            workspace = torch.empty((rows * d * 4 + 255) // 256 * 256 + rows * 4, dtype=_U8,
+                                    device=dev)
         wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-        st = lib().attn_decode_fp8(q.data_ptr(), kn, vn, *ptrs, kv_lens.data_ptr(), num_splits, wp,
-                                   wn, out.data_ptr(), lse.data_ptr(), *sizes, scale, window_left,
-                                   softcap, al, _stream(None))
-    check(name, st)
+        st = lib().attn_decode_fp8(q.data_ptr(), kn, vn, *ptrs, num_splits, wp, wn, out.data_ptr(),
+                                   lse.data_ptr(), *sizes, scale, window_left, softcap, al,
+                                   _raw_stream(dev.index))
+    check("attn_decode_fp8", st)
     return out, lse
 
 
@@ -873,9 +889,9 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     (``attn_decode_fp8``): returns (O (B, n_q, d), LSE (B, n_q)), fp32.
     Arguments as :func:`decode_fp8_splitkv`; ``workspace`` (uint8, allocated
     when not given) holds the split partials."""
-    return _decode_fp8("attn_decode_fp8", q, None, k_cache, v_cache, k_scales, v_scales, kv_lens,
-                       block_table, num_splits, max_kv_len, scale, out, lse, workspace, stream,
-                       window_left, softcap, alibi_slopes, block_size)
+    return _decode_fp8(q, None, None, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
+                       num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left,
+                       softcap, alibi_slopes, block_size)
 
 
 def decode_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -893,6 +909,8 @@ def decode_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     :func:`cache_write_fp8` does, and its query attends over kv_lens[b] + 1
     tokens (``attn_decode_fp8``).  Returns (O, LSE) as :func:`decode_fp8`;
     kv_lens is left to the caller to increment."""
-    return _decode_fp8("attn_decode_fp8", q, (k_new, v_new), k_cache, v_cache, k_scales, v_scales,
-                       kv_lens, block_table, num_splits, max_kv_len, scale, out, lse, workspace,
-                       stream, window_left, softcap, alibi_slopes, block_size)
+    if k_new is None or v_new is None:
+        raise TypeError("k_new and v_new must be torch.Tensors")
+    return _decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
+                       num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left,
+                       softcap, alibi_slopes, block_size)
