@@ -622,6 +622,11 @@ int validate_decode_fp8(const attn::DecodeFp8Args& a) {
       a.batch < 1 || a.batch > 65535 || a.n_q_heads < 1 || !valid_scale(a.scale))
     return ATTN_ERR_SHAPE;
   if (st == ATTN_ERR_HEADDIM) return st;
+  // the decode counts the cache's rows (one token of one head) in 32 bits
+  const unsigned long long tokens =
+      a.c.block_table ? (unsigned long long)a.c.num_blocks * a.c.block_size
+                      : (unsigned long long)a.batch * a.c.max_kv_len;
+  if (tokens > 0xffffffffull / a.c.n_kv_heads) return ATTN_ERR_SHAPE;
   if (a.n_q_heads % a.c.n_kv_heads != 0 || a.n_q_heads / a.c.n_kv_heads > 64) return ATTN_ERR_GQA;
   if (a.num_splits < 0 || a.num_splits > ATTN_MAX_SPLITS) return ATTN_ERR_SPLITS;
   if (st != ATTN_OK) return st;

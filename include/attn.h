@@ -684,7 +684,7 @@ int attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const fl
  * every sum in fp32.  Keys and values of masked positions (past kv_lens, left
  * of the window) may hold anything, NaN included.
  * Limits: those of the cache; n_q_heads / n_kv_heads <= 64; batch and
- *   n_kv_heads <= 65535.
+ *   n_kv_heads <= 65535; the cache's slots times n_kv_heads below 2^32.
  * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _GQA, _SPLITS, _ALIGN, _ARCH, _LAUNCH.
  */
 int attn_decode_fp8_splitkv(const attn_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
