@@ -62,7 +62,7 @@ SIGNATURES = {
                             + [c_void_p]),
     "attn_decode_fp8_splitkv": (c_int, [c_void_p] * 7 + [c_int] + [c_void_p] * 2 + [c_int] * 8
                                 + [c_float, c_int, c_float, c_void_p, c_void_p]),
-    "attn_decode_fp8_workspace_bytes": (c_size_t, [c_int] * 4),
+    "attn_decode_fp8_workspace_bytes": (c_size_t, [c_int] * 7),
     "attn_decode_fp8": (c_int, [c_void_p] * 9 + [c_int, c_void_p, c_size_t] + [c_void_p] * 2
                         + [c_int] * 8 + [c_float, c_int, c_float, c_void_p, c_void_p]),
     "attn_decode_noalloc": (c_int, [c_void_p] * 5 + [c_int] + [c_void_p] * 2 + [c_int] * 8

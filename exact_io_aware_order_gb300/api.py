@@ -609,9 +609,11 @@ def _scope(dev, stream):
 
 def _need_all(dev, *checks) -> None:
     """Each of (tensor, name, dtype, shape): a contiguous tensor of that type
-    and shape on dev.  A call checks all of its tensors in one test and comes
-    here only if it fails, to say what is wrong."""
+    and shape on dev."""
     for t, name, dtype, shape in checks:
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.device == dev and t.is_contiguous()):
+            continue
         _need(t, name, dtype, len(shape))
         if t.device != dev:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
@@ -683,6 +685,17 @@ def _lens(t, name: str, n, dev) -> int:
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
     return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(num_splits: int, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                     max_kv_len: int, window_left: int, device: int) -> int:
+    """attn_decode_fp8_workspace_bytes on a device (which has to be current); 0
+    for counts that the call refuses."""
+    if not 0 <= num_splits <= ATTN_MAX_SPLITS:
+        return 0
+    return lib().attn_decode_fp8_workspace_bytes(num_splits, batch, n_q_heads, n_kv_heads, head_dim,
+                                                 max_kv_len, window_left)
 
 
 @functools.lru_cache(maxsize=256)
@@ -852,8 +865,6 @@ def _decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, 
         _need_all(dev, (k_new, "k_new", _BF16, (B, n_kv, d)), (v_new, "v_new", _BF16, (B, n_kv, d)))
         kn, vn = k_new.data_ptr(), v_new.data_ptr()
     with _scope(dev, stream):
-        if num_splits == 0:
-            num_splits = _splits(B, n_kv, sizes[7], dev.index)
         if out is None:
             out = torch.empty((B, n_q, d), dtype=_F32, device=dev)
         else:
@@ -865,10 +876,9 @@ def _decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, 
         if workspace is not None:
             _need(workspace, "workspace", _U8, 1)
             _need_all(dev, (workspace, "workspace", _U8, workspace.shape))
-        elif 1 < num_splits <= ATTN_MAX_SPLITS:  # other counts need none, or are refused below
-            rows = num_splits * B * n_q          # attn_decode_fp8_workspace_bytes
-            workspace = torch.empty((rows * d * 4 + 255) // 256 * 256 + rows * 4, dtype=_U8,
-                                    device=dev)
+        else:
+            n = _workspace_bytes(num_splits, B, n_q, n_kv, d, sizes[7], window_left, dev.index)
+            workspace = torch.empty(n, dtype=_U8, device=dev) if n else None
         wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
         st = lib().attn_decode_fp8(q.data_ptr(), kn, vn, *ptrs, num_splits, wp, wn, out.data_ptr(),
                                    lse.data_ptr(), *sizes, scale, window_left, softcap, al,
@@ -887,8 +897,9 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                block_size: Optional[int] = None):
     """Decode over an 8-bit cache, split and combined in one call
     (``attn_decode_fp8``): returns (O (B, n_q, d), LSE (B, n_q)), fp32.
-    Arguments as :func:`decode_fp8_splitkv`; ``workspace`` (uint8, allocated
-    when not given) holds the split partials."""
+    Arguments as :func:`decode_fp8_splitkv`, except that num_splits 0 lets the
+    library divide the tokens of all sequences in equal shares; ``workspace``
+    (uint8, allocated when not given) holds the partials."""
     return _decode_fp8(q, None, None, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
                        num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left,
                        softcap, alibi_slopes, block_size)

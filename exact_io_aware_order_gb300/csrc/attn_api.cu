@@ -644,11 +644,35 @@ attn::CacheFp8 cache_fp8(const uint8_t* k, const uint8_t* v, const float* ks, co
                         max_kv_len};
 }
 
-// Where the LSE partials begin in attn_decode_fp8's workspace (after the
-// output partials), and its size.
-size_t fp8_lse_offset(int num_splits, int batch, int n_q_heads, int head_dim) {
-  const size_t rows = (size_t)num_splits * (size_t)batch * (size_t)n_q_heads;
+// attn_decode_fp8's workspace: output partials, LSE partials from the next
+// 256-byte boundary and, with shares, the pairs' blocks from the one after.
+size_t fp8_lse_offset(size_t rows, int head_dim) {
   return (rows * (size_t)head_dim * sizeof(float) + 255) / 256 * 256;
+}
+size_t fp8_pairs_offset(size_t rows) { return (rows * sizeof(float) + 255) / 256 * 256; }
+
+// Blocks that share a decode's tiles (num_splits = 0): all that are resident
+// together, but none for less than kFp8MinTiles tiles, which it could not spread
+// over its warps and which would cost the combine more than they save.  0 where
+// a pair is one block's work: sequences of up to kFp8OneBlock tokens, where the
+// combine alone would cost more, and batches beyond the shares' scan.
+constexpr int kFp8MinTiles = 8, kFp8OneBlock = 512;
+int fp8_parts(int batch, int n_q_heads, int n_kv_heads, int head_dim, long long max_len,
+              int window_left, int num_sms) {
+  if (batch > attn::kMaxSharedBatch) return 0;
+  long long most = max_len;
+  if (window_left >= 0) most = std::min(most, window_left + 1LL);
+  if (most <= kFp8OneBlock) return 0;
+  const long long tiles = (most + 31) / 32 * batch * n_kv_heads;
+  const long long parts = (tiles + kFp8MinTiles - 1) / kFp8MinTiles;
+  const int top = attn::decode_fp8_max_parts(n_q_heads, n_kv_heads, head_dim, num_sms);
+  return (int)std::min(parts, (long long)top);
+}
+size_t fp8_shares_bytes(int parts, int batch, int n_q_heads, int n_kv_heads, int head_dim) {
+  if (parts == 0) return 0;
+  const size_t rows = 2 * (size_t)parts * (size_t)(n_q_heads / n_kv_heads);
+  return fp8_lse_offset(rows, head_dim) + fp8_pairs_offset(rows) +
+         (size_t)batch * (size_t)n_kv_heads * sizeof(int2);
 }
 
 }  // namespace
@@ -717,10 +741,25 @@ int attn_decode_fp8_splitkv(const attn_bf16* q, const uint8_t* k_cache, const ui
   return ATTN_OK;
 }
 
-size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int head_dim) {
-  if (num_splits <= 1 || batch < 1 || n_q_heads < 1 || head_dim < 1) return 0;
-  return fp8_lse_offset(num_splits, batch, n_q_heads, head_dim) +
-         (size_t)num_splits * (size_t)batch * (size_t)n_q_heads * sizeof(float);
+size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int n_kv_heads,
+                                       int head_dim, int max_kv_len, int window_left) {
+  if (num_splits < 0 || num_splits == 1 || batch < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
+      head_dim < 1)
+    return 0;
+  if (num_splits > 1) {
+    const size_t rows = (size_t)num_splits * (size_t)batch * (size_t)n_q_heads;
+    return fp8_lse_offset(rows, head_dim) + rows * sizeof(float);
+  }
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  // with or without an appended token
+  const int parts =
+      fp8_parts(batch, n_q_heads, n_kv_heads, head_dim, (long long)max_kv_len + 1, window_left, sms);
+  return fp8_shares_bytes(parts, batch, n_q_heads, n_kv_heads, head_dim);
 }
 
 int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new,
@@ -751,20 +790,35 @@ int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16*
   }
   DeviceState* ds = device_state(&st);
   if (!ds) return st;
-  if (a.num_splits == 0) a.num_splits = split_policy(batch, n_kv_heads, max_kv_len, ds->num_sms);
-  const int S = a.num_splits;
-  if (S > 1) {
-    if (workspace_bytes < attn_decode_fp8_workspace_bytes(S, batch, n_q_heads, head_dim))
-      return ATTN_ERR_SCRATCH;
+  int S = num_splits;
+  if (S == 0) {
+    a.parts = fp8_parts(batch, n_q_heads, n_kv_heads, head_dim, (long long)max_kv_len + a.append,
+                        window_left, ds->num_sms);
+    S = a.num_splits = 1;  // without shares
+  }
+  if (S > 1 || a.parts > 0) {
+    const size_t rows =
+        a.parts > 0 ? 2 * (size_t)a.parts * (size_t)(n_q_heads / n_kv_heads)
+                    : (size_t)S * (size_t)batch * (size_t)n_q_heads;
+    const size_t need =
+        a.parts > 0 ? fp8_shares_bytes(a.parts, batch, n_q_heads, n_kv_heads, head_dim)
+                    : fp8_lse_offset(rows, head_dim) + rows * sizeof(float);
+    if (workspace_bytes < need) return ATTN_ERR_SCRATCH;
     if (!workspace) return ATTN_ERR_NULL;
-    a.o_partial = static_cast<float*>(workspace);
-    a.lse_partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
-                                             fp8_lse_offset(S, batch, n_q_heads, head_dim));
+    unsigned char* at = static_cast<unsigned char*>(workspace);
+    a.o_partial = reinterpret_cast<float*>(at);
+    at += fp8_lse_offset(rows, head_dim);
+    a.lse_partial = reinterpret_cast<float*>(at);
+    a.pair_blocks = reinterpret_cast<int2*>(at + fp8_pairs_offset(rows));
+    a.o_final = o;
+    a.lse_final = lse;
   }
   const attn::LaunchCtx ctx = make_ctx(stream, ds);
   if (append && attn::launch_cache_write_fp8(w, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
   if (attn::launch_decode_fp8(a, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  if (S > 1) {  // one split's partial is the result
+  if (a.parts > 0) {
+    if (attn::launch_combine_fp8(a, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  } else if (S > 1) {  // one split's partial is the result
     attn::CombineArgs c{a.o_partial, a.lse_partial, S, batch, n_q_heads, head_dim, o, lse};
     if (attn::launch_combine(c, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
   }

@@ -164,7 +164,16 @@ struct DecodeFp8Args {
   float softcap;
   const float* alibi_slopes;
   int append;  // 1: each sequence holds one token more than kv_lens says (just written)
+  // Shares (parts > 0; num_splits is then not used): the tiles of all pairs in
+  // equal shares for `parts` blocks.  o_partial / lse_partial hold two partials
+  // (n_q_heads / n_kv_heads rows each) a block, pair_blocks (batch, n_kv_heads)
+  // the first and last block of each pair; results go to o_final / lse_final.
+  int parts = 0;
+  float* o_final = nullptr;
+  float* lse_final = nullptr;
+  int2* pair_blocks = nullptr;
 };
+constexpr int kMaxSharedBatch = 1024;  // sequences a block scans to find its share
 
 // Each returns cudaSuccess or the launch error.  Arguments are already
 // validated by the caller.
@@ -181,6 +190,10 @@ cudaError_t launch_quantize_qkv(const QuantArgs& q, const QuantArgs& k, const Qu
 cudaError_t launch_cache_write_fp8(const CacheRowsArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_cache_read_fp8(const CacheRowsArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_decode_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
+// The combine of the shares, and the most blocks that share an 8-bit decode's
+// tiles (those that are resident together).
+cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
+int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms);
 
 // Resolves the current device's launch context (architecture check, error
 // word, SM count) for a call on `stream`; returns an attn_status code.

@@ -183,7 +183,6 @@ __global__ void __launch_bounds__(kThreads) cache_write_fp8_kernel(const RowsKPa
   __shared__ uint32_t s_amax[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  grid_dep_launch();
   check_cu_seqlens(p);
   const int wpu = p.warps_per_unit;
   const int sub = warp % wpu;  // this warp among its unit's
@@ -270,7 +269,6 @@ __global__ void __launch_bounds__(kThreads) cache_read_fp8_kernel(const RowsKPar
   constexpr int kSteps = kChunkRows / kRowsPerStep;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  grid_dep_launch();
   check_cu_seqlens(p);
   const int wpu = p.warps_per_unit;
   const int sub = warp % wpu;

@@ -71,10 +71,10 @@ __host__ __device__ constexpr int q_smem_bytes(int D, bool wide, int groups) {
   return q_in_smem(D, wide) ? groups * (D / 32) * 32 * (wide ? 32 : 16) : 0;
 }
 // Blocks that share an SM, by their registers.
-constexpr int blocks_per_sm(int D, bool wide) { return D == 256 ? 2 : (wide ? 3 : 4); }
+constexpr int blocks_per_sm(int D, bool wide) { return D == 256 ? 2 : 3; }
 
 // Half tiles of a warp's ring: what those blocks' shared memory holds.
-constexpr int ring_slots(int D) { return D == 64 ? 6 : 3; }
+constexpr int ring_slots(int D) { return D == 64 ? 8 : (D == 128 ? 4 : 3); }
 
 template <int D>
 struct Smem {
@@ -201,6 +201,44 @@ struct DecodeFp8KParams {
   uint32_t* err_word;
 };
 
+// The tokens a sequence's query attends to.
+struct Span {
+  int len;     // with the appended token
+  int lo_tok;  // first token of the window
+  int lo16;    // rounded down to the split granule
+};
+__device__ __forceinline__ Span span_of(const DecodeFp8Args& a, int len, uint32_t* err_word) {
+  const long long capacity = a.c.capacity();
+  if (len < 0 || (long long)len + a.append > capacity) {
+    if (err_word) atomicOr(err_word, kErrKvLen);
+    len = len < 0 ? 0 : (int)capacity - a.append;
+  }
+  Span s;
+  s.len = len + a.append;
+  s.lo_tok = a.window_left >= 0 ? max(0, s.len - 1 - a.window_left) : 0;
+  s.lo16 = s.lo_tok / kSplitGranule * kSplitGranule;
+  return s;
+}
+__device__ __forceinline__ int tiles_of(const Span& s) {
+  return (s.len - s.lo16 + kTile - 1) / kTile;
+}
+
+// Two ways to divide the work.  With `parts` 0 block (split, kv head, sequence)
+// takes one split of the C header's rule.  With parts > 0 the tiles of all
+// (sequence, kv head) pairs form one list that `parts` blocks take equal shares
+// of, so that no length, however different from the others, leaves an SM idle.
+// A share is a run of segments, each a part of one pair.  A segment that is a
+// whole pair is the result; of the others a block has at most two, its first
+// (which began in an earlier block: partial slot 2 p) and its last (slot 2 p + 1).
+// The block that holds a pair's first tile notes the pair's first and last block
+// for the combine.
+//
+// x / y; the 64-bit division is a long sequence, and almost no list needs it.
+__device__ __forceinline__ long long div_small(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+
 // kWide: more than 8 query heads per kv head (up to 64).  The four warps form G
 // teams, one for each 16 heads; team rg's warps take the tiles in turn, and the
 // teams copy the same tiles each for itself (they are bound by arithmetic).
@@ -210,8 +248,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   using L = Smem<D>;
   const DecodeFp8Args& a = kp.a;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-  const int S = a.num_splits, n_kv = a.c.n_kv_heads, bs = a.c.block_size;
+  const int n_kv = a.c.n_kv_heads, bs = a.c.block_size;
   const int g = a.n_q_heads / n_kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = !kWide ? 1 : (g <= 16 ? 1 : (g <= 32 ? 2 : 4));
@@ -221,32 +258,138 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- this split's tokens (split rule: see the C header) ----
-  const long long capacity = a.c.capacity();
-  int len = a.kv_lens[b];
-  if (len < 0 || (long long)len + a.append > capacity) {
-    if (threadIdx.x == 0 && split == 0) atomicOr(kp.err_word, kErrKvLen);
-    len = len < 0 ? 0 : (int)capacity - a.append;
+  int b, kvh;             // the segment's pair
+  Span sp;
+  int tile, seg_tiles;    // its first tile in the pair and how many
+  int pair_tiles = 0;     // (shares) tiles of the pair
+  // (shares) Of the list: where this block is and up to where it goes; the first
+  // `more` blocks that take part have `share` + 1 tiles, the others `share`.
+  long long pos = 0, end = 0, share = 0;
+  int more = 0;
+  if (a.parts == 0) {
+    b = blockIdx.z, kvh = blockIdx.y;
+    sp = span_of(a, a.kv_lens[b], threadIdx.x == 0 && blockIdx.x == 0 ? kp.err_word : nullptr);
+    tile = 0, seg_tiles = 0;  // set below, in tokens
+  } else {
+    // Tiles before each sequence (of one head): every warp scans the batch for
+    // itself, 32 sequences at a time (twice, where there are more: for the whole
+    // and for its place).
+    long long all = 0;
+    int raw = 0, n = 0, scan = 0;  // this lane's length, tiles, tiles up to it (32 sequences)
+    auto scan32 = [&](int i0, bool report) {
+      const int i = i0 + lane;
+      raw = n = 0;
+      if (i < a.batch) {
+        raw = a.kv_lens[i];
+        n = tiles_of(span_of(a, raw, report ? kp.err_word : nullptr));
+        // A sequence without tokens: o = 0, lse = -inf, written by one of the blocks.
+        if (n == 0 && report && i % a.parts == (int)blockIdx.x) {
+          for (int e = 0; e < a.n_q_heads * D; ++e)
+            a.o_final[(size_t)i * a.n_q_heads * D + e] = 0.f;
+          for (int e = 0; e < a.n_q_heads; ++e)
+            a.lse_final[(size_t)i * a.n_q_heads + e] = -INFINITY;
+          for (int e = 0; e < n_kv; ++e) a.pair_blocks[(size_t)i * n_kv + e] = make_int2(0, 0);
+        }
+      }
+      scan = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+      }
+    };
+    for (int i0 = 0; i0 < a.batch; i0 += 32) {
+      scan32(i0, warp == 0);
+      all += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    const long long total = all * n_kv;
+    const int parts = (int)min((long long)a.parts, total);  // each has a tile
+    if ((int)blockIdx.x >= parts) return;
+    share = div_small(total, parts);
+    more = (int)(total - share * parts);
+    pos = blockIdx.x * share + min((int)blockIdx.x, more);
+    end = pos + share + ((int)blockIdx.x < more ? 1 : 0);
+    long long before = 0;  // tiles of the sequences before the 32 that hold pos
+    int i0 = 0;
+    unsigned here;
+    for (;; i0 += 32) {
+      if (a.batch > 32) scan32(i0, false);
+      here = __ballot_sync(0xffffffffu, pos < (before + scan) * n_kv);
+      if (here) break;
+      before += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    const int at = __ffs(here) - 1;
+    b = i0 + at;
+    sp = span_of(a, __shfl_sync(0xffffffffu, raw, at), nullptr);
+    pair_tiles = __shfl_sync(0xffffffffu, n, at);
+    const long long in_seq =
+        pos - (before + __shfl_sync(0xffffffffu, scan - n, at)) * n_kv;
+    kvh = (int)div_small(in_seq, pair_tiles);
+    tile = (int)(in_seq - (long long)kvh * pair_tiles);
   }
-  len += a.append;
-  const int lo_tok = a.window_left >= 0 ? max(0, len - 1 - a.window_left) : 0;
-  const int lo16 = lo_tok / kSplitGranule * kSplitGranule;
-  const int n_att = len - lo16;
-  const int per = (n_att + S - 1) / S;
-  const int chunk = (per + kSplitGranule - 1) / kSplitGranule * kSplitGranule;
-  const int t0 = lo16 + (int)min((long long)split * chunk, (long long)n_att);
-  const int t1 = min(t0 + chunk, len);
-  const int n_tok = t1 - t0;
 
-  float* o_out = a.o_partial + (((size_t)split * a.batch + b) * a.n_q_heads + (size_t)kvh * g) * D;
-  float* lse_out = a.lse_partial + ((size_t)split * a.batch + b) * a.n_q_heads + (size_t)kvh * g;
-  if (n_tok <= 0) {  // empty split: o = 0, lse = -inf
-    for (int i = threadIdx.x; i < g * D; i += kThreads) o_out[i] = 0.f;
-    for (int i = threadIdx.x; i < g; i += kThreads) lse_out[i] = -INFINITY;
-    return;
+  // ---- the segment's tokens, and where its result goes ----
+  for (;;) {
+  const int len = sp.len, lo_tok = sp.lo_tok;
+  int t0, t1;
+  float *o_out, *lse_out;
+  if (a.parts == 0) {
+    // (split rule: see the C header)
+    const int S = a.num_splits, split = blockIdx.x, n_att = len - sp.lo16;
+    const int per = (n_att + S - 1) / S;
+    const int chunk = (per + kSplitGranule - 1) / kSplitGranule * kSplitGranule;
+    t0 = sp.lo16 + (int)min((long long)split * chunk, (long long)n_att);
+    t1 = min(t0 + chunk, len);
+    o_out = a.o_partial + (((size_t)split * a.batch + b) * a.n_q_heads + (size_t)kvh * g) * D;
+    lse_out = a.lse_partial + ((size_t)split * a.batch + b) * a.n_q_heads + (size_t)kvh * g;
+    if (t1 <= t0) {  // empty split: o = 0, lse = -inf
+      for (int i = threadIdx.x; i < g * D; i += kThreads) o_out[i] = 0.f;
+      for (int i = threadIdx.x; i < g; i += kThreads) lse_out[i] = -INFINITY;
+      return;
+    }
+  } else {
+    seg_tiles = (int)min(end - pos, (long long)(pair_tiles - tile));
+    t0 = sp.lo16 + tile * kTile;
+    t1 = min(t0 + seg_tiles * kTile, len);
+    const bool whole = seg_tiles == pair_tiles;
+    if (whole) {
+      o_out = a.o_final + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D;
+      lse_out = a.lse_final + (size_t)b * a.n_q_heads + (size_t)kvh * g;
+    } else {
+      const size_t part = 2 * (size_t)blockIdx.x + (tile == 0 ? 1 : 0);
+      o_out = a.o_partial + part * g * D;
+      lse_out = a.lse_partial + part * g;
+    }
+    if (tile == 0 && threadIdx.x == 0) {
+      // The block of the pair's last tile x.
+      const long long x = pos + pair_tiles - 1, big = (share + 1) * more;
+      const long long q = x < big ? div_small(x, share + 1) : more + div_small(x - big, share);
+      a.pair_blocks[(size_t)b * n_kv + kvh] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : (int)q);
+    }
   }
-  const int n_tiles = (n_tok + kTile - 1) / kTile;
+  const int n_tiles = (t1 - t0 + kTile - 1) / kTile;
   const int my_tiles = col < n_tiles ? (n_tiles - col + team - 1) / team : 0;
+
+  // ================= q: asked for first, used while the first tiles fly =================
+  const int row0 = kWide ? rg * 16 : 0;
+  const int gid = lane >> 2, quad = lane & 3;
+  constexpr int kRows = kWide ? 2 : 1;  // query rows a thread looks after
+  constexpr int kSteps = D / 32;        // k steps of q k
+  constexpr bool kQSmem = q_in_smem(D, kWide);
+  // Columns 16 i + 4 quad .. + 3 of rows gid (and gid + 8).
+  uint2 qx[kRows][2 * kSteps];
+  {
+    const uint16_t* qsrc = a.q + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D + quad * 4;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = row0 + gid + 8 * r;
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i) {
+        qx[r][i] = make_uint2(0u, 0u);
+        if (row < g) qx[r][i] = *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
+      }
+    }
+  }
 
   // ================= this warp's ring =================
   // Half 2 j is K and half 2 j + 1 is V of the warp's tile j (the block's tile
@@ -329,33 +472,21 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
     for (int h = 0; h < L::kSlots; ++h) put();
   }
 
-  // ================= q =================
-  const int row0 = kWide ? rg * 16 : 0;
-  const int gid = lane >> 2, quad = lane & 3;
-  constexpr int kRows = kWide ? 2 : 1;  // query rows a thread looks after
-  constexpr int kSteps = D / 32;        // k steps of q k
-  constexpr bool kQSmem = q_in_smem(D, kWide);
-
-  // q as A fragments (rows gid and gid + 8, columns 4 quad .. + 3 and 16 + 4
-  // quad .. + 3 of each 32): hi and lo parts of 8 rows in one, or of 16 in two.
+  // ================= q's fragments =================
+  // A fragments (rows gid and gid + 8, columns 4 quad .. + 3 and 16 + 4 quad .. +
+  // 3 of each 32): hi and lo parts of 8 rows in one, or of 16 in two.
   uint4 qf[kQSmem ? 1 : kSteps];
-  uint4* qs = reinterpret_cast<uint4*>(smem + L::kQ) +
-              rg * kSteps * 32 * (kWide ? 2 : 1);
+  uint4* qs = reinterpret_cast<uint4*>(smem + L::kQ) + rg * kSteps * 32 * (kWide ? 2 : 1);
   float sl2[kRows], cap_in[kRows];
   {
-    const uint16_t* qsrc = a.q + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D + quad * 4;
     float up[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int row = row0 + gid + 8 * r;
       uint32_t top = 0u;
-      if (row < g) {
 #pragma unroll
-        for (int i = 0; i < 2 * kSteps; ++i) {
-          const uint2 x = *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
-          top = max(max(top, x.x & 0x7fffu), (x.x >> 16) & 0x7fffu);
-          top = max(max(top, x.y & 0x7fffu), (x.y >> 16) & 0x7fffu);
-        }
+      for (int i = 0; i < 2 * kSteps; ++i) {
+        top = max(max(top, qx[r][i].x & 0x7fffu), (qx[r][i].x >> 16) & 0x7fffu);
+        top = max(max(top, qx[r][i].y & 0x7fffu), (qx[r][i].y >> 16) & 0x7fffu);
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -370,10 +501,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         sl2[r] = a.softcap * kLog2e;
       }
     }
-    auto part = [&](int row, int i, float f, uint32_t& hi, uint32_t& lo) {
-      hi = lo = 0u;
-      if (row >= g) return;
-      const uint2 x = *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
+    auto part = [&](const uint2& x, float f, uint32_t& hi, uint32_t& lo) {
       const float v0 = __uint_as_float(x.x << 16) * f, v1 = __uint_as_float(x.x & 0xffff0000u) * f;
       const float v2 = __uint_as_float(x.y << 16) * f, v3 = __uint_as_float(x.y & 0xffff0000u) * f;
       hi = e4m3x4_pack(v0, v1, v2, v3);
@@ -388,17 +516,17 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       uint4 f;
       if constexpr (kWide) {
         uint4 fl;
-        part(row0 + gid, 2 * i, up[0], f.x, fl.x);
-        part(row0 + gid + 8, 2 * i, up[1], f.y, fl.y);
-        part(row0 + gid, 2 * i + 1, up[0], f.z, fl.z);
-        part(row0 + gid + 8, 2 * i + 1, up[1], f.w, fl.w);
+        part(qx[0][2 * i], up[0], f.x, fl.x);
+        part(qx[1][2 * i], up[1], f.y, fl.y);
+        part(qx[0][2 * i + 1], up[0], f.z, fl.z);
+        part(qx[1][2 * i + 1], up[1], f.w, fl.w);
         if (col == 0) {
           qs[(2 * i) * 32 + lane] = f;
           qs[(2 * i + 1) * 32 + lane] = fl;
         }
       } else {
-        part(gid, 2 * i, up[0], f.x, f.y);
-        part(gid, 2 * i + 1, up[0], f.z, f.w);
+        part(qx[0][2 * i], up[0], f.x, f.y);
+        part(qx[0][2 * i + 1], up[0], f.z, f.w);
         if constexpr (kQSmem) {
           if (col == 0) qs[i * 32 + lane] = f;
         } else {
@@ -640,7 +768,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       sum += f * ml[w * 16 + lr];
       mf[w * 16 + lr] = f;
     }
-    const float inv = 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: every score is -inf
     for (int w = w0; w < w0 + team; ++w) mf[w * 16 + lr] *= inv;
     lse_out[threadIdx.x] = (mt - kShift + log2f(sum)) * kLn2;
   }
@@ -660,6 +788,104 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
     }
     *reinterpret_cast<float4*>(o_out + (size_t)r * D + c) = o;
   }
+  // ---- the next segment of the share ----
+  if (a.parts == 0) return;
+  pos += seg_tiles;
+  if (pos >= end) return;
+  tile = 0;
+  if (++kvh == n_kv) {
+    kvh = 0;
+    do {
+      ++b;
+      sp = span_of(a, a.kv_lens[b], nullptr);
+      pair_tiles = tiles_of(sp);
+    } while (pair_tiles == 0);
+  }
+  __syncthreads();  // the merged rows have been read: the rings are free again
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine of the shares: one block per (sequence, query head, kCols columns)
+// merges the pair's partials, those of blocks first .. last of the list, by their
+// LSE weights.  Each warp takes every kCombineWarps-th, kAtOnce at a time (their
+// loads in flight together), with a running maximum; then the warps' states are
+// merged.  Narrow slices of columns where there are few rows: one sequence of
+// 30720 tokens has 28 rows of some 115 partials each.
+//
+// It does not let the next kernel start early: a decode whose blocks came in
+// while this grid's still hold their places would not find all SMs free, and the
+// blocks that came last would run behind the others (paged batch of 16: 139
+// against 106 us).
+// ---------------------------------------------------------------------------
+constexpr int kCombineWarps = 8, kAtOnce = 8;
+
+template <int D, int kCols>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+combine_shares_kernel(const DecodeFp8Args a) {
+  constexpr int kVec = kCols / 32;  // columns of a lane
+  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps], s_o[kCombineWarps][kCols];
+  const int h = blockIdx.x, b = blockIdx.y, col0 = blockIdx.z * kCols;
+  const int g = a.n_q_heads / a.c.n_kv_heads, kvh = h / g, row = h % g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  const int2 blocks = a.pair_blocks[(size_t)b * a.c.n_kv_heads + kvh];
+  const int n = blocks.y - blocks.x + 1;
+  if (n <= 1) return;  // the result is already there
+  float m = -INFINITY, l = 0.f, o[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) o[e] = 0.f;
+  for (int i0 = warp; i0 < n; i0 += kCombineWarps * kAtOnce) {
+    float w[kAtOnce], x[kAtOnce][kVec];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kCombineWarps;
+      w[u] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
+      if (i < n) {
+        const size_t part = (2 * (size_t)(blocks.x + i) + (i == 0 ? 1 : 0)) * g + row;
+        w[u] = a.lse_partial[part] * kLog2e;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[u][e] = a.o_partial[part * D + col0 + e * 32 + lane];
+      }
+    }
+    float now = m;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) now = fmax_nan(now, w[u]);
+    const float ref = now == -INFINITY ? 0.f : now;
+    const float c = ex2_approx(m - ref);  // 0 at first
+    l *= c;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) o[e] *= c;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const float p = ex2_approx(w[u] - ref);
+      l += p;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) o[e] = fmaf(p, x[u][e], o[e]);
+    }
+    m = now;
+  }
+  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) s_o[warp][e * 32 + lane] = o[e];
+  __syncthreads();
+  if (threadIdx.x >= kCols) return;
+  float top = s_m[0];
+#pragma unroll
+  for (int w = 1; w < kCombineWarps; ++w) top = fmax_nan(top, s_m[w]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float v = 0.f, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) {
+    const float f = ex2_approx(s_m[w] - ref);  // 0 for a warp that had none
+    sum = fmaf(f, s_l[w], sum);
+    v = fmaf(f, s_o[w][threadIdx.x], v);
+  }
+  const size_t at = (size_t)b * a.n_q_heads + h;
+  a.o_final[at * D + col0 + threadIdx.x] = sum == 0.f ? 0.f : v / sum;
+  if (threadIdx.x == 0 && col0 == 0) a.lse_final[at] = (top + log2f(sum)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -695,7 +921,7 @@ cudaError_t launch_t(const DecodeFp8Args& a, const LaunchCtx& ctx) {
     if (dev < 64) configured[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.num_splits, a.c.n_kv_heads, a.batch);
+  cfg.gridDim = a.parts > 0 ? dim3(a.parts) : dim3(a.num_splits, a.c.n_kv_heads, a.batch);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::total(q_smem_bytes(D, kWide, groups));
   cfg.stream = ctx.stream;
@@ -713,6 +939,35 @@ cudaError_t launch_d(const DecodeFp8Args& a, const LaunchCtx& ctx) {
 }
 
 }  // namespace
+
+int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms) {
+  const int g = n_q_heads / n_kv_heads;
+  const bool wide = g > 8;
+  int n = blocks_per_sm(head_dim, wide);
+  if (head_dim == 256 && g > 16) n = 1;  // q's fragments leave room for one block's rings
+  return n * num_sms;
+}
+
+cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int D = a.c.head_dim;
+  // 32 columns a block while that fits into one wave, whole rows beyond.
+  const bool slices = (long long)a.n_q_heads * a.batch * (D / 32) <= 8LL * ctx.num_sms;
+  cfg.gridDim = dim3(a.n_q_heads, a.batch, slices ? D / 32 : 1);
+  auto run = [&](auto slice, auto row) {
+    return slices ? cudaLaunchKernelEx(&cfg, slice, a) : cudaLaunchKernelEx(&cfg, row, a);
+  };
+  if (D == 256) return run(combine_shares_kernel<256, 32>, combine_shares_kernel<256, 256>);
+  return D == 128 ? run(combine_shares_kernel<128, 32>, combine_shares_kernel<128, 128>)
+                  : run(combine_shares_kernel<64, 32>, combine_shares_kernel<64, 64>);
+}
 
 cudaError_t launch_decode_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx) {
   if (a.c.head_dim == 256) return launch_d<256>(a, ctx);

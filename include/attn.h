@@ -695,9 +695,11 @@ int attn_decode_fp8_splitkv(const attn_bf16* q, const uint8_t* k_cache, const ui
                             int num_blocks, int max_kv_len, float scale, int window_left,
                             float softcap, const float* alibi_slopes, void* stream);
 
-/* Bytes of workspace that attn_decode_fp8 needs (0 for num_splits = 1, and for
- * arguments out of range).  Pure host function. */
-size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int head_dim);
+/* Bytes of workspace that attn_decode_fp8 needs on the current device, with or
+ * without an appended token (0 where it needs none, and for arguments out of
+ * range).  Launches nothing. */
+size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int n_kv_heads,
+                                       int head_dim, int max_kv_len, int window_left);
 
 /*
  * attn_decode_fp8 -- a decode step over an 8-bit cache in one call: the new
@@ -710,17 +712,23 @@ size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads,
  *                attended as the last of kv_lens[b] + 1 tokens (what the cache
  *                then holds of it); or both NULL: nothing is written (the
  *                cache's pointers are then only read)
- *   num_splits : >= 1, or 0 for attn_decode_num_splits(batch, n_kv_heads,
- *                max_kv_len, 0)
+ *   num_splits : >= 1: the split rule of attn_decode_splitkv_ex; or 0: the
+ *                library divides the work.  It then lets the blocks of one wave
+ *                take equal shares of all (sequence, kv head) pairs' tokens, so
+ *                lengths may differ as they like; batches of more than 1024
+ *                sequences, and caches whose max_kv_len (or window) is 512 tokens
+ *                at most, take one split.  The results depend on the division
+ *                only in the order of fp32 sums.
  *   workspace  : attn_decode_fp8_workspace_bytes(num_splits, ...) bytes, 16-byte
  *                aligned (NULL where that is 0); overwritten.  Calls that may
  *                overlap on the device need one each.
  *   workspace_bytes: its size; less than needed is ATTN_ERR_SCRATCH
  *   o, lse     : (batch, n_q_heads, head_dim) and (batch, n_q_heads) fp32
  *                outputs, 16- and 4-byte aligned
- * The results equal attn_cache_write_fp8, attn_decode_fp8_splitkv (over
- * kv_lens + 1 tokens when appending) and attn_combine.  Other arguments,
- * limits and errors as those.
+ * With num_splits >= 1 the results equal attn_cache_write_fp8,
+ * attn_decode_fp8_splitkv (over kv_lens + 1 tokens when appending) and
+ * attn_combine.  max_kv_len (paged): the largest kv_len; a larger one is attended
+ * in full all the same.  Other arguments, limits and errors as those.
  */
 int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new,
                     uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,

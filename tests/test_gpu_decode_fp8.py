@@ -136,7 +136,40 @@ def test_decode(dev, lens, S, bs, d, n_q, n_kv, paged, window, softcap, alibi):
         o2, lse2 = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, num_splits=S, out=out,
                                    **kw)
         assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    # The library's division: one block a pair, or shares of the tiles for the
+    # blocks that this many tokens would take (a paged cache's max_kv_len).
+    for most in ([300, 600, 4000, 100000] if paged else [None]):
+        o3, lse3 = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, max_kv_len=most,
+                                   out=nan_like((B, n_q, d), dev), lse=nan_like((B, n_q), dev), **kw)
+        attn.check_device_status()
+        close(o3, lse3, want, bound, what + f" shares for {most}")
     assert_cache(tensors, c.ref(), c, what)                 # only read
+
+
+@pytest.mark.parametrize("B", [150, 1024, 1025])
+def test_many_sequences_in_shares(dev, B):
+    """Lengths from none to some hundred over many sequences (1025: beyond the
+    shares' scan), first and last ones empty, two kv heads."""
+    gen = torch.Generator().manual_seed(B)
+    lens = (torch.randint(0, 3, (B,), generator=gen) * torch.randint(0, 160, (B,), generator=gen))
+    lens[[0, 1, B - 1]] = 0
+    lens[B // 2] = 900
+    lens = lens.tolist()
+    c = filled(lens, 2, 64, 16, True, seed=B)
+    q = queries(B, 6, 64, 1)
+    want, bound, _ = reference(c, q, lens, 0.125)
+    tensors, table = c.on(dev)
+    for most in (900, 20000):
+        o, lse = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, max_kv_len=most,
+                                 scale=0.125, out=nan_like((B, 6, 64), dev),
+                                 lse=nan_like((B, 6), dev))
+        attn.check_device_status()
+        close(o, lse, want, bound, f"{B} sequences, shares for {most}")
+    none = torch.zeros(B, dtype=torch.int32, device=dev)
+    o, lse = attn.decode_fp8(q.to(dev), *tensors, none, table, out=nan_like((B, 6, 64), dev),
+                             lse=nan_like((B, 6), dev))
+    attn.check_device_status()
+    assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
 
 
 @pytest.mark.parametrize("paged,n,n_q,n_kv,d", [(False, 30720, 28, 4, 128), (True, 30720, 8, 2, 64),
@@ -201,9 +234,9 @@ def test_scales_far_apart(dev, n_q):
         q = (queries(1, n_q, d, 2).float() * amp).to(torch.bfloat16)
         want, bound, _ = reference(c, q, lens, scale)
         tensors, table = c.on(dev)
-        for S in (1, 3):
+        for S in (1, 3, 0):
             o, lse = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, num_splits=S,
-                                     scale=scale)
+                                     max_kv_len=2000, scale=scale)
             attn.check_device_status()
             # each weight's product with its scale keeps 22 bits, or 2^-36 of the largest
             floor = 2.0 ** -30 * max(lens) * 448.0 * 2.0 ** 40
@@ -223,8 +256,9 @@ def test_scales_need_not_be_powers_of_two(dev):
     close(o, lse, want, bound, "other scales")
 
 
+@pytest.mark.parametrize("S", [3, 0])
 @pytest.mark.parametrize("n_q", [8, 24])
-def test_nan_in_live_and_masked_places(dev, n_q):
+def test_nan_in_live_and_masked_places(dev, n_q, S):
     """A NaN value in an attended token reaches the outputs that it belongs to
     (V: its own column; K: the whole row); left of the window, or past the
     end, it reaches nothing."""
@@ -232,7 +266,8 @@ def test_nan_in_live_and_masked_places(dev, n_q):
     c = filled([n], n_kv, d, bs, True, seed=13)
     q = queries(1, n_q, d, 5)
     base, table = c.on(dev)
-    run = lambda t, **kw: attn.decode_fp8(q.to(dev), *t, i32([n], dev), table, num_splits=3, **kw)
+    run = lambda t, **kw: attn.decode_fp8(q.to(dev), *t, i32([n], dev), table, num_splits=S,
+                                       max_kv_len=2000, **kw)
     o0, l0 = run(base)
     w0, wl0 = run(base, window_left=W)
     bad = [t.clone() for t in base]
@@ -293,6 +328,13 @@ def test_append(dev, lens, S, bs, d, n_q, n_kv, paged, window, softcap, alibi):
     # The same as the write and the decode apart, bit for bit.
     o2, lse2 = attn.decode_fp8(q.to(dev), *tensors, i32(after, dev), table, **kw)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # Again (the token is there already: the same bytes), in shares.
+    kw["num_splits"] = 0
+    o3, lse3 = attn.decode_append_fp8(q.to(dev), kn.to(dev), vn.to(dev), *tensors, i32(lens, dev),
+                                      table, max_kv_len=3000 if paged else None, **kw)
+    attn.check_device_status()
+    close(o3, lse3, ref, bound, f"append {lens} in shares")
+    assert_cache(tensors, want, c, f"append {lens} again")
 
 
 def test_append_to_a_full_cache_is_flagged_and_not_written(dev):
@@ -320,15 +362,15 @@ def test_bad_block_is_flagged_in_bounds(dev):
     tensors, table = c.on(dev)
     q = queries(1, 8, 128, 1).to(dev)
     good, _ = attn.decode_fp8(q, *tensors, i32([100], dev), table, num_splits=2)
-    for bad in (-1, c.k.shape[0], 1 << 30):
+    for bad, S in ((-1, 2), (c.k.shape[0], 0), (1 << 30, 1)):
         t = table.clone()
         t[0, 3] = bad
-        attn.decode_fp8(q, *tensors, i32([100], dev), t, num_splits=2)
+        attn.decode_fp8(q, *tensors, i32([100], dev), t, num_splits=S, max_kv_len=1000)
         with pytest.raises(AttnError) as e:
             attn.check_device_status()
         assert e.value.status == status_codes()["ATTN_ERR_DEVICE"]
-    for n in (-5, 113, 1 << 30):                            # lengths outside [0, 112]
-        attn.decode_fp8(q, *tensors, i32([n], dev), table, num_splits=2)
+    for n, S in ((-5, 2), (113, 0), (1 << 30, 1), (-1, 0)):  # lengths outside [0, 112]
+        attn.decode_fp8(q, *tensors, i32([n], dev), table, num_splits=S, max_kv_len=1000)
         with pytest.raises(AttnError) as e:
             attn.check_device_status()
         assert e.value.status == status_codes()["ATTN_ERR_DEVICE"]

@@ -107,8 +107,8 @@ def test_decode_outputs_validation(L, E):
 
 
 def test_workspace_bytes(L):
-    f = L.attn_decode_fp8_workspace_bytes
-    assert f(1, 4, 32, 128) == 0 and f(0, 4, 32, 128) == 0 and f(4, 0, 32, 128) == 0
+    f = lambda S, B, H, Hk, d: L.attn_decode_fp8_workspace_bytes(S, B, H, Hk, d, 5000, -1)
+    assert f(1, 4, 32, 8, 128) == 0 and f(-1, 4, 32, 8, 128) == 0 and f(4, 0, 32, 8, 128) == 0
     for S, B, H, d in [(2, 1, 1, 64), (76, 1, 28, 128), (1024, 65535, 64, 256)]:
-        n = f(S, B, H, d)
+        n = f(S, B, H, 1, d)
         assert n == -(-S * B * H * d * 4 // 256) * 256 + S * B * H * 4
