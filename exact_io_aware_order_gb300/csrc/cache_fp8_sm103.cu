@@ -10,7 +10,8 @@
 // codes already there move by whole exponents and are rounded again only where
 // they fall among e4m3's subnormals.
 //
-// Work split: one unit per (block touched, kv head, K or V).  Which blocks a
+// Work split: one unit per (block touched, kv head), K and V together, so that
+// one search serves both and a warp has twice the bytes in flight.  Which blocks a
 // call touches is known on the device only (kv_lens and cu_seqlens are there),
 // so units are numbered by slots that every warp can place by itself: sequence
 // s owns the slots from cu[s] / block_size + 2 s on, at least
@@ -20,7 +21,8 @@
 // to be scanned first and the launch needs one kernel.
 //
 // Both kernels are bound by HBM on long inputs and by the latency of the
-// chain cu_seqlens -> kv_lens -> block table -> rows on short ones.
+// chain cu_seqlens, kv_lens -> block table -> rows on short ones; the write's rows
+// do not wait for the block table.
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -31,13 +33,14 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunkRows = 16;  // rows of a block that a warp holds in registers
+// Rows of a block, of K and of V, that a warp takes at a time.
+constexpr int chunk_rows(int D) { return D == 256 ? 8 : 16; }
 
 struct RowsKParams {
   CacheRowsArgs a;
-  int warps_per_unit;  // 1, 2, 4 or 8
+  int warps_per_unit;  // 1, 2 or 4
   long long units;
   uint32_t* err_word;
 };
@@ -46,78 +49,85 @@ struct RowsKParams {
 struct Unit {
   int rows;             // rows of the call in this block (0: nothing to do)
   int before;           // write: rows of the block in front of them
-  long long src_row;    // first row in the packed tensor
-  long long cache_row;  // first row in the cache, in rows of all kv heads
-  long long block_row;  // the block's first row
-  long long scale;      // index into the scales
+  int src_row;          // first row in the packed tensors
   int head;
-  bool is_v;
+  int entry;            // the block as the table has it (contiguous: unused)
+  long long block_row;  // contiguous: the block's first row, of all kv heads
+  long long scale;      // contiguous: index of its scales
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
-// First slot of sequence s.
-__device__ __forceinline__ long long first_slot(const CacheRowsArgs& a, int s) {
-  return (long long)(clampi(a.cu_seqlens[s], 0, a.total_tokens) / a.c.block_size) + 2LL * s;
-}
-
 __device__ Unit find_unit(const RowsKParams& p, long long u, int lane) {
   const CacheRowsArgs& a = p.a;
+  const int bs = a.c.block_size, total = a.total_tokens;
   Unit r;
   r.rows = 0;
-  r.is_v = (u & 1) != 0;
-  r.head = (int)((u >> 1) % a.c.n_kv_heads);
-  const long long slot = (u >> 1) / a.c.n_kv_heads;
+  r.head = (int)(u % a.c.n_kv_heads);
+  const long long slot = u / a.c.n_kv_heads;
   if (u >= p.units) return r;
-  int s = 0, c0 = 0, n = 1, j = 0;
+  int s = 0, c0 = 0, n = 1, j = 0, start = 0;
+  auto first_slot = [&](int c, int i) { return (long long)(c / bs) + 2LL * i; };
   if (a.cu_seqlens == nullptr) {
     s = c0 = (int)slot;
+    start = a.starts[s];
   } else {
-    int lo = 0, hi = a.num_seqs;  // the sequence is in [lo, hi)
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int probe = lo + lane * step;
-      const bool at_or_before = probe < hi && (lane == 0 || first_slot(a, probe) <= slot);
-      const int top = 31 - __clz(__ballot_sync(0xffffffffu, at_or_before));
+    // The sequence is in [lo, hi); the last round's probes are neighbours, and
+    // each lane has its probe's start at hand.
+    int lo = 0, hi = a.num_seqs, step, top, c, c_next, st;
+    do {
+      step = (hi - lo + 31) / 32;
+      const int probe = min(lo + lane * step, a.num_seqs - 1);
+      c = clampi(a.cu_seqlens[probe], 0, total);
+      c_next = clampi(a.cu_seqlens[probe + 1], 0, total);
+      st = a.starts ? a.starts[probe] : 0;
+      const bool at_or_before =
+          lo + lane * step < hi && (lane == 0 || first_slot(c, probe) <= slot);
+      top = 31 - __clz(__ballot_sync(0xffffffffu, at_or_before));
       lo += top * step;
       hi = min(hi, lo + step);
-    }
+    } while (step > 1);
     s = lo;
-    c0 = clampi(a.cu_seqlens[s], 0, a.total_tokens);
-    n = clampi(a.cu_seqlens[s + 1], 0, a.total_tokens) - c0;
-    const long long off = slot - first_slot(a, s);
-    if (n <= 0 || off < 0 || off > n / a.c.block_size + 1) return r;
+    c0 = __shfl_sync(0xffffffffu, c, top);
+    n = __shfl_sync(0xffffffffu, c_next, top) - c0;
+    start = __shfl_sync(0xffffffffu, st, top);
+    const long long off = slot - first_slot(c0, s);
+    if (n <= 0 || off < 0 || off > n / bs + 1) return r;
     j = (int)off;
   }
-  const int start = a.starts ? a.starts[s] : 0;
-  const long long cap = a.c.capacity();
-  if (start < 0 || (long long)start + n > cap) {
+  if (start < 0 || (long long)start + n > a.c.capacity()) {
     if (lane == 0) atomicOr(p.err_word, kErrKvLen);
     return r;
   }
-  const int blk = start / a.c.block_size + j;
-  const long long b0 = (long long)blk * a.c.block_size;
+  const int blk = start / bs + j;
+  const long long b0 = (long long)blk * bs;
   const long long w0 = max((long long)start, b0);
-  const long long w1 = min((long long)start + n, b0 + a.c.block_size);
+  const long long w1 = min((long long)start + n, b0 + bs);
   if (w0 >= w1) return r;
   if (a.c.block_table != nullptr) {
-    const int phys = a.c.block_table[(size_t)s * a.c.max_blocks_per_seq + blk];
-    if (phys < 0 || phys >= a.c.num_blocks) {
-      if (lane == 0) atomicOr(p.err_word, kErrBlockIndex);
-      return r;
-    }
-    r.block_row = (long long)phys * a.c.block_size;
-    r.scale = (long long)phys * a.c.n_kv_heads + r.head;
+    r.entry = a.c.block_table[(size_t)s * a.c.max_blocks_per_seq + blk];
   } else {
-    const int per_seq = (a.c.max_kv_len + a.c.block_size - 1) / a.c.block_size;
+    const int per_seq = (a.c.max_kv_len + bs - 1) / bs;
     r.block_row = (long long)s * a.c.max_kv_len + b0;
     r.scale = ((long long)s * per_seq + blk) * a.c.n_kv_heads + r.head;
   }
   r.rows = (int)(w1 - w0);
   r.before = (int)(w0 - b0);
-  r.cache_row = r.block_row + r.before;
-  r.src_row = c0 + (w0 - start);
+  r.src_row = c0 + (int)(w0 - start);
   return r;
+}
+
+// Follows the block table's entry; false where it leads outside the cache.
+__device__ __forceinline__ bool resolve(const RowsKParams& p, Unit& u, int lane) {
+  const CacheFp8& c = p.a.c;
+  if (c.block_table == nullptr) return true;
+  if (u.entry < 0 || u.entry >= c.num_blocks) {
+    if (lane == 0) atomicOr(p.err_word, kErrBlockIndex);
+    return false;
+  }
+  u.block_row = (long long)u.entry * c.block_size;
+  u.scale = (long long)u.entry * c.n_kv_heads + u.head;
+  return true;
 }
 
 // cu_seqlens has to start at 0 and not decrease up to total_tokens; one block
@@ -172,88 +182,123 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
 
 // ---------------------------------------------------------------------------
 // Write: amax over the unit's rows, the block's scale, the codes.  Up to
-// kChunkRows rows a warp stay in registers between the two (blocks of up to
-// 128 tokens are read once); larger blocks are read again, from L2.
+// chunk_rows rows a warp stay in shared memory between the two (blocks of up to
+// 4 times that are read once; held in registers they would allow 16 warps an SM
+// instead of 24: 50 against 43 us for 16 prompts of 256-4096 tokens); larger blocks are read again, from L2.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kThreads) cache_write_fp8_kernel(const RowsKParams p) {
   constexpr int kLanes = D / 8;             // lanes of a row, 8 values each
   constexpr int kRowsPerStep = 32 / kLanes;
-  constexpr int kSteps = kChunkRows / kRowsPerStep;
-  __shared__ uint32_t s_amax[kWarps];
+  constexpr int kChunkRows = chunk_rows(D), kSteps = kChunkRows / kRowsPerStep;
+  __shared__ uint32_t s_amax[2][kWarps];
+  __shared__ uint4 s_rows[kWarps * 2 * kSteps * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   check_cu_seqlens(p);
   const int wpu = p.warps_per_unit;
   const int sub = warp % wpu;  // this warp among its unit's
-  const Unit u = find_unit(p, ((long long)blockIdx.x * kWarps + warp) / wpu, lane);
+  Unit u = find_unit(p, ((long long)blockIdx.x * kWarps + warp) / wpu, lane);
   const CacheRowsArgs& a = p.a;
-  const uint16_t* src = u.is_v ? a.v : a.k;
-  const long long ts = u.is_v ? a.v_token_stride : a.k_token_stride;
-  const long long hs = u.is_v ? a.v_head_stride : a.k_head_stride;
-  uint8_t* codes = u.is_v ? a.c.v : a.c.k;
-  float* scales = u.is_v ? a.c.v_scales : a.c.k_scales;
   const int lr = lane / kLanes, lc = lane % kLanes;
   const bool again = u.rows > kChunkRows * wpu;
+  const uint16_t* src[2] = {a.k + u.head * a.k_head_stride + lc * 8,
+                            a.v + u.head * a.v_head_stride + lc * 8};
+  const long long ts[2] = {a.k_token_stride, a.v_token_stride};
 
-  uint4 x[kSteps];
-  uint32_t amax = 0u;
+  // Each lane's own 16 bytes of a step, in shared memory: no other thread reads them.
+  uint4* x = s_rows + (warp * 2 * kSteps) * 32 + lane;
+  auto load = [&](int c) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = c + i * kRowsPerStep + lr;
+        if (r < u.rows) cp_async16(smem_u32(x + (w * kSteps + i) * 32), src[w] + (u.src_row + r) * ts[w]);
+      }
+  };
+  if (u.rows > 0) load(sub * kChunkRows);
+  const bool found = u.rows <= 0 || resolve(p, u, lane);
+  uint32_t amax[2] = {0u, 0u};
   for (int c = sub * kChunkRows; c < u.rows; c += kChunkRows * wpu) {
+    if (c != sub * kChunkRows) load(c);
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = c + i * kRowsPerStep + lr;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (r < u.rows)
-        x[i] = *reinterpret_cast<const uint4*>(src + (u.src_row + r) * ts + u.head * hs + lc * 8);
-    }
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      amax = finite_max(amax, x[i].x);
-      amax = finite_max(amax, x[i].y);
-      amax = finite_max(amax, x[i].z);
-      amax = finite_max(amax, x[i].w);
-    }
+      for (int i = 0; i < kSteps; ++i) {
+        if (c + i * kRowsPerStep + lr >= u.rows) continue;
+        const uint4 y = x[(w * kSteps + i) * 32];
+        amax[w] = finite_max(amax[w], y.x);
+        amax[w] = finite_max(amax[w], y.y);
+        amax[w] = finite_max(amax[w], y.z);
+        amax[w] = finite_max(amax[w], y.w);
+      }
   }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  const float was = u.rows > 0 && u.before > 0 ? scales[u.scale] : 0.f;
+  if (!found) u.rows = 0;
+  float was[2] = {0.f, 0.f};
+  if (u.rows > 0 && u.before > 0) {
+    was[0] = a.c.k_scales[u.scale];
+    was[1] = a.c.v_scales[u.scale];
+  }
+  amax[0] = __reduce_max_sync(0xffffffffu, amax[0]);
+  amax[1] = __reduce_max_sync(0xffffffffu, amax[1]);
   if (wpu > 1) {  // the unit's maximum; `was` is read by every warp before it is replaced
-    if (lane == 0) s_amax[warp] = amax;
+    if (lane == 0) s_amax[0][warp] = amax[0], s_amax[1][warp] = amax[1];
     __syncthreads();
-    for (int w = 0; w < wpu; ++w) amax = max(amax, s_amax[warp - sub + w]);
+    for (int i = 0; i < wpu; ++i) {
+      amax[0] = max(amax[0], s_amax[0][warp - sub + i]);
+      amax[1] = max(amax[1], s_amax[1][warp - sub + i]);
+    }
   }
   if (u.rows <= 0) return;
   __syncwarp();
-  const float scale = fmaxf(scale_of(amax), was);
-  if (sub == 0 && lane == 0 && scale != was) scales[u.scale] = scale;
-
-  const float inv = 1.f / scale;  // exact: a power of two
-  for (int c = sub * kChunkRows; c < u.rows; c += kChunkRows * wpu) {
+  const long long pitch = (long long)a.c.n_kv_heads * D;
+  float inv[2], ratio[2];
+  uint8_t* codes[2];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = c + i * kRowsPerStep + lr;
-      if (r >= u.rows) continue;
-      if (again)
-        x[i] = *reinterpret_cast<const uint4*>(src + (u.src_row + r) * ts + u.head * hs + lc * 8);
-      uint2 out;
-      out.x = e4m3x4(bf16_lo(x[i].x) * inv, bf16_hi(x[i].x) * inv, bf16_lo(x[i].y) * inv,
-                     bf16_hi(x[i].y) * inv);
-      out.y = e4m3x4(bf16_lo(x[i].z) * inv, bf16_hi(x[i].z) * inv, bf16_lo(x[i].w) * inv,
-                     bf16_hi(x[i].w) * inv);
-      *reinterpret_cast<uint2*>(codes + ((u.cache_row + r) * a.c.n_kv_heads + u.head) * D +
-                                lc * 8) = out;
+  for (int w = 0; w < 2; ++w) {
+    const float scale = fmaxf(scale_of(amax[w]), was[w]);
+    if (sub == 0 && lane == 0 && scale != was[w])
+      (w ? a.c.v_scales : a.c.k_scales)[u.scale] = scale;
+    inv[w] = 1.f / scale;  // exact: a power of two
+    ratio[w] = scale != was[w] ? was[w] * inv[w] : 1.f;
+    codes[w] = (w ? a.c.v : a.c.k) + u.block_row * pitch + u.head * D + lc * 8;
+  }
+  for (int c = sub * kChunkRows; c < u.rows; c += kChunkRows * wpu) {
+    if (again) {
+      load(c);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = c + i * kRowsPerStep + lr;
+        if (r >= u.rows) continue;
+        const uint4 y = x[(w * kSteps + i) * 32];
+        const float f = inv[w];
+        uint2 out;
+        out.x = e4m3x4(bf16_lo(y.x) * f, bf16_hi(y.x) * f, bf16_lo(y.y) * f, bf16_hi(y.y) * f);
+        out.y = e4m3x4(bf16_lo(y.z) * f, bf16_hi(y.z) * f, bf16_lo(y.w) * f, bf16_hi(y.w) * f);
+        *reinterpret_cast<uint2*>(codes[w] + (u.before + r) * pitch) = out;
+      }
     }
   }
   // The block's earlier rows, when its scale grew.
-  if (u.before > 0 && scale != was) {
-    const float ratio = was * inv;
-    for (int r = sub * kRowsPerStep + lr; r < u.before; r += kRowsPerStep * wpu) {
-      uint2* at = reinterpret_cast<uint2*>(
-          codes + ((u.block_row + r) * a.c.n_kv_heads + u.head) * D + lc * 8);
-      const uint2 old = *at;
-      const float2 f0 = from_e4m3x2(old.x), f1 = from_e4m3x2(old.x >> 16);
-      const float2 f2 = from_e4m3x2(old.y), f3 = from_e4m3x2(old.y >> 16);
-      *at = make_uint2(e4m3x4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio),
-                       e4m3x4(f2.x * ratio, f2.y * ratio, f3.x * ratio, f3.y * ratio));
+  if (u.before > 0) {
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+      const float f = w ? ratio[1] : ratio[0];
+      if (f == 1.f) continue;
+      for (int r = sub * kRowsPerStep + lr; r < u.before; r += kRowsPerStep * wpu) {
+        uint2* at = reinterpret_cast<uint2*>((w ? codes[1] : codes[0]) + r * pitch);
+        const uint2 old = *at;
+        const float2 f0 = from_e4m3x2(old.x), f1 = from_e4m3x2(old.x >> 16);
+        const float2 f2 = from_e4m3x2(old.y), f3 = from_e4m3x2(old.y >> 16);
+        *at = make_uint2(e4m3x4(f0.x * f, f0.y * f, f1.x * f, f1.y * f),
+                         e4m3x4(f2.x * f, f2.y * f, f3.x * f, f3.y * f));
+      }
     }
   }
 }
@@ -266,41 +311,46 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) cache_read_fp8_kernel(const RowsKParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kRowsPerStep = 32 / kLanes;
-  constexpr int kSteps = kChunkRows / kRowsPerStep;
+  constexpr int kChunkRows = chunk_rows(D), kSteps = kChunkRows / kRowsPerStep;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   check_cu_seqlens(p);
   const int wpu = p.warps_per_unit;
   const int sub = warp % wpu;
-  const Unit u = find_unit(p, ((long long)blockIdx.x * kWarps + warp) / wpu, lane);
-  if (u.rows <= 0) return;
+  Unit u = find_unit(p, ((long long)blockIdx.x * kWarps + warp) / wpu, lane);
+  if (u.rows <= 0 || !resolve(p, u, lane)) return;
   const CacheRowsArgs& a = p.a;
-  uint16_t* dst = u.is_v ? a.v : a.k;
-  const long long ts = u.is_v ? a.v_token_stride : a.k_token_stride;
-  const long long hs = u.is_v ? a.v_head_stride : a.k_head_stride;
-  const uint8_t* codes = u.is_v ? a.c.v : a.c.k;
-  const float scale = (u.is_v ? a.c.v_scales : a.c.k_scales)[u.scale];
   const int lr = lane / kLanes, lc = lane % kLanes;
+  const long long pitch = (long long)a.c.n_kv_heads * D;
+  const long long from = (u.block_row + u.before) * pitch + u.head * D + lc * 8;
+  const float scale[2] = {a.c.k_scales[u.scale], a.c.v_scales[u.scale]};
+  uint16_t* dst[2] = {a.k + u.head * a.k_head_stride + lc * 8,
+                      a.v + u.head * a.v_head_stride + lc * 8};
+  const long long ts[2] = {a.k_token_stride, a.v_token_stride};
   for (int c = sub * kChunkRows; c < u.rows; c += kChunkRows * wpu) {
-    uint2 x[kSteps];
+    uint2 x[2][kSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = c + i * kRowsPerStep + lr;
-      x[i] = make_uint2(0, 0);
-      if (r < u.rows)
-        x[i] = *reinterpret_cast<const uint2*>(
-            codes + ((u.cache_row + r) * a.c.n_kv_heads + u.head) * D + lc * 8);
-    }
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = c + i * kRowsPerStep + lr;
-      if (r >= u.rows) continue;
-      const float2 f0 = from_e4m3x2(x[i].x), f1 = from_e4m3x2(x[i].x >> 16);
-      const float2 f2 = from_e4m3x2(x[i].y), f3 = from_e4m3x2(x[i].y >> 16);
-      *reinterpret_cast<uint4*>(dst + (u.src_row + r) * ts + u.head * hs + lc * 8) = make_uint4(
-          pack_bf16x2(f0.x * scale, f0.y * scale), pack_bf16x2(f1.x * scale, f1.y * scale),
-          pack_bf16x2(f2.x * scale, f2.y * scale), pack_bf16x2(f3.x * scale, f3.y * scale));
-    }
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = c + i * kRowsPerStep + lr;
+        x[w][i] = make_uint2(0, 0);
+        if (r < u.rows)
+          x[w][i] = *reinterpret_cast<const uint2*>((w ? a.c.v : a.c.k) + from + r * pitch);
+      }
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = c + i * kRowsPerStep + lr;
+        if (r >= u.rows) continue;
+        const float2 f0 = from_e4m3x2(x[w][i].x), f1 = from_e4m3x2(x[w][i].x >> 16);
+        const float2 f2 = from_e4m3x2(x[w][i].y), f3 = from_e4m3x2(x[w][i].y >> 16);
+        const float f = scale[w];
+        *reinterpret_cast<uint4*>(dst[w] + (u.src_row + r) * ts[w]) =
+            make_uint4(pack_bf16x2(f0.x * f, f0.y * f), pack_bf16x2(f1.x * f, f1.y * f),
+                       pack_bf16x2(f2.x * f, f2.y * f), pack_bf16x2(f3.x * f, f3.y * f));
+      }
   }
 }
 
@@ -309,12 +359,13 @@ cudaError_t launch_rows(Kernel kernel, const CacheRowsArgs& a, const LaunchCtx& 
   RowsKParams p;
   p.a = a;
   p.err_word = ctx.err_word;
-  const int chunks = (a.c.block_size + kChunkRows - 1) / kChunkRows;
-  p.warps_per_unit = chunks <= 1 ? 1 : (chunks <= 2 ? 2 : (chunks <= 4 ? 4 : 8));
+  const int rows = chunk_rows(a.c.head_dim);
+  const int chunks = (a.c.block_size + rows - 1) / rows;
+  p.warps_per_unit = chunks <= 1 ? 1 : (chunks <= 2 ? 2 : 4);
   const long long slots = a.cu_seqlens
                               ? a.total_tokens / a.c.block_size + 2LL * a.num_seqs
                               : (long long)a.num_seqs;
-  p.units = slots * a.c.n_kv_heads * 2;
+  p.units = slots * a.c.n_kv_heads;
   const long long blocks = (p.units * p.warps_per_unit + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;  // refused by the caller
   cudaLaunchConfig_t cfg = {};
