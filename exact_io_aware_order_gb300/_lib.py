@@ -111,6 +111,27 @@ def lib() -> ctypes.CDLL:
     return _LIB
 
 
+_BINDING = None
+
+
+def binding():
+    """The ``_binding`` module (csrc/binding.cpp), bound to the library."""
+    global _BINDING
+    if _BINDING is None:
+        L = lib()
+        path = os.path.join(PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is not built; run exact_io_aware_order_gb300.build.build() first")
+        from . import _binding as B
+
+        B.init(*(ctypes.cast(getattr(L, name), c_void_p).value
+                 for name in ("attn_cache_write_fp8", "attn_cache_read_fp8", "attn_decode_fp8",
+                              "attn_decode_fp8_workspace_bytes")))
+        _BINDING = B
+    return _BINDING
+
+
 def check(fn: str, status: int) -> None:
     if status != 0:
         msg = lib().attn_status_string(status).decode()

@@ -14,7 +14,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import ATTN_MAX_SPLITS, check, lib
+from ._lib import ATTN_MAX_SPLITS, binding, check, lib
 
 _BF16 = torch.bfloat16
 
@@ -577,7 +577,9 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 
 # ---------------------------------------------------------------------------
 # A key/value cache held in 8 bits (include/attn.h, "A key/value cache held in
-# 8 bits").
+# 8 bits").  The calls go to csrc/binding.cpp first, which takes the plain case
+# (ordinary tensors on the current device, the current stream, nothing to
+# refuse) at a third of the cost, and come here otherwise.
 # ---------------------------------------------------------------------------
 
 _NO_SCOPE = contextlib.nullcontext()
@@ -724,6 +726,10 @@ def cache_write_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Ten
     n_kv) or (B, ceil(L / block_size), n_kv).  Caches and scales are written
     in place; kv_lens is left to the caller to increment.
     """
+    if stream is None and binding().cache_write_fp8(
+            k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, cu_seqlens, block_table,
+            block_size) is None:
+        return
     if not isinstance(k_new, torch.Tensor) or not isinstance(v_new, torch.Tensor):
         raise TypeError("k_new and v_new must be torch.Tensors")
     dev = k_new.device
@@ -764,6 +770,11 @@ def cache_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch
     into ``k_out`` / ``v_out`` when given (rows contiguous, other strides
     multiples of 8); rows outside every sequence are left as they were.
     """
+    if stream is None and k_out is None and v_out is None:
+        r = binding().cache_read_fp8(k_cache, v_cache, k_scales, v_scales, cu_seqlens, total,
+                                     block_table, starts, block_size)
+        if r is not NotImplemented:
+            return r
     if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
         _need(k_cache, "k_cache", _U8, 4)
     dev = k_cache.device
@@ -900,6 +911,12 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     Arguments as :func:`decode_fp8_splitkv`, except that num_splits 0 lets the
     library divide the tokens of all sequences in equal shares; ``workspace``
     (uint8, allocated when not given) holds the partials."""
+    if stream is None:
+        r = binding().decode_fp8(q, None, None, k_cache, v_cache, k_scales, v_scales, kv_lens,
+                                 block_table, num_splits, max_kv_len, scale, out, lse, workspace,
+                                 window_left, softcap, alibi_slopes, block_size)
+        if r is not NotImplemented:
+            return r
     return _decode_fp8(q, None, None, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
                        num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left,
                        softcap, alibi_slopes, block_size)
@@ -922,6 +939,12 @@ def decode_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     kv_lens is left to the caller to increment."""
     if k_new is None or v_new is None:
         raise TypeError("k_new and v_new must be torch.Tensors")
+    if stream is None:
+        r = binding().decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens,
+                                 block_table, num_splits, max_kv_len, scale, out, lse, workspace,
+                                 window_left, softcap, alibi_slopes, block_size)
+        if r is not NotImplemented:
+            return r
     return _decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, block_table,
                        num_splits, max_kv_len, scale, out, lse, workspace, stream, window_left,
                        softcap, alibi_slopes, block_size)

@@ -1,6 +1,8 @@
-"""Builds ``libattn.so`` (all CUDA sources, sm_103a only) in-tree with nvcc.
+"""Builds ``libattn.so`` (all CUDA sources, sm_103a only) in-tree with nvcc, and
+``_binding.so`` (the Python calls of the 8-bit cache, against the torch that is
+installed) with the host compiler.
 
-Object files go to ``_build/`` at the repository root; the shared library is
+Object files go to ``_build/`` at the repository root; the shared libraries are
 written next to this file.  Translation units compile in parallel.
 """
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libattn.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -41,17 +46,40 @@ def _deps_newer(target: str) -> bool:
         return True
     t = os.path.getmtime(target)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-    deps += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+    deps += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__), BINDING_SRC]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every ``csrc/*.cu`` for sm_103a and link ``libattn.so``.
+def _build_binding() -> None:
+    """Compiles ``csrc/binding.cpp`` against Python's and torch's headers."""
+    import torch
 
-    Returns the library path.  Raises ``RuntimeError`` with nvcc's output on
-    failure.
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared",
+           "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, BINDING_SRC, "-o", tmp,
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile every ``csrc/*.cu`` for sm_103a and link ``libattn.so``, and
+    build ``_binding.so``.
+
+    Returns the library path.  Raises ``RuntimeError`` with the compiler's
+    output on failure.
     """
+    binding = force or _deps_newer(BINDING_PATH)
     if not force and not _deps_newer(LIB_PATH):
+        if binding:
+            _build_binding()
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -68,8 +96,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(9, os.cpu_count() or 1))) as ex:
+        other = ex.submit(_build_binding) if binding else None
         objs = list(ex.map(compile_one, sources()))
+        if other is not None:
+            other.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

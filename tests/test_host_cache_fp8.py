@@ -112,3 +112,23 @@ def test_workspace_bytes(L):
     for S, B, H, d in [(2, 1, 1, 64), (76, 1, 28, 128), (1024, 65535, 64, 256)]:
         n = f(S, B, H, 1, d)
         assert n == -(-S * B * H * d * 4 // 256) * 256 + S * B * H * 4
+
+
+def test_binding_takes_only_what_it_knows(L):
+    """csrc/binding.cpp on the CPU: everything is refused (NotImplemented), so
+    api.py's checks and messages decide."""
+    import torch
+
+    from exact_io_aware_order_gb300._lib import binding
+
+    b = binding()
+    x = torch.zeros(2, 3, 64, dtype=torch.bfloat16)
+    u = torch.zeros(2, 16, 3, 64, dtype=torch.uint8)
+    s, n = torch.ones(2, 3), torch.zeros(2, dtype=torch.int32)
+    for args in ((), (1,) * 10, (x, x, u, u, s, s, n, None, None, 16), (None,) * 10):
+        assert b.cache_write_fp8(*args) is NotImplemented
+    for args in ((), (u, u, s, s, n, 4, None, None, 16), (None,) * 9, (u, u, s, s, n, "4", None, None, 16)):
+        assert b.cache_read_fp8(*args) is NotImplemented
+    for args in ((), (x, None, None, u, u, s, s, n, None, 0, None, None, None, None, None, -1, 0.0,
+                      None, 16), (None,) * 19):
+        assert b.decode_fp8(*args) is NotImplemented
