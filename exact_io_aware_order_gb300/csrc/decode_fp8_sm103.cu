@@ -71,10 +71,10 @@ __host__ __device__ constexpr int q_smem_bytes(int D, bool wide, int groups) {
   return q_in_smem(D, wide) ? groups * (D / 32) * 32 * (wide ? 32 : 16) : 0;
 }
 // Blocks that share an SM, by their registers.
-constexpr int blocks_per_sm(int D, bool wide) { return D == 256 ? 2 : 3; }
+constexpr int blocks_per_sm(int D) { return D == 64 ? 3 : 2; }
 
 // Half tiles of a warp's ring: what those blocks' shared memory holds.
-constexpr int ring_slots(int D) { return D == 64 ? 8 : (D == 128 ? 4 : 3); }
+constexpr int ring_slots(int D) { return D == 256 ? 3 : 4; }
 
 template <int D>
 struct Smem {
@@ -243,7 +243,7 @@ __device__ __forceinline__ long long div_small(long long x, long long y) {
 // teams, one for each 16 heads; team rg's warps take the tiles in turn, and the
 // teams copy the same tiles each for itself (they are bound by arithmetic).
 template <int D, bool kWide>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kWide))
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(D))
 decode_fp8_kernel(const DecodeFp8KParams kp) {
   using L = Smem<D>;
   const DecodeFp8Args& a = kp.a;
@@ -259,6 +259,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   grid_dep_launch();
 
   int b, kvh;             // the segment's pair
+  int raw_len = 0;        // (splits) its length, asked for before q and used after
   Span sp;
   int tile, seg_tiles;    // its first tile in the pair and how many
   int pair_tiles = 0;     // (shares) tiles of the pair
@@ -268,7 +269,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   int more = 0;
   if (a.parts == 0) {
     b = blockIdx.z, kvh = blockIdx.y;
-    sp = span_of(a, a.kv_lens[b], threadIdx.x == 0 && blockIdx.x == 0 ? kp.err_word : nullptr);
+    raw_len = a.kv_lens[b];
     tile = 0, seg_tiles = 0;  // set below, in tokens
   } else {
     // Tiles before each sequence (of one head): every warp scans the batch for
@@ -330,6 +331,29 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 
   // ---- the segment's tokens, and where its result goes ----
   for (;;) {
+  // ================= q: asked for first, used while the first tiles fly =================
+  const int row0 = kWide ? rg * 16 : 0;
+  const int gid = lane >> 2, quad = lane & 3;
+  constexpr int kRows = kWide ? 2 : 1;  // query rows a thread looks after
+  constexpr int kSteps = D / 32;        // k steps of q k
+  constexpr bool kQSmem = q_in_smem(D, kWide);
+  // Columns 16 i + 4 quad .. + 3 of rows gid (and gid + 8).
+  uint2 qx[kRows][2 * kSteps];
+  {
+    const uint16_t* qsrc = a.q + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D + quad * 4;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = row0 + gid + 8 * r;
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i) {
+        qx[r][i] = make_uint2(0u, 0u);
+        if (row < g) qx[r][i] = *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
+      }
+    }
+  }
+
+  if (a.parts == 0)
+    sp = span_of(a, raw_len, threadIdx.x == 0 && blockIdx.x == 0 ? kp.err_word : nullptr);
   const int len = sp.len, lo_tok = sp.lo_tok;
   int t0, t1;
   float *o_out, *lse_out;
@@ -369,27 +393,6 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   }
   const int n_tiles = (t1 - t0 + kTile - 1) / kTile;
   const int my_tiles = col < n_tiles ? (n_tiles - col + team - 1) / team : 0;
-
-  // ================= q: asked for first, used while the first tiles fly =================
-  const int row0 = kWide ? rg * 16 : 0;
-  const int gid = lane >> 2, quad = lane & 3;
-  constexpr int kRows = kWide ? 2 : 1;  // query rows a thread looks after
-  constexpr int kSteps = D / 32;        // k steps of q k
-  constexpr bool kQSmem = q_in_smem(D, kWide);
-  // Columns 16 i + 4 quad .. + 3 of rows gid (and gid + 8).
-  uint2 qx[kRows][2 * kSteps];
-  {
-    const uint16_t* qsrc = a.q + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D + quad * 4;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = row0 + gid + 8 * r;
-#pragma unroll
-      for (int i = 0; i < 2 * kSteps; ++i) {
-        qx[r][i] = make_uint2(0u, 0u);
-        if (row < g) qx[r][i] = *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
-      }
-    }
-  }
 
   // ================= this warp's ring =================
   // Half 2 j is K and half 2 j + 1 is V of the warp's tile j (the block's tile
@@ -943,7 +946,7 @@ cudaError_t launch_d(const DecodeFp8Args& a, const LaunchCtx& ctx) {
 int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms) {
   const int g = n_q_heads / n_kv_heads;
   const bool wide = g > 8;
-  int n = blocks_per_sm(head_dim, wide);
+  int n = blocks_per_sm(head_dim);
   if (head_dim == 256 && g > 16) n = 1;  // q's fragments leave room for one block's rings
   return n * num_sms;
 }
