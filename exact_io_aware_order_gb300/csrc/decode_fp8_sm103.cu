@@ -224,14 +224,21 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
 }
 
 // Two ways to divide the work.  With `parts` 0 block (split, kv head, sequence)
-// takes one split of the C header's rule.  With parts > 0 the tiles of all
-// (sequence, kv head) pairs form one list that `parts` blocks take equal shares
-// of, so that no length, however different from the others, leaves an SM idle.
-// A share is a run of segments, each a part of one pair.  A segment that is a
-// whole pair is the result; of the others a block has at most two, its first
-// (which began in an earlier block: partial slot 2 p) and its last (slot 2 p + 1).
-// The block that holds a pair's first tile notes the pair's first and last block
-// for the combine.
+// takes one split of the C header's rule.  With parts > 0 the blocks share the
+// tiles of all (sequence, kv head) pairs, whatever their lengths:
+//   * few pairs (4 pairs <= parts): each pair gets as many blocks as it takes at
+//     c tiles a block, the smallest c for which all of them surely fit, and its
+//     tiles evenly over those.  Every block has one segment (a part of one pair).
+//   * otherwise all tiles form one list that the blocks take equal shares of, so
+//     that no SM idles; a share may run over several segments.  Going on to the
+//     next segment costs a block 4 to 8 us (merge, q, the first tiles' latency),
+//     which long shares bear and short ones do not (head_dim 256 with a window of
+//     4096 tokens, 4 sequences x 8 heads over 304 blocks: 25 us in shares, 23 us
+//     with blocks of their own).
+// A segment that is a whole pair is the result; of the others a block has at most
+// two, its first (which began in an earlier block: partial slot 2 p) and its last
+// (slot 2 p + 1).  The block that holds a pair's first tile notes the pair's first
+// and last block for the combine.
 //
 // x / y; the 64-bit division is a long sequence, and almost no list needs it.
 __device__ __forceinline__ long long div_small(long long x, long long y) {
@@ -267,17 +274,16 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   // `more` blocks that take part have `share` + 1 tiles, the others `share`.
   long long pos = 0, end = 0, share = 0;
   int more = 0;
+  int last_block = -1;  // (blocks of their own) the pair's last
   if (a.parts == 0) {
     b = blockIdx.z, kvh = blockIdx.y;
     raw_len = a.kv_lens[b];
     tile = 0, seg_tiles = 0;  // set below, in tokens
   } else {
-    // Tiles before each sequence (of one head): every warp scans the batch for
-    // itself, 32 sequences at a time (twice, where there are more: for the whole
-    // and for its place).
-    long long all = 0;
-    int raw = 0, n = 0, scan = 0;  // this lane's length, tiles, tiles up to it (32 sequences)
-    auto scan32 = [&](int i0, bool report) {
+    // Every warp scans the batch for itself, 32 sequences at a time (twice, where
+    // there are more: for all tiles, and for its place).
+    int raw = 0, n = 0;  // this lane's length and tiles (of one head)
+    auto tiles32 = [&](int i0, bool report) {
       const int i = i0 + lane;
       raw = n = 0;
       if (i < a.batch) {
@@ -292,41 +298,61 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
           for (int e = 0; e < n_kv; ++e) a.pair_blocks[(size_t)i * n_kv + e] = make_int2(0, 0);
         }
       }
-      scan = n;
+    };
+    long long all = 0;
+    for (int i0 = 0; i0 < a.batch; i0 += 32) {
+      tiles32(i0, warp == 0);
+      all += __reduce_add_sync(0xffffffffu, n);
+    }
+    const long long total = all * n_kv, pairs = (long long)a.batch * n_kv;
+    const int parts = (int)min((long long)a.parts, total);  // each has a tile
+    if ((int)blockIdx.x >= parts) return;
+    const bool own = 4 * pairs <= parts;  // blocks of their own for each pair
+    int most = 0;
+    if (own) {
+      most = (int)div_small(total + parts - pairs - 1, parts - pairs);
+      pos = blockIdx.x;
+    } else {
+      share = div_small(total, parts);
+      more = (int)(total - share * parts);
+      pos = blockIdx.x * share + min((int)blockIdx.x, more);
+      end = pos + share + ((int)blockIdx.x < more ? 1 : 0);
+    }
+    // Where pos (of the blocks, or of the tiles) lies.
+    long long before = 0;  // blocks, or tiles, of one head before the 32 sequences
+    int i0 = 0, count, scan;
+    unsigned here;
+    for (;;) {
+      if (a.batch > 32) tiles32(i0, false);
+      scan = count = own ? (n + most - 1) / most : n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += y;
       }
-    };
-    for (int i0 = 0; i0 < a.batch; i0 += 32) {
-      scan32(i0, warp == 0);
-      all += __shfl_sync(0xffffffffu, scan, 31);
-    }
-    const long long total = all * n_kv;
-    const int parts = (int)min((long long)a.parts, total);  // each has a tile
-    if ((int)blockIdx.x >= parts) return;
-    share = div_small(total, parts);
-    more = (int)(total - share * parts);
-    pos = blockIdx.x * share + min((int)blockIdx.x, more);
-    end = pos + share + ((int)blockIdx.x < more ? 1 : 0);
-    long long before = 0;  // tiles of the sequences before the 32 that hold pos
-    int i0 = 0;
-    unsigned here;
-    for (;; i0 += 32) {
-      if (a.batch > 32) scan32(i0, false);
       here = __ballot_sync(0xffffffffu, pos < (before + scan) * n_kv);
       if (here) break;
       before += __shfl_sync(0xffffffffu, scan, 31);
+      i0 += 32;
+      if (i0 >= a.batch) return;  // more blocks than the pairs take
     }
     const int at = __ffs(here) - 1;
     b = i0 + at;
     sp = span_of(a, __shfl_sync(0xffffffffu, raw, at), nullptr);
     pair_tiles = __shfl_sync(0xffffffffu, n, at);
+    count = __shfl_sync(0xffffffffu, count, at);
     const long long in_seq =
-        pos - (before + __shfl_sync(0xffffffffu, scan - n, at)) * n_kv;
-    kvh = (int)div_small(in_seq, pair_tiles);
-    tile = (int)(in_seq - (long long)kvh * pair_tiles);
+        pos - (before + __shfl_sync(0xffffffffu, scan, at) - count) * n_kv;
+    kvh = (int)div_small(in_seq, count);
+    const int i = (int)(in_seq - (long long)kvh * count);
+    if (own) {
+      tile = (int)div_small((long long)i * pair_tiles, count);
+      pos = 0;
+      end = div_small((i + 1LL) * pair_tiles, count) - tile;
+      last_block = blockIdx.x + count - 1;
+    } else {
+      tile = i;
+    }
   }
 
   // ---- the segment's tokens, and where its result goes ----
@@ -385,9 +411,11 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       lse_out = a.lse_partial + part * g;
     }
     if (tile == 0 && threadIdx.x == 0) {
-      // The block of the pair's last tile x.
-      const long long x = pos + pair_tiles - 1, big = (share + 1) * more;
-      const long long q = x < big ? div_small(x, share + 1) : more + div_small(x - big, share);
+      long long q = last_block;
+      if (q < 0) {  // of the pair's last tile x
+        const long long x = pos + pair_tiles - 1, big = (share + 1) * more;
+        q = x < big ? div_small(x, share + 1) : more + div_small(x - big, share);
+      }
       a.pair_blocks[(size_t)b * n_kv + kvh] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : (int)q);
     }
   }
@@ -811,7 +839,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 // ---------------------------------------------------------------------------
 // Combine of the shares: one block per (sequence, query head, kCols columns)
 // merges the pair's partials, those of blocks first .. last of the list, by their
-// LSE weights.  Each warp takes every kCombineWarps-th, kAtOnce at a time (their
+// LSE weights.  Each warp takes every 16th (8th), kAtOnce at a time (their
 // loads in flight together), with a running maximum; then the warps' states are
 // merged.  Narrow slices of columns where there are few rows: one sequence of
 // 30720 tokens has 28 rows of some 115 partials each.
@@ -821,11 +849,13 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 // blocks that came last would run behind the others (paged batch of 16: 139
 // against 106 us).
 // ---------------------------------------------------------------------------
-constexpr int kCombineWarps = 8, kAtOnce = 8;
+constexpr int kAtOnce = 8;
+constexpr int combine_warps(int cols) { return cols == 32 ? 16 : 8; }
 
 template <int D, int kCols>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+__global__ void __launch_bounds__(32 * combine_warps(kCols))
 combine_shares_kernel(const DecodeFp8Args a) {
+  constexpr int kCombineWarps = combine_warps(kCols);
   constexpr int kVec = kCols / 32;  // columns of a lane
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps], s_o[kCombineWarps][kCols];
   const int h = blockIdx.x, b = blockIdx.y, col0 = blockIdx.z * kCols;
@@ -953,7 +983,6 @@ int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sm
 
 cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx) {
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.stream = ctx.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -964,6 +993,7 @@ cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx) {
   // 32 columns a block while that fits into one wave, whole rows beyond.
   const bool slices = (long long)a.n_q_heads * a.batch * (D / 32) <= 8LL * ctx.num_sms;
   cfg.gridDim = dim3(a.n_q_heads, a.batch, slices ? D / 32 : 1);
+  cfg.blockDim = dim3(32 * combine_warps(slices ? 32 : D));
   auto run = [&](auto slice, auto row) {
     return slices ? cudaLaunchKernelEx(&cfg, slice, a) : cudaLaunchKernelEx(&cfg, row, a);
   };
