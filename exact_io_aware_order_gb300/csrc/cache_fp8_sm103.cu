@@ -224,16 +224,32 @@ __global__ void __launch_bounds__(kThreads) cache_write_fp8_kernel(const RowsKPa
     if (c != sub * kChunkRows) load(c);
     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int w = 0; w < 2; ++w) {
+      // Both halves of each word at once; an infinity or NaN (0x7f80 and above)
+      // sends the lane through them again.
+      uint32_t two = 0u;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         if (c + i * kRowsPerStep + lr >= u.rows) continue;
         const uint4 y = x[(w * kSteps + i) * 32];
-        amax[w] = finite_max(amax[w], y.x);
-        amax[w] = finite_max(amax[w], y.y);
-        amax[w] = finite_max(amax[w], y.z);
-        amax[w] = finite_max(amax[w], y.w);
+        two = __vmaxu2(two, y.x & 0x7fff7fffu);
+        two = __vmaxu2(two, y.y & 0x7fff7fffu);
+        two = __vmaxu2(two, y.z & 0x7fff7fffu);
+        two = __vmaxu2(two, y.w & 0x7fff7fffu);
       }
+      uint32_t top = max(two & 0xffffu, two >> 16);
+      if (top >= 0x7f80u) {
+        top = 0u;
+#pragma unroll 1
+        for (int i = 0; i < kSteps; ++i) {
+          if (c + i * kRowsPerStep + lr >= u.rows) continue;
+          const uint4 y = x[(w * kSteps + i) * 32];
+          top = finite_max(finite_max(top, y.x), y.y);
+          top = finite_max(finite_max(top, y.z), y.w);
+        }
+      }
+      amax[w] = max(amax[w], top);
+    }
   }
   if (!found) u.rows = 0;
   float was[2] = {0.f, 0.f};
