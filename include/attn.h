@@ -714,12 +714,12 @@ size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads,
  *                cache's pointers are then only read)
  *   num_splits : >= 1: the split rule of attn_decode_splitkv_ex; or 0: the
  *                library divides the work.  It then lets the blocks of one wave
- *                take equal shares of all (sequence, kv head) pairs' tokens, so
- *                lengths may differ as they like; batches of more than 1024
- *                sequences, and caches whose max_kv_len (or window) is 512 tokens
- *                at most, take one split.  The results depend on the division
- *                only in the order of fp32 sums.
- *   workspace  : attn_decode_fp8_workspace_bytes(num_splits, ...) bytes, 16-byte
+ *                share the tokens of all (sequence, kv head) pairs, so lengths may
+ *                differ as they like; batches of more than 1024 sequences, and
+ *                short caches (by max_kv_len or the window: up to 800 tokens, 2048
+ *                where the pairs fill half a wave), take one split.  The results
+ *                depend on the division only in the order of fp32 sums.
+ *   workspace  : attn_decode_fp8_workspace_bytes of the same arguments, 16-byte
  *                aligned (NULL where that is 0); overwritten.  Calls that may
  *                overlap on the device need one each.
  *   workspace_bytes: its size; less than needed is ATTN_ERR_SCRATCH

@@ -520,3 +520,56 @@ def test_same_call_same_bits(dev):
     for _ in range(5):
         o, lse = attn.decode_fp8(q, *tensors, i32([5000, 10, 777], dev), table)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("n_q", [8, 24])
+def test_query_that_is_not_finite(dev, n_q, bad):
+    """An infinity or a NaN in q makes its own row NaN and no other."""
+    c = filled([300], 2, 64, 16, True, seed=61)
+    tensors, table = c.on(dev)
+    q = queries(1, n_q, 64, 7).to(dev)
+    for S in (1, 0):
+        kw = dict(num_splits=S, max_kv_len=3000)
+        want = attn.decode_fp8(q, *tensors, i32([300], dev), table, **kw)
+        q2 = q.clone()
+        q2[0, 3, 17] = bad
+        o, lse = attn.decode_fp8(q2, *tensors, i32([300], dev), table, **kw)
+        attn.check_device_status()
+        assert bool(torch.isnan(o[0, 3]).all()) and bool(torch.isnan(lse[0, 3]))
+        rest = [h for h in range(n_q) if h != 3]
+        assert torch.equal(o[0, rest], want[0][0, rest])
+        assert torch.equal(lse[0, rest], want[1][0, rest])
+
+
+def test_tiny_and_zero_queries(dev):
+    """Rows of zeros, and of bf16 subnormals: uniform weights."""
+    c = filled([77], 2, 128, 16, True, seed=62)
+    tensors, table = c.on(dev)
+    q = queries(1, 8, 128, 8)
+    q[0, 0] = 0.0
+    q[0, 1] = 1e-39
+    q[0, 5] = -0.0
+    want, bound, _ = reference(c, q, [77], 0.1)
+    o, lse = attn.decode_fp8(q.to(dev), *tensors, i32([77], dev), table, scale=0.1)
+    attn.check_device_status()
+    close(o, lse, want, bound, "tiny queries")
+
+
+def test_queries_with_one_large_value(dev):
+    """A row whose largest value is 2^12 times the others: the two e4m3 terms
+    still carry the others (2^-15 of the maximum and above exactly)."""
+    c = filled([333], 2, 128, 32, True, seed=63)
+    tensors, table = c.on(dev)
+    q = queries(1, 8, 128, 9)
+    q[0, :, 40] = 0.0
+    big = q.clone()
+    big[0, 2, 40] = 4096.0
+    scale = 0.05
+    want, bound, (kv, vv) = reference(c, big, [333], scale)
+    # below 2^-15 of the row's maximum a value of q may be off by 2^-23 of it
+    d_s = scale * 2.0 ** -23 * 4096.0 * np.abs(kv[0]).sum(axis=2).max()
+    o, lse = attn.decode_fp8(big.to(dev), *tensors, i32([333], dev), table, scale=scale)
+    attn.check_device_status()
+    extra = 2 * d_s * np.abs(vv[0]).max()
+    close(o, lse, want, (bound[0] + extra, bound[1] + d_s), "one large value")
