@@ -597,10 +597,13 @@ int validate_rows(const attn::CacheRowsArgs& a, bool read) {
   for (long long s : {a.k_token_stride, a.k_head_stride, a.v_token_stride, a.v_head_stride})
     if (s < 0 || s % 8 != 0) return ATTN_ERR_SHAPE;
   if (read) {  // rows that are written must not lie on one another
-    for (long long s : {a.k_token_stride, a.v_token_stride})
-      if (a.total_tokens > 1 && s < a.c.head_dim) return ATTN_ERR_SHAPE;
-    for (long long s : {a.k_head_stride, a.v_head_stride})
-      if (a.c.n_kv_heads > 1 && s < a.c.head_dim) return ATTN_ERR_SHAPE;
+    const long long T = a.total_tokens, H = a.c.n_kv_heads, d = a.c.head_dim;
+    auto apart = [&](long long token, long long head) {
+      if ((T > 1 && token < d) || (H > 1 && head < d)) return false;
+      return T == 1 || H == 1 || token <= (head - d) / (T - 1) || head <= (token - d) / (H - 1);
+    };
+    if (!apart(a.k_token_stride, a.k_head_stride) || !apart(a.v_token_stride, a.v_head_stride))
+      return ATTN_ERR_SHAPE;
   }
   // units of work (at most total / block_size + 2 num_seqs blocks, K and V of
   // every head) are counted in 32 bits, eight warps each at most

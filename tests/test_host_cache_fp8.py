@@ -83,6 +83,18 @@ def test_rows_validation_of_one_direction(L, E):
     assert rows(L, True, vh=64) == E["SHAPE"]
 
 
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_read_into_rows_on_one_another(L, E, which):
+    """3 tokens of 2 heads, 128 columns: refused unless every row has a place of
+    its own (16 bytes off: what is refused for that has passed the strides)."""
+    at = lambda t, h: rows(L, True, **{which: P + 8, which + "t": t, which + "h": h}, T=3)
+    assert at(128, 384) == at(256, 128) == at(128, 400) == at(512, 256) == E["ALIGN"]
+    assert at(128, 128) == at(128, 376) == at(128, 256) == at(248, 128) == E["SHAPE"]
+    for T, n_kv, t, h in ((1, 2, 0, 128), (3, 1, 128, 0)):
+        assert rows(L, True, **{which: P + 8, which + "t": t, which + "h": h}, T=T,
+                    n_kv=n_kv) == E["ALIGN"]
+
+
 DECODE = [("NULL", dict(q=None)), ("NULL", dict(lens=None)), ("SHAPE", dict(B=0)),
           ("SHAPE", dict(B=65536)), ("SHAPE", dict(scale=0.0)), ("SHAPE", dict(scale=float("nan"))),
           ("SHAPE", dict(w=-2)), ("SHAPE", dict(cap=-1.0)), ("SHAPE", dict(cap=float("inf"))),
