@@ -42,9 +42,10 @@
 // other warp touches, and asks for the next half as soon as it has read one.
 // There is no producer warp and no barrier in the stream, and any block size
 // takes the same path (a row's address is one shuffle and one multiply-add).
-// Measured on the paged batch of 16 sequences (555 MB, head_dim 128): TMA boxes
-// of 16 tokens by a producer warp 157 us (the copies' issue by one warp was the
-// limit), TMA boxes by every warp 114 us.
+// Measured on a paged batch of 16 sequences (555 MB, head_dim 128; 83 us at the
+// measured copy rate): TMA boxes of 16 tokens by a producer warp 157 us (the
+// copies' issue by one warp was the limit), TMA boxes by every warp 114 us, this
+// form 104 us with its combine.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -177,9 +178,12 @@ __device__ __forceinline__ void split_f16x2(float x, float y, uint32_t& hi, uint
   const float2 h = unpack_f16x2(hi);
   lo = pack_f16x2(x - h.x, y - h.y);
 }
-// floor(log2 x) of a positive normal float, as a float (2^23 + e - (2^23 + 127)).
+// floor(log2 x) of a scale, as a float (2^23 + e - (2^23 + 127)); the least one's
+// for 0 (a block that is zero as it was allocated), so that the reference stays
+// within 60 of the score and a weight within fp32.
 __device__ __forceinline__ float exponent_of(float x) {
-  return __uint_as_float(0x4b000000u | (__float_as_uint(x) >> 23)) - 8388735.f;
+  const uint32_t e = max(__float_as_uint(x) >> 23, (uint32_t)(127 + kScaleExpMin));
+  return __uint_as_float(0x4b000000u | e) - 8388735.f;
 }
 // 4 bytes to shared memory, or zero without a read where !ok.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
@@ -975,7 +979,6 @@ cudaError_t launch_d(const DecodeFp8Args& a, const LaunchCtx& ctx) {
 
 int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms) {
   const int g = n_q_heads / n_kv_heads;
-  const bool wide = g > 8;
   int n = blocks_per_sm(head_dim);
   if (head_dim == 256 && g > 16) n = 1;  // q's fragments leave room for one block's rings
   return n * num_sms;

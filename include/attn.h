@@ -646,11 +646,11 @@ int attn_cache_write_fp8(const attn_bf16* k, const attn_bf16* v, int64_t k_token
  *
  * Page: same, section "Decode: a different bottleneck" (paged caches).
  *
- *   k, v       : bf16 OUTPUTS, strides as attn_cache_write_fp8 but at least
- *                head_dim wherever there is more than one token or head: row
- *                cu[s] + i receives position starts[s] + i of sequence s, for
- *                i < cu[s+1] - cu[s].  Rows outside every sequence are not
- *                written.
+ *   k, v       : bf16 OUTPUTS, strides as attn_cache_write_fp8, but with the
+ *                rows apart (each head's tokens behind the one's before, or each
+ *                token's heads): row cu[s] + i receives position starts[s] + i
+ *                of sequence s, for i < cu[s+1] - cu[s].  Rows outside every
+ *                sequence are not written.
  *   cu_seqlens : (num_seqs + 1,) int32, as attn_prefill_varlen
  *   starts     : (num_seqs,) int32 first position read of each sequence, or
  *                NULL: 0
@@ -676,12 +676,12 @@ int attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const fl
  *
  *   q          : (batch, n_q_heads, head_dim) bf16, 16-byte aligned
  *   k_cache, v_cache, k_scales, v_scales: the cache (num_seqs = batch).  Any
- *                scales in [2^-60, 2^60] do, not only powers of two.
+ *                scales in [2^-60, 2^60] do, not only powers of two, and 0.
  *   kv_lens, num_splits, o_partial, lse_partial, scale, window_left, softcap,
  *   alibi_slopes: as attn_decode_splitkv_ex, with its split rule
- * q, the codes and the scales are used as they are (q's bf16 values and the
- * codes are exact as fp16 operands), the weights with 22 significant bits and
- * every sum in fp32.  Keys and values of masked positions (past kv_lens, left
+ * The codes and the scales are used as they are, q as it is down to 2^-15 of its
+ * row's largest magnitude and to within 2^-23 of that below, the weights with 22
+ * significant bits and every sum in fp32.  Keys and values of masked positions (past kv_lens, left
  * of the window) may hold anything, NaN included.
  * Limits: those of the cache; n_q_heads / n_kv_heads <= 64; batch and
  *   n_kv_heads <= 65535; the cache's slots times n_kv_heads below 2^32.

@@ -3,6 +3,11 @@ the float64 oracle on the values that the cache stands for: the combined
 result, every split's partials, the append, and a run of all the cache's
 operators together."""
 
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -573,3 +578,113 @@ def test_queries_with_one_large_value(dev):
     attn.check_device_status()
     extra = 2 * d_s * np.abs(vv[0]).max()
     close(o, lse, want, (bound[0] + extra, bound[1] + d_s), "one large value")
+
+
+def test_captured_shares_follow_the_lengths(dev):
+    """A step captured with num_splits 0 divides the tokens by the lengths of
+    the replay, not of the capture: sequences that grow, and ones that are
+    replaced by others between replays (an empty one among them)."""
+    n_kv, n_q, d, bs, B = 2, 8, 128, 16, 4
+    at = [[5, 16, 130, 1000], [1000, 0, 700, 3], [0, 0, 0, 0], [1000, 1000, 1000, 1000]]
+    c = filled([1000] * B, n_kv, d, bs, True, seed=42, room=[1001] * B)
+    q = queries(B, n_q, d, 1).to(dev)
+    tensors, table = c.on(dev)
+    lens = i32(at[0], dev)
+    call = lambda: attn.decode_fp8(q, *tensors, lens, table, max_kv_len=4000)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call()
+    for now in at + at[:1]:
+        lens.copy_(i32(now, dev))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, call()):
+            assert torch.equal(a, b), now
+        want, bound, _ = reference(c, q.cpu(), now, d ** -0.5)
+        close(*got, want, bound, str(now))
+    attn.check_device_status()
+
+
+FIRST_CALL = """
+import torch
+import exact_io_aware_order_gb300 as attn
+dev = torch.device("cuda", 0)
+k = torch.zeros(8, 16, 2, 64, dtype=torch.uint8, device=dev)
+v, ks = k.clone(), torch.zeros(8, 2, device=dev)
+vs, table = ks.clone(), torch.arange(8, dtype=torch.int32, device=dev).view(1, 8)
+x = torch.ones(1, 2, 64, dtype=torch.bfloat16, device=dev)
+lens = torch.zeros(1, dtype=torch.int32, device=dev)
+q = torch.ones(1, 4, 64, dtype=torch.bfloat16, device=dev)
+attn.cache_write_fp8(x, x, k, v, ks, vs, lens, None, table)
+lens += 1
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    o, lse = attn.decode_append_fp8(q, x, x, k, v, ks, vs, lens, table, max_kv_len=5000)
+g.replay()
+torch.cuda.synchronize()
+attn.check_device_status()
+assert bool((o == 1).all()), o
+print("replayed")
+"""
+
+
+def test_first_decode_of_a_process_is_captured():
+    """Nothing of the decode's set-up gets in the way of a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_threads_at_once(dev):
+    """The calls drop the interpreter's lock while they launch."""
+    lens = [2000, 100]
+    c = filled(lens, 2, 128, 16, True, seed=33)
+    tensors, table = c.on(dev)
+    q = [queries(2, 8, 128, s).to(dev) for s in range(2)]
+    ln = i32(lens, dev)
+    want = [attn.decode_fp8(x, *tensors, ln, table) for x in q]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got[i].append(attn.decode_fp8(q[i], *tensors, ln, table))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 50
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("n_q", [4, 20])
+@pytest.mark.parametrize("S", [2, 0])
+def test_scales_of_zero(dev, n_q, S):
+    """A cache that is zero as it was allocated, scales too, and blocks of zeros
+    among written ones: values of 0, whatever the codes' scale."""
+    lens = [3000, 33]
+    q = queries(2, n_q, 64, 3)
+    kw = dict(num_splits=S, max_kv_len=3000)
+    for some in (False, True):
+        c = filled(lens, 2, 64, 16, True, seed=71)
+        zero = torch.zeros(len(c.ks), dtype=torch.bool)
+        zero[::2] = True
+        zero = zero if some else torch.ones_like(zero)
+        for codes, scales in ((c.k, c.ks), (c.v, c.vs)):
+            codes[zero], scales[zero] = 0, 0.0
+        tensors, table = c.on(dev)
+        want, bound, _ = reference(c, q, lens, 0.125)
+        o, lse = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, **kw)
+        attn.check_device_status()
+        close(o, lse, want, bound, f"zero scales, some {some}")
+        if not some:
+            assert not o.any()
