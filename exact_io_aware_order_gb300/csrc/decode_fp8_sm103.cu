@@ -241,13 +241,41 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
 //     with blocks of their own).
 // A segment that is a whole pair is the result; of the others a block has at most
 // two, its first (which began in an earlier block: partial slot 2 p) and its last
-// (slot 2 p + 1).  The block that holds a pair's first tile notes the pair's first
-// and last block for the combine.
-//
+// (slot 2 p + 1).  The combine needs a pair's first and last block: it works them
+// out for itself where one load holds all lengths, and else finds them noted by
+// the block that has the pair's first tile.
+constexpr int kNoteBeyond = 32;  // sequences
+
 // x / y; the 64-bit division is a long sequence, and almost no list needs it.
 __device__ __forceinline__ long long div_small(long long x, long long y) {
   if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
   return x / y;
+}
+
+struct Shares {
+  int parts;        // blocks that have work: at most one a tile
+  bool own;         // blocks of their own for each pair
+  int most;         // (own) tiles a block, at most
+  long long share;  // (otherwise) the first `more` blocks have share + 1 tiles,
+  int more;         // the others share
+};
+__device__ __forceinline__ Shares shares_of(int parts, long long total, long long pairs) {
+  Shares s = {};
+  s.parts = (int)min((long long)parts, total);
+  if (s.parts == 0) return s;
+  s.own = 4 * pairs <= s.parts;
+  if (s.own) {
+    s.most = (int)div_small(total + s.parts - pairs - 1, s.parts - pairs);
+  } else {
+    s.share = div_small(total, s.parts);
+    s.more = (int)(total - s.share * s.parts);
+  }
+  return s;
+}
+// (not own) The block that has tile x of the list.
+__device__ __forceinline__ int block_of(const Shares& s, long long x) {
+  const long long big = (s.share + 1) * s.more;
+  return (int)(x < big ? div_small(x, s.share + 1) : s.more + div_small(x - big, s.share));
 }
 
 // kWide: more than 8 query heads per kv head (up to 64).  The four warps form G
@@ -274,10 +302,9 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   Span sp;
   int tile, seg_tiles;    // its first tile in the pair and how many
   int pair_tiles = 0;     // (shares) tiles of the pair
-  // (shares) Of the list: where this block is and up to where it goes; the first
-  // `more` blocks that take part have `share` + 1 tiles, the others `share`.
-  long long pos = 0, end = 0, share = 0;
-  int more = 0;
+  // (shares) Of the list: where this block is and up to where it goes.
+  long long pos = 0, end = 0;
+  Shares sh = {};
   int last_block = -1;  // (blocks of their own) the pair's last
   if (a.parts == 0) {
     b = blockIdx.z, kvh = blockIdx.y;
@@ -299,7 +326,8 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
             a.o_final[(size_t)i * a.n_q_heads * D + e] = 0.f;
           for (int e = 0; e < a.n_q_heads; ++e)
             a.lse_final[(size_t)i * a.n_q_heads + e] = -INFINITY;
-          for (int e = 0; e < n_kv; ++e) a.pair_blocks[(size_t)i * n_kv + e] = make_int2(0, 0);
+          if (a.batch > kNoteBeyond)
+            for (int e = 0; e < n_kv; ++e) a.pair_blocks[(size_t)i * n_kv + e] = make_int2(0, 0);
         }
       }
     };
@@ -308,19 +336,13 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       tiles32(i0, warp == 0);
       all += __reduce_add_sync(0xffffffffu, n);
     }
-    const long long total = all * n_kv, pairs = (long long)a.batch * n_kv;
-    const int parts = (int)min((long long)a.parts, total);  // each has a tile
-    if ((int)blockIdx.x >= parts) return;
-    const bool own = 4 * pairs <= parts;  // blocks of their own for each pair
-    int most = 0;
-    if (own) {
-      most = (int)div_small(total + parts - pairs - 1, parts - pairs);
+    sh = shares_of(a.parts, all * n_kv, (long long)a.batch * n_kv);
+    if ((int)blockIdx.x >= sh.parts) return;
+    if (sh.own) {
       pos = blockIdx.x;
     } else {
-      share = div_small(total, parts);
-      more = (int)(total - share * parts);
-      pos = blockIdx.x * share + min((int)blockIdx.x, more);
-      end = pos + share + ((int)blockIdx.x < more ? 1 : 0);
+      pos = blockIdx.x * sh.share + min((int)blockIdx.x, sh.more);
+      end = pos + sh.share + ((int)blockIdx.x < sh.more ? 1 : 0);
     }
     // Where pos (of the blocks, or of the tiles) lies.
     long long before = 0;  // blocks, or tiles, of one head before the 32 sequences
@@ -328,7 +350,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
     unsigned here;
     for (;;) {
       if (a.batch > 32) tiles32(i0, false);
-      scan = count = own ? (n + most - 1) / most : n;
+      scan = count = sh.own ? (n + sh.most - 1) / sh.most : n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, scan, o);
@@ -349,7 +371,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         pos - (before + __shfl_sync(0xffffffffu, scan, at) - count) * n_kv;
     kvh = (int)div_small(in_seq, count);
     const int i = (int)(in_seq - (long long)kvh * count);
-    if (own) {
+    if (sh.own) {
       tile = (int)div_small((long long)i * pair_tiles, count);
       pos = 0;
       end = div_small((i + 1LL) * pair_tiles, count) - tile;
@@ -414,13 +436,9 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       o_out = a.o_partial + part * g * D;
       lse_out = a.lse_partial + part * g;
     }
-    if (tile == 0 && threadIdx.x == 0) {
-      long long q = last_block;
-      if (q < 0) {  // of the pair's last tile x
-        const long long x = pos + pair_tiles - 1, big = (share + 1) * more;
-        q = x < big ? div_small(x, share + 1) : more + div_small(x - big, share);
-      }
-      a.pair_blocks[(size_t)b * n_kv + kvh] = make_int2(blockIdx.x, whole ? (int)blockIdx.x : (int)q);
+    if (a.batch > kNoteBeyond && tile == 0 && threadIdx.x == 0) {
+      const int last = last_block >= 0 ? last_block : block_of(sh, pos + pair_tiles - 1);
+      a.pair_blocks[(size_t)b * n_kv + kvh] = make_int2(blockIdx.x, last);
     }
   }
   const int n_tiles = (t1 - t0 + kTile - 1) / kTile;
@@ -845,8 +863,10 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 // merges the pair's partials, those of blocks first .. last of the list, by their
 // LSE weights.  Each warp takes every 16th (8th), kAtOnce at a time (their
 // loads in flight together), with a running maximum; then the warps' states are
-// merged.  Narrow slices of columns where there are few rows: one sequence of
-// 30720 tokens has 28 rows of some 115 partials each.
+// merged.  Narrow slices of columns where that makes no more blocks than SMs (one
+// sequence of 30720 tokens: 28 rows of 76 partials each, 14.8 us with the decode
+// against 15.9 in whole rows); more of them cost more than they hide (8 sequences,
+// 64 heads of 64: 23.6 against 20.7).
 //
 // It does not let the next kernel start early: a decode whose blocks came in
 // while this grid's still hold their places would not find all SMs free, and the
@@ -865,9 +885,35 @@ combine_shares_kernel(const DecodeFp8Args a) {
   const int h = blockIdx.x, b = blockIdx.y, col0 = blockIdx.z * kCols;
   const int g = a.n_q_heads / a.c.n_kv_heads, kvh = h / g, row = h % g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_wait();
-  const int2 blocks = a.pair_blocks[(size_t)b * a.c.n_kv_heads + kvh];
-  const int n = blocks.y - blocks.x + 1;
+  int first, n;  // the pair's blocks
+  if (a.batch <= kNoteBeyond) {
+    // The lengths are there before the decode ends: its blocks waited for the
+    // kernels in front of it before they let this one start.
+    const int len = lane < a.batch ? a.kv_lens[lane] : 0;
+    const int tiles = lane < a.batch ? tiles_of(span_of(a, len, nullptr)) : 0;
+    const int n_kv = a.c.n_kv_heads;
+    const Shares sh = shares_of(a.parts, (long long)__reduce_add_sync(0xffffffffu, tiles) * n_kv,
+                                (long long)a.batch * n_kv);
+    const int count = sh.own ? (tiles + sh.most - 1) / sh.most : tiles;
+    const int mine = __shfl_sync(0xffffffffu, count, b);
+    const long long at =
+        (long long)__reduce_add_sync(0xffffffffu, lane < b ? count : 0) * n_kv + (long long)kvh * mine;
+    if (mine == 0) {
+      first = n = 0;
+    } else if (sh.own) {
+      first = (int)at;
+      n = mine;
+    } else {
+      first = block_of(sh, at);
+      n = block_of(sh, at + mine - 1) - first + 1;
+    }
+    grid_dep_wait();
+  } else {
+    grid_dep_wait();
+    const int2 blocks = a.pair_blocks[(size_t)b * a.c.n_kv_heads + kvh];
+    first = blocks.x;
+    n = blocks.y - blocks.x + 1;
+  }
   if (n <= 1) return;  // the result is already there
   float m = -INFINITY, l = 0.f, o[kVec];
 #pragma unroll
@@ -881,7 +927,7 @@ combine_shares_kernel(const DecodeFp8Args a) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
       if (i < n) {
-        const size_t part = (2 * (size_t)(blocks.x + i) + (i == 0 ? 1 : 0)) * g + row;
+        const size_t part = (2 * (size_t)(first + i) + (i == 0 ? 1 : 0)) * g + row;
         w[u] = a.lse_partial[part] * kLog2e;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) x[u][e] = a.o_partial[part * D + col0 + e * 32 + lane];
@@ -993,8 +1039,8 @@ cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int D = a.c.head_dim;
-  // 32 columns a block while that fits into one wave, whole rows beyond.
-  const bool slices = (long long)a.n_q_heads * a.batch * (D / 32) <= 8LL * ctx.num_sms;
+  // 32 columns a block, or whole rows (see the kernel).
+  const bool slices = (long long)a.n_q_heads * a.batch * (D / 32) <= ctx.num_sms;
   cfg.gridDim = dim3(a.n_q_heads, a.batch, slices ? D / 32 : 1);
   cfg.blockDim = dim3(32 * combine_warps(slices ? 32 : D));
   auto run = [&](auto slice, auto row) {
