@@ -655,15 +655,15 @@ size_t fp8_lse_offset(size_t rows, int head_dim) {
 size_t fp8_pairs_offset(size_t rows) { return (rows * sizeof(float) + 255) / 256 * 256; }
 
 // Blocks that share a decode's tiles (num_splits = 0): all that are resident
-// together, but none for less than kFp8MinTiles tiles, which it could not spread
-// over its warps and which would cost the combine more than they save.  0 where
-// a pair is one block's work: batches beyond the shares' scan, and short
-// sequences, where the combine costs more than it saves.  28 / 4 heads, one
-// sequence of 700 / 1000 tokens: 10.9 / 13.3 us in one block a pair, 12.3 / 10.6
-// in shares; 32 / 8 heads, 32 equal sequences (pairs for most of the SMs) of 1000 /
-// 2000 / 3000: 16.4 / 30 / 42 against 23 / 35 / 45, where shares only pay once
-// lengths differ.
-constexpr int kFp8MinTiles = 8, kFp8OneBlock = 800, kFp8OneBlockMany = 2048;
+// together, but no more than one for kFp8MinTiles tiles (one for each warp) and one
+// for each pair, which may be its pairs' last and shorter.  0 where a pair is one
+// block's work: batches beyond the shares' scan, and short sequences, where the
+// combine costs more than it saves.  How short depends on how many blocks there are
+// to a pair.  Equal lengths, head_dim 128, one block a pair / shared: 1 sequence
+// x 4 kv heads of 300 / 500 tokens 7.0 / 8.4 us against 7.4 / 7.6; 16 x 8 of 700 / 1500
+// 10.7 / 19.4 against 13.4 / 20.0; 32 x 8 of 1000 / 2500 18 / 36 against 27 / 42,
+// where sharing only pays once lengths differ (24 x 8 of 800 to 4000: 47 against 34).
+constexpr int kFp8MinTiles = 4;
 int fp8_parts(int batch, int n_q_heads, int n_kv_heads, int head_dim, long long max_len,
               int window_left, int num_sms) {
   if (batch > attn::kMaxSharedBatch) return 0;
@@ -671,10 +671,9 @@ int fp8_parts(int batch, int n_q_heads, int n_kv_heads, int head_dim, long long 
   if (window_left >= 0) most = std::min(most, window_left + 1LL);
   const int top = attn::decode_fp8_max_parts(n_q_heads, n_kv_heads, head_dim, num_sms);
   const long long pairs = (long long)batch * n_kv_heads;
-  if (most <= (2 * pairs >= top ? kFp8OneBlockMany : kFp8OneBlock)) return 0;
+  if (most <= (4 * pairs <= top ? 400 : 2 * pairs <= top ? 1000 : 2048)) return 0;
   const long long tiles = (most + 31) / 32 * pairs;
-  const long long parts = (tiles + kFp8MinTiles - 1) / kFp8MinTiles;
-  return (int)std::min(parts, (long long)top);
+  return (int)std::min((tiles + kFp8MinTiles - 1) / kFp8MinTiles + pairs, (long long)top);
 }
 size_t fp8_shares_bytes(int parts, int batch, int n_q_heads, int n_kv_heads, int head_dim) {
   if (parts == 0) return 0;

@@ -230,15 +230,18 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
 // Two ways to divide the work.  With `parts` 0 block (split, kv head, sequence)
 // takes one split of the C header's rule.  With parts > 0 the blocks share the
 // tiles of all (sequence, kv head) pairs, whatever their lengths:
-//   * few pairs (4 pairs <= parts): each pair gets as many blocks as it takes at
-//     c tiles a block, the smallest c for which all of them surely fit, and its
-//     tiles evenly over those.  Every block has one segment (a part of one pair).
-//   * otherwise all tiles form one list that the blocks take equal shares of, so
+//   * blocks of their own: each pair gets as many blocks as it takes at `most` tiles a
+//     block, the smallest number for which all of them surely fit (or one, where that
+//     covers the longest pair), and its tiles evenly over those.  Every block has one
+//     segment (a part of one pair).
+//   * equal shares: all tiles form one list that the blocks take equal parts of, so
 //     that no SM idles; a share may run over several segments.  Going on to the
-//     next segment costs a block 4 to 8 us (merge, q, the first tiles' latency),
-//     which long shares bear and short ones do not (head_dim 256 with a window of
-//     4096 tokens, 4 sequences x 8 heads over 304 blocks: 25 us in shares, 23 us
-//     with blocks of their own).
+//     next segment costs a block 4 to 8 us (merge, q, the first tiles' latency), as
+//     much as some 16 tiles do.
+// So a pair gets blocks of its own where the longest of them has at most kOwnMore
+// tiles more than an equal share.  8 kv heads of 128, own / shares: 16 sequences of
+// 1500 tokens (14 more) 20.0 / 21.7 us, 8 of 12000 (21 more) 45.7 / 43.5; 36 of 4000
+// (one block each, 7 more) 59.7 / 64.2.
 // A segment that is a whole pair is the result; of the others a block has at most
 // two, its first (which began in an earlier block: partial slot 2 p) and its last
 // (slot 2 p + 1).  The combine needs a pair's first and last block: it works them
@@ -252,6 +255,7 @@ __device__ __forceinline__ long long div_small(long long x, long long y) {
   return x / y;
 }
 
+constexpr int kOwnMore = 16;
 struct Shares {
   int parts;        // blocks that have work: at most one a tile
   bool own;         // blocks of their own for each pair
@@ -259,14 +263,19 @@ struct Shares {
   long long share;  // (otherwise) the first `more` blocks have share + 1 tiles,
   int more;         // the others share
 };
-__device__ __forceinline__ Shares shares_of(int parts, long long total, long long pairs) {
+// total: tiles of all pairs; longest: those of the longest pair.
+__device__ __forceinline__ Shares shares_of(int parts, long long total, long long pairs,
+                                            int longest) {
   Shares s = {};
   s.parts = (int)min((long long)parts, total);
   if (s.parts == 0) return s;
-  s.own = 4 * pairs <= s.parts;
-  if (s.own) {
-    s.most = (int)div_small(total + s.parts - pairs - 1, s.parts - pairs);
-  } else {
+  if (pairs <= s.parts) {
+    const int spare = s.parts - (int)pairs;
+    s.most = longest;
+    if (spare > 0) s.most = (int)min((long long)longest, div_small(total + spare - 1, spare));
+    s.own = (long long)(s.most - kOwnMore) * s.parts <= total;
+  }
+  if (!s.own) {
     s.share = div_small(total, s.parts);
     s.more = (int)(total - s.share * s.parts);
   }
@@ -332,11 +341,13 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       }
     };
     long long all = 0;
+    int longest = 0;
     for (int i0 = 0; i0 < a.batch; i0 += 32) {
       tiles32(i0, warp == 0);
       all += __reduce_add_sync(0xffffffffu, n);
+      longest = max(longest, __reduce_max_sync(0xffffffffu, n));
     }
-    sh = shares_of(a.parts, all * n_kv, (long long)a.batch * n_kv);
+    sh = shares_of(a.parts, all * n_kv, (long long)a.batch * n_kv, longest);
     if ((int)blockIdx.x >= sh.parts) return;
     if (sh.own) {
       pos = blockIdx.x;
@@ -864,9 +875,9 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 // LSE weights.  Each warp takes every 16th (8th), kAtOnce at a time (their
 // loads in flight together), with a running maximum; then the warps' states are
 // merged.  Narrow slices of columns where that makes no more blocks than SMs (one
-// sequence of 30720 tokens: 28 rows of 76 partials each, 14.8 us with the decode
-// against 15.9 in whole rows); more of them cost more than they hide (8 sequences,
-// 64 heads of 64: 23.6 against 20.7).
+// sequence of 30720 tokens, 28 rows of 76 partials each: 1.1 us less than in whole
+// rows); more of them cost more than they hide (8 sequences, 64 heads of 64: 2.9 us
+// more).
 //
 // It does not let the next kernel start early: a decode whose blocks came in
 // while this grid's still hold their places would not find all SMs free, and the
@@ -893,7 +904,7 @@ combine_shares_kernel(const DecodeFp8Args a) {
     const int tiles = lane < a.batch ? tiles_of(span_of(a, len, nullptr)) : 0;
     const int n_kv = a.c.n_kv_heads;
     const Shares sh = shares_of(a.parts, (long long)__reduce_add_sync(0xffffffffu, tiles) * n_kv,
-                                (long long)a.batch * n_kv);
+                                (long long)a.batch * n_kv, __reduce_max_sync(0xffffffffu, tiles));
     const int count = sh.own ? (tiles + sh.most - 1) / sh.most : tiles;
     const int mine = __shfl_sync(0xffffffffu, count, b);
     const long long at =

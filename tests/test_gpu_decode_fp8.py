@@ -688,3 +688,27 @@ def test_scales_of_zero(dev, n_q, S):
         close(o, lse, want, bound, f"zero scales, some {some}")
         if not some:
             assert not o.any()
+
+
+@pytest.mark.parametrize("B,n_kv,d,lo,hi", [
+    (36, 8, 64, 300, 300),     # a block for each pair
+    (36, 8, 64, 10, 2500),     # too uneven for that
+    (40, 1, 128, 0, 900),      # more sequences than a warp has lanes, several blocks a pair
+    (33, 2, 256, 500, 600),
+    (304, 1, 128, 33, 64),     # as many pairs as blocks
+    (305, 1, 128, 33, 64),     # one more
+    (2, 3, 128, 31, 33),       # fewer tiles than pairs have blocks
+])
+def test_every_division(dev, B, n_kv, d, lo, hi):
+    """num_splits 0 over batches for which each pair takes one block, several,
+    or parts of shared ones."""
+    gen = np.random.default_rng(B)
+    lens = [int(n) for n in gen.integers(lo, hi + 1, B)]
+    n_q = 2 * n_kv
+    c = filled(lens, n_kv, d, 16, True, seed=B)
+    tensors, table = c.on(dev)
+    q = queries(B, n_q, d, 5)
+    want, bound, _ = reference(c, q, lens, d ** -0.5)
+    o, lse = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, max_kv_len=8192)
+    attn.check_device_status()
+    close(o, lse, want, bound, f"{B} x {n_kv}, {lo} to {hi}")
