@@ -909,7 +909,7 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     """Decode over an 8-bit cache, split and combined in one call
     (``attn_decode_fp8``): returns (O (B, n_q, d), LSE (B, n_q)), fp32.
     Arguments as :func:`decode_fp8_splitkv`, except that num_splits 0 lets the
-    library divide the tokens of all sequences in equal shares; ``workspace``
+    library divide the tokens of all sequences among its blocks; ``workspace``
     (uint8, allocated when not given) holds the partials."""
     if stream is None:
         r = binding().decode_fp8(q, None, None, k_cache, v_cache, k_scales, v_scales, kv_lens,

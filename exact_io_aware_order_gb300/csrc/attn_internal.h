@@ -164,10 +164,10 @@ struct DecodeFp8Args {
   float softcap;
   const float* alibi_slopes;
   int append;  // 1: each sequence holds one token more than kv_lens says (just written)
-  // Shares (parts > 0; num_splits is then not used): the tiles of all pairs in
-  // equal shares for `parts` blocks.  o_partial / lse_partial hold two partials
-  // (n_q_heads / n_kv_heads rows each) a block, pair_blocks (batch, n_kv_heads)
-  // the first and last block of each pair; results go to o_final / lse_final.
+  // Shares (parts > 0; num_splits is then not used): `parts` blocks divide the
+  // tiles of all pairs.  o_partial / lse_partial hold two partials (n_q_heads /
+  // n_kv_heads rows each) a block, pair_blocks (batch, n_kv_heads) the first and last
+  // block of each pair (larger batches only); results go to o_final / lse_final.
   int parts = 0;
   float* o_final = nullptr;
   float* lse_final = nullptr;

@@ -718,8 +718,8 @@ size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads,
  *                differ as they like; batches of more than 1024 sequences, and
  *                short caches (by max_kv_len or the window: up to 400 tokens, 1000
  *                or 2048 where a wave has less than 4 or 2 blocks a pair), take
- *                one split.  The results
- *                depend on the division only in the order of fp32 sums.
+ *                one split.  The results depend on the division only in the order
+ *                of fp32 sums.
  *   workspace  : attn_decode_fp8_workspace_bytes of the same arguments, 16-byte
  *                aligned (NULL where that is 0); overwritten.  Calls that may
  *                overlap on the device need one each.
