@@ -790,7 +790,7 @@ int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16*
     return ATTN_ERR_ALIGN;
   const long long row = (long long)n_kv_heads * head_dim;
   attn::CacheRowsArgs w{a.c, const_cast<attn_bf16*>(k_new), const_cast<attn_bf16*>(v_new), row,
-                        head_dim, row, head_dim, nullptr, kv_lens, batch, batch};
+                        head_dim, row, head_dim, nullptr, kv_lens, batch, batch, true};
   if (append) {
     st = validate_rows(w, false);
     if (st != ATTN_OK) return st;

@@ -149,6 +149,7 @@ struct CacheRowsArgs {
   const int32_t* cu_seqlens;  // (num_seqs + 1,); null (write): one row a sequence
   const int32_t* starts;      // (num_seqs,) first cache position of each sequence; null (read): 0
   int num_seqs, total_tokens;
+  bool before_decode = false;  // write: a decode step's; the decode waits for it by itself
 };
 
 struct DecodeFp8Args {

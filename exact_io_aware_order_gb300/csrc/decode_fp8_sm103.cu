@@ -303,7 +303,11 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   const int team = kWarps / G;                       // warps of a team
   const int col = warp % team, rg = warp / team;     // place in the team, row group
 
-  grid_dep_wait();
+  // Behind its step's write, which has waited for the kernels in front of both, the
+  // decode finds its place and asks for q while the write runs, and waits before
+  // it reads the cache (one sequence of 30719 tokens: 17.9 -> 15.6 us).
+  bool to_wait = a.append != 0;
+  if (!to_wait) grid_dep_wait();
   grid_dep_launch();
 
   int b, kvh;             // the segment's pair
@@ -532,6 +536,10 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   if (my_tiles > 0) {
     next_a = entry(0);
     next_b = entry(1);
+  }
+  if (to_wait) grid_dep_wait();
+  to_wait = false;
+  if (my_tiles > 0) {
 #pragma unroll 1
     for (int h = 0; h < L::kSlots; ++h) put();
   }
@@ -898,8 +906,8 @@ combine_shares_kernel(const DecodeFp8Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int first, n;  // the pair's blocks
   if (a.batch <= kNoteBeyond) {
-    // The lengths are there before the decode ends: its blocks waited for the
-    // kernels in front of it before they let this one start.
+    // The lengths are there before the decode ends: the kernels in front of the call
+    // had ended before the decode's blocks let this one start.
     const int len = lane < a.batch ? a.kv_lens[lane] : 0;
     const int tiles = lane < a.batch ? tiles_of(span_of(a, len, nullptr)) : 0;
     const int n_kv = a.c.n_kv_heads;

@@ -712,3 +712,37 @@ def test_every_division(dev, B, n_kv, d, lo, hi):
     o, lse = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, max_kv_len=8192)
     attn.check_device_status()
     close(o, lse, want, bound, f"{B} x {n_kv}, {lo} to {hi}")
+
+
+@pytest.mark.parametrize("B,n_kv", [(1, 2), (6, 2), (40, 16)])
+def test_steps_in_a_row(dev, B, n_kv):
+    """Steps one behind the other, each attending what the one before wrote, with
+    scales that grow in the block being filled, against the write, a pause and the
+    decode (a decode of a small step starts while its write runs)."""
+    d, bs, steps = 64, 16, 24
+    start = [(7 * b) % 23 for b in range(B)]
+    c = filled(start, n_kv, d, bs, True, seed=81, room=[n + steps for n in start])
+    apart, table = c.on(dev)
+    joined = [t.clone() for t in apart]
+    q = queries(B, 4 * n_kv, d, 1).to(dev)
+    new = [(rows(n_kv, B, d, 100 + i).permute(1, 0, 2) * 2.0 ** (i / 2)).contiguous().to(dev)
+           for i in range(steps)]
+    want = []
+    lens = i32(start, dev)
+    for x in new:
+        attn.cache_write_fp8(x, x, *apart, lens, None, table)
+        lens += 1
+        torch.cuda.synchronize()
+        want.append(attn.decode_fp8(q, *apart, lens, table, max_kv_len=3000))
+        torch.cuda.synchronize()
+    got = []
+    lens = [i32([n + i for n in start], dev) for i in range(steps)]
+    torch.cuda.synchronize()
+    for x, ln in zip(new, lens):
+        got.append(attn.decode_append_fp8(q, x, x, *joined, ln, table, max_kv_len=2999))
+    torch.cuda.synchronize()
+    attn.check_device_status()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), i
+    for a, b in zip(joined, apart):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
