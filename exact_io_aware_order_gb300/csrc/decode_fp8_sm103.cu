@@ -74,22 +74,25 @@ __host__ __device__ constexpr int q_smem_bytes(int D, bool wide, int groups) {
 // Blocks that share an SM, by their registers.
 constexpr int blocks_per_sm(int D) { return D == 64 ? 3 : 2; }
 
-// Half tiles of a warp's ring: what those blocks' shared memory holds.
-constexpr int ring_slots(int D) { return D == 256 ? 3 : 4; }
+// Half tiles of a warp's ring: what those blocks' shared memory holds.  Two blocks
+// with two halves a warp beat one with three (8 sequences of 8000-16000 tokens, 4
+// kv heads of 256, 64 heads each: 217 against 307 us; 16 heads each: 64 against 76).
+constexpr int ring_slots(int D, bool wide) { return D == 256 ? (wide ? 2 : 3) : 4; }
 
-template <int D>
+template <int D, bool kWide>
 struct Smem {
-  static constexpr int kSlots = ring_slots(D);
+  static constexpr int kSlots = ring_slots(D, kWide);
   static constexpr int kHalfBytes = kTile * D;             // K or V of a tile
   static constexpr int kScaleBytes = kTile * 4;
   static constexpr int kPitch = D + 8;                     // floats of a merged row
   static constexpr int kRing = 0;                          // [warp][slot]
-  static constexpr int kScale = kWarps * kSlots * kHalfBytes;
+  // The warps' rows are merged in the rings.
+  static constexpr int kRingBytes = kWarps * kSlots * kHalfBytes;
+  static constexpr int kRowsBytes = kWarps * (kWide ? 16 : 8) * kPitch * 4;
+  static constexpr int kScale = kRingBytes > kRowsBytes ? kRingBytes : kRowsBytes;
   static constexpr int kMerge = kScale + kWarps * kSlots * kScaleBytes;  // m, l, weight
   static constexpr int kQ = kMerge + 3 * kWarps * 16 * 4;  // q's fragments, where kept here
   static constexpr int total(int q_bytes) { return kQ + q_bytes; }
-  // The warps' rows are merged in the rings.
-  static_assert(kWarps * 16 * kPitch * 4 <= kScale, "merged rows fit");
 };
 
 // Row r of a half has its 16-byte chunk c at chunk c ^ swizzle(r).  ldmatrix reads
@@ -293,7 +296,7 @@ __device__ __forceinline__ int block_of(const Shares& s, long long x) {
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(D))
 decode_fp8_kernel(const DecodeFp8KParams kp) {
-  using L = Smem<D>;
+  using L = Smem<D, kWide>;
   const DecodeFp8Args& a = kp.a;
   extern __shared__ __align__(128) uint8_t smem[];
   const int n_kv = a.c.n_kv_heads, bs = a.c.block_size;
@@ -995,7 +998,7 @@ combine_shares_kernel(const DecodeFp8Args a) {
 // ---------------------------------------------------------------------------
 template <int D, bool kWide>
 cudaError_t launch_t(const DecodeFp8Args& a, const LaunchCtx& ctx) {
-  using L = Smem<D>;
+  using L = Smem<D, kWide>;
   const int g = a.n_q_heads / a.c.n_kv_heads;  // at most 64 (validated)
   const int groups = g <= 16 ? 1 : (g <= 32 ? 2 : 4);
   DecodeFp8KParams kp;
@@ -1043,10 +1046,7 @@ cudaError_t launch_d(const DecodeFp8Args& a, const LaunchCtx& ctx) {
 }  // namespace
 
 int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms) {
-  const int g = n_q_heads / n_kv_heads;
-  int n = blocks_per_sm(head_dim);
-  if (head_dim == 256 && g > 16) n = 1;  // q's fragments leave room for one block's rings
-  return n * num_sms;
+  return blocks_per_sm(head_dim) * num_sms;
 }
 
 cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx) {
