@@ -2,7 +2,7 @@
 // their cost.
 //
 // A decode step over a short cache takes the GPU a few microseconds; api.py's
-// checks, three allocations and a ctypes call of 29 arguments take 18.  These
+// checks, three allocations and a ctypes call of 27 arguments take 18.  These
 // functions make the same checks on the tensors themselves, allocate, and call
 // the same C entry points.  They take the plain case only: ordinary tensors on
 // the current device, the current stream, every check passed and the call
@@ -30,9 +30,13 @@ decltype(&attn_decode_fp8_workspace_bytes) g_workspace_bytes = nullptr;
 
 PyObject* refuse() { Py_RETURN_NOTIMPLEMENTED; }
 
-// An ordinary tensor (no subclass), or null.
+// An ordinary tensor, or null: no subclass, and none of those that have a shape
+// and a device but no storage (what torch.vmap or torch.func.grad hands its
+// function is a plain torch.Tensor to Python).
 const at::Tensor* tensor(PyObject* o) {
-  return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr;
+  if (!THPVariable_CheckExact(o)) return nullptr;
+  const at::Tensor* t = &THPVariable_Unpack(o);
+  return t->has_storage() ? t : nullptr;
 }
 bool is(const at::Tensor* t, at::ScalarType type, int64_t ndim, c10::Device dev) {
   return t && t->scalar_type() == type && t->dim() == ndim && t->device() == dev &&
@@ -57,6 +61,7 @@ bool number(PyObject* o, double* x) {
   *x = static_cast<double>(i);
   return true;
 }
+// data_ptr() may throw, so it is called with the interpreter's lock held.
 template <typename T>
 T* data(const at::Tensor* t) {
   return t ? static_cast<T*>(t->data_ptr()) : nullptr;
@@ -68,49 +73,62 @@ bool on_current_device(const at::Tensor* t) {
 }
 void* stream_of(c10::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
+// The interpreter's lock given up for a scope, and taken again however it ends.
+class WithoutLock {
+ public:
+  WithoutLock() : state_(PyEval_SaveThread()) {}
+  ~WithoutLock() { PyEval_RestoreThread(state_); }
+  WithoutLock(const WithoutLock&) = delete;
+  WithoutLock& operator=(const WithoutLock&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 struct Cache {
-  const at::Tensor *k, *v, *ks, *vs, *table;
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int32_t* table;
   int n_kv, d, block_size, max_blocks, num_blocks, capacity;
 };
 
 // k_cache, v_cache, k_scales, v_scales at a[0..3], the block table and block_size.
 bool cache(PyObject* const* a, PyObject* table, PyObject* block_size, c10::Device dev,
            int64_t num_seqs, Cache* c) {
-  c->k = tensor(a[0]);
-  c->v = tensor(a[1]);
-  c->ks = tensor(a[2]);
-  c->vs = tensor(a[3]);
-  if (!is(c->k, at::kByte, 4, dev) || !is(c->v, at::kByte, 4, dev) ||
-      c->v->sizes() != c->k->sizes())
+  const at::Tensor *k = tensor(a[0]), *v = tensor(a[1]), *ks = tensor(a[2]), *vs = tensor(a[3]);
+  const at::Tensor* bt = nullptr;
+  if (!is(k, at::kByte, 4, dev) || !is(v, at::kByte, 4, dev) ||
+      v->sizes() != k->sizes())
     return false;
-  const int64_t n = c->k->size(0), rows = c->k->size(1), n_kv = c->k->size(2);
+  const int64_t n = k->size(0), rows = k->size(1), n_kv = k->size(2);
   int64_t bs = 0;
   if (block_size != Py_None && (!integer(block_size, &bs) || bs < 1)) return false;
   int64_t scale_dims;
   if (table != Py_None) {
-    c->table = tensor(table);
-    if (!is(c->table, at::kInt, 2, dev) || c->table->size(0) != num_seqs || (bs && bs != rows))
+    bt = tensor(table);
+    if (!is(bt, at::kInt, 2, dev) || bt->size(0) != num_seqs || (bs && bs != rows))
       return false;
-    const int64_t most = c->table->size(1);
+    const int64_t most = bt->size(1);
     if (rows > INT32_MAX || n > INT32_MAX || most > INT32_MAX || rows * most > INT32_MAX)
       return false;
     c->block_size = (int)rows, c->max_blocks = (int)most, c->num_blocks = (int)n;
     c->capacity = (int)(rows * most);
     scale_dims = 2;
   } else {
-    c->table = nullptr;
     if (n != num_seqs || bs < 1 || rows > INT32_MAX) return false;
     c->block_size = (int)bs, c->max_blocks = 0, c->num_blocks = 0, c->capacity = (int)rows;
     scale_dims = 3;
   }
-  for (const at::Tensor* s : {c->ks, c->vs}) {
+  for (const at::Tensor* s : {ks, vs}) {
     if (!is(s, at::kFloat, scale_dims, dev) || s->size(0) != n) return false;
     if (scale_dims == 2 ? s->size(1) != n_kv
                         : s->size(1) != (rows + bs - 1) / bs || s->size(2) != n_kv)
       return false;
   }
-  if (n_kv > INT32_MAX || c->k->size(3) > INT32_MAX) return false;
-  c->n_kv = (int)n_kv, c->d = (int)c->k->size(3);
+  if (n_kv > INT32_MAX || k->size(3) > INT32_MAX) return false;
+  c->n_kv = (int)n_kv, c->d = (int)k->size(3);
+  c->k = data<uint8_t>(k), c->v = data<uint8_t>(v);
+  c->ks = data<float>(ks), c->vs = data<float>(vs), c->table = data<int32_t>(bt);
   return true;
 }
 
@@ -139,15 +157,17 @@ PyObject* cache_write_fp8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if ((packed ? !is_lens(cu, dev, B + 1) : total != B) || k->size(head) != c.n_kv ||
       k->size(2) != c.d || total > INT32_MAX || B > INT32_MAX)
     return refuse();
+  const attn_bf16 *kp = data<attn_bf16>(k), *vp = data<attn_bf16>(v);
+  const int32_t *cup = data<int32_t>(cu), *lensp = data<int32_t>(lens);
+  const int64_t kt = k->stride(tok), kh = k->stride(head), vt = v->stride(tok), vh = v->stride(head);
   void* stream = stream_of(dev);
   int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = g_write(data<attn_bf16>(k), data<attn_bf16>(v), k->stride(tok), k->stride(head),
-               v->stride(tok), v->stride(head), data<uint8_t>(c.k), data<uint8_t>(c.v),
-               data<float>(c.ks), data<float>(c.vs), data<int32_t>(c.table), data<int32_t>(cu),
-               data<int32_t>(lens), (int)B, (int)total, c.n_kv, c.d, c.block_size, c.max_blocks,
-               c.num_blocks, c.capacity, stream);
-  Py_END_ALLOW_THREADS
+  {
+    WithoutLock unlocked;
+    st = g_write(kp, vp, kt, kh, vt, vh, c.k, c.v, c.ks, c.vs, c.table, cup, lensp, (int)B,
+                 (int)total, c.n_kv, c.d, c.block_size, c.max_blocks, c.num_blocks, c.capacity,
+                 stream);
+  }
   if (st != ATTN_OK) return refuse();
   Py_RETURN_NONE;
 }
@@ -168,15 +188,17 @@ PyObject* cache_read_fp8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return refuse();
   const auto opt = at::TensorOptions().dtype(at::kBFloat16).device(dev);
   const at::Tensor k = at::empty({c.n_kv, total, c.d}, opt), v = at::empty({c.n_kv, total, c.d}, opt);
+  attn_bf16 *kp = data<attn_bf16>(&k), *vp = data<attn_bf16>(&v);
+  const int32_t *cup = data<int32_t>(cu), *startsp = data<int32_t>(starts);
+  const int64_t head = total * c.d;
   void* stream = stream_of(dev);
   int st;
-  Py_BEGIN_ALLOW_THREADS
-  const int64_t head = total * c.d;
-  st = g_read(data<uint8_t>(c.k), data<uint8_t>(c.v), data<float>(c.ks), data<float>(c.vs),
-              data<attn_bf16>(&k), data<attn_bf16>(&v), c.d, head, c.d, head,
-              data<int32_t>(c.table), data<int32_t>(cu), data<int32_t>(starts), (int)B, (int)total,
-              c.n_kv, c.d, c.block_size, c.max_blocks, c.num_blocks, c.capacity, stream);
-  Py_END_ALLOW_THREADS
+  {
+    WithoutLock unlocked;
+    st = g_read(c.k, c.v, c.ks, c.vs, kp, vp, c.d, head, c.d, head, c.table, cup, startsp, (int)B,
+                (int)total, c.n_kv, c.d, c.block_size, c.max_blocks, c.num_blocks, c.capacity,
+                stream);
+  }
   if (st != ATTN_OK) return refuse();
   return Py_BuildValue("(NN)", THPVariable_Wrap(k), THPVariable_Wrap(v));
 }
@@ -186,14 +208,14 @@ PyObject* cache_read_fp8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 // softcap, alibi_slopes, block_size)
 PyObject* decode_fp8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (n_args != 19) return refuse();
-  const at::Tensor* q = tensor(a[0]);
+  const at::Tensor *q = tensor(a[0]), *lens = tensor(a[7]);
   if (!on_current_device(q) || !is(q, at::kBFloat16, 3, q->device())) return refuse();
   const c10::Device dev = q->device();
   const int64_t B = q->size(0), n_q = q->size(1), d = q->size(2);
   Cache c;
   int64_t splits, window;
   double softcap, scale;
-  if (B > INT32_MAX || n_q > INT32_MAX || !is_lens(tensor(a[7]), dev, B) ||
+  if (B > INT32_MAX || n_q > INT32_MAX || !is_lens(lens, dev, B) ||
       !cache(a + 3, a[8], a[18], dev, B, &c) || c.d != d || !integer(a[9], &splits) ||
       splits < 0 || splits > ATTN_MAX_SPLITS || !integer(a[15], &window) ||
       !number(a[16], &softcap))
@@ -210,8 +232,8 @@ PyObject* decode_fp8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   int64_t max_len = c.capacity;
   if (a[10] != Py_None) {
     int64_t x;
-    if (!integer(a[10], &x) || (!c.table && x > c.capacity)) return refuse();
-    if (c.table) max_len = x;
+    if (!integer(a[10], &x) || (a[8] == Py_None && x > c.capacity)) return refuse();
+    if (a[8] != Py_None) max_len = x;
   }
   if (a[11] == Py_None) scale = 1.0 / std::sqrt((double)d);
   else if (!number(a[11], &scale)) return refuse();
@@ -243,17 +265,20 @@ PyObject* decode_fp8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                        (int)window);
     if (n > 0) ws = at::empty({(int64_t)n}, f32.dtype(at::kByte));
   }
+  const attn_bf16 *qp = data<attn_bf16>(q), *knp = data<attn_bf16>(kn), *vnp = data<attn_bf16>(vn);
+  const int32_t* lensp = data<int32_t>(lens);
+  const float* slopesp = data<float>(slopes);
+  float *outp = data<float>(&out), *lsep = data<float>(&lse);
+  void* wsp = ws.defined() ? ws.data_ptr() : nullptr;
+  const size_t wsn = ws.defined() ? (size_t)ws.numel() : 0;
   void* stream = stream_of(dev);
   int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = g_decode(data<attn_bf16>(q), data<attn_bf16>(kn), data<attn_bf16>(vn), data<uint8_t>(c.k),
-                data<uint8_t>(c.v), data<float>(c.ks), data<float>(c.vs), data<int32_t>(c.table),
-                data<int32_t>(tensor(a[7])), (int)splits, ws.defined() ? ws.data_ptr() : nullptr,
-                ws.defined() ? (size_t)ws.numel() : 0, data<float>(&out), data<float>(&lse),
-                (int)B, (int)n_q, c.n_kv, c.d, c.block_size, c.max_blocks, c.num_blocks,
-                (int)max_len, (float)scale, (int)window, (float)softcap, data<float>(slopes),
-                stream);
-  Py_END_ALLOW_THREADS
+  {
+    WithoutLock unlocked;
+    st = g_decode(qp, knp, vnp, c.k, c.v, c.ks, c.vs, c.table, lensp, (int)splits, wsp, wsn, outp,
+                  lsep, (int)B, (int)n_q, c.n_kv, c.d, c.block_size, c.max_blocks, c.num_blocks,
+                  (int)max_len, (float)scale, (int)window, (float)softcap, slopesp, stream);
+  }
   if (st != ATTN_OK) return refuse();
   return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
@@ -270,6 +295,10 @@ PyObject* init(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+// takes(x): whether x is a tensor whose memory these functions would look at (the
+// tests ask, on tensors that no GPU is needed for).
+PyObject* takes(PyObject*, PyObject* x) { return PyBool_FromLong(tensor(x) != nullptr); }
+
 // No C++ exception leaves for the interpreter.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -282,6 +311,7 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef kMethods[] = {
     {"init", init, METH_VARARGS, nullptr},
+    {"takes", takes, METH_O, nullptr},
     {"cache_write_fp8", (PyCFunction)(void (*)(void))guarded<cache_write_fp8>, METH_FASTCALL, nullptr},
     {"cache_read_fp8", (PyCFunction)(void (*)(void))guarded<cache_read_fp8>, METH_FASTCALL, nullptr},
     {"decode_fp8", (PyCFunction)(void (*)(void))guarded<decode_fp8>, METH_FASTCALL, nullptr},
