@@ -45,6 +45,14 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: int) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _columns(block_table: torch.Tensor) -> int:
+    """A block table's columns: at least one.  A table without any has no
+    address, and the C entry points take that for a contiguous cache."""
+    if block_table.shape[1] < 1:
+        raise ValueError("block_table must have at least one column")
+    return block_table.shape[1]
+
+
 def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
             causal: bool = True, out: Optional[torch.Tensor] = None,
             lse: Optional[torch.Tensor] = None, stream=None, window_left: int = -1,
@@ -365,7 +373,7 @@ def _decode_call(q, k_cache, v_cache, kv_lens, block_table, num_splits, max_kv_l
         if block_table.shape[0] != B:
             raise ValueError("block_table must have one row per sequence")
         num_blocks, block_size = k_cache.shape[0], k_cache.shape[1]
-        max_blocks = block_table.shape[1]
+        max_blocks = _columns(block_table)
         if max_kv_len is None:
             max_kv_len = max_blocks * block_size
         bt_ptr = block_table.data_ptr()
@@ -551,7 +559,7 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     n_kv = k_cache.shape[2]
     if block_table is not None:
         _need(block_table, "block_table", torch.int32, 2)
-        num_blocks, block_size, max_blocks = k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+        num_blocks, block_size, max_blocks = *k_cache.shape[:2], _columns(block_table)
         if max_kv_len is None:
             max_kv_len = max_blocks * block_size
         bt_ptr = block_table.data_ptr()
@@ -654,7 +662,7 @@ def _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_siz
             raise ValueError("block_table must have one row per sequence")
         if block_size is not None and block_size != rows:
             raise ValueError(f"block_size {block_size} does not match the paged cache's {rows}")
-        most = block_table.shape[1]
+        most = _columns(block_table)
         geom, want, bt = (rows, most, n, rows * most), (n, n_kv), block_table.data_ptr()
     else:
         if n != num_seqs:

@@ -109,7 +109,9 @@ bool cache(PyObject* const* a, PyObject* table, PyObject* block_size, c10::Devic
     if (!is(bt, at::kInt, 2, dev) || bt->size(0) != num_seqs || (bs && bs != rows))
       return false;
     const int64_t most = bt->size(1);
-    if (rows > INT32_MAX || n > INT32_MAX || most > INT32_MAX || rows * most > INT32_MAX)
+    // A table without columns has no address, which would mean a contiguous cache.
+    if (most < 1 || rows > INT32_MAX || n > INT32_MAX || most > INT32_MAX ||
+        rows * most > INT32_MAX)
       return false;
     c->block_size = (int)rows, c->max_blocks = (int)most, c->num_blocks = (int)n;
     c->capacity = (int)(rows * most);
