@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import functools
 import math
+import operator
 from typing import Optional
 
 import torch
@@ -598,6 +599,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _int32(x, name: str) -> int:
+    """A whole number as the C entry points take it: ctypes would drop the bits
+    beyond 32 without a word."""
+    x = operator.index(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def _scope(dev, stream):
     """What a call runs under: `dev` current, and `stream` as torch's current
     stream, so that what the call allocates belongs to that stream (a
@@ -651,6 +661,8 @@ def _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_siz
     table's, (block_size, max_blocks, num_blocks, capacity))."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         _need(k_cache, "k_cache", _U8, 4)
+    if block_size is not None:
+        block_size = _int32(block_size, "block_size")
     shape = k_cache.shape
     n, rows, n_kv = shape[:3]
     if block_table is not None:
@@ -790,7 +802,7 @@ def cache_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch
     B = cu_seqlens.shape[0] - 1
     ptrs, geom = _cache_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, block_size, B)
     first = None if starts is None else _lens(starts, "starts", B, dev)
-    n_kv, d, total = k_cache.shape[2], k_cache.shape[3], int(total)
+    n_kv, d, total = k_cache.shape[2], k_cache.shape[3], _int32(int(total), "total")
     with _scope(dev, stream):
         if k_out is None:
             k_out = torch.empty((n_kv, total, d), dtype=_BF16, device=dev)
@@ -824,7 +836,7 @@ def _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens, block_tab
         raise ValueError("the cache's head_dim does not match q")
     if max_kv_len is not None:
         if block_table is not None:
-            geom = (*geom[:3], int(max_kv_len))
+            geom = (*geom[:3], _int32(int(max_kv_len), "max_kv_len"))
         elif max_kv_len > geom[3]:
             raise ValueError("max_kv_len exceeds the contiguous cache's length")
     al = None
@@ -853,6 +865,7 @@ def decode_fp8_splitkv(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     ptrs, sizes, scale, al = _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens,
                                               block_table, block_size, max_kv_len, scale,
                                               alibi_slopes)
+    num_splits, window_left = _int32(num_splits, "num_splits"), _int32(window_left, "window_left")
     B, n_q, n_kv, d = sizes[:4]
     dev = q.device
     with _scope(dev, stream):
@@ -877,6 +890,7 @@ def _decode_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, kv_lens, 
     ptrs, sizes, scale, al = _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens,
                                               block_table, block_size, max_kv_len, scale,
                                               alibi_slopes)
+    num_splits, window_left = _int32(num_splits, "num_splits"), _int32(window_left, "window_left")
     B, n_q, n_kv, d = sizes[:4]
     dev = q.device
     kn = vn = None
