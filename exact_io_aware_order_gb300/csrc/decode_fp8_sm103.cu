@@ -188,6 +188,14 @@ __device__ __forceinline__ float exponent_of(float x) {
   const uint32_t e = max(__float_as_uint(x) >> 23, (uint32_t)(127 + kScaleExpMin));
   return __uint_as_float(0x4b000000u | e) - 8388735.f;
 }
+// l 2^d, d <= 0, where 2^d may be too small for a float and l large: references
+// lie up to 120 octaves apart for the same score (V's scales 2^-60 and 2^60), and
+// a sum of weights taken against the lower one is that much larger.
+__device__ __forceinline__ float scaled_sum(float l, float d, float two_d) {
+  if (d > -126.f) return l * two_d;
+  const float half = ex2_approx(0.5f * d);
+  return l * half * half;
+}
 // 4 bytes to shared memory, or zero without a read where !ok.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
@@ -748,9 +756,9 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
         const float now = fmaxf(m[r], mx[r]);
         corr[r] = now == -INFINITY ? 1.f : ex2_approx(m[r] - now);  // 0 at the first token
+        l[r] = scaled_sum(l[r], now == -INFINITY ? 0.f : m[r] - now, corr[r]);
         m[r] = now;
         mr[r] = now == -INFINITY ? 0.f : now - kShift;
-        l[r] *= corr[r];
       }
 #pragma unroll
       for (int j8 = 0; j8 < D / 8; ++j8)
@@ -839,8 +847,9 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
     for (int w = w0; w < w0 + team; ++w) {
       // A warp that saw no token has m = -inf and l = 0; one whose scores are all
       // NaN has m = -inf and l = NaN, which stays.
-      const float f = mm[w * 16 + lr] == -INFINITY ? 1.f : ex2_approx(mm[w * 16 + lr] - mt);
-      sum += f * ml[w * 16 + lr];
+      const float d = mm[w * 16 + lr] == -INFINITY ? 0.f : mm[w * 16 + lr] - mt;
+      const float f = ex2_approx(d);
+      sum += scaled_sum(ml[w * 16 + lr], d, f);
       mf[w * 16 + lr] = f;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: every score is -inf
