@@ -7,11 +7,21 @@
 // products has to be half of the bf16 kernel's.
 //
 //   * q k runs on the tensor core's e4m3 products, which take K's codes as
-//     ldmatrix delivers them.  q, 8 significant bits a value, is split into two
-//     e4m3 terms hi + lo / 32, each row scaled by a power of two to a maximum in
-//     [2^7, 2^8): exact down to 2^-15 of the row's maximum, off by at most 2^-23
-//     of it below.  K's scale is a factor of the score and V's of the weight,
-//     one number a token each.
+//     ldmatrix delivers them.  q, 8 significant bits a value, is split into e4m3
+//     terms, each row scaled by a power of two to a maximum in [2^7, 2^8).  Two of
+//     them, hi + lo / 32, hold values down to 2^-14 of the row's maximum exactly
+//     and leave at most 2^-22 of it of smaller ones.  Rows for which that may count
+//     take two more, (t3 + t4 / 32) / 2^23, in a second pass over K's tile: exact
+//     down to 2^-37 of the maximum, at most 2^-45 of it left below.  It counts
+//     where the n values below 2^-14 of the maximum, which leave up to 2^-15 each
+//     (scaled), leave more than 2^-21 sqrt(head_dim) times the geometric mean of the
+//     row: a sum of products in fp32 is off by as much.  The geometric mean, because
+//     a few large channels, which keys may be small in, hardly move it.  Normally
+//     distributed rows have n = 0 or 1 and do not take the second pass; with a
+//     channel of 8 times the others and more most do (16 sequences of 1024-32768
+//     tokens: 105 us, with a channel of 2^5 / 2^12 in every row 119 / 125).
+//     K's scale is a factor of the score and V's of the weight, one number a token
+//     each.
 //   * p v runs in fp16: codes are converted (exactly: e4m3 is a subset of
 //     fp16).  The byte form of the transposed ldmatrix gives a thread 4
 //     neighbouring tokens of one column, which two conversions turn into the two
@@ -47,6 +57,7 @@
 // copies' issue by one warp was the limit), TMA boxes by every warp 114 us, this
 // form 104 us with its combine.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
@@ -62,14 +73,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 4.f;       // log2 units a score may exceed the reference by
 constexpr float kShift = 10.f;     // log2 of the weight at the reference
-constexpr float kQLo = 32.f;       // q = hi + lo / kQLo
+constexpr float kQLo = 32.f;       // q = hi + lo / kQLo + (t3 + t4 / kQLo) / kQFine: what
+constexpr float kQFine = 8388608.f;  // hi and lo leave, 2^-15 at most, becomes 2^8 (kQFine 2^23)
+constexpr float kQNoise = 0.015625f;  // 2^-21 / 2^-15: n that counts, see above
 constexpr uint32_t kNoRow = 0xffffffffu;
 
 // Where q's fragments live during the stream: registers, or shared memory
 // where the accumulators leave no room for them.
 __host__ __device__ constexpr bool q_in_smem(int D, bool wide) { return wide || D == 256; }
+// Whether q's finer terms are kept in shared memory; else (where two blocks an SM
+// leave no room) they are made again from q in each tile.
+__host__ __device__ constexpr bool fine_in_smem(int D, int groups) {
+  return D < 256 || groups < 4;
+}
 __host__ __device__ constexpr int q_smem_bytes(int D, bool wide, int groups) {
-  return q_in_smem(D, wide) ? groups * (D / 32) * 32 * (wide ? 32 : 16) : 0;
+  return (q_in_smem(D, wide) + fine_in_smem(D, groups)) * groups * D * (wide ? 32 : 16);
 }
 // Blocks that share an SM, by their registers.
 constexpr int blocks_per_sm(int D) { return D == 64 ? 3 : 2; }
@@ -174,6 +192,60 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
       : "=f"(f.x), "=f"(f.y)
       : "r"(x));
   return f;
+}
+// Four neighbouring bf16 values, times f.
+__device__ __forceinline__ void scaled4(const uint2& x, float f, float (&v)[4]) {
+  v[0] = __uint_as_float(x.x << 16) * f, v[1] = __uint_as_float(x.x & 0xffff0000u) * f;
+  v[2] = __uint_as_float(x.y << 16) * f, v[3] = __uint_as_float(x.y & 0xffff0000u) * f;
+}
+// The e4m3 numbers nearest to four values, which become what those leave of
+// them, times kQLo (exactly).
+__device__ __forceinline__ uint32_t e4m3_term(float (&v)[4]) {
+  const uint32_t t = e4m3x4_pack(v[0], v[1], v[2], v[3]);
+  uint32_t t01, t23;
+  e4m3x4_to_f16(t, t01, t23);
+  const float2 a = unpack_f16x2(t01), b = unpack_f16x2(t23);
+  v[0] = (v[0] - a.x) * kQLo, v[1] = (v[1] - a.y) * kQLo;
+  v[2] = (v[2] - b.x) * kQLo, v[3] = (v[3] - b.y) * kQLo;
+  return t;
+}
+// hi and lo of four values of q, by way of fp16, which holds the scaled values down
+// to 2^-17 exactly (smaller ones are off by 2^-25 at most).
+__device__ __forceinline__ void coarse2(uint32_t two, float f, uint32_t& hi, uint32_t& lo) {
+  const uint32_t v = pack_f16x2(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xffff0000u) * f);
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 t;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 t, h;\n\t"
+      "sub.rn.f16x2 t, %2, t;\n\t"
+      "mul.rn.f16x2 t, t, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, t;\n\t"
+      "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+      : "=r"(hi), "=r"(lo)
+      : "r"(v), "r"(0x50005000u));  // 32, 32
+}
+__device__ __forceinline__ void coarse_terms(const uint2& x, float f, uint32_t& hi, uint32_t& lo) {
+  uint32_t h0, l0, h1, l1;
+  coarse2(x.x, f, h0, l0);
+  coarse2(x.y, f, h1, l1);
+  hi = h0 | h1 << 16;
+  lo = l0 | l1 << 16;
+}
+// t3 and t4 of four values of q.
+__device__ __forceinline__ void fine_terms(const uint2& x, float f, uint32_t& t3, uint32_t& t4) {
+  uint32_t hi, lo, h01, h23, l01, l23;
+  coarse_terms(x, f, hi, lo);
+  e4m3x4_to_f16(hi, h01, h23);
+  e4m3x4_to_f16(lo, l01, l23);
+  const float2 a0 = unpack_f16x2(h01), a1 = unpack_f16x2(h23);
+  const float2 b0 = unpack_f16x2(l01), b1 = unpack_f16x2(l23);
+  float v[4];
+  scaled4(x, f, v);
+  v[0] = ((v[0] - a0.x) * kQLo - b0.x) * (kQFine / kQLo);
+  v[1] = ((v[1] - a0.y) * kQLo - b0.y) * (kQFine / kQLo);
+  v[2] = ((v[2] - a1.x) * kQLo - b1.x) * (kQFine / kQLo);
+  v[3] = ((v[3] - a1.y) * kQLo - b1.y) * (kQFine / kQLo);
+  t3 = e4m3_term(v);
+  t4 = e4m3_term(v);
 }
 // x, y as hi + lo, each a pair of fp16.
 __device__ __forceinline__ void split_f16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -416,19 +488,17 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   constexpr int kSteps = D / 32;        // k steps of q k
   constexpr bool kQSmem = q_in_smem(D, kWide);
   // Columns 16 i + 4 quad .. + 3 of rows gid (and gid + 8).
+  const uint16_t* qsrc = a.q + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D + quad * 4;
+  auto load_q = [&](int r, int i) -> uint2 {
+    const int row = row0 + gid + 8 * r;
+    if (row >= g) return make_uint2(0u, 0u);
+    return *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
+  };
   uint2 qx[kRows][2 * kSteps];
-  {
-    const uint16_t* qsrc = a.q + ((size_t)b * a.n_q_heads + (size_t)kvh * g) * D + quad * 4;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = row0 + gid + 8 * r;
+  for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int i = 0; i < 2 * kSteps; ++i) {
-        qx[r][i] = make_uint2(0u, 0u);
-        if (row < g) qx[r][i] = *reinterpret_cast<const uint2*>(qsrc + (size_t)row * D + i * 16);
-      }
-    }
-  }
+    for (int i = 0; i < 2 * kSteps; ++i) qx[r][i] = load_q(r, i);
 
   if (a.parts == 0)
     sp = span_of(a, raw_len, threadIdx.x == 0 && blockIdx.x == 0 ? kp.err_word : nullptr);
@@ -560,23 +630,59 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   // 3 of each 32): hi and lo parts of 8 rows in one, or of 16 in two.
   uint4 qf[kQSmem ? 1 : kSteps];
   uint4* qs = reinterpret_cast<uint4*>(smem + L::kQ) + rg * kSteps * 32 * (kWide ? 2 : 1);
+  // The finer terms, where some row needs them (`fine`: the same in all warps that
+  // have these rows): behind the coarse ones, or made again from q.
+  const bool fine_smem = fine_in_smem(D, G);
+  uint4* qt = reinterpret_cast<uint4*>(
+                  smem + L::kQ + (kQSmem ? (kWide ? G : 1) * D * (kWide ? 32 : 16) : 0)) +
+              rg * kSteps * 32 * (kWide ? 2 : 1);
+  bool fine = false;
+  float up_fine[kRows];  // (made again) of the rows that need them; others get zeros
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) up_fine[r] = 0.f;
   float sl2[kRows], cap_in[kRows];
   {
     float up[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      uint32_t top = 0u;
+      uint32_t tops[2] = {0u, 0u};  // two halves each
 #pragma unroll
       for (int i = 0; i < 2 * kSteps; ++i) {
-        top = max(max(top, qx[r][i].x & 0x7fffu), (qx[r][i].x >> 16) & 0x7fffu);
-        top = max(max(top, qx[r][i].y & 0x7fffu), (qx[r][i].y >> 16) & 0x7fffu);
+        tops[0] = __vmaxu2(tops[0], qx[r][i].x & 0x7fff7fffu);
+        tops[1] = __vmaxu2(tops[1], qx[r][i].y & 0x7fff7fffu);
       }
+      uint32_t top = __vmaxu2(tops[0], tops[1]);
+      top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = min(max((int)(top >> 7) - 127, -110), 127);
+      // How many values lie below 2^(e - 14), but for zeros (in units of 1 / 128), and the
+      // sum of the magnitudes' bit patterns, 128 (log2 x + 127) to within 11.  Bit 15 of
+      // `from` - (x - 1) says x < limit; a zero less 1 is made the largest (its borrow
+      // from the upper half costs that one step).
+      const uint32_t limit = (uint32_t)(e + 127 - 14) << 7;
+      const uint32_t from = (0x8000u + limit - 2u) * 0x00010001u;
+      uint32_t counts[2] = {0u, 0u}, log_sums[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t x = (w ? qx[r][i].y : qx[r][i].x) & 0x7fff7fffu;
+          const uint32_t y = __vminu2(x - 0x00010001u, 0x7fff7fffu);
+          counts[w] = __dp4a((from - y) & 0x80008000u, 0x01000100u, counts[w]);
+          log_sums[w] = __dp2a_lo(x, 0x0101u, log_sums[w]);
+        }
+      uint32_t count = counts[0] + counts[1], logs = log_sums[0] + log_sums[1];
+      count += __shfl_xor_sync(0xffffffffu, count, 1);
+      count += __shfl_xor_sync(0xffffffffu, count, 2);
+      logs += __shfl_xor_sync(0xffffffffu, logs, 1);
+      logs += __shfl_xor_sync(0xffffffffu, logs, 2);
+      const float mean = (float)logs / (128 * D) - (float)(e + 127 - 7);
+      const bool need = (float)count > 128.f * kQNoise * sqrtf((float)D) * ex2_approx(mean);
       up[r] = __int_as_float((7 - e + 127) << 23);            // 2^(7 - e)
       float down = __int_as_float((e - 7 + 127) << 23);
       if (top >= 0x7f80u) down = __int_as_float(0x7fc00000);  // an infinity or NaN: the row is NaN
+      else if (need) up_fine[r] = up[r];
       sl2[r] = a.scale * kLog2e * down;
       cap_in[r] = 0.f;
       if (a.softcap > 0.f) {
@@ -584,32 +690,23 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         sl2[r] = a.softcap * kLog2e;
       }
     }
-    auto part = [&](const uint2& x, float f, uint32_t& hi, uint32_t& lo) {
-      const float v0 = __uint_as_float(x.x << 16) * f, v1 = __uint_as_float(x.x & 0xffff0000u) * f;
-      const float v2 = __uint_as_float(x.y << 16) * f, v3 = __uint_as_float(x.y & 0xffff0000u) * f;
-      hi = e4m3x4_pack(v0, v1, v2, v3);
-      uint32_t h01, h23;
-      e4m3x4_to_f16(hi, h01, h23);
-      const float2 a01 = unpack_f16x2(h01), a23 = unpack_f16x2(h23);
-      lo = e4m3x4_pack((v0 - a01.x) * kQLo, (v1 - a01.y) * kQLo, (v2 - a23.x) * kQLo,
-                       (v3 - a23.y) * kQLo);
-    };
+    fine = __any_sync(0xffffffffu, up_fine[0] != 0.f || up_fine[kRows - 1] != 0.f);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       uint4 f;
       if constexpr (kWide) {
         uint4 fl;
-        part(qx[0][2 * i], up[0], f.x, fl.x);
-        part(qx[1][2 * i], up[1], f.y, fl.y);
-        part(qx[0][2 * i + 1], up[0], f.z, fl.z);
-        part(qx[1][2 * i + 1], up[1], f.w, fl.w);
+        coarse_terms(qx[0][2 * i], up[0], f.x, fl.x);
+        coarse_terms(qx[1][2 * i], up[1], f.y, fl.y);
+        coarse_terms(qx[0][2 * i + 1], up[0], f.z, fl.z);
+        coarse_terms(qx[1][2 * i + 1], up[1], f.w, fl.w);
         if (col == 0) {
           qs[(2 * i) * 32 + lane] = f;
           qs[(2 * i + 1) * 32 + lane] = fl;
         }
       } else {
-        part(qx[0][2 * i], up[0], f.x, f.y);
-        part(qx[0][2 * i + 1], up[0], f.z, f.w);
+        coarse_terms(qx[0][2 * i], up[0], f.x, f.y);
+        coarse_terms(qx[0][2 * i + 1], up[0], f.z, f.w);
         if constexpr (kQSmem) {
           if (col == 0) qs[i * 32 + lane] = f;
         } else {
@@ -617,7 +714,24 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         }
       }
     }
-    if constexpr (kQSmem) __syncthreads();
+    if (fine && fine_smem && col == 0) {
+#pragma unroll 1
+      for (int i = 0; i < kSteps; ++i) {
+        uint4 f, fl;
+        fine_terms(load_q(0, 2 * i), up_fine[0], f.x, fl.x);
+        fine_terms(load_q(0, 2 * i + 1), up_fine[0], f.z, fl.z);
+        if constexpr (kWide) {
+          fine_terms(load_q(1, 2 * i), up_fine[1], f.y, fl.y);
+          fine_terms(load_q(1, 2 * i + 1), up_fine[1], f.w, fl.w);
+          qt[(2 * i) * 32 + lane] = f;
+          qt[(2 * i + 1) * 32 + lane] = fl;
+        } else {
+          qt[i * 32 + lane] = make_uint4(f.x, fl.x, f.z, fl.z);
+        }
+      }
+    }
+    // (without kQSmem there is one team, and `fine` the same in all warps)
+    if (kQSmem || fine) __syncthreads();
   }
   const bool capped = a.softcap > 0.f, alibi = a.alibi_slopes != nullptr;
   float al2[kRows];
@@ -653,6 +767,10 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
                                              (warp * L::kSlots + slot) * L::kScaleBytes);
     if (++slot == L::kSlots) slot = 0;
   };
+  // The tiles.  head_dim 256 with more than 8 heads, which is short of registers, has
+  // the loop twice, without a trace of q's finer terms in the usual one (8 sequences,
+  // 64 heads a kv head: 217 against 225 us; the other forms gain nothing by it).
+  auto stream = [&](auto with_fine) {
   for (int j = 0; j < my_tiles; ++j) {
     const int first = t0 + (col + j * team) * kTile;
     const bool ragged = first + kTile > t1 || first < lo_tok;
@@ -683,6 +801,48 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         mma16832_e4m3(sl[3], i == 0, f, y[2], y[3]);
       }
     }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 2 * kRows; ++e)
+        s[n][e] = fmaf(kWide ? sl[kWide ? n : 0][e] : s[n][2 + e], 1.f / kQLo, s[n][e]);
+    // ---- what hi and lo leave of q ----
+    if (with_fine && fine) {
+      float ft[kWide ? 8 : 4][4];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t at = half + (k_off ^ (uint32_t)(2 * i << 4));
+        uint32_t x[4], y[4];
+        ldsm_x4(at, x);
+        ldsm_x4(at + 16 * D, y);
+        uint4 f, f4;
+        if (fine_smem) {
+          f = qt[(kWide ? 2 * i : i) * 32 + lane];
+          if constexpr (kWide) f4 = qt[(2 * i + 1) * 32 + lane];
+        } else {
+          fine_terms(load_q(0, 2 * i), up_fine[0], f.x, f4.x);
+          fine_terms(load_q(1, 2 * i), up_fine[kRows - 1], f.y, f4.y);
+          fine_terms(load_q(0, 2 * i + 1), up_fine[0], f.z, f4.z);
+          fine_terms(load_q(1, 2 * i + 1), up_fine[kRows - 1], f.w, f4.w);
+        }
+        mma16832_e4m3(ft[0], i == 0, f, x[0], x[1]);
+        mma16832_e4m3(ft[1], i == 0, f, x[2], x[3]);
+        mma16832_e4m3(ft[2], i == 0, f, y[0], y[1]);
+        mma16832_e4m3(ft[3], i == 0, f, y[2], y[3]);
+        if constexpr (kWide) {
+          mma16832_e4m3(ft[4], i == 0, f4, x[0], x[1]);
+          mma16832_e4m3(ft[5], i == 0, f4, x[2], x[3]);
+          mma16832_e4m3(ft[6], i == 0, f4, y[0], y[1]);
+          mma16832_e4m3(ft[7], i == 0, f4, y[2], y[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2 * kRows; ++e)
+          s[n][e] = fmaf(fmaf(kWide ? ft[kWide ? 4 + n : 0][e] : ft[n][2 + e], 1.f / kQLo, ft[n][e]),
+                         1.f / kQFine, s[n][e]);
+    }
     // ---- in log2 units, with K's scales ----
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -694,7 +854,6 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           float& x = s[n][2 * r + e];
-          x = fmaf(kWide ? sl[kWide ? n : 0][2 * r + e] : s[n][2 + e], 1.f / kQLo, x);
           if (capped)
             x = tanhf(x * (cap_in[r] * ks[i])) * sl2[r];
           else
@@ -810,6 +969,9 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
     __syncwarp();
     put();
   }
+  };
+  if (kWide && D == 256 && !fine) stream(std::false_type{});
+  else stream(std::true_type{});
 
   // ================= merge the warps' states =================
 #pragma unroll
