@@ -860,7 +860,8 @@ def decode_fp8_splitkv(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     """Split-KV single-token decode over an 8-bit cache
     (``attn_decode_fp8_splitkv``): q (B, n_q, d) bf16, the cache that of
     :func:`cache_write_fp8`, everything else as :func:`decode_splitkv`.
-    Returns (o_partial (S, B, n_q, d), lse_partial (S, B, n_q)), fp32, for
+    ``max_kv_len`` (the largest kv_len) is a hint for paged caches; a
+    contiguous cache's length takes its place.  Returns (o_partial (S, B, n_q, d), lse_partial (S, B, n_q)), fp32, for
     :func:`combine`."""
     ptrs, sizes, scale, al = _decode_fp8_args(q, k_cache, v_cache, k_scales, v_scales, kv_lens,
                                               block_table, block_size, max_kv_len, scale,

@@ -605,8 +605,9 @@ int validate_rows(const attn::CacheRowsArgs& a, bool read) {
     if (!apart(a.k_token_stride, a.k_head_stride) || !apart(a.v_token_stride, a.v_head_stride))
       return ATTN_ERR_SHAPE;
   }
-  // units of work (at most total / block_size + 2 num_seqs blocks, K and V of
-  // every head) are counted in 32 bits, eight warps each at most
+  // units of work (K and V together of at most total / block_size + 2 num_seqs
+  // blocks of every head) take one to four warps each, four to a block of the
+  // grid, whose blocks are counted in 31 bits; the header's limit is half of that
   if (((long long)a.total_tokens / a.c.block_size + 2LL * a.num_seqs) * a.c.n_kv_heads * 2 >
       0x7fffffffLL)
     return ATTN_ERR_SHAPE;
@@ -664,12 +665,12 @@ size_t fp8_pairs_offset(size_t rows) { return (rows * sizeof(float) + 255) / 256
 // 10.7 / 19.4 against 13.4 / 20.0; 32 x 8 of 1000 / 2500 18 / 36 against 27 / 42,
 // where sharing only pays once lengths differ (24 x 8 of 800 to 4000: 47 against 34).
 constexpr int kFp8MinTiles = 4;
-int fp8_parts(int batch, int n_q_heads, int n_kv_heads, int head_dim, long long max_len,
-              int window_left, int num_sms) {
+int fp8_parts(int batch, int n_kv_heads, int head_dim, long long max_len, int window_left,
+              int num_sms) {
   if (batch > attn::kMaxSharedBatch) return 0;
   long long most = max_len;
   if (window_left >= 0) most = std::min(most, window_left + 1LL);
-  const int top = attn::decode_fp8_max_parts(n_q_heads, n_kv_heads, head_dim, num_sms);
+  const int top = attn::decode_fp8_max_parts(head_dim, num_sms);
   const long long pairs = (long long)batch * n_kv_heads;
   if (most <= (4 * pairs <= top ? 400 : 2 * pairs <= top ? 1000 : 2048)) return 0;
   const long long tiles = (most + 31) / 32 * pairs;
@@ -765,7 +766,7 @@ size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads,
   }
   // with or without an appended token
   const int parts =
-      fp8_parts(batch, n_q_heads, n_kv_heads, head_dim, (long long)max_kv_len + 1, window_left, sms);
+      fp8_parts(batch, n_kv_heads, head_dim, (long long)max_kv_len + 1, window_left, sms);
   return fp8_shares_bytes(parts, batch, n_q_heads, n_kv_heads, head_dim);
 }
 
@@ -799,8 +800,8 @@ int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16*
   if (!ds) return st;
   int S = num_splits;
   if (S == 0) {
-    a.parts = fp8_parts(batch, n_q_heads, n_kv_heads, head_dim, (long long)max_kv_len + a.append,
-                        window_left, ds->num_sms);
+    a.parts = fp8_parts(batch, n_kv_heads, head_dim, (long long)max_kv_len + a.append, window_left,
+                        ds->num_sms);
     S = a.num_splits = 1;  // without shares
   }
   if (S > 1 || a.parts > 0) {

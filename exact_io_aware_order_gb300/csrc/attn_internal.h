@@ -194,7 +194,7 @@ cudaError_t launch_decode_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 // The combine of the shares, and the most blocks that share an 8-bit decode's
 // tiles (those that are resident together).
 cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
-int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms);
+int decode_fp8_max_parts(int head_dim, int num_sms);
 
 // Resolves the current device's launch context (architecture check, error
 // word, SM count) for a call on `stream`; returns an attn_status code.

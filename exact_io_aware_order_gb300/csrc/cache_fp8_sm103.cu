@@ -2,8 +2,10 @@
 //
 // A cache block (block_size tokens of one kv head, K or V) has one scale
 // 2^k, k the smallest integer with amax <= 448 * 2^k, and e4m3 codes
-// e4m3(x * 2^-k).  The power of two costs no precision (e4m3 is a floating
-// format: its relative step does not depend on the scale) and makes every
+// e4m3(x * 2^-k).  e4m3 is a floating format, so its relative step does not depend on
+// the scale; what the power of two costs against amax / 448 is that the scale may be
+// nearly twice as large, and e4m3's subnormals (values 2^-15 of the largest and less)
+// then begin up to one binade higher.  It makes every
 // step but the one rounding exact: x * 2^-k is exact, so a code is the same in
 // any arithmetic; a value read back, code * 2^k with 4 significant bits, is a
 // bf16 number; and when a token that needs a larger scale joins a block, the
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_fp8_kernel(const RowsKPa
     const float scale = fmaxf(scale_of(amax[w]), was[w]);
     if (sub == 0 && lane == 0 && scale != was[w])
       (w ? a.c.v_scales : a.c.k_scales)[u.scale] = scale;
-    inv[w] = 1.f / scale;  // exact: a power of two
+    inv[w] = 1.f / scale;  // exact for a power of two (a caller's own scale may be none)
     ratio[w] = scale != was[w] ? was[w] * inv[w] : 1.f;
     codes[w] = (w ? a.c.v : a.c.k) + u.block_row * pitch + u.head * D + lc * 8;
   }

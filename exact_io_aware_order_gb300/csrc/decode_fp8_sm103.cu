@@ -39,7 +39,8 @@
 //     100000 tokens in one split O came out 3e-5 too small).  That also halves
 //     the accumulators of the form with up to 8 heads.
 //   * the exponentials' reference m bounds score + log2(V's scale), the size of
-//     a weight times its scale: weights lie below 2^(kShift + kGrow) = 2^14 and
+//     a weight times its scale: those lie below 2^(kShift + kGrow) = 2^14 (2^15 for
+//     scales that are no powers of two) and
 //     those down to 2^-24 of the largest keep full fp16 precision in hi.  The
 //     sum l is taken over the unscaled weights in fp32.  The row maximum is
 //     only reduced over the quad when some score exceeds m by 2^kGrow.
@@ -388,7 +389,8 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
 
   // Behind its step's write, which has waited for the kernels in front of both, the
   // decode finds its place and asks for q while the write runs, and waits before
-  // it reads the cache (one sequence of 30719 tokens: 17.9 -> 15.6 us).
+  // it reads the cache (one sequence of 30719 tokens, steps on 12 caches in one graph:
+  // 19.7 -> 17.6 us; called from Python on one cache, 17.6 -> 16.1).
   bool to_wait = a.append != 0;
   if (!to_wait) grid_dep_wait();
   grid_dep_launch();
@@ -1216,7 +1218,7 @@ cudaError_t launch_d(const DecodeFp8Args& a, const LaunchCtx& ctx) {
 
 }  // namespace
 
-int decode_fp8_max_parts(int n_q_heads, int n_kv_heads, int head_dim, int num_sms) {
+int decode_fp8_max_parts(int head_dim, int num_sms) {
   return blocks_per_sm(head_dim) * num_sms;
 }
 

@@ -624,6 +624,8 @@ int attn_decode_noalloc(const attn_bf16* q, const attn_bf16* k_cache, const attn
  * (infinities, or |x| > 448 * 2^60) saturate to +-448, NaN stays NaN.  Every
  * step but the rounding is exact, so the codes do not depend on how a
  * sequence's rows are divided over calls as long as no block's scale grows.
+ * (A present scale that the caller set and that is not a power of two is kept where
+ * it is the larger; x / scale is then rounded to fp32 before it is rounded to e4m3.)
  * A sequence whose rows do not fit its capacity, or whose kv_lens is negative,
  * is flagged and nothing of it is written; a block-table entry outside [0,
  * num_blocks) is flagged and that block's rows are not written.  Two
@@ -655,8 +657,8 @@ int attn_cache_write_fp8(const attn_bf16* k, const attn_bf16* v, int64_t k_token
  *   starts     : (num_seqs,) int32 first position read of each sequence, or
  *                NULL: 0
  *   total_tokens: rows of k and v
- * Each value is code * scale rounded to bf16: exact for scales that
- * attn_cache_write_fp8 set.  A sequence whose positions leave its capacity is
+ * Each value is code * scale rounded to bf16 (by way of fp32): exact for scales
+ * that attn_cache_write_fp8 set.  A sequence whose positions leave its capacity is
  * flagged and nothing of it is written; so is a bad block-table entry, for
  * that block's rows.  Limits and errors as attn_cache_write_fp8.
  */
