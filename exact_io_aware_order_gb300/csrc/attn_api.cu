@@ -751,8 +751,12 @@ int attn_decode_fp8_splitkv(const attn_bf16* q, const uint8_t* k_cache, const ui
 
 size_t attn_decode_fp8_workspace_bytes(int num_splits, int batch, int n_q_heads, int n_kv_heads,
                                        int head_dim, int max_kv_len, int window_left) {
-  if (num_splits < 0 || num_splits == 1 || batch < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
-      head_dim < 1)
+  // what the call itself refuses, so that nobody sets memory aside for it
+  if (num_splits < 0 || num_splits == 1 || num_splits > ATTN_MAX_SPLITS || batch < 1 ||
+      batch > 65535 || n_kv_heads < 1 || n_kv_heads > 65535 || n_q_heads < n_kv_heads ||
+      n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > 64 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_kv_len < 0 ||
+      max_kv_len > (1 << 30) || window_left < -1)
     return 0;
   if (num_splits > 1) {
     const size_t rows = (size_t)num_splits * (size_t)batch * (size_t)n_q_heads;
