@@ -689,7 +689,8 @@ int attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const fl
  * or 2^-35 of the largest in its split where that is more.  The tensor cores sum the
  * products of a score, and those of 32 tokens in O; all other sums, and those over the
  * tokens, are fp32.  Keys and values of masked positions (past kv_lens, left of the
- * window) may hold anything, NaN included.
+ * window) may hold anything, NaN included.  The largest magnitude of a row of q times a
+ * K scale times scale has to stay inside fp32.
  * Limits: those of the cache; n_q_heads / n_kv_heads <= 64; batch and
  *   n_kv_heads <= 65535; the cache's slots times n_kv_heads below 2^32.
  * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _GQA, _SPLITS, _ALIGN, _ARCH, _LAUNCH.
