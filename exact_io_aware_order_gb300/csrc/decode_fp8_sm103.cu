@@ -10,16 +10,15 @@
 //     ldmatrix delivers them.  q, 8 significant bits a value, is split into e4m3
 //     terms, each row scaled by a power of two to a maximum in [2^7, 2^8).  Two of
 //     them, hi + lo / 32, hold values down to 2^-14 of the row's maximum exactly
-//     and leave at most 2^-22 of it of smaller ones.  Rows for which that may count
-//     take two more, (t3 + t4 / 32) / 2^23, in a second pass over K's tile: exact
-//     down to 2^-37 of the maximum, at most 2^-45 of it left below.  It counts
-//     where the n values below 2^-14 of the maximum, which leave up to 2^-15 each
-//     (scaled), leave more than 2^-21 sqrt(head_dim) times the geometric mean of the
-//     row: a sum of products in fp32 is off by as much.  The geometric mean, because
-//     a few large channels, which keys may be small in, hardly move it.  Normally
-//     distributed rows have n = 0 or 1 and do not take the second pass; with a
-//     channel of 8 times the others and more most do (16 sequences of 1024-32768
-//     tokens: 105 us, with a channel of 2^5 / 2^12 in every row 119 / 125).
+//     and leave at most 2^-22 of it of smaller ones.  Two more, (t3 + t4 / 32) / 2^23,
+//     are exact down to 2^-37 of the maximum (at most 2^-45 of it left below) and
+//     take a second pass over K's tile.  A tile takes it where n 2^-15 448 (n values
+//     below 2^-14 of the maximum, times the largest code) times K's scale, in units
+//     of the score, is above 2^-18: otherwise what hi and lo leave cannot change a
+//     score's base 2 logarithm by more, whatever the keys.  Normally distributed rows
+//     have n = 0 or 1, and ordinary scores stay below that; where a channel of q or of
+//     the keys is far larger than the rest most tiles take it (16 sequences of
+//     1024-32768 tokens: 104 us, with a channel of 2^5 / 2^12 in every row of q 120 / 129).
 //     K's scale is a factor of the score and V's of the weight, one number a token
 //     each.
 //   * p v runs in fp16: codes are converted (exactly: e4m3 is a subset of
@@ -56,7 +55,7 @@
 // Measured on a paged batch of 16 sequences (555 MB, head_dim 128; 83 us at the
 // measured copy rate): TMA boxes of 16 tokens by a producer warp 157 us (the
 // copies' issue by one warp was the limit), TMA boxes by every warp 114 us, this
-// form 104 us with its combine.
+// form 104 us with its combine (107 since small values of q are looked after).
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -76,7 +75,7 @@ constexpr float kGrow = 4.f;       // log2 units a score may exceed the referenc
 constexpr float kShift = 10.f;     // log2 of the weight at the reference
 constexpr float kQLo = 32.f;       // q = hi + lo / kQLo + (t3 + t4 / kQLo) / kQFine: what
 constexpr float kQFine = 8388608.f;  // hi and lo leave, 2^-15 at most, becomes 2^8 (kQFine 2^23)
-constexpr float kQNoise = 0.015625f;  // 2^-21 / 2^-15: n that counts, see above
+constexpr float kQNoise = 3.8146973e-6f;  // 2^-18, see above
 constexpr uint32_t kNoRow = 0xffffffffu;
 
 // Where q's fragments live during the stream: registers, or shared memory
@@ -109,7 +108,7 @@ struct Smem {
   static constexpr int kRingBytes = kWarps * kSlots * kHalfBytes;
   static constexpr int kRowsBytes = kWarps * (kWide ? 16 : 8) * kPitch * 4;
   static constexpr int kScale = kRingBytes > kRowsBytes ? kRingBytes : kRowsBytes;
-  static constexpr int kMerge = kScale + kWarps * kSlots * kScaleBytes;  // m, l, weight
+  static constexpr int kMerge = kScale + kWarps * kSlots * kScaleBytes;  // m, l, weight; before: rows' scales
   static constexpr int kQ = kMerge + 3 * kWarps * 16 * 4;  // q's fragments, where kept here
   static constexpr int total(int q_bytes) { return kQ + q_bytes; }
 };
@@ -632,19 +631,18 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
   // 3 of each 32): hi and lo parts of 8 rows in one, or of 16 in two.
   uint4 qf[kQSmem ? 1 : kSteps];
   uint4* qs = reinterpret_cast<uint4*>(smem + L::kQ) + rg * kSteps * 32 * (kWide ? 2 : 1);
-  // The finer terms, where some row needs them (`fine`: the same in all warps that
-  // have these rows): behind the coarse ones, or made again from q.
+  // The finer terms, for tiles with a K scale above fine_ks: behind the coarse ones, where
+  // the first tile that needs them puts them (every warp for itself: they are the
+  // same), or made again from q.
   const bool fine_smem = fine_in_smem(D, G);
   uint4* qt = reinterpret_cast<uint4*>(
                   smem + L::kQ + (kQSmem ? (kWide ? G : 1) * D * (kWide ? 32 : 16) : 0)) +
               rg * kSteps * 32 * (kWide ? 2 : 1);
-  bool fine = false;
-  float up_fine[kRows];  // (made again) of the rows that need them; others get zeros
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) up_fine[r] = 0.f;
+  float fine_ks = INFINITY;
+  float* row_up = reinterpret_cast<float*>(smem + L::kMerge) + row0 + gid;  // `up`, till the merge
   float sl2[kRows], cap_in[kRows];
   {
-    float up[kRows];
+    float up[kRows];  // 2^(7 - e) of a row whose largest value is 2^e .. 2^(e + 1)
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       uint32_t tops[2] = {0u, 0u};  // two halves each
@@ -658,13 +656,12 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = min(max((int)(top >> 7) - 127, -110), 127);
-      // How many values lie below 2^(e - 14), but for zeros (in units of 1 / 128), and the
-      // sum of the magnitudes' bit patterns, 128 (log2 x + 127) to within 11.  Bit 15 of
-      // `from` - (x - 1) says x < limit; a zero less 1 is made the largest (its borrow
-      // from the upper half costs that one step).
+      // How many values lie below 2^(e - 14) = `limit` but for zeros: bit 15 of `from` -
+      // (x - 1) says x < limit; a zero less 1 is made the largest (its borrow from
+      // the upper half costs that one step of the format).
       const uint32_t limit = (uint32_t)(e + 127 - 14) << 7;
       const uint32_t from = (0x8000u + limit - 2u) * 0x00010001u;
-      uint32_t counts[2] = {0u, 0u}, log_sums[2] = {0u, 0u};
+      uint32_t counts[2] = {0u, 0u};  // times 128
 #pragma unroll
       for (int i = 0; i < 2 * kSteps; ++i)
 #pragma unroll
@@ -672,19 +669,16 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
           const uint32_t x = (w ? qx[r][i].y : qx[r][i].x) & 0x7fff7fffu;
           const uint32_t y = __vminu2(x - 0x00010001u, 0x7fff7fffu);
           counts[w] = __dp4a((from - y) & 0x80008000u, 0x01000100u, counts[w]);
-          log_sums[w] = __dp2a_lo(x, 0x0101u, log_sums[w]);
         }
-      uint32_t count = counts[0] + counts[1], logs = log_sums[0] + log_sums[1];
+      uint32_t count = counts[0] + counts[1];
       count += __shfl_xor_sync(0xffffffffu, count, 1);
       count += __shfl_xor_sync(0xffffffffu, count, 2);
-      logs += __shfl_xor_sync(0xffffffffu, logs, 1);
-      logs += __shfl_xor_sync(0xffffffffu, logs, 2);
-      const float mean = (float)logs / (128 * D) - (float)(e + 127 - 7);
-      const bool need = (float)count > 128.f * kQNoise * sqrtf((float)D) * ex2_approx(mean);
       up[r] = __int_as_float((7 - e + 127) << 23);            // 2^(7 - e)
       float down = __int_as_float((e - 7 + 127) << 23);
       if (top >= 0x7f80u) down = __int_as_float(0x7fc00000);  // an infinity or NaN: the row is NaN
-      else if (need) up_fine[r] = up[r];
+      // Keys whose scale is above this take the second pass (0 * inf: none do).
+      const float left = (float)count * (448.f / 128.f / 32768.f) * fabsf(a.scale * kLog2e) * down;
+      if (left > 0.f) fine_ks = fminf(fine_ks, __fdividef(kQNoise, left));
       sl2[r] = a.scale * kLog2e * down;
       cap_in[r] = 0.f;
       if (a.softcap > 0.f) {
@@ -692,7 +686,7 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         sl2[r] = a.softcap * kLog2e;
       }
     }
-    fine = __any_sync(0xffffffffu, up_fine[0] != 0.f || up_fine[kRows - 1] != 0.f);
+    fine_ks = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(fine_ks)));
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       uint4 f;
@@ -716,24 +710,12 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
         }
       }
     }
-    if (fine && fine_smem && col == 0) {
-#pragma unroll 1
-      for (int i = 0; i < kSteps; ++i) {
-        uint4 f, fl;
-        fine_terms(load_q(0, 2 * i), up_fine[0], f.x, fl.x);
-        fine_terms(load_q(0, 2 * i + 1), up_fine[0], f.z, fl.z);
-        if constexpr (kWide) {
-          fine_terms(load_q(1, 2 * i), up_fine[1], f.y, fl.y);
-          fine_terms(load_q(1, 2 * i + 1), up_fine[1], f.w, fl.w);
-          qt[(2 * i) * 32 + lane] = f;
-          qt[(2 * i + 1) * 32 + lane] = fl;
-        } else {
-          qt[i * 32 + lane] = make_uint4(f.x, fl.x, f.z, fl.z);
-        }
-      }
+    if (fine_ks < INFINITY) {  // (every warp of these rows the same)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) row_up[8 * r] = up[r];
+      __syncwarp();
     }
-    // (without kQSmem there is one team, and `fine` the same in all warps)
-    if (kQSmem || fine) __syncthreads();
+    if constexpr (kQSmem) __syncthreads();
   }
   const bool capped = a.softcap > 0.f, alibi = a.alibi_slopes != nullptr;
   float al2[kRows];
@@ -769,16 +751,51 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
                                              (warp * L::kSlots + slot) * L::kScaleBytes);
     if (++slot == L::kSlots) slot = 0;
   };
-  // The tiles.  head_dim 256 with more than 8 heads, which is short of registers, has
-  // the loop twice, without a trace of q's finer terms in the usual one (8 sequences,
-  // 64 heads a kv head: 217 against 225 us; the other forms gain nothing by it).
-  auto stream = [&](auto with_fine) {
-  for (int j = 0; j < my_tiles; ++j) {
+  // Puts q's finer terms where a tile looks for them.
+  auto make_fine = [&]() {
+    if (!fine_smem) return;
+    float up[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) up[r] = row_up[8 * r];
+#pragma unroll 1
+    for (int i = 0; i < kSteps; ++i) {
+      uint4 f, fl;
+      fine_terms(load_q(0, 2 * i), up[0], f.x, fl.x);
+      fine_terms(load_q(0, 2 * i + 1), up[0], f.z, fl.z);
+      if constexpr (kWide) {
+        fine_terms(load_q(1, 2 * i), up[1], f.y, fl.y);
+        fine_terms(load_q(1, 2 * i + 1), up[1], f.w, fl.w);
+        qt[(2 * i) * 32 + lane] = f;
+        qt[(2 * i + 1) * 32 + lane] = fl;
+      } else {
+        qt[i * 32 + lane] = make_uint4(f.x, fl.x, f.z, fl.z);
+      }
+    }
+    __syncwarp();
+  };
+  // The tiles.  With up to 8 heads one loop looks at each tile whether it needs the
+  // finer terms.  The forms with more, which are short of registers, have the loop
+  // twice: the first ends at the first tile that needs them, the second has them in
+  // every tile (8 sequences, 4 kv heads of 128 / 256, 64 heads each: 116 / 213 us, as one
+  // loop 120 / 281).
+  int j = 0;
+  bool made = false;
+  auto stream = [&](auto mode) {
+  constexpr int kMode = decltype(mode)::value;  // 0: without, 1: with, 2: as each tile needs
+  auto needs_fine = [&](const float4* sc) {
+    return fine_ks < INFINITY &&
+           __any_sync(0xffffffffu, reinterpret_cast<const float*>(sc)[lane] > fine_ks);
+  };
+  for (; j < my_tiles; ++j) {
     const int first = t0 + (col + j * team) * kTile;
     const bool ragged = first + kTile > t1 || first < lo_tok;
     uint32_t half;
     const float4* sc;
     take(half, sc);  // K
+    if (kMode == 0 && needs_fine(sc)) {
+      slot = slot == 0 ? L::kSlots - 1 : slot - 1;  // this half is taken again
+      return;
+    }
 
     // ---- scores of 32 tokens: four n tiles of 8 ----
     float s[4][4], sl[kWide ? 4 : 1][4];
@@ -809,9 +826,15 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
       for (int e = 0; e < 2 * kRows; ++e)
         s[n][e] = fmaf(kWide ? sl[kWide ? n : 0][e] : s[n][2 + e], 1.f / kQLo, s[n][e]);
     // ---- what hi and lo leave of q ----
-    if (with_fine && fine) {
+    if (kMode == 1 || (kMode == 2 && needs_fine(sc))) {
+      if (kMode == 2 && !made) {
+        make_fine();
+        made = true;
+      }
       float ft[kWide ? 8 : 4][4];
 #pragma unroll
+      for (int n = 0; n < (kWide ? 8 : 4); ++n) ft[n][0] = ft[n][1] = ft[n][2] = ft[n][3] = 0.f;
+#pragma unroll (kWide && D != 128 ? 1 : kSteps)
       for (int i = 0; i < kSteps; ++i) {
         const uint32_t at = half + (k_off ^ (uint32_t)(2 * i << 4));
         uint32_t x[4], y[4];
@@ -822,20 +845,20 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
           f = qt[(kWide ? 2 * i : i) * 32 + lane];
           if constexpr (kWide) f4 = qt[(2 * i + 1) * 32 + lane];
         } else {
-          fine_terms(load_q(0, 2 * i), up_fine[0], f.x, f4.x);
-          fine_terms(load_q(1, 2 * i), up_fine[kRows - 1], f.y, f4.y);
-          fine_terms(load_q(0, 2 * i + 1), up_fine[0], f.z, f4.z);
-          fine_terms(load_q(1, 2 * i + 1), up_fine[kRows - 1], f.w, f4.w);
+          fine_terms(load_q(0, 2 * i), row_up[0], f.x, f4.x);
+          fine_terms(load_q(1, 2 * i), row_up[8 * (kRows - 1)], f.y, f4.y);
+          fine_terms(load_q(0, 2 * i + 1), row_up[0], f.z, f4.z);
+          fine_terms(load_q(1, 2 * i + 1), row_up[8 * (kRows - 1)], f.w, f4.w);
         }
-        mma16832_e4m3(ft[0], i == 0, f, x[0], x[1]);
-        mma16832_e4m3(ft[1], i == 0, f, x[2], x[3]);
-        mma16832_e4m3(ft[2], i == 0, f, y[0], y[1]);
-        mma16832_e4m3(ft[3], i == 0, f, y[2], y[3]);
+        mma16832_e4m3(ft[0], false, f, x[0], x[1]);
+        mma16832_e4m3(ft[1], false, f, x[2], x[3]);
+        mma16832_e4m3(ft[2], false, f, y[0], y[1]);
+        mma16832_e4m3(ft[3], false, f, y[2], y[3]);
         if constexpr (kWide) {
-          mma16832_e4m3(ft[4], i == 0, f4, x[0], x[1]);
-          mma16832_e4m3(ft[5], i == 0, f4, x[2], x[3]);
-          mma16832_e4m3(ft[6], i == 0, f4, y[0], y[1]);
-          mma16832_e4m3(ft[7], i == 0, f4, y[2], y[3]);
+          mma16832_e4m3(ft[4], false, f4, x[0], x[1]);
+          mma16832_e4m3(ft[5], false, f4, x[2], x[3]);
+          mma16832_e4m3(ft[6], false, f4, y[0], y[1]);
+          mma16832_e4m3(ft[7], false, f4, y[2], y[3]);
         }
       }
 #pragma unroll
@@ -972,8 +995,15 @@ decode_fp8_kernel(const DecodeFp8KParams kp) {
     put();
   }
   };
-  if (kWide && D == 256 && !fine) stream(std::false_type{});
-  else stream(std::true_type{});
+  if constexpr (kWide) {
+    stream(std::integral_constant<int, 0>{});
+    if (j < my_tiles) {
+      make_fine();
+      stream(std::integral_constant<int, 1>{});
+    }
+  } else {
+    stream(std::integral_constant<int, 2>{});
+  }
 
   // ================= merge the warps' states =================
 #pragma unroll

@@ -682,13 +682,12 @@ int attn_cache_read_fp8(const uint8_t* k_cache, const uint8_t* v_cache, const fl
  *   kv_lens, num_splits, o_partial, lse_partial, scale, window_left, softcap,
  *   alibi_slopes: as attn_decode_splitkv_ex, with its split rule
  * The codes and the scales are used as they are.  q's values down to 2^-14 of their
- * row's largest magnitude are too, and smaller ones down to 2^-37 (to within 2^-45 below
- * that), unless they count for less than the rounding of a sum in fp32: unless there are
- * so few that 2^-22 of the largest each is below 2^-21 sqrt(head_dim) times the geometric
- * mean of the row.  A weight times its V scale keeps 22 significant bits (two fp16 parts),
- * or 2^-35 of the largest in its split where that is more.  The tensor cores sum the
- * products of a score, and those of 32 tokens in O; all other sums, and those over the
- * tokens, are fp32.  Keys and values of masked positions (past kv_lens, left of the
+ * row's largest magnitude are too, and smaller ones down to 2^-37 (to within 2^-45 of it
+ * below that) wherever leaving them at 2^-22 of it could change a score, in units of
+ * log 2, by more than 2^-18.  A weight times its V scale keeps 22 significant bits (two
+ * fp16 parts), or 2^-35 of the largest in its split where that is more.  The tensor cores
+ * sum the products of a score, and those of 32 tokens in O; all other sums, and those
+ * over the tokens, are fp32.  Keys and values of masked positions (past kv_lens, left of the
  * window) may hold anything, NaN included.  The largest magnitude of a row of q times a
  * K scale times scale has to stay inside fp32.
  * Limits: those of the cache; n_q_heads / n_kv_heads <= 64; batch and

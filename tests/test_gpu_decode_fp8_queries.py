@@ -1,6 +1,7 @@
-"""Decode over an 8-bit cache with queries that have one channel far larger
-than the rest, and keys that are as much smaller there: every channel counts
-alike in the scores, so the small values of q have to be used as they are."""
+"""Decode over an 8-bit cache with queries that have channels far larger than
+the rest, and keys that are as much smaller there (few such channels, or all but
+a few: keys with a large channel): every channel counts alike in the scores,
+so the small values of q have to be used as they are."""
 
 import numpy as np
 import pytest
@@ -16,16 +17,17 @@ pytestmark = pytest.mark.gpu
 AT = 40                                                    # the large channel
 
 
-def uneven(n_q, n_kv, d, lens, p, rows, paged=True):
-    """A cache whose keys are 2^-p in channel AT, and queries 2^p there in the
-    rows given (the others 0 there)."""
+def uneven(n_q, n_kv, d, lens, p, rows, paged=True, at=(AT,)):
+    """A cache whose keys are 2^-p in the channels `at`, and queries 2^p there in
+    the rows given (the others 0 there)."""
     c = filled(lens, n_kv, d, 16, paged, seed=n_q + p)
+    at = list(at)
     kv = C.decode_code(c.k.numpy())
-    kv[..., AT] *= 2.0 ** -p
+    kv[..., at] *= 2.0 ** -p
     c.k.copy_(code_bytes(C.encode_value(kv)).view(c.k.shape))
     q = queries(len(lens), n_q, d, p)
     for h in range(n_q):
-        q[:, h, AT] = q[:, h, AT] * 2.0 ** p if h in rows else 0.0
+        q[:, h, at] = q[:, h, at] * 2.0 ** p if h in rows else 0.0
     return c, q
 
 
@@ -54,6 +56,32 @@ def test_one_large_channel(dev, n_q, n_kv, d, p):
             a = scale * np.einsum("hd,nhd->nh", np.abs(q[b].double().numpy()), k).max()
             e = np.linalg.norm(o[b].double().cpu().numpy() - want[0][b]) / np.linalg.norm(want[0][b])
             assert e <= 2 * (d / 32 + 8) * 2.0 ** -23 * a, (p, S, b, e, a)
+
+
+@pytest.mark.parametrize("p", [9, 12])
+@pytest.mark.parametrize("n_q,n_kv,d,few", [(8, 2, 64, 1), (8, 2, 64, 8), (28, 4, 128, 1),
+                                            (28, 4, 128, 6), (6, 2, 256, 8), (24, 1, 128, 2),
+                                            (64, 1, 64, 3), (16, 1, 256, 8), (40, 1, 256, 1)])
+def test_all_channels_but_a_few_large(dev, n_q, n_kv, d, few, p):
+    """The other way round, as with keys that have `few` large channels.  Norm of
+    O's error as above, and 2^-18 of a base 2 logarithm in every score: twice 2^-18 log
+    2 < 2^-17.5 in the weights.  (A norm over the head's row of d values.)"""
+    lens = [700, 33]
+    c, q = uneven(n_q, n_kv, d, lens, p, range(n_q), at=[i for i in range(d) if i % d >= few])
+    scale = 4 * d ** -0.5
+    want, bound, (kc, _) = reference(c, q, lens, scale)
+    tensors, table = c.on(dev)
+    for S in (1, 0):
+        o, lse = attn.decode_fp8(q.to(dev), *tensors, i32(lens, dev), table, num_splits=S,
+                                 max_kv_len=3000, scale=scale)
+        attn.check_device_status()
+        close(o, lse, want, bound, f"p={p} S={S}")
+        for b, n in enumerate(lens):
+            k = np.abs(kc[b, :n]).repeat(n_q // n_kv, axis=1)
+            a = scale * np.einsum("hd,nhd->nh", np.abs(q[b].double().numpy()), k).max()
+            e = np.linalg.norm(o[b].double().cpu().numpy() - want[0][b], axis=1)
+            e = (e / np.linalg.norm(want[0][b], axis=1)).max()
+            assert e <= 2 * (d / 32 + 8) * 2.0 ** -23 * a + 2.0 ** -17.5, (p, S, b, e, a)
 
 
 @pytest.mark.parametrize("n_q,d", [(8, 64), (8, 128), (5, 256), (20, 128), (40, 256)])
