@@ -29,4 +29,9 @@ from .api import (  # noqa: F401
     decode_fp8,
     decode_append_fp8,
 )
+from .drafts import (  # noqa: F401
+    rope_inv_freq,
+    rope,
+    cache_append,
+)
 from ._lib import AttnError, lib  # noqa: F401

@@ -2,10 +2,12 @@
 // (error word, architecture check) and kernel launches on the caller's stream.
 // The operations themselves are defined in include/attn.h.
 #include <algorithm>
+#include <array>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <utility>
 #include <cuda_runtime.h>
 
 #include "attn.h"
@@ -561,6 +563,150 @@ int attn_quantize_fp8_qkv(const attn_bf16* q, const attn_bf16* k, const attn_bf1
   attn::QuantArgs av{v, v_codes_t, v_scales, nullptr, planes_kv, rows, head_dim, 0, 1, inv};
   if (attn::launch_quantize_qkv(aq, ak, av, make_ctx(stream, ds)) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+namespace {
+
+// Whether the rows (d values each) of up to three strided dimensions have places of
+// their own: from the smallest stride on, each one is past all that it repeats.
+bool rows_apart(long long d, std::array<std::pair<long long, long long>, 3> dims) {
+  std::sort(dims.begin(), dims.end(),
+            [](const auto& x, const auto& y) { return x.second < y.second; });
+  long long span = d;
+  for (const auto& [n, stride] : dims) {
+    if (n <= 1) continue;
+    if (stride < span) return false;
+    span += stride * (n - 1);
+  }
+  return true;
+}
+
+// Element strides: multiples of 8 (rows start at 16-byte boundaries), none negative.
+bool valid_strides(const attn::RowStrides& s) {
+  for (long long x : {s.batch, s.head, s.token})
+    if (x < 0 || x % 8 != 0 || x > (1LL << 40)) return false;
+  return true;
+}
+
+// What rope and the cache append share: the rotation and the two sizes it needs.
+int validate_rotation(int head_dim, int rotary_dim, float magnitude) {
+  if (!std::isfinite(magnitude)) return ATTN_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return ATTN_ERR_HEADDIM;
+  if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int attn_rope(const attn_bf16* q, int64_t q_batch_stride, int64_t q_head_stride,
+              int64_t q_token_stride, attn_bf16* q_out, int64_t q_out_batch_stride,
+              int64_t q_out_head_stride, int64_t q_out_token_stride, const attn_bf16* k,
+              int64_t k_batch_stride, int64_t k_head_stride, int64_t k_token_stride,
+              attn_bf16* k_out, int64_t k_out_batch_stride, int64_t k_out_head_stride,
+              int64_t k_out_token_stride, const double* inv_freq, const int32_t* positions,
+              int64_t positions_batch_stride, int batch, int n_q_heads, int n_kv_heads, int seqlen,
+              int head_dim, int rotary_dim, int interleaved, int inverse, float magnitude,
+              void* stream) {
+  if (!q || !q_out || !inv_freq || (n_kv_heads > 0 && (!k || !k_out))) return ATTN_ERR_NULL;
+  if (batch < 1 || seqlen < 1 || n_q_heads < 1 || n_q_heads > 65535 || n_kv_heads < 0 ||
+      n_kv_heads > 65535 || (long long)batch * seqlen > (1LL << 30) ||
+      (positions_batch_stride != 0 && positions_batch_stride < seqlen))
+    return ATTN_ERR_SHAPE;
+  int st = validate_rotation(head_dim, rotary_dim, magnitude);
+  if (st != ATTN_OK) return st;
+  attn::RopeArgs a{};
+  a.q = q, a.q_out = q_out;
+  a.q_s = {q_batch_stride, q_head_stride, q_token_stride};
+  a.qo_s = {q_out_batch_stride, q_out_head_stride, q_out_token_stride};
+  if (n_kv_heads > 0) {
+    a.k = k, a.k_out = k_out;
+    a.k_s = {k_batch_stride, k_head_stride, k_token_stride};
+    a.ko_s = {k_out_batch_stride, k_out_head_stride, k_out_token_stride};
+  }
+  auto apart = [&](const attn::RowStrides& s, int heads) {
+    return rows_apart(head_dim, {{{batch, s.batch}, {heads, s.head}, {seqlen, s.token}}});
+  };
+  if (!valid_strides(a.q_s) || !valid_strides(a.qo_s) || !valid_strides(a.k_s) ||
+      !valid_strides(a.ko_s) || !apart(a.qo_s, n_q_heads) ||
+      (n_kv_heads > 0 && !apart(a.ko_s, n_kv_heads)))
+    return ATTN_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(a.k, 16) || !aligned(a.k_out, 16) ||
+      !aligned(inv_freq, 8) || !aligned(positions, 4))
+    return ATTN_ERR_ALIGN;
+  a.n_q_heads = n_q_heads, a.n_kv_heads = n_kv_heads;
+  a.batch = batch, a.tokens = seqlen;
+  a.head_dim = head_dim, a.rotary_dim = rotary_dim, a.interleaved = interleaved ? 1 : 0;
+  a.inv_freq = inv_freq;
+  a.positions = positions, a.pos_batch_stride = positions_batch_stride;
+  a.magnitude = magnitude, a.sin_factor = inverse ? -magnitude : magnitude;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  if (attn::launch_rope(a, make_ctx(stream, ds)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+int attn_cache_append(const attn_bf16* k, const attn_bf16* v, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                      const attn_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                      attn_bf16* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                      attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* block_table,
+                      const int32_t* cu_seqlens, const int32_t* kv_lens, const double* inv_freq,
+                      const int32_t* positions, int num_seqs, int total_tokens, int n_q_heads,
+                      int n_kv_heads, int head_dim, int rotary_dim, int interleaved,
+                      float magnitude, int block_size, int max_blocks_per_seq, int num_blocks,
+                      int max_kv_len, void* stream) {
+  const bool queries = n_q_heads > 0;
+  if (!k || !v || !k_cache || !v_cache || !kv_lens || (queries && (!q || !q_out)) ||
+      ((queries || rotary_dim != 0) && !inv_freq))
+    return ATTN_ERR_NULL;
+  if (num_seqs < 1 || num_seqs > (1 << 20) || total_tokens < 1 || total_tokens > (1 << 24) ||
+      (!cu_seqlens && total_tokens != num_seqs) || n_q_heads < 0 || n_q_heads > 65535 ||
+      n_kv_heads < 1 || n_kv_heads > 65535)
+    return ATTN_ERR_SHAPE;
+  if (block_table ? (block_size < 1 || max_blocks_per_seq < 1 || num_blocks < 1 ||
+                     (long long)block_size * max_blocks_per_seq > (1LL << 30))
+                  : (max_kv_len < 1 || max_kv_len > (1 << 30)))
+    return ATTN_ERR_SHAPE;
+  int st = validate_rotation(head_dim, inv_freq ? rotary_dim : 16, magnitude);
+  if (st != ATTN_OK) return st;
+  attn::RopeArgs a{};
+  a.k = k, a.k_out = k_cache, a.v = v, a.v_out = v_cache;
+  a.k_s = {0, k_head_stride, k_token_stride};
+  a.v_s = {0, v_head_stride, v_token_stride};
+  if (queries) {
+    a.q = q, a.q_out = q_out;
+    a.q_s = {0, q_head_stride, q_token_stride};
+    a.qo_s = {0, q_out_head_stride, q_out_token_stride};
+  }
+  if (!valid_strides(a.k_s) || !valid_strides(a.v_s) || !valid_strides(a.q_s) ||
+      !valid_strides(a.qo_s) ||
+      (queries && !rows_apart(head_dim, {{{1, 0}, {n_q_heads, a.qo_s.head},
+                                          {total_tokens, a.qo_s.token}}})))
+    return ATTN_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(a.q, 16) || !aligned(a.q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !aligned(inv_freq, 8) ||
+      !aligned(positions, 4))
+    return ATTN_ERR_ALIGN;
+  a.n_q_heads = n_q_heads, a.n_kv_heads = n_kv_heads;
+  a.batch = num_seqs, a.tokens = total_tokens;
+  a.head_dim = head_dim, a.rotary_dim = inv_freq ? rotary_dim : 0;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.magnitude = a.sin_factor = magnitude;
+  a.cu_seqlens = cu_seqlens, a.kv_lens = kv_lens;
+  a.block_table = block_table;
+  if (block_table) {
+    a.block_size = block_size;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+  }
+  a.max_kv_len = max_kv_len;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  if (attn::launch_cache_append(a, make_ctx(stream, ds)) != cudaSuccess) return ATTN_ERR_LAUNCH;
   return ATTN_OK;
 }
 

@@ -176,6 +176,39 @@ struct DecodeFp8Args {
 };
 constexpr int kMaxSharedBatch = 1024;  // sequences a block scans to find its share
 
+// Rows of (batch, heads, tokens, head_dim) bf16: element strides.
+struct RowStrides {
+  long long batch, head, token;
+};
+
+// Rotary positions, of queries and keys (rope), or of keys on their way into a
+// bf16 cache with their values, and of the queries beside them (append).
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;  // append: the key cache, rows of n_kv_heads * head_dim
+  RowStrides q_s, k_s, qo_s, ko_s;
+  int n_q_heads, n_kv_heads;  // 0 where there is no q (append) or no k (rope)
+  int batch, tokens;          // append: sequences, and the packed tokens of all
+  int head_dim, rotary_dim, interleaved;
+  const double* inv_freq;     // (rotary_dim / 2,)
+  const int32_t* positions;   // null: the row's index (rope), the token's slot (append)
+  long long pos_batch_stride;
+  float magnitude, sin_factor;  // the factors of cos and sin
+  // append
+  const uint16_t* v = nullptr;
+  uint16_t* v_out = nullptr;
+  RowStrides v_s = {0, 0, 0};
+  const int32_t* cu_seqlens = nullptr;  // null: one token a sequence
+  const int32_t* kv_lens = nullptr;
+  const int32_t* block_table = nullptr;
+  int block_size = 0, max_blocks_per_seq = 0, num_blocks = 0, max_kv_len = 0;
+  __host__ __device__ long long capacity() const {
+    return block_table ? (long long)max_blocks_per_seq * block_size : (long long)max_kv_len;
+  }
+};
+
 // Each returns cudaSuccess or the launch error.  Arguments are already
 // validated by the caller.
 cudaError_t launch_prefill(const PrefillArgs& a, const LaunchCtx& ctx);
@@ -195,6 +228,9 @@ cudaError_t launch_decode_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 // tiles (those that are resident together).
 cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 int decode_fp8_max_parts(int head_dim, int num_sms);
+
+cudaError_t launch_rope(const RopeArgs& a, const LaunchCtx& ctx);
+cudaError_t launch_cache_append(const RopeArgs& a, const LaunchCtx& ctx);
 
 // Resolves the current device's launch context (architecture check, error
 // word, SM count) for a call on `stream`; returns an attn_status code.

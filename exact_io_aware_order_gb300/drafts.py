@@ -1,0 +1,229 @@
+"""Rotary positions, and a decode step with drafted tokens, over the C ABI in
+``include/attn.h``: argument marshalling, like ``api.py``.
+
+A step of speculative decoding, for each sequence's nodes (its last token, node 0,
+and the drafted tokens behind it)::
+
+    q = cache_append(k, v, k_cache, v_cache, kv_lens, cu, table, inv_freq, positions, q=q)
+    o, lse = decode_tree(q.transpose(0, 1), k_cache, v_cache, kv_lens, cu, mask, table)
+    ...                                             # the rest of the model, its probabilities
+    n, path, token = verify_tree(probs, tokens, parents, cu, u, u_last, draft_probs)
+"""
+
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+
+from ._lib import check, lib
+from .api import (_BF16, _F32, _I32, _columns, _int32, _lens, _need, _need_all, _raw_stream, _rows_stride,
+                  _scope)
+
+_F64 = torch.float64
+
+
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                  factor: float = 1.0, original_len: int = 8192, slow_turns: float = 1.0,
+                  fast_turns: float = 4.0, device="cuda") -> torch.Tensor:
+    """The angles a position of :func:`rope` (float64, radians): base^(-2 i /
+    rotary_dim) for pair i, for contexts ``factor`` times as long
+
+    * ``scaling="linear"``: divided by factor;
+    * ``"base"``: with base * factor^(rotary_dim / (rotary_dim - 2)), which leaves the
+      fastest pair as it is and divides the slowest by factor;
+    * ``"parts"``: pairs that make fewer than slow_turns in original_len tokens
+      divided by factor, those with more than fast_turns kept, a ramp between.
+    """
+    if rotary_dim < 16 or rotary_dim % 16:
+        raise ValueError("rotary_dim must be a multiple of 16")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    if scaling == "base":
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=_F64) / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if not slow_turns < fast_turns:
+            raise ValueError("slow_turns must be below fast_turns")
+        turns = original_len * f / (2 * math.pi)
+        keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device)
+
+
+def _sizes(*sizes: int) -> tuple[int, ...]:
+    """Sizes as the C entry points take them."""
+    return tuple(_int32(x, "a size") for x in sizes)
+
+
+def _strided(t, name: str, dev, ndim: int) -> None:
+    """A strided bf16 tensor on dev: contiguous rows, other strides multiples of 8."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    st = t.stride()
+    if st[-1] != 1 or any(s % 8 for s in st[:-1]):
+        raise ValueError(f"{name} must have contiguous rows and strides that are multiples of 8, "
+                         f"got strides {st}")
+
+
+def _frequencies(inv_freq, dev) -> tuple[int, int]:
+    """inv_freq's pointer and the rotary_dim it stands for."""
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        _need(inv_freq, "inv_freq", _F64, 1)
+    _need_all(dev, (inv_freq, "inv_freq", _F64, inv_freq.shape))
+    return inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
+         positions: Optional[torch.Tensor] = None, interleaved: bool = False,
+         inverse: bool = False, magnitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions of queries and keys (``attn_rope``).
+
+    q: (B, n_q, N, d) bf16, or packed (n_q, total, d); k the same with n_kv heads, or
+    None.  Rows contiguous, the other strides multiples of 8 (a projection's output,
+    tokens first, seen through ``transpose``).  inv_freq: (rotary_dim / 2,) float64
+    (:func:`rope_inv_freq`); positions: int32 (B, N) or (N,), packed (total,), None:
+    the row's index.  ``inverse`` rotates back; with gradients for q and k it gives
+    the gradients of this call's inputs.  Returns (q_out, k_out), allocated with
+    the inputs' layout when not given; an output may be its input.
+    """
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dev, ndim = q.device, q.dim()
+    if ndim not in (3, 4):
+        raise ValueError(f"q must have 3 or 4 dimensions, got shape {tuple(q.shape)}")
+    _strided(q, "q", dev, ndim)
+    lead, n, d = q.shape[:-3], q.shape[-2], q.shape[-1]
+    if k is not None:
+        _strided(k, "k", dev, ndim)
+        if k.shape[:-3] != lead or k.shape[-2:] != q.shape[-2:]:
+            raise ValueError("k must match q in all but its heads")
+    f, rot = _frequencies(inv_freq, dev)
+    pos, pos_stride = None, 0
+    if positions is not None:
+        shape = (*lead, n) if isinstance(positions, torch.Tensor) and positions.dim() > 1 else (n,)
+        _need_all(dev, (positions, "positions", _I32, shape))
+        pos, pos_stride = positions.data_ptr(), n if len(shape) > 1 else 0
+    with _scope(dev, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        rows = []
+        for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+            if x is None:
+                if out is not None:
+                    raise ValueError("k_out without k")
+                rows += [None, 0, 0, 0, None, 0, 0, 0]
+                continue
+            _strided(out, name, dev, ndim)
+            if out.shape != x.shape:
+                raise ValueError(f"{name} must have shape {tuple(x.shape)}")
+            for t in (x, out):
+                rows += [t.data_ptr(), *((0,) * (4 - ndim)), *t.stride()[:-1]]
+        st = lib().attn_rope(*rows, f, pos, pos_stride,
+                             *_sizes(lead[0] if lead else 1, q.shape[-3],
+                                     0 if k is None else k.shape[-3], n, d, rot),
+                             int(bool(interleaved)),
+                             int(bool(inverse)), float(magnitude), _raw_stream(dev.index))
+    check("attn_rope", st)
+    return q_out, k_out
+
+
+def _cache_bf16(dev, k_cache, v_cache, block_table, num_seqs: int):
+    """Checks a bf16 cache; returns (its two pointers and the block table's,
+    (block_size, max_blocks, num_blocks, capacity))."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _need(k_cache, "k_cache", _BF16, 4)
+    shape = k_cache.shape
+    _need_all(dev, (k_cache, "k_cache", _BF16, shape), (v_cache, "v_cache", _BF16, shape))
+    if block_table is None:
+        if shape[0] != num_seqs:
+            raise ValueError("a contiguous cache must be (num_seqs, L, n_kv, d)")
+        return (k_cache.data_ptr(), v_cache.data_ptr(), None), _sizes(0, 0, 0, shape[1])
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        _need(block_table, "block_table", _I32, 2)
+    if block_table.shape[0] != num_seqs:
+        raise ValueError("block_table must have one row per sequence")
+    most = _columns(block_table)
+    _need_all(dev, (block_table, "block_table", _I32, (num_seqs, most)))
+    return ((k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()),
+            _sizes(shape[1], most, shape[0], shape[1] * most))
+
+
+def cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, kv_lens: torch.Tensor,
+                 cu_seqlens: Optional[torch.Tensor] = None,
+                 block_table: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, magnitude: float = 1.0,
+                 q_out: Optional[torch.Tensor] = None, stream=None):
+    """New keys and values into a bf16 cache behind the kv_lens[s] tokens that each
+    sequence has there, the keys rotated on the way (``attn_cache_append``).
+
+    k_new, v_new: bf16, (n_kv, total, d) with sequence s on rows [cu_seqlens[s],
+    cu_seqlens[s + 1]), or without cu_seqlens (B, n_kv, d), one token a sequence; q
+    (optional): the same tokens' queries, n_q heads.  Rows contiguous, the other
+    strides multiples of 8.  The cache is that of :func:`decode`, written in place;
+    kv_lens is left to the caller to increment.  inv_freq as :func:`rope` (None: keys
+    are written as they are); positions: (total,) int32, None: a token's slot.
+    Returns the rotated queries, allocated with q's layout when ``q_out`` is not
+    given (None without q); rows outside every sequence are left as they were.
+    """
+    if not isinstance(k_new, torch.Tensor) or not isinstance(v_new, torch.Tensor):
+        raise TypeError("k_new and v_new must be torch.Tensors")
+    dev = k_new.device
+    _rows_stride(k_new, "k_new", dev)
+    _rows_stride(v_new, "v_new", dev)
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    lens = _lens(kv_lens, "kv_lens", None, dev)
+    B = kv_lens.shape[0]
+    ptrs, geom = _cache_bf16(dev, k_cache, v_cache, block_table, B)
+    tok = 0 if cu_seqlens is None else 1
+    cu = None if cu_seqlens is None else _lens(cu_seqlens, "cu_seqlens", B + 1, dev)
+    total, n_kv, d = k_new.shape[tok], k_new.shape[1 - tok], k_new.shape[2]
+    if cu_seqlens is None and total != B:
+        raise ValueError("without cu_seqlens k_new and v_new must be (B, n_kv, d)")
+    if tuple(k_cache.shape[2:]) != (n_kv, d):
+        raise ValueError("the cache's heads or head_dim do not match k_new")
+    f, rot = (None, 0) if inv_freq is None else _frequencies(inv_freq, dev)
+    pos = None
+    if positions is not None:
+        _need_all(dev, (positions, "positions", _I32, (total,)))
+        pos = positions.data_ptr()
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q is rotated: inv_freq is needed")
+        _rows_stride(q, "q", dev)
+        if q.shape[tok] != total or q.shape[2] != d:
+            raise ValueError("q must have k_new's tokens and head_dim")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    strides = lambda t: (t.stride(tok), t.stride(1 - tok))
+    with _scope(dev, stream):
+        rows, n_q = (None, 0, 0, None, 0, 0), 0
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty_like(q)
+            _rows_stride(q_out, "q_out", dev)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out must have shape {tuple(q.shape)}")
+            rows, n_q = (q.data_ptr(), *strides(q), q_out.data_ptr(), *strides(q_out)), q.shape[1 - tok]
+        st = lib().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(), *strides(k_new),
+                                     *strides(v_new), *rows, *ptrs, cu, lens, f, pos,
+                                     *_sizes(B, total, n_q, n_kv, d, rot), int(bool(interleaved)),
+                                     float(magnitude), *geom, _raw_stream(dev.index))
+    check("attn_cache_append", st)
+    return q_out

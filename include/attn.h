@@ -746,6 +746,95 @@ int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16*
                     int max_blocks_per_seq, int num_blocks, int max_kv_len, float scale,
                     int window_left, float softcap, const float* alibi_slopes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and a decode step with drafted tokens.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * attn_rope -- rotary positions of queries and keys, or back.
+ *
+ * Page: same, section "Interaction with post-trained models" (what a model does
+ * to queries and keys before the attention).
+ *
+ *   q, k   : (batch, heads, seqlen, head_dim) bf16 seen through strides: row
+ *            (b, h, t) starts at q + b * q_batch_stride + h * q_head_stride +
+ *            t * q_token_stride (elements; multiples of 8, 0 .. 2^40), its head_dim
+ *            values contiguous; 16-byte aligned.  n_kv_heads = 0: no k.
+ *   q_out, k_out: the same shapes, rows apart from one another, strides of their
+ *            own.  Either is its input (same pointer, same strides: in place) or
+ *            does not overlap any input.
+ *   inv_freq: (rotary_dim / 2,) float64 on the device, 8-byte aligned: the angle of
+ *            pair i at position p is p * inv_freq[i] (radians)
+ *   positions: int32, that of row (b, t) at positions[b * positions_batch_stride + t]
+ *            (a stride of 0 shares one list; otherwise >= seqlen); or NULL: t.  Any
+ *            value, negative ones too.
+ *   rotary_dim: the columns that are rotated, a multiple of 16 from 16 to head_dim;
+ *            the others are copied
+ *   interleaved: zero -> pair i is columns (i, i + rotary_dim / 2); nonzero ->
+ *            columns (2i, 2i + 1)
+ *   inverse: nonzero -> the angles' signs are turned: the inverse rotation, and
+ *            (magnitude kept) the gradient of this call with respect to its inputs
+ *   magnitude: finite; multiplies cosines and sines (so rotated columns only)
+ * y1 = magnitude (x1 cos a - x2 sin a), y2 = magnitude (x2 cos a + x1 sin a) in
+ * fp32, rounded to bf16 once.  The angle is exact to 2^-24 half turns at any position
+ * (it is kept modulo a turn in 64-bit whole numbers).
+ * Limits: head_dim in {64, 128, 256}; batch * seqlen <= 2^30; heads <= 65535.
+ * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _ALIGN, _ARCH, _LAUNCH.
+ */
+int attn_rope(const attn_bf16* q, int64_t q_batch_stride, int64_t q_head_stride,
+              int64_t q_token_stride, attn_bf16* q_out, int64_t q_out_batch_stride,
+              int64_t q_out_head_stride, int64_t q_out_token_stride, const attn_bf16* k,
+              int64_t k_batch_stride, int64_t k_head_stride, int64_t k_token_stride,
+              attn_bf16* k_out, int64_t k_out_batch_stride, int64_t k_out_head_stride,
+              int64_t k_out_token_stride, const double* inv_freq, const int32_t* positions,
+              int64_t positions_batch_stride, int batch, int n_q_heads, int n_kv_heads, int seqlen,
+              int head_dim, int rotary_dim, int interleaved, int inverse, float magnitude,
+              void* stream);
+
+/*
+ * attn_cache_append -- new keys and values into a bf16 cache, the keys rotated
+ * on the way, and the queries of the same tokens rotated beside them.
+ *
+ * Page: same, section "Minimal implementation" (new keys and values go into the
+ * cache in place; the caller increments the counts afterwards).
+ *
+ *   k, v, q    : bf16, 16-byte aligned, row t (0 <= t < total_tokens) of head h at
+ *                t * token_stride + h * head_stride (elements, as attn_rope).
+ *                n_q_heads = 0: no q.
+ *   q_out      : receives the rotated queries; rows apart; q itself (same pointer
+ *                and strides) or nothing that overlaps an input
+ *   k_cache, v_cache: the cache of attn_decode_splitkv, WRITTEN: the rows of the new
+ *                tokens' slots; nothing else changes
+ *   cu_seqlens : (num_seqs + 1,) int32, as attn_prefill_varlen: sequence s is rows
+ *                [cu[s], cu[s+1]); or NULL: one row a sequence (total_tokens ==
+ *                num_seqs).  A list that breaks the rule is clamped and flagged.
+ *   kv_lens    : (num_seqs,) int32 tokens already cached (read, not modified);
+ *                sequence s's rows go to slots kv_lens[s], kv_lens[s] + 1, ...
+ *   inv_freq, rotary_dim, interleaved, magnitude: as attn_rope; inv_freq NULL and
+ *                rotary_dim 0: keys are written as they are (then no q)
+ *   positions  : (total_tokens,) int32, the position each row is rotated by (nodes of
+ *                a tree: kv_len + depth); or NULL: the row's slot
+ * Rows outside every sequence are left alone (cache and q_out).  A sequence whose
+ * rows do not fit its capacity, or whose kv_lens is negative, is flagged and none of
+ * its keys and values is written; a block-table entry outside [0, num_blocks) is
+ * flagged and its rows are not written.  Two rows must not go to one slot (sequences
+ * that share a block), and the call must not overlap, on the device, another call
+ * that reads or writes the same slots.
+ * Limits: 1 <= num_seqs <= 2^20; 1 <= total_tokens <= 2^24; head_dim in {64, 128,
+ *   256}; heads <= 65535; block_size * max_blocks_per_seq, max_kv_len <= 2^30.
+ * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _ALIGN, _ARCH, _LAUNCH.
+ */
+int attn_cache_append(const attn_bf16* k, const attn_bf16* v, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                      const attn_bf16* q, int64_t q_token_stride, int64_t q_head_stride,
+                      attn_bf16* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                      attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* block_table,
+                      const int32_t* cu_seqlens, const int32_t* kv_lens, const double* inv_freq,
+                      const int32_t* positions, int num_seqs, int total_tokens, int n_q_heads,
+                      int n_kv_heads, int head_dim, int rotary_dim, int interleaved,
+                      float magnitude, int block_size, int max_blocks_per_seq, int num_blocks,
+                      int max_kv_len, void* stream);
+
 /* Library version string, e.g. "0.1.0 sm_103a". */
 const char* attn_version(void);
 
