@@ -33,5 +33,7 @@ from .drafts import (  # noqa: F401
     rope_inv_freq,
     rope,
     cache_append,
+    tree_mask,
+    decode_tree,
 )
 from ._lib import AttnError, lib  # noqa: F401

@@ -712,6 +712,93 @@ int attn_cache_append(const attn_bf16* k, const attn_bf16* v, int64_t k_token_st
 
 namespace {
 
+constexpr int kMostNodes = 64;  // nodes of a tree
+
+// How attn_decode_tree lays out its work and its workspace.
+struct TreePlan {
+  int blocks, whole, part_rows;
+  size_t lse_offset, o_offset, bytes;
+};
+
+// Key tiles that a block takes whole at most, so that nothing has to be joined.
+constexpr int kTreeWholeTiles = 4;
+
+TreePlan tree_plan(int total_nodes, int n_q_heads, int n_kv_heads, int head_dim, int batch,
+                   int max_kv_len, int window_left, int num_sms) {
+  TreePlan t{};
+  const int g = n_q_heads / n_kv_heads;
+  t.part_rows = attn::decode_tree_part_rows(head_dim, std::min(total_nodes, kMostNodes) * g);
+  t.blocks = std::max(num_sms, 1);
+  long long keys = max_kv_len;
+  if (window_left >= 0) keys = std::min(keys, window_left + 1LL + kMostNodes);
+  const int tile = attn::decode_tree_key_tile(head_dim);
+  t.whole = (keys + tile - 1) / tile <= kTreeWholeTiles;
+  if (t.whole) return t;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = 2 * (size_t)t.blocks * (size_t)t.part_rows;
+  t.lse_offset = up((size_t)t.blocks * sizeof(attn::TreeJoin));
+  t.o_offset = t.lse_offset + up(rows * sizeof(float));
+  t.bytes = t.o_offset + rows * (size_t)head_dim * sizeof(float);
+  return t;
+}
+
+}  // namespace
+
+size_t attn_decode_tree_workspace_bytes(int batch, int total_nodes, int n_q_heads, int n_kv_heads,
+                                        int head_dim, int max_kv_len, int window_left) {
+  if (batch < 1 || total_nodes < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
+      n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > 64 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_kv_len < 0 ||
+      window_left < -1)
+    return 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return tree_plan(total_nodes, n_q_heads, n_kv_heads, head_dim, batch, max_kv_len, window_left, sms)
+      .bytes;
+}
+
+int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                     const int32_t* block_table, const int32_t* kv_lens, const int32_t* cu_nodes,
+                     const int64_t* tree_mask, void* workspace, size_t workspace_bytes, void* o,
+                     float* lse, int batch, int total_nodes, int n_q_heads, int n_kv_heads,
+                     int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                     int max_kv_len, float scale, int window_left, float softcap,
+                     const float* alibi_slopes, unsigned flags, void* stream) {
+  if (!cu_nodes) return ATTN_ERR_NULL;
+  if (flags & ~ATTN_TREE_OUT_BF16) return ATTN_ERR_SHAPE;
+  if (total_nodes < 1 || total_nodes > (1 << 24) || max_kv_len > (1 << 30)) return ATTN_ERR_SHAPE;
+  int st = attn::validate_decode(q, nullptr, nullptr, k_cache, v_cache, block_table, kv_lens, 1,
+                                 static_cast<const float*>(o), lse, batch, n_q_heads, n_kv_heads,
+                                 head_dim, block_size, max_blocks_per_seq, num_blocks, max_kv_len,
+                                 scale, false, window_left, softcap, alibi_slopes);
+  if (st != ATTN_OK) return st;
+  if (!aligned(cu_nodes, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 16))
+    return ATTN_ERR_ALIGN;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  const TreePlan t = tree_plan(total_nodes, n_q_heads, n_kv_heads, head_dim, batch, max_kv_len,
+                               window_left, ds->num_sms);
+  if (t.bytes > 0 && !workspace) return ATTN_ERR_NULL;
+  if (workspace_bytes < t.bytes) return ATTN_ERR_SCRATCH;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  attn::DecodeTreeArgs a{q, k_cache, v_cache, block_table, kv_lens, cu_nodes, tree_mask, o, lse,
+                         batch, total_nodes, n_q_heads, n_kv_heads, head_dim,
+                         block_table ? block_size : 0, block_table ? max_blocks_per_seq : 0,
+                         block_table ? num_blocks : 0, max_kv_len, scale, window_left, softcap,
+                         alibi_slopes, (flags & ATTN_TREE_OUT_BF16) ? 0 : 1, t.blocks, t.whole,
+                         t.part_rows, reinterpret_cast<attn::TreeJoin*>(ws),
+                         reinterpret_cast<float*>(ws + t.lse_offset),
+                         reinterpret_cast<float*>(ws + t.o_offset)};
+  if (attn::launch_decode_tree(a, make_ctx(stream, ds)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+namespace {
+
 // Checks of an 8-bit cache shared by its entry points.
 int validate_cache_fp8(const attn::CacheFp8& c) {
   if (!c.k || !c.v || !c.k_scales || !c.v_scales) return ATTN_ERR_NULL;

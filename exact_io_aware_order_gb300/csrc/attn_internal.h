@@ -209,6 +209,40 @@ struct RopeArgs {
   }
 };
 
+// A cut item of a tree decode, left by the block where it ended: the block where it
+// began (-1: none ended there), its rows and where they go.
+struct TreeJoin {
+  int first_block, rows, q0, row0, kvh, pad0, pad1, pad2;
+};
+
+struct DecodeTreeArgs {
+  const uint16_t* q;  // (total_nodes, n_q_heads, head_dim)
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  const int32_t* block_table;  // null: contiguous
+  const int32_t* kv_lens;      // tokens in front of the nodes
+  const int32_t* cu_nodes;     // (batch + 1,)
+  const int64_t* tree_mask;    // (total_nodes,); null: chains
+  void* o;                     // bf16, or fp32 with wide
+  float* lse;                  // (total_nodes, n_q_heads)
+  int batch, total_nodes, n_q_heads, n_kv_heads, head_dim;
+  int block_size, max_blocks_per_seq, num_blocks, max_kv_len;
+  float scale;
+  int window_left;
+  float softcap;
+  const float* alibi_slopes;
+  int wide;
+  int blocks;     // of the persistent grid
+  int whole;      // items are not cut (no partials)
+  int part_rows;  // rows of a partial
+  TreeJoin* joins;   // (blocks,)
+  float* lse_part;   // (blocks, 2, part_rows)
+  float* o_part;     // (blocks, 2, part_rows, head_dim)
+  __host__ __device__ long long capacity() const {
+    return block_table ? (long long)max_blocks_per_seq * block_size : (long long)max_kv_len;
+  }
+};
+
 // Each returns cudaSuccess or the launch error.  Arguments are already
 // validated by the caller.
 cudaError_t launch_prefill(const PrefillArgs& a, const LaunchCtx& ctx);
@@ -230,6 +264,10 @@ cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 int decode_fp8_max_parts(int head_dim, int num_sms);
 
 cudaError_t launch_rope(const RopeArgs& a, const LaunchCtx& ctx);
+// Rows of a partial (max_rows: the most that a kv head can have), and a key tile's tokens.
+int decode_tree_part_rows(int head_dim, int max_rows);
+int decode_tree_key_tile(int head_dim);
+cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_cache_append(const RopeArgs& a, const LaunchCtx& ctx);
 
 // Resolves the current device's launch context (architecture check, error

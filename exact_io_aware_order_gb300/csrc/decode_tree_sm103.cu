@@ -1,0 +1,863 @@
+// Attention of a tree of drafted tokens over a cache, sm_103a: cp.async + tcgen05 + TMEM.
+//
+// A sequence's nodes (its last token and the drafted ones, at most 64) lie in the
+// cache behind the kv_len tokens cached before them.  Node i's query sees those
+// tokens, and the nodes whose bits are set in its mask word (its ancestors and
+// itself):  O = softmax(scale q K^T) V  with the online softmax, over a paged or
+// contiguous cache, all nodes and all query heads of a kv head together, so that a
+// key or value is read once for up to 256 rows.
+//
+// What bounds it: HBM for up to about 150 rows a kv head (a tile of 128 tokens at
+// head_dim 128 is 64 KB, 1.5 us of an SM's share of the copy rate; a row tile of 128
+// rows takes the pipeline 0.85 us), the tensor cores and the exponentials beyond.
+// Even a few rows go through 128-row products: they hide behind the copies, and one
+// path serves every size.
+//
+// Design:
+//   * persistent blocks, one an SM.  The work of all (sequence, kv head, row group)
+//     items is counted in key tiles on the device, from kv_lens and cu_nodes, and
+//     every block takes an equal run of them, across items; an item that is cut
+//     leaves a normalised partial and its log-sum-exp for each block, which a second
+//     kernel joins.  A block starts at most one cut item in its run and ends at most
+//     one, so there are two places a block.  Short caches (by max_kv_len) go whole
+//     items to a block, without the second kernel;
+//   * four producer warps copy 16 bytes a thread (cp.async) from wherever the block
+//     table says into the 128-byte-swizzled layout that the MMAs read: any block
+//     size, blocks that end inside a tile, rows past the end filled with zeros.  A
+//     tile is announced when its copies have landed, two or three tiles behind the
+//     newest, so that many are in flight;
+//   * S = Q K^T and O += P V by two issuing threads, S in two TMEM buffers, P over
+//     S, one O a row tile; with two row tiles in an item they take turns, so the
+//     tensor cores work on one while the other is in the softmax;
+//   * the softmax is one row a thread, four warps a row tile, in two passes over S:
+//     the row maximum (after masks, soft-capping and ALiBi, which are written back),
+//     then the exponentials.  Reading S twice costs 2 x 32 clocks a warp and saves
+//     the registers that 14 warps do not have;
+//   * P is rounded to bf16 for a bf16 O (2^-8 of a weight, no more than O's own
+//     rounding), and split into two bf16 parts (2^-16) for an fp32 one;
+//   * row statistics, O and the partials are fp32; O is rescaled when a row's maximum
+//     has grown by more than 2^8 (exact: the same stale one is used for l and O);
+//   * every wait is bounded, as in the other kernels.
+#include <algorithm>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "attn_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kSoftmaxThreads = 128;   // of a row tile
+constexpr int kProducerThreads = 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kMostNodes = 64;
+
+// Row tiles of an item (TMEM: two S buffers of kBN columns and an O of D for each).
+template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
+template <int D> __host__ __device__ constexpr int key_tile() { return D == 256 ? 64 : 128; }
+template <int D> __host__ __device__ constexpr int threads_of() {
+  return row_tiles<D>() * kSoftmaxThreads + kProducerThreads + 64;
+}
+
+template <int D>
+struct TreeSmem {
+  static constexpr int kBN = key_tile<D>();
+  static constexpr int kQTileBytes = 128 * D * 2;
+  static constexpr int kTileBytes = kBN * D * 2;
+  static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
+  static constexpr int kChunkBytes = kBN * 128;
+  static constexpr int kMaxSlots = 8;
+  // barriers: full / empty for each slot, q_empty, s_full[row tile][2], p_full[2],
+  // pv_done[2], o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item
+  // of fewer rows would otherwise miss phases, and take an old one for its next.
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 4 + 2 + 2 + 2 + 2;
+  static constexpr int kMiscBytes = 1024;  // barriers, then the block's share of the work
+  static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
+  // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
+  static constexpr int slots(int q_tiles) {
+    const int room = 226 * 1024 - kMiscBytes - kDepthBytes - 1024 - q_tiles * kQTileBytes;
+    const int n = room / kTileBytes;
+    return n < kMaxSlots ? n : kMaxSlots;
+  }
+  static constexpr int total(int q_tiles) {
+    return q_tiles * kQTileBytes + slots(q_tiles) * kTileBytes + kMiscBytes + kDepthBytes + 1024;
+  }
+};
+
+struct TreeKParams {
+  DecodeTreeArgs a;
+  int q_tiles, slots;   // row tiles that an item may have here, ring slots
+  float sl2;            // scale * log2(e)
+  float cap_in, cap_l2; // soft-capping: scale / softcap, softcap * log2(e)
+  uint32_t* err_word;
+  uint64_t timeout_ns;
+};
+
+// A sequence as the kernel takes it (bad lengths clamped to nothing).
+struct Seq {
+  int q0, nodes;  // first packed row, nodes
+  int kv_len;     // tokens in front of the nodes
+  int end;        // tokens and nodes: keys [lo, end)
+  int lo;
+  int tiles;      // key tiles, at least 1
+  int groups;     // row groups
+  bool bad_nodes, bad_len;
+};
+
+template <int D>
+__device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
+  const DecodeTreeArgs& a = p.a;
+  Seq s;
+  const int x = a.cu_nodes[b], y = a.cu_nodes[b + 1];
+  s.q0 = min(max(x, 0), a.total_nodes);
+  const int e = min(max(y, s.q0), a.total_nodes);
+  s.nodes = min(e - s.q0, kMostNodes);
+  s.bad_nodes = x != s.q0 || y != e || e - s.q0 > kMostNodes || (b == 0 && x != 0);
+  const int len = a.kv_lens[b];
+  s.bad_len = len < 0 || (long long)len + s.nodes > a.capacity();
+  s.kv_len = s.bad_len ? 0 : len;
+  s.end = s.bad_len ? 0 : len + s.nodes;
+  // Every node's position is kv_len or more: a window starts no earlier than this.
+  s.lo = a.window_left >= 0 ? max(0, s.kv_len - a.window_left) : 0;
+  s.tiles = max(1, (s.end - s.lo + key_tile<D>() - 1) / key_tile<D>());
+  const int g = a.n_q_heads / a.n_kv_heads, rows = 128 * p.q_tiles;
+  s.groups = (s.nodes * g + rows - 1) / rows;
+  return s;
+}
+
+// Units of work of a sequence: key tiles, or items where items go whole.
+__device__ __forceinline__ long long units_of(const TreeKParams& p, const Seq& s) {
+  return (long long)p.a.n_kv_heads * s.groups * (p.a.whole ? 1 : s.tiles);
+}
+
+// This block's run of units, in shared memory: [u0, u1) of total, beginning in
+// sequence b0, whose units start at base0.
+struct Share {
+  long long u0, u1, total, base0;
+  int b0;
+};
+
+// A run of key tiles of one item.
+struct Seg {
+  Seq s;
+  int b, kvh, row0, rows, nr;  // rows [row0, row0 + rows) of the kv head, row tiles
+  int t0, tiles;               // key tiles [t0, t0 + tiles)
+  bool first, last;            // whether it starts and ends its item
+  long long item_u0;           // the item's first unit
+};
+
+template <int D>
+struct Walk {
+  const TreeKParams& p;
+  long long u, u1, base;
+  int b;
+  Seq s;
+  __device__ Walk(const TreeKParams& p_, const Share& sh)
+      : p(p_), u(sh.u0), u1(sh.u1), base(sh.base0), b(sh.b0) {
+    if (u < u1) s = seq_of<D>(p, b);
+  }
+  __device__ bool next(Seg& g) {
+    if (u >= u1) return false;
+    long long n = units_of(p, s);
+    while (u >= base + n) {
+      if (b + 1 >= p.a.batch) return false;  // (lengths that changed under the call)
+      base += n;
+      s = seq_of<D>(p, ++b);
+      n = units_of(p, s);
+    }
+    const int T = p.a.whole ? 1 : s.tiles;
+    const long long local = u - base;
+    const int item = (int)(local / T), t = (int)(local - (long long)item * T);
+    const int rows = 128 * p.q_tiles;
+    const int n_units = (int)min((long long)(T - t), u1 - u);
+    g.s = s;
+    g.b = b;
+    g.kvh = item / s.groups;
+    g.row0 = (item % s.groups) * rows;
+    g.rows = min(rows, s.nodes * (p.a.n_q_heads / p.a.n_kv_heads) - g.row0);
+    g.nr = (g.rows + 127) / 128;
+    g.t0 = t;
+    g.tiles = p.a.whole ? s.tiles : n_units;
+    g.first = t == 0;
+    g.last = t + n_units == T;
+    g.item_u0 = base + (long long)item * T;
+    u += n_units;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_dyn(int n) {
+  switch (n) {
+    case 0: cp_async_wait<0>(); break;
+    case 1: cp_async_wait<1>(); break;
+    case 2: cp_async_wait<2>(); break;
+    case 3: cp_async_wait<3>(); break;
+    default: cp_async_wait<4>(); break;
+  }
+}
+
+// VAR: window, soft-capping or ALiBi.  WIDE: fp32 O, P in two bf16 parts.
+template <int D, bool VAR, bool WIDE>
+__global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const TreeKParams p) {
+  using L = TreeSmem<D>;
+  constexpr int kBN = L::kBN, NQ = row_tiles<D>(), kThreads = threads_of<D>();
+  constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 4, kPVWarp = kSWarp + 1;
+  static_assert(2 * kBN + NQ * D <= (int)kTmemCols, "TMEM budget");
+  const DecodeTreeArgs& a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slots = p.slots;
+  uint8_t* ring = smem + p.q_tiles * L::kQTileBytes;
+  uint8_t* misc = ring + slots * L::kTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
+                kPFull = kSFull + 4, kPVDone = kPFull + 2, kOFull = kPVDone + 2,
+                kDrain = kOFull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
+  Share* share = reinterpret_cast<Share*>(misc + L::kNumBars * 8 + 16);
+  long long* warp_sums = reinterpret_cast<long long*>(share + 1);  // one a warp
+  static_assert(L::kNumBars * 8 + 16 + sizeof(Share) + 16 * 8 <= L::kMiscBytes, "misc");
+  int* depth_tab = reinterpret_cast<int*>(misc + L::kMiscBytes);
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    for (int i = 0; i < slots; ++i) {
+      mbar_init(bar(kFull + i), kProducerThreads);
+      mbar_init(bar(kEmpty + i), 1);
+    }
+    mbar_init(bar(kQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kSFull + 2 + i), 1);
+      mbar_init(bar(kPFull + i), kSoftmaxThreads);
+      mbar_init(bar(kPVDone + i), 1);
+      mbar_init(bar(kOFull + i), 1);
+      mbar_init(bar(kDrain + i), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // ---- this block's share: each thread counts the units of a run of sequences ----
+  {
+    const int per = (a.batch + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.batch), b1 = min(b0 + per, a.batch);
+    long long mine = 0;
+    bool bad_nodes = false, bad_len = false;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_of<D>(p, b);
+      mine += units_of(p, s);
+      bad_nodes |= s.bad_nodes;
+      bad_len |= s.bad_len;
+    }
+    if (blockIdx.x == 0) {
+      if (bad_nodes) atomicOr(p.err_word, kErrSeqLens);
+      if (bad_len) atomicOr(p.err_word, kErrKvLen);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long v = warp_sums[w];
+      if (w < warp) before += v;
+      total += v;
+    }
+    long long at = before + incl - mine;  // units in front of this thread's sequences
+    // Blocks beyond the units get none, so that those with some are neighbours.
+    const long long G = max(min((long long)gridDim.x, total), 1LL), c = blockIdx.x;
+    const long long u0 = min(c * total / G, total), u1 = min((c + 1) * total / G, total);
+    if (threadIdx.x == 0) {
+      share->u0 = u0;
+      share->u1 = u1;
+      share->total = total;
+      share->b0 = 0;
+      share->base0 = 0;
+    }
+    __syncthreads();
+    if (u0 < u1 && u0 >= at && u0 < at + mine) {
+      int b = b0;
+      for (; b + 1 < b1; ++b) {
+        const long long n = units_of(p, seq_of<D>(p, b));
+        if (u0 < at + n) break;
+        at += n;
+      }
+      share->b0 = b;
+      share->base0 = at;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tO = tmem + 2 * kBN;
+  const WaitCtl ctl{abort_flag, p.err_word, p.timeout_ns};
+  const Share sh = *share;
+  const int g = a.n_q_heads / a.n_kv_heads;
+
+  // Roles walk the same segments; S products count over all of them (n: buffer n & 1),
+  // and so do the ring's tiles (K and V of key tile j: 2 j and 2 j + 1).
+  const uint32_t id_s = idesc_bf16_f32(128, kBN, false, false);
+  const uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
+  const uint32_t dhi = sw128_desc_hi(1024);
+
+  if (warp >= kProducerWarp && warp < kSWarp) {
+    // ============================ producers ============================
+    constexpr int kRowChunks = D / 8;                      // 16-byte pieces of a row
+    constexpr int kRowsPass = kProducerThreads / kRowChunks;
+    constexpr int kPasses = kBN / kRowsPass;               // rows of a tile a thread copies
+    const int tid = threadIdx.x - kProducerWarp * 32;
+    const int pc = tid % kRowChunks, pr = tid / kRowChunks;
+    // The swizzled place of this thread's piece of a row, in a tile of spans of chunk_bytes.
+    auto place = [&](int row, int chunk_bytes) {
+      return (uint32_t)((pc >> 3) * chunk_bytes + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+    };
+    const int lag = slots - 2 < 4 ? slots - 2 : 4;         // tiles in flight behind the newest
+    int issued = 0, announced = 0, slot = 0, phase = 0, ann_slot = 0, n_seg = 0;
+    auto announce = [&](int left) {
+      cp_async_wait_dyn(left);
+      fence_proxy_async_smem();
+      while (issued - announced > left) {
+        mbar_arrive(bar(kFull + ann_slot));
+        if (++ann_slot == slots) ann_slot = 0;
+        ++announced;
+      }
+    };
+    Walk<D> walk(p, sh);
+    Seg sg;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      if (n_seg > 0) {
+        // The last segment's S products have to be through with Q, and need all their keys.
+        announce(0);
+        if (!mbar_wait(bar(kQEmpty), (n_seg - 1) & 1, ctl)) break;
+      }
+      ++n_seg;
+      // Q: row i of the kv head is node i / g, head i % g; announced with the first keys.
+      for (int i = pr; i < 128 * sg.nr; i += kRowsPass) {
+        const int row = sg.row0 + i, node = row / g, h = row - node * g;
+        const bool real = i < sg.rows;
+        const uint16_t* src =
+            a.q + (real ? ((size_t)(sg.s.q0 + node) * a.n_q_heads + (size_t)sg.kvh * g + h) * D + pc * 8
+                        : 0);
+        const uint32_t dst = smem_u32(smem + (i >> 7) * L::kQTileBytes) +
+                             place(i & 127, L::kQChunkBytes);
+        cp_async16_or_zero(dst, src, real);
+      }
+      const int32_t* table =
+          a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
+      for (int t = 0; t < sg.tiles && ok; ++t) {
+        const int tok0 = sg.s.lo + (sg.t0 + t) * kBN;
+        // Cache rows (a token of all kv heads) of this thread's rows; -1: none.
+        long long row[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int tok = tok0 + pr + i * kRowsPass;
+          row[i] = -1;
+          if (tok < sg.s.end) {
+            if (table == nullptr) {
+              row[i] = (long long)sg.b * a.max_kv_len + tok;
+            } else {
+              const int blk = table[tok / a.block_size];
+              if (blk >= 0 && blk < a.num_blocks)
+                row[i] = (long long)blk * a.block_size + tok % a.block_size;
+              else if (pc == 0)
+                atomicOr(p.err_word, kErrBlockIndex);
+            }
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (issued >= slots && !mbar_wait(bar(kEmpty + slot), phase ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint16_t* base = (kv ? a.v_cache : a.k_cache) + (size_t)sg.kvh * D + pc * 8;
+          const uint32_t dst0 = smem_u32(ring + slot * L::kTileBytes);
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i) {
+            const bool real = row[i] >= 0;
+            cp_async16_or_zero(dst0 + place(pr + i * kRowsPass, L::kChunkBytes),
+                               base + (real ? row[i] : 0) * (long long)a.n_kv_heads * D, real);
+          }
+          cp_async_commit();
+          ++issued;
+          if (++slot == slots) slot = 0, phase ^= 1;
+          if (issued - announced > lag) announce(lag);
+        }
+      }
+    }
+    announce(0);
+  } else if (warp == kSWarp) {
+    // ============================ S = Q K^T issuer ============================
+    if (lane == 0) {
+      Walk<D> walk(p, sh);
+      Seg sg;
+      bool ok = true;
+      int n = 0, slot = 0, phase = 0;
+      const uint32_t q_lo0 = sw128_desc_lo(smem_u32(smem), 16);
+      while (ok && walk.next(sg)) {
+        for (int t = 0; t < sg.tiles && ok; ++t) {
+          if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
+          const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
+          for (int r = 0; r < sg.nr; ++r, ++n) {
+            const int b = n & 1;
+            // Buffer b last held P(n - 2).
+            if (n >= 2 && !mbar_wait(bar(kPVDone + b), ((n >> 1) - 1) & 1, ctl)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t dS = tmem + b * kBN;
+            const uint32_t q_lo = q_lo0 + (uint32_t)((r * L::kQTileBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t qoff = ((kk >> 2) * L::kQChunkBytes + (kk & 3) * 32) >> 4;
+              const uint32_t koff = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+              mma_ss_lo(dS, q_lo + qoff, k_lo + koff, dhi, id_s, kk > 0);
+            }
+            mma_commit(bar(kSFull + 2 * r + b));
+          }
+          mma_commit(bar(kEmpty + slot));
+          // K tiles are every other one of the ring.
+          for (int i = 0; i < 2; ++i)
+            if (++slot == slots) slot = 0, phase ^= 1;
+        }
+        mma_commit(bar(kQEmpty));
+      }
+      mma_commit(bar(kDrain));
+      volatile uint32_t no_abort = 0u;
+      WaitCtl drain{&no_abort, p.err_word, p.timeout_ns};
+      mbar_wait(bar(kDrain), 0, drain);
+    }
+    __syncwarp();
+  } else if (warp == kPVWarp) {
+    // ============================ O += P V issuer ============================
+    if (lane == 0) {
+      Walk<D> walk(p, sh);
+      Seg sg;
+      bool ok = true;
+      int n = 0, slot = 1, phase = 0;
+      while (ok && walk.next(sg)) {
+        for (int t = 0; t < sg.tiles && ok; ++t) {
+          if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
+          const uint32_t v_lo =
+              sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
+          for (int r = 0; r < sg.nr; ++r, ++n) {
+            const int b = n & 1;
+            if (!mbar_wait(bar(kPFull + b), (n >> 1) & 1, ctl)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t aP = tmem + b * kBN, tOr = tO + r * D;
+#pragma unroll
+            for (int part = 0; part < (WIDE ? 2 : 1); ++part)
+#pragma unroll
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
+                          id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
+            mma_commit(bar(kPVDone + b));
+            if (t == sg.tiles - 1) mma_commit(bar(kOFull + r));
+          }
+          mma_commit(bar(kEmpty + slot));
+          for (int i = 0; i < 2; ++i)
+            if (++slot == slots) slot = 0, phase ^= 1;
+        }
+      }
+      mma_commit(bar(kDrain + 1));
+      volatile uint32_t no_abort = 0u;
+      WaitCtl drain{&no_abort, p.err_word, p.timeout_ns};
+      mbar_wait(bar(kDrain + 1), 0, drain);
+    }
+    __syncwarp();
+  } else if (warp < kProducerWarp) {
+    // ============================ softmax, epilogue ============================
+    const int r = warp >> 2;                                // row tile
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int trow = (warp & 3) * 32 + lane;                // row within the tile (TMEM lane)
+    int* depths = depth_tab + warp * kMostNodes;            // the nodes' depths, each warp its own
+    Walk<D> walk(p, sh);
+    Seg sg;
+    bool ok = true;
+    int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
+    uint32_t s_phase = 0;   // s_full's phase, a bit for each buffer
+    for (; ok && walk.next(sg); n0 += sg.tiles * sg.nr) {
+      if (r >= sg.nr) continue;
+      const int i = r * 128 + trow;                         // row of the group
+      const bool real = i < sg.rows;
+      const int node = (sg.row0 + i) / g, head = sg.kvh * g + (sg.row0 + i) % g;
+      // The nodes this row sees.
+      const unsigned long long all =
+          sg.s.nodes >= 64 ? ~0ull : (1ull << sg.s.nodes) - 1ull;
+      auto word_of = [&](int u) {
+        const unsigned long long w = a.tree_mask
+                                         ? (unsigned long long)a.tree_mask[sg.s.q0 + u]
+                                         : (2ull << u) - 1ull;
+        return w & all;
+      };
+      unsigned long long word = real ? word_of(node) : 0ull;
+      if (sg.s.end == 0) word = 0ull;                       // a length that was refused
+      int depth = 0;
+      float slope_l2 = 0.f;
+      if constexpr (VAR) {
+        depth = max(__popcll(word) - 1, 0);
+        __syncwarp();                                       // the last segment's readers
+        for (int u = lane; u < sg.s.nodes; u += 32) depths[u] = max(__popcll(word_of(u)) - 1, 0);
+        __syncwarp();
+        if (a.window_left >= 0 && a.window_left < kMostNodes)
+          for (int u = 0; u < sg.s.nodes; ++u)
+            if (depth - depths[u] > a.window_left) word &= ~(1ull << u);
+        if (a.alibi_slopes != nullptr && real) slope_l2 = a.alibi_slopes[head] * kLog2e;
+      }
+      const int pos = sg.s.kv_len + depth;
+      float m = -INFINITY, l = 0.f;
+      const float sl2 = VAR ? 1.f : p.sl2;
+      for (int t = 0; t < sg.tiles; ++t) {
+        const int n = n0 + t * sg.nr + r, b = n & 1;
+        const int kv0 = sg.s.lo + (sg.t0 + t) * kBN;
+        // Visible columns, a bit each, where some may not be.
+        const bool edge = kv0 + kBN > sg.s.kv_len ||
+                          (VAR && a.window_left >= 0 && kv0 < sg.s.kv_len + kMostNodes - a.window_left);
+        uint32_t vis[kBN / 32];
+        if (edge) {
+          const int sft = sg.s.kv_len - kv0;                // column of node 0
+          const int lo_c = (VAR && a.window_left >= 0)
+                               ? min(pos - a.window_left, sg.s.kv_len) - kv0 : 0;
+#pragma unroll
+          for (int c = 0; c < kBN / 32; ++c) {
+            const int s = sft - 32 * c;
+            uint32_t w = s >= 32 ? 0xffffffffu : s > 0 ? (1u << s) - 1u : 0u;
+            if (s < 32) w |= s >= 0 ? (uint32_t)(word << s) : s > -64 ? (uint32_t)(word >> -s) : 0u;
+            const int q = lo_c - 32 * c;
+            if (q > 0) w &= q >= 32 ? 0u : ~((1u << q) - 1u);
+            vis[c] = w;
+          }
+        }
+        if (!mbar_wait_warp(bar(kSFull + 2 * r + b), (s_phase >> b) & 1u, ctl)) { ok = false; break; }
+        s_phase ^= 1u << b;
+        tc_fence_after();
+        const uint32_t tS = tmem + b * kBN + lane_base;
+        // ---- pass 1: masks and variants, the row's maximum ----
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c2 = 0; c2 < kBN / 64; ++c2) {
+          uint32_t x[2][32];
+          tmem_ld32(tS + c2 * 64, x[0]);
+          tmem_ld32(tS + c2 * 64 + 32, x[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * c2 + h;
+            if constexpr (VAR) {
+              if (a.softcap > 0.f) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  x[h][k] = __float_as_uint(p.cap_l2 * tanhf(__uint_as_float(x[h][k]) * p.cap_in));
+              } else {
+                const float d0 = (float)(pos - kv0 - 32 * c);
+                const int u0 = kv0 + 32 * c - sg.s.kv_len;  // node of the chunk's first column
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  float dist = d0 - (float)k;
+                  if (u0 + k >= 0) dist = (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
+                  // (slope 0 without ALiBi)
+                  x[h][k] = __float_as_uint(
+                      fmaf(__uint_as_float(x[h][k]), p.sl2, slope_l2 == 0.f ? 0.f : -slope_l2 * dist));
+                }
+              }
+            }
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((vis[c] >> k) & 1u)) x[h][k] = 0xff800000u;  // -inf
+            }
+            float mc[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mc[k] = __uint_as_float(x[h][k]);
+#pragma unroll
+            for (int k = 4; k < 28; k += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mc[q] = fmax3(mc[q], __uint_as_float(x[h][k + q]), __uint_as_float(x[h][k + q + 4]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mc[q] = fmaxf(mc[q], __uint_as_float(x[h][28 + q]));
+            mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            if (VAR || edge) tmem_st32(tS + c * 32, x[h]);
+          }
+        }
+        if (VAR || edge) tmem_wait_st();
+        // ---- the reference: raised only when some row of the warp gained 2^8 ----
+        const float m_new = fmaxf(m, mx * sl2);
+        float corr = 1.f;
+        bool rescale_o = false;
+        if (m == -INFINITY) m = m_new;  // nothing seen so far: O and l are 0
+        if (t > 0 && __any_sync(0xffffffffu, m_new - m > kRescaleThreshold)) {
+          corr = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
+          m = m_new;
+          l *= corr;
+          rescale_o = true;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        // ---- pass 2: P over S ----
+        const float2 sl2v = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
+        float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t lo[WIDE ? kBN / 32 : 1][WIDE ? 16 : 1];
+#pragma unroll
+        for (int c = 0; c < kBN / 32; ++c) {
+          uint32_t x[32], hi[16];
+          tmem_ld32(tS + c * 32, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 e = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
+                                  sl2v, nmv);
+            const float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            rs[k & 1] = add2(rs[k & 1], pp);
+            hi[k] = pack_bf16x2(pp.x, pp.y);
+            if constexpr (WIDE)
+              lo[c][k] = pack_bf16x2(pp.x - __uint_as_float(hi[k] << 16),
+                                  pp.y - __uint_as_float(hi[k] & 0xffff0000u));
+          }
+          tmem_st16(tS + c * 16, hi);
+          if constexpr (WIDE) {
+            // The low parts go over the second half of S, each as soon as the columns that
+            // it overwrites have been read.
+#pragma unroll
+            for (int q = 0; q < kBN / 32; ++q) {
+              const int end = kBN / 2 + 16 * (q + 1);
+              if (end <= 32 * (c + 1) && end > 32 * c) tmem_st16(tS + end - 16, lo[q]);
+            }
+          }
+        }
+        const float2 rsum = add2(rs[0], rs[1]);
+        l += rsum.x + rsum.y;
+        if (rescale_o) {
+          const int pn = n - sg.nr;                         // this row tile's last product
+          if (!mbar_wait_warp(bar(kPVDone + (pn & 1)), (pn >> 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            const uint32_t at = tO + r * D + lane_base + c * 32;
+            tmem_ld32(at, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * corr);
+            tmem_st32(at, x);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + b));
+      }
+      if (!ok) break;
+      // ---- epilogue of the segment ----
+      if (!mbar_wait_warp(bar(kOFull + r), n_seg & 1, ctl)) { ok = false; break; }
+      ++n_seg;
+      tc_fence_after();
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a NaN stays)
+      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      const bool whole = sg.first && sg.last;
+      // A cut item's partial: place 0 of the block for one that began before, else 1.
+      const size_t prow = ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * a.part_rows + i;
+      const size_t orow = (size_t)(sg.s.q0 + node) * a.n_q_heads + head;
+      if (real) {
+        if (whole) a.lse[orow] = lse;
+        else a.lse_part[prow] = lse;
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld32(tO + r * D + lane_base + c * 32, x);
+        tmem_wait_ld();
+        if (!real) continue;
+        auto f = [&](int k) { return __uint_as_float(x[k]) * inv; };
+        if (!WIDE && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * D + c * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(pack_bf16x2(f(8 * k), f(8 * k + 1)), pack_bf16x2(f(8 * k + 2), f(8 * k + 3)),
+                                pack_bf16x2(f(8 * k + 4), f(8 * k + 5)),
+                                pack_bf16x2(f(8 * k + 6), f(8 * k + 7)));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(
+              (whole ? static_cast<float*>(a.o) + orow * D : a.o_part + prow * D) + c * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(f(4 * k), f(4 * k + 1), f(4 * k + 2), f(4 * k + 3));
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  // ---- what the second kernel joins: the item that ends here and began before ----
+  if (!a.whole && threadIdx.x == 0) {
+    TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
+    Walk<D> walk(p, sh);
+    Seg sg;
+    if (walk.next(sg) && !sg.first && sg.last) {
+      // The block that holds unit u is the last c with c total / G <= u.
+      j.first_block =
+          (int)(((sg.item_u0 + 1) * min((long long)gridDim.x, sh.total) - 1) / sh.total);
+      j.rows = sg.rows;
+      j.q0 = sg.s.q0;
+      j.row0 = sg.row0;
+      j.kvh = sg.kvh;
+    }
+    a.joins[blockIdx.x] = j;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The partials of a cut item, one warp a row: O = sum w_i O_i / sum w_i with
+// w_i = exp(lse_i - max), blocks in order, so the result does not depend on which came
+// first.  blockIdx.x: the block of the first kernel where the item ended.
+// ---------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const DecodeTreeArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  const int c = blockIdx.x;
+  const TreeJoin j = a.joins[c];
+  const int i = blockIdx.y * kJoinWarps + warp;
+  if (j.first_block < 0 || i >= j.rows) return;
+  const int parts = c - j.first_block + 1;
+  auto at = [&](int k) {  // the first block left it at its place 1, the others at place 0
+    return ((size_t)(j.first_block + k) * 2 + (k == 0 ? 1 : 0)) * a.part_rows + i;
+  };
+  float top = -INFINITY;
+  for (int k = lane; k < parts; k += 32) top = fmax_nan(top, a.lse_part[at(k)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
+  constexpr int kV = D / 32;  // values of a lane: columns lane * kV ...
+  float acc[kV], sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const size_t row = at(k);
+    const float w = ex2_approx((a.lse_part[row] - ref) * kLog2e);
+    sum += w;
+    const float* src = a.o_part + row * D + lane * kV;
+    float x[kV];
+    if constexpr (kV == 2) {
+      const float2 y = *reinterpret_cast<const float2*>(src);
+      x[0] = y.x, x[1] = y.y;
+    } else {
+#pragma unroll
+      for (int v = 0; v < kV; v += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src + v);
+        x[v] = y.x, x[v + 1] = y.y, x[v + 2] = y.z, x[v + 3] = y.w;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[v] = fmaf(w, x[v], acc[v]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int g = a.n_q_heads / a.n_kv_heads;
+  const int node = (j.row0 + i) / g, head = j.kvh * g + (j.row0 + i) % g;
+  const size_t orow = (size_t)(j.q0 + node) * a.n_q_heads + head;
+  if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : ref + log2f(sum) * kLn2;
+  if constexpr (WIDE) {
+    float* dst = static_cast<float*>(a.o) + orow * D + lane * kV;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) dst[v] = acc[v] * inv;
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + orow * D + lane * kV);
+#pragma unroll
+    for (int v = 0; v < kV; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+  }
+}
+
+template <int D, bool VAR, bool WIDE>
+cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
+  using L = TreeSmem<D>;
+  TreeKParams p;
+  p.a = a;
+  const int g = a.n_q_heads / a.n_kv_heads;
+  p.q_tiles = std::min(row_tiles<D>(), (std::min(a.total_nodes, kMostNodes) * g + 127) / 128);
+  p.slots = L::slots(p.q_tiles);
+  p.sl2 = a.scale * kLog2e;
+  p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  p.cap_l2 = a.softcap * kLog2e;
+  p.err_word = ctx.err_word;
+  p.timeout_ns = ctx.timeout_ns;
+  auto kernel = decode_tree_kernel<D, VAR, WIDE>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         std::max(L::total(1), L::total(row_tiles<D>())));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.blocks);
+  cfg.blockDim = dim3(threads_of<D>());
+  cfg.dynamicSmemBytes = L::total(p.q_tiles);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess || a.whole) return e;
+  cfg.gridDim = dim3((unsigned)a.blocks, (unsigned)((a.part_rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_tree_kernel<D, WIDE>, a);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
+  const bool var = a.window_left >= 0 || a.softcap > 0.f || a.alibi_slopes != nullptr;
+  if (a.wide) return var ? launch_t<D, true, true>(a, ctx) : launch_t<D, false, true>(a, ctx);
+  return var ? launch_t<D, true, false>(a, ctx) : launch_t<D, false, false>(a, ctx);
+}
+
+}  // namespace
+
+int decode_tree_part_rows(int head_dim, int max_rows) {
+  return std::min(128 * (head_dim == 256 ? 1 : 2), max_rows);
+}
+int decode_tree_key_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
+
+cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
+  if (a.head_dim == 256) return launch_d<256>(a, ctx);
+  if (a.head_dim == 128) return launch_d<128>(a, ctx);
+  return launch_d<64>(a, ctx);
+}
+
+}  // namespace attn

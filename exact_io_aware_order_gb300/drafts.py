@@ -12,6 +12,7 @@ and the drafted tokens behind it)::
 
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional
 
@@ -22,6 +23,8 @@ from .api import (_BF16, _F32, _I32, _columns, _int32, _lens, _need, _need_all, 
                   _scope)
 
 _F64 = torch.float64
+_I64 = torch.int64
+TREE_OUT_BF16 = 1  # ATTN_TREE_OUT_BF16
 
 
 def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -227,3 +230,109 @@ def cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor
                                      float(magnitude), *geom, _raw_stream(dev.index))
     check("attn_cache_append", st)
     return q_out
+
+
+def tree_mask(parents: torch.Tensor, cu_nodes: torch.Tensor) -> torch.Tensor:
+    """The mask words of :func:`decode_tree` for trees: each node's ancestors and
+    itself.  parents: (total,) int32, a node's parent by its index within its sequence
+    (smaller than the node's), the root's -1; cu_nodes: (B + 1,) int32.  Returns
+    (total,) int64 on parents' device; of rows outside every sequence, 0."""
+    t = torch.arange(parents.shape[0], dtype=_I64, device=parents.device)
+    cu = cu_nodes.to(_I64)
+    seq = torch.searchsorted(cu[1:].contiguous(), t, right=True)
+    real = seq < cu.shape[0] - 1
+    first = cu[seq.clamp(max=cu.shape[0] - 2)]
+    i = (t - first).clamp(0, 63)
+    one = torch.ones_like(t)
+    word = torch.where(real, one << i, 0)
+    # The ancestor 1, 2, 4, ... generations up, itself for none.
+    up = torch.where(real & (parents >= 0), first + parents, -1)
+    for _ in range(6):
+        at = up.clamp(min=0)
+        word = torch.where(up >= 0, word | word[at], word)
+        up = torch.where(up >= 0, up[at], -1)
+    return word
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(batch: int, total: int, n_q: int, n_kv: int, d: int, max_kv_len: int,
+                    window_left: int, device: int) -> int:
+    """attn_decode_tree_workspace_bytes on a device (which has to be current)."""
+    return lib().attn_decode_tree_workspace_bytes(batch, total, n_q, n_kv, d, max_kv_len,
+                                                  window_left)
+
+
+def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                kv_lens: torch.Tensor, cu_nodes: torch.Tensor,
+                tree_mask: Optional[torch.Tensor] = None,
+                block_table: Optional[torch.Tensor] = None, max_kv_len: Optional[int] = None,
+                scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None, window_left: int = -1, softcap: float = 0.0,
+                alibi_slopes: Optional[torch.Tensor] = None,
+                out_dtype: torch.dtype = torch.float32):
+    """Attention of trees of drafted tokens over a bf16 cache (``attn_decode_tree``).
+
+    q: (total, n_q, d) bf16, sequence b's nodes (its last token, then the drafted ones, 64
+    at most) on rows [cu_nodes[b], cu_nodes[b + 1]).  The cache is that of
+    :func:`decode`; it holds the nodes' keys and values at slots kv_lens[b],
+    kv_lens[b] + 1, ... (:func:`cache_append`).  tree_mask: (total,) int64, bit j: the node
+    sees node j (:func:`tree_mask` makes it from parents), None: chains.  max_kv_len: the
+    most tokens and nodes of a sequence, a hint for paged caches.  Variants as
+    :func:`decode_splitkv`, a node at position kv_lens[b] + depth.  ``workspace``
+    (uint8, allocated when not given) holds partials.  Returns (O (total, n_q, d) fp32 or
+    bf16, LSE (total, n_q) fp32); rows outside every sequence are left as they were.
+    """
+    if not isinstance(q, torch.Tensor) or q.dtype is not _BF16 or q.dim() != 3 or \
+            not q.is_cuda or not q.is_contiguous():
+        _need(q, "q", _BF16, 3)
+    dev = q.device
+    total, n_q, d = q.shape
+    lens = _lens(kv_lens, "kv_lens", None, dev)
+    B = kv_lens.shape[0]
+    cu = _lens(cu_nodes, "cu_nodes", B + 1, dev)
+    ptrs, geom = _cache_bf16(dev, k_cache, v_cache, block_table, B)
+    n_kv = k_cache.shape[2]
+    if k_cache.shape[3] != d:
+        raise ValueError("the cache's head_dim does not match q")
+    if max_kv_len is not None:
+        max_kv_len = _int32(max_kv_len, "max_kv_len")
+        if block_table is not None:
+            geom = (*geom[:3], max_kv_len)
+        elif max_kv_len > geom[3]:
+            raise ValueError("max_kv_len exceeds the contiguous cache's length")
+    mask = al = None
+    if tree_mask is not None:
+        _need_all(dev, (tree_mask, "tree_mask", _I64, (total,)))
+        mask = tree_mask.data_ptr()
+    if alibi_slopes is not None:
+        _need_all(dev, (alibi_slopes, "alibi_slopes", _F32, (n_q,)))
+        al = alibi_slopes.data_ptr()
+    if out_dtype not in (_F32, _BF16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    window_left = _int32(window_left, "window_left")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((total, n_q, d), dtype=out_dtype, device=dev)
+        else:
+            _need_all(dev, (out, "out", out_dtype, (total, n_q, d)))
+        if lse is None:
+            lse = torch.empty((total, n_q), dtype=_F32, device=dev)
+        else:
+            _need_all(dev, (lse, "lse", _F32, (total, n_q)))
+        if workspace is None:
+            n = _tree_workspace(*_sizes(B, total, n_q, n_kv, d, geom[3]), window_left, dev.index)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        else:
+            _need(workspace, "workspace", torch.uint8, 1)
+            _need_all(dev, (workspace, "workspace", torch.uint8, workspace.shape))
+        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        st = lib().attn_decode_tree(q.data_ptr(), *ptrs, lens, cu, mask, wp, wn, out.data_ptr(),
+                                    lse.data_ptr(), *_sizes(B, total, n_q, n_kv, d), *geom,
+                                    float(scale), window_left, float(softcap), al,
+                                    TREE_OUT_BF16 if out_dtype is _BF16 else 0,
+                                    _raw_stream(dev.index))
+    check("attn_decode_tree", st)
+    return out, lse

@@ -835,6 +835,65 @@ int attn_cache_append(const attn_bf16* k, const attn_bf16* v, int64_t k_token_st
                       float magnitude, int block_size, int max_blocks_per_seq, int num_blocks,
                       int max_kv_len, void* stream);
 
+/* Bytes of workspace that attn_decode_tree needs on the current device (0 where it
+ * needs none, and for arguments out of range).  Launches nothing. */
+size_t attn_decode_tree_workspace_bytes(int batch, int total_nodes, int n_q_heads, int n_kv_heads,
+                                        int head_dim, int max_kv_len, int window_left);
+
+/*
+ * attn_decode_tree -- attention of a tree of drafted tokens over a cache.
+ *
+ * Page: same, section "Decode: a different bottleneck" (split-KV, GQA-aware
+ * key/value sharing, paged caches), for several query tokens a sequence.
+ *
+ *   q          : (total_nodes, n_q_heads, head_dim) bf16, 16-byte aligned: sequence b's
+ *                nodes are rows [cu_nodes[b], cu_nodes[b+1]), its last token (the
+ *                tree's root) first, then the drafted tokens
+ *   k_cache, v_cache, block_table, block_size, max_blocks_per_seq, num_blocks,
+ *   max_kv_len : the cache of attn_decode_splitkv (paged: max_kv_len is the largest
+ *                number of tokens and nodes together, a hint; a longer one is attended
+ *                in full all the same).  Node i's key and value lie at slot kv_lens[b] +
+ *                i (attn_cache_append puts them there).
+ *   kv_lens    : (batch,) int32 tokens in front of the nodes
+ *   cu_nodes   : (batch + 1,) int32, 0 = cu[0] <= cu[1] <= ... <= total_nodes; at most
+ *                64 nodes a sequence (none is allowed)
+ *   tree_mask  : (total_nodes,) int64: bit j of a node's word: it sees node j of its
+ *                sequence (bits past the nodes are ignored); 8-byte aligned.  Or NULL: a
+ *                chain, node i sees nodes 0 .. i.  Every node sees the kv_lens[b] tokens.
+ *   o          : (total_nodes, n_q_heads, head_dim) output, 16-byte aligned: fp32, or
+ *                bf16 with ATTN_TREE_OUT_BF16
+ *   lse        : (total_nodes, n_q_heads) fp32 output (natural log), 4-byte aligned
+ *   scale, window_left, softcap, alibi_slopes: as attn_decode_splitkv_ex, with token j
+ *                at position j and a node at position kv_lens[b] + depth, where its depth
+ *                is the number of nodes that it sees, less one (at least 0): the window
+ *                keeps keys whose position is at least the node's less window_left, ALiBi
+ *                adds -slope * (the node's position - the key's)
+ *   workspace  : attn_decode_tree_workspace_bytes of the same arguments, 16-byte aligned
+ *                (NULL where that is 0); overwritten.  Calls that may overlap on the
+ *                device need one each; less than needed is ATTN_ERR_SCRATCH.
+ *   flags      : 0 or ATTN_TREE_OUT_BF16; any other bit is ATTN_ERR_SHAPE
+ * A row that sees nothing (no cached token, no bit) has O = 0 and LSE = -inf.  With
+ * fp32 outputs the softmax weights enter the product with V in two bf16 parts (good to
+ * 2^-16 of each), with bf16 outputs in one (2^-8), as in attn_prefill; all else is fp32.  Keys that a
+ * node does not see may hold anything; values have to be finite unless no node of the
+ * sequence sees them and they lie behind its nodes or in front of every window.
+ * Rows outside every sequence are not written.  A cu_nodes that breaks its rule is clamped
+ * into it (more than 64 nodes: to the first 64) and flagged; a sequence with a negative
+ * kv_lens, or whose nodes do not fit the capacity, is flagged and its rows are O = 0 and
+ * LSE = -inf; a block-table entry outside [0, num_blocks) is flagged and its tokens are
+ * taken as zeros.  Results do not depend on timing: cut items are joined in order.
+ * Limits: those of attn_decode_splitkv; total_nodes <= 2^24; max_kv_len <= 2^30.
+ * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _GQA, _ALIGN, _SCRATCH, _ARCH, _LAUNCH.
+ */
+#define ATTN_TREE_OUT_BF16 1u
+int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                     const int32_t* block_table, const int32_t* kv_lens, const int32_t* cu_nodes,
+                     const int64_t* tree_mask, void* workspace, size_t workspace_bytes, void* o,
+                     float* lse, int batch, int total_nodes, int n_q_heads, int n_kv_heads,
+                     int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                     int max_kv_len, float scale, int window_left, float softcap,
+                     const float* alibi_slopes, unsigned flags, void* stream);
+
 /* Library version string, e.g. "0.1.0 sm_103a". */
 const char* attn_version(void);
 

@@ -39,3 +39,50 @@ def tree(n, seed, chain=False):
     """Parents of n nodes (the root's is -1)."""
     rng = random.Random(seed)
     return [-1] + [i - 1 if chain or rng.random() < 0.4 else rng.randrange(i) for i in range(1, n)]
+
+
+def words_of(parents):
+    """Mask words of a tree: each node's ancestors and itself."""
+    w = []
+    for i, j in enumerate(parents):
+        w.append((w[j] if j >= 0 else 0) | 1 << i)
+    return w
+
+
+def signed(words):
+    return [w - (1 << 64) if w >> 63 else w for w in words]
+
+
+def tree_attention(q, k, v, kv_len, words, scale, window=-1, softcap=0.0, slopes=None):
+    """One sequence in 64 bits: q (n, n_q, d), k, v (kv_len + n, n_kv, d), a mask word a
+    node.  Returns O (n, n_q, d), LSE (n, n_q) and, for bounds, A = sum p |v| like O, X the
+    largest sum of |q_i k_i| * scale, and Ab = sum p |bias| |v|."""
+    n, n_q, d = q.shape
+    n_kv, L = k.shape[1], k.shape[0]
+    g = n_q // n_kv
+    j = torch.arange(L)
+    bits = torch.tensor([[(w >> u) & 1 for u in range(n)] for w in words], dtype=torch.bool).view(n, n)
+    seen = torch.cat([torch.ones(n, kv_len, dtype=torch.bool), bits], dim=1)
+    depth = (bits.sum(dim=1) - 1).clamp(min=0)
+    kp = torch.cat([j[:kv_len], kv_len + depth])
+    dist = (kv_len + depth)[:, None] - kp[None]
+    if window >= 0:
+        seen &= dist <= window
+    Q, K, V = q.to(F64), k.to(F64).repeat_interleave(g, 1), v.to(F64).repeat_interleave(g, 1)
+    K = torch.where(seen.any(0)[:, None, None], K, 0.0)
+    V = torch.where(seen.any(0)[:, None, None], V, 0.0)
+    x = torch.einsum("nhd,lhd->nhl", Q, K) * scale
+    X = float(torch.einsum("nhd,lhd->nhl", Q.abs(), K.abs()).nan_to_num().max()) * scale if L else 0.0
+    if softcap > 0:
+        x = softcap * torch.tanh(x / softcap)
+    bias = torch.zeros(n, 1, L, dtype=F64)
+    if slopes is not None:
+        bias = slopes.to(F64)[None, :, None] * dist[:, None].to(F64)
+        x = x - bias
+    x = torch.where(seen[:, None], x, -torch.inf)
+    lse = torch.logsumexp(x, dim=2)
+    p = torch.where(seen[:, None], torch.exp(x - torch.where(lse == -torch.inf, 0.0, lse)[..., None]), 0.0)
+    o = torch.einsum("nhl,lhd->nhd", p, V)
+    A = torch.einsum("nhl,lhd->nhd", p, V.abs())
+    Ab = torch.einsum("nhl,lhd->nhd", p * bias.abs(), V.abs())
+    return o, lse, A, X, Ab

@@ -89,3 +89,55 @@ def test_append_accepts_what_is_documented(L, E):
         assert append(L, **{**kw, "k": P + 2}) == E["ALIGN"], kw
     assert append(L, n_q=0, q=None, qo=None, f=None) == E["NULL"]          # rot without frequencies
     assert append(L, f=None, rot=0) == E["NULL"]                           # queries without any
+
+
+def tree(L, **kw):
+    a = dict(q=P, kc=P, vc=P, bt=P, lens=P, cu=P, mask=P, ws=P, wn=1 << 40, o=P, lse=P, B=2, T=10,
+             n_q=8, n_kv=2, d=128, bs=16, mb=8, nb=16, mx=128, scale=0.1, w=-1, cap=0.0, al=None,
+             flags=0)
+    a.update(kw)
+    return L.attn_decode_tree(a["q"], a["kc"], a["vc"], a["bt"], a["lens"], a["cu"], a["mask"],
+                              a["ws"], a["wn"], a["o"], a["lse"], a["B"], a["T"], a["n_q"],
+                              a["n_kv"], a["d"], a["bs"], a["mb"], a["nb"], a["mx"], a["scale"],
+                              a["w"], a["cap"], a["al"], a["flags"], None)
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("NULL", dict(q=None)), ("NULL", dict(kc=None)), ("NULL", dict(vc=None)), ("NULL", dict(lens=None)),
+    ("NULL", dict(cu=None)), ("NULL", dict(o=None)), ("NULL", dict(lse=None)), ("SHAPE", dict(B=0)),
+    ("SHAPE", dict(B=65536)), ("SHAPE", dict(T=0)), ("SHAPE", dict(T=(1 << 24) + 1)),
+    ("SHAPE", dict(n_q=0)), ("SHAPE", dict(bs=0)), ("SHAPE", dict(mb=0)), ("SHAPE", dict(nb=0)),
+    ("SHAPE", dict(bs=1 << 16, mb=1 << 15)), ("SHAPE", dict(bt=None, mx=0)), ("SHAPE", dict(mx=-1)),
+    ("SHAPE", dict(bt=None, mx=(1 << 30) + 1)), ("SHAPE", dict(scale=float("nan"))),
+    ("SHAPE", dict(w=-2)), ("SHAPE", dict(cap=float("inf"))), ("SHAPE", dict(cap=1.0, al=P)),
+    ("SHAPE", dict(flags=2)), ("HEADDIM", dict(d=96)), ("GQA", dict(n_q=7)), ("GQA", dict(n_q=130)),
+    ("ALIGN", dict(q=P + 8)), ("ALIGN", dict(kc=P + 8)), ("ALIGN", dict(vc=P + 2)),
+    ("ALIGN", dict(bt=P + 2)), ("ALIGN", dict(lens=P + 2)), ("ALIGN", dict(cu=P + 2)),
+    ("ALIGN", dict(mask=P + 4)), ("ALIGN", dict(ws=P + 8)), ("ALIGN", dict(o=P + 8)),
+    ("ALIGN", dict(lse=P + 2)), ("ALIGN", dict(al=P + 2))])
+def test_tree_validation(L, E, name, kw):
+    assert tree(L, **kw) == E[name]
+
+
+def test_tree_workspace_of_refused_arguments(L):
+    f = L.attn_decode_tree_workspace_bytes
+    for args in ((0, 8, 8, 2, 128, 5000, -1), (1, 0, 8, 2, 128, 5000, -1), (1, 8, 7, 2, 128, 5000, -1),
+                 (1, 8, 130, 2, 128, 5000, -1), (1, 8, 8, 2, 96, 5000, -1), (1, 8, 8, 2, 128, -1, -1),
+                 (1, 8, 8, 2, 128, 5000, -2), (1, 8, 8, 0, 128, 5000, -1)):
+        assert f(*args) == 0
+
+
+def test_tree_masks():
+    """The words from parents, on the CPU: a chain of 64, trees, rows of no sequence."""
+    import torch
+
+    import exact_io_aware_order_gb300 as attn
+    from drafts_util import signed, tree as parents, words_of
+
+    ps = [parents(n, s, s == 1) for s, n in enumerate([1, 64, 7, 30, 64])]
+    cu = [0]
+    for p in ps:
+        cu.append(cu[-1] + len(p))
+    cu.insert(2, cu[2])                                     # an empty sequence
+    w = attn.tree_mask(torch.tensor(sum(ps, []) + [0, 5], dtype=torch.int32), torch.tensor(cu, dtype=torch.int32))
+    assert w.tolist() == signed(sum((words_of(p) for p in ps), [])) + [0, 0]
