@@ -35,5 +35,6 @@ from .drafts import (  # noqa: F401
     cache_append,
     tree_mask,
     decode_tree,
+    verify_tree,
 )
 from ._lib import AttnError, lib  # noqa: F401

@@ -73,6 +73,8 @@ SIGNATURES = {
     "attn_decode_tree_workspace_bytes": (c_size_t, [c_int] * 7),
     "attn_decode_tree": (c_int, [c_void_p] * 8 + [c_size_t] + [c_void_p] * 2 + [c_int] * 9
                          + [c_float, c_int, c_float, c_void_p, c_uint, c_void_p]),
+    "attn_verify_tree": (c_int, [c_void_p, c_int64] * 2 + [c_void_p] * 8 + [c_int] * 3
+                         + [c_void_p]),
     "attn_decode_noalloc": (c_int, [c_void_p] * 5 + [c_int] + [c_void_p] * 2 + [c_int] * 8
                             + [c_float, c_void_p]),
 }

@@ -797,6 +797,34 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
   return ATTN_OK;
 }
 
+int attn_verify_tree(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                     int64_t draft_stride, const int32_t* draft_tokens, const int32_t* parents,
+                     const int32_t* cu_nodes, const float* u_accept, const float* u_sample,
+                     int32_t* num_accepted, int32_t* path, int32_t* next_token, int batch,
+                     int total_nodes, int vocab, void* stream) {
+  if (!target_probs || !draft_tokens || !parents || !cu_nodes || !u_accept || !u_sample ||
+      !num_accepted || !path || !next_token)
+    return ATTN_ERR_NULL;
+  if (batch < 1 || batch > (1 << 20) || total_nodes < 1 || total_nodes > (1 << 24) || vocab < 1 ||
+      vocab > (1 << 30) || target_stride < vocab || target_stride > (1LL << 40) ||
+      (draft_probs && (draft_stride < vocab || draft_stride > (1LL << 40))))
+    return ATTN_ERR_SHAPE;
+  for (const void* x : {(const void*)target_probs, (const void*)draft_probs,
+                        (const void*)draft_tokens, (const void*)parents, (const void*)cu_nodes,
+                        (const void*)u_accept, (const void*)u_sample, (const void*)num_accepted,
+                        (const void*)path, (const void*)next_token})
+    if (!aligned(x, 4)) return ATTN_ERR_ALIGN;
+  int st = ATTN_OK;
+  DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  const attn::LaunchCtx ctx = make_ctx(stream, ds);
+  attn::VerifyArgs a{target_probs, draft_probs, target_stride, draft_stride, draft_tokens, parents,
+                     cu_nodes, u_accept, u_sample, num_accepted, path, next_token, batch,
+                     total_nodes, vocab, ctx.err_word};
+  if (attn::launch_verify(a, ctx) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
 namespace {
 
 // Checks of an 8-bit cache shared by its entry points.

@@ -243,6 +243,22 @@ struct DecodeTreeArgs {
   }
 };
 
+struct VerifyArgs {
+  const float* target_probs;  // row of node t at t * p_stride
+  const float* draft_probs;   // null: drafts that are certain
+  long long p_stride, q_stride;
+  const int32_t* tokens;      // (total_nodes,)
+  const int32_t* parents;     // (total_nodes,)
+  const int32_t* cu_nodes;    // (batch + 1,)
+  const float* u_accept;      // (total_nodes,)
+  const float* u_sample;      // (batch,)
+  int32_t* num_accepted;      // (batch,)
+  int32_t* path;              // (batch, 64)
+  int32_t* next_token;        // (batch,)
+  int batch, total_nodes, vocab;
+  uint32_t* err_word;
+};
+
 // Each returns cudaSuccess or the launch error.  Arguments are already
 // validated by the caller.
 cudaError_t launch_prefill(const PrefillArgs& a, const LaunchCtx& ctx);
@@ -268,6 +284,7 @@ cudaError_t launch_rope(const RopeArgs& a, const LaunchCtx& ctx);
 int decode_tree_part_rows(int head_dim, int max_rows);
 int decode_tree_key_tile(int head_dim);
 cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx);
+cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_cache_append(const RopeArgs& a, const LaunchCtx& ctx);
 
 // Resolves the current device's launch context (architecture check, error

@@ -1,0 +1,322 @@
+// Verification of drafted tokens against the target's probabilities, sm_103a.
+//
+// From the root on, the children of the node reached are tried in index order.  With
+// p and q the target's and the draft's probabilities there, w = p and Z = 1 at first,
+// a child with token x is accepted where u q(x) Z < w(x); where it is not, w becomes
+// max(w - q Z, 0) and Z its sum, and the next child is tried against those.  Where no
+// child is left, the next token is the smallest v with w(0) + .. + w(v) > u' sum(w).
+// A drafted token so accepted, or one so drawn, is distributed as the target's.
+// Without q (drafts that are certain) a refused child only loses its weight: w(x) = 0,
+// Z less that.
+//
+// All of it in whole multiples of 2^-60: sums and products of 64-bit integers are the
+// same in any order, so the drawn index is the same however the vocabulary is divided,
+// and two probabilities that differ are never taken for equal by rounding (an fp32
+// running sum over 128k entries moves a border by 1e-6, the size of many entries).
+// 64-bit integer additions are two instructions; fp64 ones would run at 1/64 rate.
+//
+// Work split: a cluster of blocks a sequence, the vocabulary in equal runs, a run a
+// warp.  The walk itself is scalar: one thread of the first block does it on numbers that
+// 64 threads gathered (a child's p and q do not depend on the walk), and asks the cluster
+// for a pass over the vocabulary only where it needs one: a sum after a refusal that has a
+// sibling behind it, and the last draw.  That thread decides for all blocks, so they meet
+// at the same barriers whatever the memory holds.
+// Bound by HBM for large batches (one row of p, and of q, a sequence), by the latency
+// of the gathers and the cluster's barriers for small ones.
+#include <algorithm>
+#include <cstdint>
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostNodes = 64;
+constexpr int kMostBlocks = 8;
+constexpr int kUnroll = 8;
+constexpr unsigned long long kOne = 1ull << 60;
+
+// Multiples of 2^-60 in x, rounded down; 0 for what is not in [0, 2).
+__device__ __forceinline__ unsigned long long fixed60(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const int e = (int)(b >> 23);                 // a set sign makes it 256 or more
+  if (e >= 128 || e < 67) return 0ull;          // (below 2^-60: 0)
+  const unsigned long long m = (b & 0x7fffffu) | 0x800000u;
+  const int s = e - 90;
+  return s >= 0 ? m << s : m >> -s;
+}
+// a b / 2^60, rounded down.
+__device__ __forceinline__ unsigned long long times60(unsigned long long a, unsigned long long b) {
+  return (__umul64hi(a, b) << 4) | ((a * b) >> 60);
+}
+
+enum Command : int { kEnd = 0, kSum = 1, kFind = 2 };
+
+// What the first block tells the others.
+struct Order {
+  int kind;
+  int node;       // whose rows (local index)
+  int levels;     // refusals so far (0 for the plain p)
+  int rank;       // kFind: the block that holds the border
+  unsigned long long rest;  // kFind: what of the drawn sum is left there
+};
+
+struct Shared {
+  Order order;
+  unsigned long long Z[kMostNodes];      // with q: Z at each level
+  int gone[kMostNodes];                  // without q: the refused tokens
+  unsigned long long totals[kMostBlocks];  // the blocks' sums (in the first block)
+  unsigned long long warp_sums[kWarps];
+  // gathered
+  int parent[kMostNodes], token[kMostNodes];
+  unsigned long long p[kMostNodes], q[kMostNodes], u[kMostNodes];
+};
+
+template <bool DRAFTS>
+__device__ __forceinline__ unsigned long long weight(float pv, float qv, int v, int levels,
+                                                     const unsigned long long* Z, const int* gone) {
+  unsigned long long w = fixed60(pv);
+  if constexpr (DRAFTS) {
+    if (levels > 0) {
+      const unsigned long long q = fixed60(qv);
+      for (int i = 0; i < levels; ++i) {
+        const unsigned long long qz = i == 0 ? q : times60(q, Z[i]);  // Z[0] is one
+        w = w > qz ? w - qz : 0ull;
+      }
+    }
+  } else {
+    for (int i = 0; i < levels; ++i)
+      if (gone[i] == v) w = 0ull;
+  }
+  return w;
+}
+
+template <bool DRAFTS>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int b = blockIdx.x / blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Shared* first = cluster.map_shared_rank(&sh, 0);
+  grid_dep_wait();
+
+  const int x0 = a.cu_nodes[b], x1 = a.cu_nodes[b + 1];
+  const int n0 = min(max(x0, 0), a.total_nodes), n1 = min(max(x1, n0), a.total_nodes);
+  const int n = min(n1 - n0, kMostNodes);
+  if (rank == 0) {
+    if (threadIdx.x == 0 &&
+        (x0 != n0 || x1 != n1 || n1 - n0 > kMostNodes || (b == 0 && x0 != 0)))
+      atomicOr(a.err_word, kErrSeqLens);
+    for (int i = threadIdx.x; i < kMostNodes; i += kThreads) {
+      a.path[(size_t)b * kMostNodes + i] = i == 0 && n > 0 ? 0 : -1;
+      int up = -1, tok = -1;
+      if (i < n) {
+        up = a.parents[n0 + i];
+        if (i == 0 ? up != -1 : (up < 0 || up >= i)) {
+          atomicOr(a.err_word, kErrSeqLens);
+          up = -1;
+        }
+      }
+      if (i > 0 && up >= 0) {
+        tok = a.tokens[n0 + i];
+        if (tok < 0 || tok >= a.vocab) {
+          atomicOr(a.err_word, kErrSeqLens);
+          up = -1;  // it cannot be accepted
+        } else {
+          const size_t at = (size_t)(n0 + up) * a.p_stride + tok;
+          sh.p[i] = fixed60(a.target_probs[at]);
+          if constexpr (DRAFTS) sh.q[i] = fixed60(a.draft_probs[(size_t)(n0 + up) * a.q_stride + tok]);
+          sh.u[i] = fixed60(a.u_accept[n0 + i]);
+        }
+      }
+      sh.parent[i] = up;
+      sh.token[i] = tok;
+    }
+    __syncthreads();
+  }
+
+  // The walk, in the first block's first thread: it stands at node `at`, `levels` of
+  // whose children were refused; `next` is the node to be looked at.
+  int at = 0, next = 1, levels = 0, count = 0;
+  unsigned long long Z = kOne;
+  bool have_z = true, drawing = false;
+  auto sum_of_totals = [&] {
+    unsigned long long t = 0ull;
+    for (int r = 0; r < blocks; ++r) t += sh.totals[r];
+    return t;
+  };
+  auto decide = [&]() -> Order {
+    if (n == 0) {
+      a.num_accepted[b] = 0;
+      a.next_token[b] = -1;
+      return Order{kEnd, 0, 0, 0, 0ull};
+    }
+    if (drawing) {  // the sums of the last draw are in
+      const unsigned long long total = sum_of_totals();
+      if (total == 0ull && levels > 0) {
+        levels = 0;  // nothing is left: the target's own probabilities
+        return Order{kSum, at, 0, 0, 0ull};
+      }
+      a.num_accepted[b] = count;
+      const unsigned long long T = times60(total, fixed60(a.u_sample[b]));
+      if (T >= total) {
+        a.next_token[b] = a.vocab - 1;
+        return Order{kEnd, 0, 0, 0, 0ull};
+      }
+      unsigned long long c = 0ull;
+      int r = 0;
+      while (r + 1 < blocks && c + sh.totals[r] <= T) c += sh.totals[r++];
+      return Order{kFind, at, levels, r, T - c};
+    }
+    if (!have_z) {  // back from a sum for a sibling
+      Z = sum_of_totals();
+      have_z = true;
+    }
+    for (; next < n; ++next) {
+      if (sh.parent[next] != at) continue;
+      if (!have_z) return Order{kSum, at, levels, 0, 0ull};
+      unsigned long long w = sh.p[next], qz = Z;
+      if constexpr (DRAFTS) {
+        for (int i = 0; i < levels; ++i) {
+          const unsigned long long y = times60(sh.q[next], sh.Z[i]);
+          w = w > y ? w - y : 0ull;
+        }
+        qz = times60(sh.q[next], Z);
+      } else {
+        for (int i = 0; i < levels; ++i)
+          if (sh.gone[i] == sh.token[next]) w = 0ull;
+      }
+      if (times60(qz, sh.u[next]) < w) {
+        at = next;
+        a.path[(size_t)b * kMostNodes + ++count] = at;
+        levels = 0;
+        Z = kOne;
+      } else if constexpr (DRAFTS) {
+        sh.Z[levels++] = Z;
+        have_z = false;
+      } else {
+        sh.gone[levels++] = sh.token[next];
+        Z = Z > w ? Z - w : 0ull;
+      }
+    }
+    drawing = true;
+    return Order{kSum, at, levels, 0, 0ull};
+  };
+  for (;;) {
+    if (rank == 0 && threadIdx.x == 0) sh.order = decide();
+    cluster.sync();
+    const Order o = first->order;
+    if (o.kind == kEnd) break;
+    // This warp's run of the vocabulary.
+    const int runs = blocks * kWarps, run = rank * kWarps + warp;
+    const int v0 = (int)((long long)a.vocab * run / runs);
+    const int v1 = (int)((long long)a.vocab * (run + 1) / runs);
+    const float* p = a.target_probs + (size_t)(n0 + o.node) * a.p_stride;
+    const float* q = DRAFTS ? a.draft_probs + (size_t)(n0 + o.node) * a.q_stride : nullptr;
+    if (rank != 0 && o.kind == kSum) {  // the levels, into this block's memory
+      for (int i = threadIdx.x; i < o.levels; i += kThreads) {
+        if constexpr (DRAFTS) sh.Z[i] = first->Z[i];
+        else sh.gone[i] = first->gone[i];
+      }
+      __syncthreads();
+    }
+    const bool use_q = DRAFTS && o.levels > 0;
+    if (o.kind == kSum) {
+      unsigned long long sum = 0ull;
+      for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
+        float x[kUnroll], y[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int i = v + 32 * k;
+          x[k] = i < v1 ? p[i] : 0.f;
+          y[k] = use_q && i < v1 ? q[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          sum += weight<DRAFTS>(x[k], y[k], v + 32 * k, o.levels, sh.Z, sh.gone);
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      if (lane == 0) sh.warp_sums[warp] = sum;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        unsigned long long t = 0ull;
+        for (int w = 0; w < kWarps; ++w) t += sh.warp_sums[w];
+        first->totals[rank] = t;
+      }
+      cluster.sync();
+    } else if (rank == o.rank) {  // kFind: the warp, then the entry
+      unsigned long long c = 0ull;
+      int w = 0;
+      while (w + 1 < kWarps && c + sh.warp_sums[w] <= o.rest) c += sh.warp_sums[w++];
+      if (warp == w) {
+        const unsigned long long T = o.rest - c;
+        unsigned long long base = 0ull;
+        bool found = false;
+        for (int v = v0; v < v1 && !found; v += 32 * kUnroll) {
+          float x[kUnroll], y[kUnroll];
+#pragma unroll
+          for (int k = 0; k < kUnroll; ++k) {
+            const int i = v + lane + 32 * k;
+            x[k] = i < v1 ? p[i] : 0.f;
+            y[k] = use_q && i < v1 ? q[i] : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < kUnroll; ++k) {
+            if (found) break;
+            const int i = v + lane + 32 * k;
+            unsigned long long s = weight<DRAFTS>(x[k], y[k], i, o.levels, sh.Z, sh.gone);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const unsigned long long up = __shfl_up_sync(0xffffffffu, s, d);
+              if (lane >= d) s += up;
+            }
+            const uint32_t over = __ballot_sync(0xffffffffu, base + s > T);
+            if (over != 0u) {
+              found = true;
+              if (lane == 0) a.next_token[b] = v + 32 * k + __ffs(over) - 1;
+            } else {
+              base += __shfl_sync(0xffffffffu, s, 31);
+            }
+          }
+        }
+        // (weights that changed between the two passes)
+        if (!found && lane == 0) a.next_token[b] = v1 - 1;
+      }
+    }
+    if (o.kind == kFind) break;
+  }
+  cluster.sync();  // nobody leaves while its memory may be read
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
+  // A cluster of 8 blocks from 8192 entries on.
+  const int blocks = a.vocab >= 8192 ? kMostBlocks : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.batch * (unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)blocks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return a.draft_probs ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a)
+                       : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a);
+}
+
+}  // namespace attn

@@ -336,3 +336,65 @@ def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                     _raw_stream(dev.index))
     check("attn_decode_tree", st)
     return out, lse
+
+
+def _probs(t, name: str, dev, total: int) -> tuple[int, int]:
+    """(total, vocab) fp32 probabilities on dev, entries of a row contiguous, rows apart;
+    the pointer and the rows' stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32:
+        raise TypeError(f"{name} must be a torch.float32 tensor")
+    if t.dim() != 2 or t.shape[0] != total:
+        raise ValueError(f"{name} must be ({total}, vocab), got shape {tuple(t.shape)}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if total > 1 else t.shape[1]
+
+
+def verify_tree(target_probs: torch.Tensor, draft_tokens: torch.Tensor, parents: torch.Tensor,
+                cu_nodes: torch.Tensor, u_accept: torch.Tensor, u_sample: torch.Tensor,
+                draft_probs: Optional[torch.Tensor] = None,
+                num_accepted: Optional[torch.Tensor] = None, path: Optional[torch.Tensor] = None,
+                next_token: Optional[torch.Tensor] = None, stream=None):
+    """Which drafted tokens stand, and the next token (``attn_verify_tree``).
+
+    target_probs: (total, vocab) fp32, the target's probabilities of the token after each
+    node; draft_probs: those that each node's children were drawn from, None: drafts that
+    are certain; draft_tokens, parents: (total,) int32; cu_nodes: (B + 1,) int32; u_accept:
+    (total,) and u_sample: (B,) fp32 random numbers in [0, 1).  Children of a node are
+    tried in index order.  Returns (num_accepted (B,), path (B, 64): the root and the accepted
+    nodes by index within the sequence, then -1; next_token (B,)), int32.
+
+    The accepted nodes' keys and values belong behind the cached tokens: with chains they
+    already lie there; of a tree, append rows path[b, :n + 1] again.
+    """
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
+        _need(target_probs, "target_probs", _F32, 2)
+    dev, (total, vocab) = target_probs.device, target_probs.shape
+    p, ps = _probs(target_probs, "target_probs", dev, total)
+    q, qs = (None, 0) if draft_probs is None else _probs(draft_probs, "draft_probs", dev, total)
+    if draft_probs is not None and draft_probs.shape[1] != vocab:
+        raise ValueError("draft_probs must have target_probs' vocabulary")
+    B = cu_nodes.shape[0] - 1 if isinstance(cu_nodes, torch.Tensor) and cu_nodes.dim() == 1 else 0
+    cu = _lens(cu_nodes, "cu_nodes", None, dev)
+    if B < 1:
+        raise ValueError("cu_nodes must have at least two entries")
+    _need_all(dev, (draft_tokens, "draft_tokens", _I32, (total,)), (parents, "parents", _I32, (total,)),
+              (u_accept, "u_accept", _F32, (total,)), (u_sample, "u_sample", _F32, (B,)))
+    with _scope(dev, stream):
+        if num_accepted is None:
+            num_accepted = torch.empty(B, dtype=_I32, device=dev)
+        if path is None:
+            path = torch.empty((B, 64), dtype=_I32, device=dev)
+        if next_token is None:
+            next_token = torch.empty(B, dtype=_I32, device=dev)
+        _need_all(dev, (num_accepted, "num_accepted", _I32, (B,)), (path, "path", _I32, (B, 64)),
+                  (next_token, "next_token", _I32, (B,)))
+        st = lib().attn_verify_tree(p, ps, q, qs, draft_tokens.data_ptr(), parents.data_ptr(), cu,
+                                    u_accept.data_ptr(), u_sample.data_ptr(),
+                                    num_accepted.data_ptr(), path.data_ptr(),
+                                    next_token.data_ptr(), *_sizes(B, total, vocab),
+                                    _raw_stream(dev.index))
+    check("attn_verify_tree", st)
+    return num_accepted, path, next_token

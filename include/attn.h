@@ -894,6 +894,49 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
                      int max_kv_len, float scale, int window_left, float softcap,
                      const float* alibi_slopes, unsigned flags, void* stream);
 
+/*
+ * attn_verify_tree -- which drafted tokens stand against the target's
+ * probabilities, and the next token, from given random numbers.
+ *
+ * Page: same, section "Decode: a different bottleneck" (a decode step costs the cache's
+ * bytes whatever it yields: drafted tokens make it yield several).
+ *
+ *   target_probs: (total_nodes, vocab) fp32, node t's row at t * target_stride (>= vocab):
+ *                the target's probabilities of the token after node t.  What is not in
+ *                [0, 2) counts as 0.
+ *   draft_probs: the same for the draft: row t is what the children of node t were drawn
+ *                from; or NULL: the drafted tokens are certain (the draft's most likely
+ *                ones, for example)
+ *   draft_tokens: (total_nodes,) int32 each node's token (a root's is not read)
+ *   parents    : (total_nodes,) int32 each node's parent, by its index within the
+ *                sequence, smaller than the node's own; the root's (node 0) is -1
+ *   cu_nodes   : as attn_decode_tree: sequence b's nodes, at most 64
+ *   u_accept   : (total_nodes,) fp32 in [0, 1), the number for each drafted node
+ *   u_sample   : (batch,) fp32 in [0, 1), the number for the next token
+ *   num_accepted: (batch,) int32 output: accepted drafted tokens (the root not counted)
+ *   path       : (batch, 64) int32 output: the root and the accepted nodes, by index
+ *                within the sequence, then -1
+ *   next_token : (batch,) int32 output
+ * At the node reached last (the root at first), with its rows p and q, w = p and Z = 1.
+ * Its children are tried in index order: one with token x is accepted, and becomes the
+ * node reached, if floor(u_accept * q(x) Z) < w(x); otherwise w = max(w - q Z, 0) and Z =
+ * sum w (without draft_probs: q(x) = 1, and a refusal sets w(x) = 0, Z = max(Z - w(x), 0)).
+ * With no child left, next_token is the smallest v with w(0) + .. + w(v) >
+ * floor(u_sample * sum w); where sum w is 0, w = p; where no v is, vocab - 1.
+ * All numbers are multiples of 2^-60: inputs and products are rounded down to them, sums
+ * are exact, so the outputs do not depend on any order.
+ * A sequence without nodes gets 0, -1s and -1.  A cu_nodes that breaks its rule is clamped
+ * into it and flagged; a parent that is not a smaller index, and a drafted token outside [0,
+ * vocab), are flagged, and that node is never accepted.
+ * Limits: batch <= 2^20; total_nodes <= 2^24; vocab <= 2^30.
+ * Errors: ATTN_ERR_NULL, _SHAPE, _ALIGN, _ARCH, _LAUNCH.
+ */
+int attn_verify_tree(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                     int64_t draft_stride, const int32_t* draft_tokens, const int32_t* parents,
+                     const int32_t* cu_nodes, const float* u_accept, const float* u_sample,
+                     int32_t* num_accepted, int32_t* path, int32_t* next_token, int batch,
+                     int total_nodes, int vocab, void* stream);
+
 /* Library version string, e.g. "0.1.0 sm_103a". */
 const char* attn_version(void);
 

@@ -141,3 +141,23 @@ def test_tree_masks():
     cu.insert(2, cu[2])                                     # an empty sequence
     w = attn.tree_mask(torch.tensor(sum(ps, []) + [0, 5], dtype=torch.int32), torch.tensor(cu, dtype=torch.int32))
     assert w.tolist() == signed(sum((words_of(p) for p in ps), [])) + [0, 0]
+
+
+def verify(L, **kw):
+    a = dict(p=P, ps=100, q=P, qs=100, tok=P, par=P, cu=P, u=P, ul=P, n=P, path=P, nt=P, B=2, T=10, V=100)
+    a.update(kw)
+    return L.attn_verify_tree(a["p"], a["ps"], a["q"], a["qs"], a["tok"], a["par"], a["cu"], a["u"],
+                              a["ul"], a["n"], a["path"], a["nt"], a["B"], a["T"], a["V"], None)
+
+
+@pytest.mark.parametrize("name,kw", [("NULL", {k: None}) for k in ("p", "tok", "par", "cu", "u", "ul", "n", "path", "nt")] + [
+    ("ALIGN", {k: P + 2}) for k in ("p", "q", "tok", "par", "cu", "u", "ul", "n", "path", "nt")] + [
+    ("SHAPE", dict(B=0)), ("SHAPE", dict(B=(1 << 20) + 1)), ("SHAPE", dict(T=0)), ("SHAPE", dict(T=(1 << 24) + 1)),
+    ("SHAPE", dict(V=0)), ("SHAPE", dict(V=(1 << 30) + 1, ps=1 << 31, qs=1 << 31)), ("SHAPE", dict(ps=99)),
+    ("SHAPE", dict(qs=99)), ("SHAPE", dict(ps=(1 << 40) + 1))])
+def test_verify_validation(L, E, name, kw):
+    assert verify(L, **kw) == E[name]
+
+
+def test_verify_without_drafts(L, E):
+    assert verify(L, q=None, qs=0, nt=P + 2) == E["ALIGN"]
