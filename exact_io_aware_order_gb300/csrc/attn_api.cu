@@ -720,8 +720,8 @@ struct TreePlan {
   size_t lse_offset, o_offset, bytes;
 };
 
-// Key tiles that a block takes whole at most, so that nothing has to be joined.
-constexpr int kTreeWholeTiles = 4;
+// Tokens of an item that a block takes whole at most, so that nothing has to be joined.
+constexpr long long kTreeWholeTokens = 512;
 
 TreePlan tree_plan(int total_nodes, int n_q_heads, int n_kv_heads, int head_dim, int batch,
                    int max_kv_len, int window_left, int num_sms) {
@@ -731,8 +731,7 @@ TreePlan tree_plan(int total_nodes, int n_q_heads, int n_kv_heads, int head_dim,
   t.blocks = std::max(num_sms, 1);
   long long keys = max_kv_len;
   if (window_left >= 0) keys = std::min(keys, window_left + 1LL + kMostNodes);
-  const int tile = attn::decode_tree_key_tile(head_dim);
-  t.whole = (keys + tile - 1) / tile <= kTreeWholeTiles;
+  t.whole = keys <= kTreeWholeTokens;
   if (t.whole) return t;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = 2 * (size_t)t.blocks * (size_t)t.part_rows;
@@ -776,6 +775,11 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
                                  head_dim, block_size, max_blocks_per_seq, num_blocks, max_kv_len,
                                  scale, false, window_left, softcap, alibi_slopes);
   if (st != ATTN_OK) return st;
+  // rows of the cache and of q are counted in 31 bits
+  const long long slots = block_table ? (long long)num_blocks * block_size
+                                      : (long long)batch * max_kv_len;
+  if (slots > 0x7fffffffLL || (long long)total_nodes * n_q_heads > 0x7fffffffLL)
+    return ATTN_ERR_SHAPE;
   if (!aligned(cu_nodes, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 16))
     return ATTN_ERR_ALIGN;
   DeviceState* ds = device_state(&st);

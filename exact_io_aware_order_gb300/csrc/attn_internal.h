@@ -280,9 +280,8 @@ cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 int decode_fp8_max_parts(int head_dim, int num_sms);
 
 cudaError_t launch_rope(const RopeArgs& a, const LaunchCtx& ctx);
-// Rows of a partial (max_rows: the most that a kv head can have), and a key tile's tokens.
+// Rows of a partial (max_rows: the most that a kv head can have).
 int decode_tree_part_rows(int head_dim, int max_rows);
-int decode_tree_key_tile(int head_dim);
 cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_cache_append(const RopeArgs& a, const LaunchCtx& ctx);

@@ -21,20 +21,22 @@
 //     kernel joins.  A block starts at most one cut item in its run and ends at most
 //     one, so there are two places a block.  Short caches (by max_kv_len) go whole
 //     items to a block, without the second kernel;
-//   * four producer warps copy 16 bytes a thread (cp.async) from wherever the block
-//     table says into the 128-byte-swizzled layout that the MMAs read: any block
-//     size, blocks that end inside a tile, rows past the end filled with zeros.  A
-//     tile is announced when its copies have landed, two or three tiles behind the
-//     newest, so that many are in flight;
+//   * two producer warps copy 16 bytes a lane (cp.async) from wherever the block table
+//     says into the 128-byte-swizzled layout that the MMAs read: any block size, blocks
+//     that end inside a tile, rows past the end filled with zeros.  The copies announce
+//     themselves on the slot's barrier, so the producers only wait for free slots; the
+//     issuing threads fence what they then read against the async proxy;
 //   * S = Q K^T and O += P V by two issuing threads, S in two TMEM buffers, P over
 //     S, one O a row tile; with two row tiles in an item they take turns, so the
 //     tensor cores work on one while the other is in the softmax;
-//   * the softmax is one row a thread, four warps a row tile, in two passes over S:
-//     the row maximum (after masks, soft-capping and ALiBi, which are written back),
-//     then the exponentials.  Reading S twice costs 2 x 32 clocks a warp and saves
-//     the registers that 14 warps do not have;
+//   * the softmax is one row a thread, four warps a row tile, in two passes over S: the
+//     row maximum, then the exponentials; two 32-column pieces are in registers at a
+//     time, and reading S twice costs 2 x 32 clocks a warp.  Masks (in tiles with nodes or a
+//     window's edge), soft-capping and ALiBi are a pass of their own in front, written back
+//     to S, which keeps the code of the ordinary tile small: the warps run six roles, and
+//     unrolled code that is run once a tile is fetched anew each time;
 //   * P is rounded to bf16 for a bf16 O (2^-8 of a weight, no more than O's own
-//     rounding), and split into two bf16 parts (2^-16) for an fp32 one;
+//     rounding), and split into three bf16 parts (2^-24) for an fp32 one;
 //   * row statistics, O and the partials are fp32; O is rescaled when a row's maximum
 //     has grown by more than 2^8 (exact: the same stale one is used for l and O);
 //   * every wait is bounded, as in the other kernels.
@@ -51,23 +53,30 @@ namespace attn {
 namespace {
 
 constexpr int kSoftmaxThreads = 128;   // of a row tile
-constexpr int kProducerThreads = 128;
+constexpr int kProducerThreads = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMostNodes = 64;
 
-// Row tiles of an item (TMEM: two S buffers of kBN columns and an O of D for each).
+// Row tiles of an item, keys of a tile, and the columns of an S buffer.  TMEM holds two S
+// buffers and an O of D columns a row tile: 2 x 128 + 2 x D, 2 x 64 + 256 at head_dim
+// 256, and with fp32 outputs 2 x 96 (three parts of P, 32 columns each) + 2 x D.
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
-template <int D> __host__ __device__ constexpr int key_tile() { return D == 256 ? 64 : 128; }
+template <int D, bool WIDE> __host__ __device__ constexpr int key_tile() {
+  return D == 256 || WIDE ? 64 : 128;
+}
+template <int D, bool WIDE> __host__ __device__ constexpr int s_pitch() {
+  return WIDE ? 96 : key_tile<D, WIDE>();
+}
 template <int D> __host__ __device__ constexpr int threads_of() {
   return row_tiles<D>() * kSoftmaxThreads + kProducerThreads + 64;
 }
 
-template <int D>
+template <int D, bool WIDE>
 struct TreeSmem {
-  static constexpr int kBN = key_tile<D>();
+  static constexpr int kBN = key_tile<D, WIDE>();
   static constexpr int kQTileBytes = 128 * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;
   static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
@@ -110,7 +119,7 @@ struct Seq {
   bool bad_nodes, bad_len;
 };
 
-template <int D>
+template <int BN>
 __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   const DecodeTreeArgs& a = p.a;
   Seq s;
@@ -125,7 +134,7 @@ __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   s.end = s.bad_len ? 0 : len + s.nodes;
   // Every node's position is kv_len or more: a window starts no earlier than this.
   s.lo = a.window_left >= 0 ? max(0, s.kv_len - a.window_left) : 0;
-  s.tiles = max(1, (s.end - s.lo + key_tile<D>() - 1) / key_tile<D>());
+  s.tiles = max(1, (s.end - s.lo + BN - 1) / BN);
   const int g = a.n_q_heads / a.n_kv_heads, rows = 128 * p.q_tiles;
   s.groups = (s.nodes * g + rows - 1) / rows;
   return s;
@@ -152,7 +161,7 @@ struct Seg {
   long long item_u0;           // the item's first unit
 };
 
-template <int D>
+template <int BN>
 struct Walk {
   const TreeKParams& p;
   long long u, u1, base;
@@ -160,7 +169,7 @@ struct Walk {
   Seq s;
   __device__ Walk(const TreeKParams& p_, const Share& sh)
       : p(p_), u(sh.u0), u1(sh.u1), base(sh.base0), b(sh.b0) {
-    if (u < u1) s = seq_of<D>(p, b);
+    if (u < u1) s = seq_of<BN>(p, b);
   }
   __device__ bool next(Seg& g) {
     if (u >= u1) return false;
@@ -168,7 +177,7 @@ struct Walk {
     while (u >= base + n) {
       if (b + 1 >= p.a.batch) return false;  // (lengths that changed under the call)
       base += n;
-      s = seq_of<D>(p, ++b);
+      s = seq_of<BN>(p, ++b);
       n = units_of(p, s);
     }
     const int T = p.a.whole ? 1 : s.tiles;
@@ -197,23 +206,50 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
                "r"(real ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_dyn(int n) {
-  switch (n) {
-    case 0: cp_async_wait<0>(); break;
-    case 1: cp_async_wait<1>(); break;
-    case 2: cp_async_wait<2>(); break;
-    case 3: cp_async_wait<3>(); break;
-    default: cp_async_wait<4>(); break;
+// The barrier receives this thread's arrival once all its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 rows of D values into a tile of 128-byte-swizzled spans (rows row0 ...): lane i's
+// `row` is the place of row i in units of `pitch` values behind `base`, -1 for zeros.
+template <int D>
+__device__ __forceinline__ void copy_rows(uint32_t tile, int chunk_bytes, int row0,
+                                          const uint16_t* base, long long pitch, int row,
+                                          int lane) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a row, rows at a time
+  const int c = lane % kLanes, r = lane / kLanes;
+  const uint32_t dst0 = tile + (c >> 3) * chunk_bytes;
+  base += c * 8;
+#pragma unroll 8
+  for (int i = 0; i < kLanes; ++i) {
+    const int k = i * kRows + r;
+    const int src = __shfl_sync(0xffffffffu, row, k);
+    const int at = row0 + k;
+    cp_async16_or_zero(dst0 + at * 128 + (((c & 7) ^ (at & 7)) << 4),
+                       base + max(src, 0) * pitch, src >= 0);
   }
+}
+
+// Ties registers that tcgen05.ld filled to the wait in front of it: what reads them stays
+// behind.
+__device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
 }
 
 // VAR: window, soft-capping or ALiBi.  WIDE: fp32 O, P in two bf16 parts.
 template <int D, bool VAR, bool WIDE>
 __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const TreeKParams p) {
-  using L = TreeSmem<D>;
-  constexpr int kBN = L::kBN, NQ = row_tiles<D>(), kThreads = threads_of<D>();
-  constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 4, kPVWarp = kSWarp + 1;
-  static_assert(2 * kBN + NQ * D <= (int)kTmemCols, "TMEM budget");
+  using L = TreeSmem<D, WIDE>;
+  constexpr int kBN = L::kBN, kPitch = s_pitch<D, WIDE>(), NQ = row_tiles<D>(), kThreads = threads_of<D>();
+  constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
+  static_assert(2 * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
   const DecodeTreeArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -265,7 +301,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
     long long mine = 0;
     bool bad_nodes = false, bad_len = false;
     for (int b = b0; b < b1; ++b) {
-      const Seq s = seq_of<D>(p, b);
+      const Seq s = seq_of<kBN>(p, b);
       mine += units_of(p, s);
       bad_nodes |= s.bad_nodes;
       bad_len |= s.bad_len;
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
     if (u0 < u1 && u0 >= at && u0 < at + mine) {
       int b = b0;
       for (; b + 1 < b1; ++b) {
-        const long long n = units_of(p, seq_of<D>(p, b));
+        const long long n = units_of(p, seq_of<kBN>(p, b));
         if (u0 < at + n) break;
         at += n;
       }
@@ -315,7 +351,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tO = tmem + 2 * kBN;
+  const uint32_t tO = tmem + 2 * kPitch;
   const WaitCtl ctl{abort_flag, p.err_word, p.timeout_ns};
   const Share sh = *share;
   const int g = a.n_q_heads / a.n_kv_heads;
@@ -328,95 +364,80 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
 
   if (warp >= kProducerWarp && warp < kSWarp) {
     // ============================ producers ============================
-    constexpr int kRowChunks = D / 8;                      // 16-byte pieces of a row
-    constexpr int kRowsPass = kProducerThreads / kRowChunks;
-    constexpr int kPasses = kBN / kRowsPass;               // rows of a tile a thread copies
-    const int tid = threadIdx.x - kProducerWarp * 32;
-    const int pc = tid % kRowChunks, pr = tid / kRowChunks;
-    // The swizzled place of this thread's piece of a row, in a tile of spans of chunk_bytes.
-    auto place = [&](int row, int chunk_bytes) {
-      return (uint32_t)((pc >> 3) * chunk_bytes + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
-    };
-    const int lag = slots - 2 < 4 ? slots - 2 : 4;         // tiles in flight behind the newest
-    int issued = 0, announced = 0, slot = 0, phase = 0, ann_slot = 0, n_seg = 0;
-    auto announce = [&](int left) {
-      cp_async_wait_dyn(left);
-      fence_proxy_async_smem();
-      while (issued - announced > left) {
-        mbar_arrive(bar(kFull + ann_slot));
-        if (++ann_slot == slots) ann_slot = 0;
-        ++announced;
-      }
-    };
-    Walk<D> walk(p, sh);
+    // Each warp copies half the rows of every tile.  A lane finds the place of its own rows
+    // (one look into the block table), the others get it by shuffles.
+    constexpr int kHalf = kBN / 2, kSets = kHalf / 32;     // rows of a warp, in sets of 32
+    const int half = warp - kProducerWarp;
+    int issued = 0, slot = 0, phase = 0, n_seg = 0;
+    Walk<kBN> walk(p, sh);
     Seg sg;
     bool ok = true;
     while (ok && walk.next(sg)) {
-      if (n_seg > 0) {
-        // The last segment's S products have to be through with Q, and need all their keys.
-        announce(0);
-        if (!mbar_wait(bar(kQEmpty), (n_seg - 1) & 1, ctl)) break;
-      }
+      // The last segment's S products have to be through with Q.
+      if (n_seg > 0 && !mbar_wait_warp(bar(kQEmpty), (n_seg - 1) & 1, ctl)) break;
       ++n_seg;
-      // Q: row i of the kv head is node i / g, head i % g; announced with the first keys.
-      for (int i = pr; i < 128 * sg.nr; i += kRowsPass) {
-        const int row = sg.row0 + i, node = row / g, h = row - node * g;
-        const bool real = i < sg.rows;
-        const uint16_t* src =
-            a.q + (real ? ((size_t)(sg.s.q0 + node) * a.n_q_heads + (size_t)sg.kvh * g + h) * D + pc * 8
-                        : 0);
-        const uint32_t dst = smem_u32(smem + (i >> 7) * L::kQTileBytes) +
-                             place(i & 127, L::kQChunkBytes);
-        cp_async16_or_zero(dst, src, real);
+      // Q: row i of the kv head is node i / g, head i % g; it counts as landed with the
+      // first keys, whose arrivals wait for all copies so far.
+      for (int set = half; set < 4 * sg.nr; set += 2) {
+        const int i = set * 32 + lane, row = sg.row0 + i, node = row / g;
+        const int src = i < sg.rows ? (sg.s.q0 + node) * a.n_q_heads + sg.kvh * g + (row - node * g) : -1;
+        copy_rows<D>(smem_u32(smem + (set >> 2) * L::kQTileBytes), L::kQChunkBytes, (set & 3) * 32,
+                     a.q, D, src, lane);
       }
       const int32_t* table =
           a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
       for (int t = 0; t < sg.tiles && ok; ++t) {
-        const int tok0 = sg.s.lo + (sg.t0 + t) * kBN;
-        // Cache rows (a token of all kv heads) of this thread's rows; -1: none.
-        long long row[kPasses];
+        const int tok0 = sg.s.lo + (sg.t0 + t) * kBN + half * kHalf + lane;
+        int row[kSets];  // cache rows (a token of all kv heads); -1: none
+        int blk[kSets];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int tok = tok0 + pr + i * kRowsPass;
+        for (int i = 0; i < kSets; ++i) {
+          const int tok = tok0 + i * 32;
+          const bool real = tok < sg.s.end;
           row[i] = -1;
-          if (tok < sg.s.end) {
-            if (table == nullptr) {
-              row[i] = (long long)sg.b * a.max_kv_len + tok;
-            } else {
-              const int blk = table[tok / a.block_size];
-              if (blk >= 0 && blk < a.num_blocks)
-                row[i] = (long long)blk * a.block_size + tok % a.block_size;
-              else if (pc == 0)
-                atomicOr(p.err_word, kErrBlockIndex);
+          blk[i] = 0;
+          if (table == nullptr) {
+            if (real) row[i] = sg.b * a.max_kv_len + tok;
+          } else if (real) {
+            const int j = tok / a.block_size;
+            blk[i] = table[j];
+            row[i] = tok - j * a.block_size;
+          }
+        }
+        if (table != nullptr) {
+#pragma unroll
+          for (int i = 0; i < kSets; ++i) {
+            if (row[i] >= 0) {
+              const bool good = blk[i] >= 0 && blk[i] < a.num_blocks;
+              if (!good) atomicOr(p.err_word, kErrBlockIndex);
+              row[i] = good ? blk[i] * a.block_size + row[i] : -1;
             }
           }
         }
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          if (issued >= slots && !mbar_wait(bar(kEmpty + slot), phase ^ 1, ctl)) {
+          if (issued >= slots && !mbar_wait_warp(bar(kEmpty + slot), phase ^ 1, ctl)) {
             ok = false;
             break;
           }
-          const uint16_t* base = (kv ? a.v_cache : a.k_cache) + (size_t)sg.kvh * D + pc * 8;
-          const uint32_t dst0 = smem_u32(ring + slot * L::kTileBytes);
+          const uint32_t tile = smem_u32(ring + slot * L::kTileBytes);
 #pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const bool real = row[i] >= 0;
-            cp_async16_or_zero(dst0 + place(pr + i * kRowsPass, L::kChunkBytes),
-                               base + (real ? row[i] : 0) * (long long)a.n_kv_heads * D, real);
-          }
-          cp_async_commit();
+          for (int i = 0; i < kSets; ++i)
+            copy_rows<D>(tile, L::kChunkBytes, half * kHalf + i * 32,
+                         (kv ? a.v_cache : a.k_cache) + (size_t)sg.kvh * D,
+                         (long long)a.n_kv_heads * D, row[i], lane);
+          cp_async_arrive(bar(kFull + slot));
           ++issued;
           if (++slot == slots) slot = 0, phase ^= 1;
-          if (issued - announced > lag) announce(lag);
         }
       }
     }
-    announce(0);
+    cp_async_commit();
+    cp_async_wait<0>();
   } else if (warp == kSWarp) {
     // ============================ S = Q K^T issuer ============================
     if (lane == 0) {
-      Walk<D> walk(p, sh);
+      Walk<kBN> walk(p, sh);
       Seg sg;
       bool ok = true;
       int n = 0, slot = 0, phase = 0;
@@ -424,13 +445,14 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
       while (ok && walk.next(sg)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
+          fence_proxy_async_smem();  // the copies' writes, before the MMAs that read them
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n & 1;
             // Buffer b last held P(n - 2).
             if (n >= 2 && !mbar_wait(bar(kPVDone + b), ((n >> 1) - 1) & 1, ctl)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t dS = tmem + b * kBN;
+            const uint32_t dS = tmem + b * kPitch;
             const uint32_t q_lo = q_lo0 + (uint32_t)((r * L::kQTileBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -456,22 +478,23 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
   } else if (warp == kPVWarp) {
     // ============================ O += P V issuer ============================
     if (lane == 0) {
-      Walk<D> walk(p, sh);
+      Walk<kBN> walk(p, sh);
       Seg sg;
       bool ok = true;
       int n = 0, slot = 1, phase = 0;
       while (ok && walk.next(sg)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
+          fence_proxy_async_smem();  // the copies' writes, before the MMAs that read them
           const uint32_t v_lo =
               sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n & 1;
             if (!mbar_wait(bar(kPFull + b), (n >> 1) & 1, ctl)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t aP = tmem + b * kBN, tOr = tO + r * D;
+            const uint32_t aP = tmem + b * kPitch, tOr = tO + r * D;
 #pragma unroll
-            for (int part = 0; part < (WIDE ? 2 : 1); ++part)
+            for (int part = 0; part < (WIDE ? 3 : 1); ++part)
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk)
                 mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
@@ -496,7 +519,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int trow = (warp & 3) * 32 + lane;                // row within the tile (TMEM lane)
     int* depths = depth_tab + warp * kMostNodes;            // the nodes' depths, each warp its own
-    Walk<D> walk(p, sh);
+    Walk<kBN> walk(p, sh);
     Seg sg;
     bool ok = true;
     int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
@@ -556,56 +579,81 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
         if (!mbar_wait_warp(bar(kSFull + 2 * r + b), (s_phase >> b) & 1u, ctl)) { ok = false; break; }
         s_phase ^= 1u << b;
         tc_fence_after();
-        const uint32_t tS = tmem + b * kBN + lane_base;
-        // ---- pass 1: masks and variants, the row's maximum ----
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c2 = 0; c2 < kBN / 64; ++c2) {
-          uint32_t x[2][32];
-          tmem_ld32(tS + c2 * 64, x[0]);
-          tmem_ld32(tS + c2 * 64 + 32, x[1]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 2 * c2 + h;
+        const uint32_t tS = tmem + b * kPitch + lane_base;
+        // ---- masks and variants, written back ----
+        if (VAR || edge) {
+#pragma unroll 1
+          for (int c = 0; c < kBN / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(tS + c * 32, x);
+            tmem_wait_ld();
             if constexpr (VAR) {
               if (a.softcap > 0.f) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                  x[h][k] = __float_as_uint(p.cap_l2 * tanhf(__uint_as_float(x[h][k]) * p.cap_in));
+                  x[k] = __float_as_uint(p.cap_l2 * tanhf(__uint_as_float(x[k]) * p.cap_in));
               } else {
                 const float d0 = (float)(pos - kv0 - 32 * c);
                 const int u0 = kv0 + 32 * c - sg.s.kv_len;  // node of the chunk's first column
+                if (u0 + 31 < 0) {
+                  const float far = -slope_l2 * d0;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  float dist = d0 - (float)k;
-                  if (u0 + k >= 0) dist = (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
-                  // (slope 0 without ALiBi)
-                  x[h][k] = __float_as_uint(
-                      fmaf(__uint_as_float(x[h][k]), p.sl2, slope_l2 == 0.f ? 0.f : -slope_l2 * dist));
+                  for (int k = 0; k < 32; ++k)
+                    x[k] = __float_as_uint(
+                        fmaf(__uint_as_float(x[k]), p.sl2, fmaf(slope_l2, (float)k, far)));
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) {
+                    const float dist = u0 + k < 0 ? d0 - (float)k
+                                                  : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
+                    x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.sl2, -slope_l2 * dist));
+                  }
                 }
               }
             }
             if (edge) {
+              uint32_t w = vis[0];
+#pragma unroll
+              for (int q = 1; q < kBN / 32; ++q)
+                if (c == q) w = vis[q];
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((vis[c] >> k) & 1u)) x[h][k] = 0xff800000u;  // -inf
+                if (!((w >> k) & 1u)) x[k] = 0xff800000u;  // -inf
             }
-            float mc[4];
+            tmem_st32(tS + c * 32, x);
+          }
+          tmem_wait_st();
+        }
+        // ---- pass 1: the row's maximum ----
+        uint32_t x[2][32];
+        float mx = -INFINITY;
+        tmem_ld32(tS, x[0]);
+        tmem_ld32(tS + 32, x[1]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mc[k] = __uint_as_float(x[h][k]);
+        for (int c = 0; c < kBN / 32; ++c) {
+          if ((c & 1) == 0) {
+            tmem_wait_ld();
+            landed(x[0]);
+            landed(x[1]);
+          }
+          const uint32_t (&y)[32] = x[c & 1];
+          float mc[4];
 #pragma unroll
-            for (int k = 4; k < 28; k += 8)
+          for (int q = 0; q < 4; ++q)
+            mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mc[q] = fmax3(mc[q], __uint_as_float(x[h][k + q]), __uint_as_float(x[h][k + q + 4]));
+          for (int k = 8; k < 32; k += 8)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) mc[q] = fmaxf(mc[q], __uint_as_float(x[h][28 + q]));
-            mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-            if (VAR || edge) tmem_st32(tS + c * 32, x[h]);
+            for (int q = 0; q < 4; ++q)
+              mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
+          mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+          if (kBN > 64 && (c & 1)) {
+            // The next two; after the last ones, the first two for the second pass.
+            const int nc = c + 1 < kBN / 32 ? c + 1 : 0;
+            tmem_ld32(tS + nc * 32, x[0]);
+            tmem_ld32(tS + nc * 32 + 32, x[1]);
           }
         }
-        if (VAR || edge) tmem_wait_st();
         // ---- the reference: raised only when some row of the warp gained 2^8 ----
         const float m_new = fmaxf(m, mx * sl2);
         float corr = 1.f;
@@ -618,35 +666,41 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
           rescale_o = true;
         }
         const float nm = m == -INFINITY ? 0.f : -m;
-        // ---- pass 2: P over S ----
+        // ---- pass 2: P over S (what it overwrites has been read) ----
         const float2 sl2v = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t lo[WIDE ? kBN / 32 : 1][WIDE ? 16 : 1];
 #pragma unroll
         for (int c = 0; c < kBN / 32; ++c) {
-          uint32_t x[32], hi[16];
-          tmem_ld32(tS + c * 32, x);
-          tmem_wait_ld();
+          if (kBN > 64 && (c & 1) == 0) {
+            tmem_wait_ld();
+            landed(x[0]);
+            landed(x[1]);
+          }
+          const uint32_t (&y)[32] = x[c & 1];
+          uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float2 e = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
+            const float2 e = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])),
                                   sl2v, nmv);
-            const float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             rs[k & 1] = add2(rs[k & 1], pp);
             hi[k] = pack_bf16x2(pp.x, pp.y);
-            if constexpr (WIDE)
-              lo[c][k] = pack_bf16x2(pp.x - __uint_as_float(hi[k] << 16),
-                                  pp.y - __uint_as_float(hi[k] & 0xffff0000u));
+            if constexpr (WIDE) {
+              pp.x -= __uint_as_float(hi[k] << 16);
+              pp.y -= __uint_as_float(hi[k] & 0xffff0000u);
+              mid[k] = pack_bf16x2(pp.x, pp.y);
+              lo[k] = pack_bf16x2(pp.x - __uint_as_float(mid[k] << 16),
+                                  pp.y - __uint_as_float(mid[k] & 0xffff0000u));
+            }
           }
           tmem_st16(tS + c * 16, hi);
           if constexpr (WIDE) {
-            // The low parts go over the second half of S, each as soon as the columns that
-            // it overwrites have been read.
-#pragma unroll
-            for (int q = 0; q < kBN / 32; ++q) {
-              const int end = kBN / 2 + 16 * (q + 1);
-              if (end <= 32 * (c + 1) && end > 32 * c) tmem_st16(tS + end - 16, lo[q]);
-            }
+            tmem_st16(tS + kBN / 2 + c * 16, mid);
+            tmem_st16(tS + kBN + c * 16, lo);
+          }
+          if (kBN > 64 && c == 1) {
+            tmem_ld32(tS + 64, x[0]);
+            tmem_ld32(tS + 96, x[1]);
           }
         }
         const float2 rsum = add2(rs[0], rs[1]);
@@ -714,7 +768,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(const T
   // ---- what the second kernel joins: the item that ends here and began before ----
   if (!a.whole && threadIdx.x == 0) {
     TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
-    Walk<D> walk(p, sh);
+    Walk<kBN> walk(p, sh);
     Seg sg;
     if (walk.next(sg) && !sg.first && sg.last) {
       // The block that holds unit u is the last c with c total / G <= u.
@@ -801,7 +855,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Decode
 
 template <int D, bool VAR, bool WIDE>
 cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
-  using L = TreeSmem<D>;
+  using L = TreeSmem<D, WIDE>;
   TreeKParams p;
   p.a = a;
   const int g = a.n_q_heads / a.n_kv_heads;
@@ -852,7 +906,6 @@ cudaError_t launch_d(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
 int decode_tree_part_rows(int head_dim, int max_rows) {
   return std::min(128 * (head_dim == 256 ? 1 : 2), max_rows);
 }
-int decode_tree_key_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
 
 cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   if (a.head_dim == 256) return launch_d<256>(a, ctx);

@@ -873,8 +873,8 @@ size_t attn_decode_tree_workspace_bytes(int batch, int total_nodes, int n_q_head
  *                device need one each; less than needed is ATTN_ERR_SCRATCH.
  *   flags      : 0 or ATTN_TREE_OUT_BF16; any other bit is ATTN_ERR_SHAPE
  * A row that sees nothing (no cached token, no bit) has O = 0 and LSE = -inf.  With
- * fp32 outputs the softmax weights enter the product with V in two bf16 parts (good to
- * 2^-16 of each), with bf16 outputs in one (2^-8), as in attn_prefill; all else is fp32.  Keys that a
+ * fp32 outputs the softmax weights enter the product with V in three bf16 parts (good to
+ * 2^-24 of each), with bf16 outputs in one (2^-8), as in attn_prefill; all else is fp32.  Keys that a
  * node does not see may hold anything; values have to be finite unless no node of the
  * sequence sees them and they lie behind its nodes or in front of every window.
  * Rows outside every sequence are not written.  A cu_nodes that breaks its rule is clamped
@@ -882,7 +882,8 @@ size_t attn_decode_tree_workspace_bytes(int batch, int total_nodes, int n_q_head
  * kv_lens, or whose nodes do not fit the capacity, is flagged and its rows are O = 0 and
  * LSE = -inf; a block-table entry outside [0, num_blocks) is flagged and its tokens are
  * taken as zeros.  Results do not depend on timing: cut items are joined in order.
- * Limits: those of attn_decode_splitkv; total_nodes <= 2^24; max_kv_len <= 2^30.
+ * Limits: those of attn_decode_splitkv; total_nodes <= 2^24; max_kv_len <= 2^30; the cache's
+ *   slots (num_blocks * block_size, batch * max_kv_len) and total_nodes * n_q_heads < 2^31.
  * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _GQA, _ALIGN, _SCRATCH, _ARCH, _LAUNCH.
  */
 #define ATTN_TREE_OUT_BF16 1u
