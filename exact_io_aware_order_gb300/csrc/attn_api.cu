@@ -728,7 +728,7 @@ TreePlan tree_plan(int total_nodes, int n_q_heads, int n_kv_heads, int head_dim,
   TreePlan t{};
   const int g = n_q_heads / n_kv_heads;
   t.part_rows = attn::decode_tree_part_rows(head_dim, std::min(total_nodes, kMostNodes) * g);
-  t.blocks = std::max(num_sms, 1);
+  t.blocks = std::min(std::max(num_sms, 1), 256);  // (what the join counts through)
   long long keys = max_kv_len;
   if (window_left >= 0) keys = std::min(keys, window_left + 1LL + kMostNodes);
   t.whole = keys <= kTreeWholeTokens;

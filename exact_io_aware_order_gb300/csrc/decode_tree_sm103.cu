@@ -33,11 +33,13 @@
 //     S, one O a row tile; with two row tiles in an item they take turns, so the
 //     tensor cores work on one while the other is in the softmax;
 //   * the softmax is one row a thread, four warps a row tile, in two passes over S: the
-//     row maximum, then the exponentials; two 32-column pieces are in registers at a
-//     time, and reading S twice costs 2 x 32 clocks a warp.  Masks (in tiles with nodes or a
-//     window's edge), soft-capping and ALiBi are a pass of their own in front, written back
-//     to S, which keeps the code of the ordinary tile small: the warps run six roles, and
-//     unrolled code that is run once a tile is fetched anew each time;
+//     row maximum, then the exponentials (tiles of 64 keys stay in registers in between);
+//     two 32-column pieces are in registers at a time, and reading S twice costs 2 x 32
+//     clocks a warp.  ALiBi is a term of the argument, linear in the column, in both passes;
+//     masks (in tiles with nodes or a window's edge) and soft-capping are written back to S
+//     in a pass of their own, which keeps the code of the ordinary tile small: the
+//     warps run six roles, and unrolled code that is run once a tile is fetched anew each
+//     time.  P is announced in halves, so that its product begins under the second;
 //   * P is rounded to bf16 for a bf16 O (2^-8 of a weight, no more than O's own
 //     rounding), and split into three bf16 parts (2^-24) for an fp32 one;
 //   * row statistics, O and the partials are fp32; O is rescaled when a row's maximum
@@ -88,10 +90,10 @@ struct TreeSmem {
   static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
   static constexpr int kChunkBytes = kBN * 128;
   static constexpr int kMaxSlots = 8;
-  // barriers: full / empty for each slot, q_empty, s_full[row tile][2], p_full[2],
+  // barriers: full / empty for each slot, q_empty, s_full[row tile][2], p_full[half][2],
   // pv_done[2], o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item
   // of fewer rows would otherwise miss phases, and take an old one for its next.
-  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 4 + 2 + 2 + 2 + 2;
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 4 + 4 + 2 + 2 + 2;
   static constexpr int kMiscBytes = 1024;  // barriers, then the block's share of the work
   static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
   // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
@@ -265,8 +267,44 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// VAR: window, soft-capping or ALiBi.  WIDE: fp32 O, P in two bf16 parts.
-template <int D, bool VAR, bool WIDE>
+// VAR: what happens to a score besides scale and window.  WIDE: fp32 O, P in three parts.
+enum Variant : int { kPlain = 0, kCap = 1, kAlibi = 2 };
+
+// softcap tanh(s scale / softcap) of 32 scores, in log2 units.  Up to 0.45 tanh(u) / u is
+// 1 - t/3 + 2 t^2/15 - ... in t = u^2 (its Taylor series; the first term left out is
+// 1.5e-3 t^7, 2e-8 there), six packed FMAs for two scores; a warp with a larger |u| takes
+// tanhf for all of them.  ex2.approx and rcp.approx would be as fast, but their 2e-7 is an
+// absolute error of tanh, 1e-5 of a score at softcap 50.
+__device__ __forceinline__ void soft_cap(uint32_t (&x)[32], float in, float out) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+    top = fmax3(top, fabsf(__uint_as_float(x[k])), fabsf(__uint_as_float(x[k + 1])));
+  if (__all_sync(0xffffffffu, top * in <= 0.45f)) {
+    const float2 in2 = make_float2(in, in), out2 = make_float2(out, out);
+    auto two = [](float c) { return make_float2(c, c); };
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const float2 u = mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), in2);
+      const float2 t = mul2(u, u);
+      float2 y = fma2(t, two(21844.f / 6081075.f), two(-1382.f / 155925.f));
+      y = fma2(t, y, two(62.f / 2835.f));
+      y = fma2(t, y, two(-17.f / 315.f));
+      y = fma2(t, y, two(2.f / 15.f));
+      y = fma2(t, y, two(-1.f / 3.f));
+      const float2 v = mul2(u, out2);
+      y = fma2(mul2(t, y), v, v);
+      x[k] = __float_as_uint(y.x);
+      x[k + 1] = __float_as_uint(y.y);
+    }
+  } else {  // (NaN too)
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      x[k] = __float_as_uint(out * tanhf(__uint_as_float(x[k]) * in));
+  }
+}
+
+template <int D, int VAR, bool WIDE>
 __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ TreeKParams p) {
@@ -285,7 +323,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
-                kPFull = kSFull + 4, kPVDone = kPFull + 2, kOFull = kPVDone + 2,
+                kPFull = kSFull + 4, kPVDone = kPFull + 4, kOFull = kPVDone + 2,
                 kDrain = kOFull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
@@ -305,6 +343,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kSFull + 2 + i), 1);
       mbar_init(bar(kPFull + i), kSoftmaxThreads);
+      mbar_init(bar(kPFull + 2 + i), kSoftmaxThreads);
       mbar_init(bar(kPVDone + i), 1);
       mbar_init(bar(kOFull + i), 1);
       mbar_init(bar(kDrain + i), 1);
@@ -384,6 +423,11 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   const Share sh = *share;
   const int g = a.n_q_heads / a.n_kv_heads;
 
+  // Whether a key tile is filled by tiled copies: all of its keys exist.
+  auto tiled = [&](const Seg& sg, int t) {
+    const int tile0 = sg.s.lo + (sg.t0 + t) * kBN;
+    return p.box > 0 && tile0 >= sg.s.first && tile0 + kBN <= sg.s.end;
+  };
   // Roles walk the same segments; S products count over all of them (n: buffer n & 1),
   // and so do the ring's tiles (K and V of key tile j: 2 j and 2 j + 1).
   const uint32_t id_s = idesc_bf16_f32(128, kBN, false, false);
@@ -416,9 +460,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
       for (int t = 0; t < sg.tiles && ok; ++t) {
         const int tile0 = sg.s.lo + (sg.t0 + t) * kBN, tok0 = tile0 + half * kHalf;
-        if (p.box > 0 && tile0 >= sg.s.first && tile0 + kBN <= sg.s.end) {
-          // A tile of keys that all exist: tiled copies, a box and span a lane.  A bad block
-          // becomes one past the cache, which reads as zeros.
+        if (tiled(sg, t)) {
+          // A box and span a lane.  A bad block becomes one past the cache, which reads as
+          // zeros.
           constexpr int kSpans = D / 64;
           const int i = lane / kSpans, span = lane % kSpans;
           const bool mine = i * p.box < kHalf;
@@ -508,7 +552,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       while (ok && walk.next(sg)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
-          fence_proxy_async_smem();  // the copies' writes, before the MMAs that read them
+          // The 16-byte copies' writes (Q's among them), before the MMAs that read them.
+          if (t == 0 || !tiled(sg, t)) fence_proxy_async_smem();
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n & 1;
@@ -548,20 +593,26 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       while (ok && walk.next(sg)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
-          fence_proxy_async_smem();  // the copies' writes, before the MMAs that read them
+          // The 16-byte copies' writes (Q's among them), before the MMAs that read them.
+          if (t == 0 || !tiled(sg, t)) fence_proxy_async_smem();
           const uint32_t v_lo =
               sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n & 1;
-            if (!mbar_wait(bar(kPFull + b), (n >> 1) & 1, ctl)) { ok = false; break; }
-            tc_fence_after();
+            // P comes in halves of 64 keys.
             const uint32_t aP = tmem + b * kPitch, tOr = tO + r * D;
 #pragma unroll
-            for (int part = 0; part < (WIDE ? 3 : 1); ++part)
+            for (int h = 0; h < kBN / 64; ++h) {
+              if (!mbar_wait(bar(kPFull + 2 * h + b), (n >> 1) & 1, ctl)) { ok = false; break; }
+              tc_fence_after();
 #pragma unroll
-              for (int kk = 0; kk < kBN / 16; ++kk)
-                mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
-                          id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
+              for (int part = 0; part < (WIDE ? 3 : 1); ++part)
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                  mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
+                            id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
+            }
+            if (!ok) break;
             mma_commit(bar(kPVDone + b));
             if (t == sg.tiles - 1) mma_commit(bar(kOFull + r));
           }
@@ -603,32 +654,31 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       };
       unsigned long long word = real ? word_of(node) : 0ull;
       if (sg.s.end == 0) word = 0ull;                       // a length that was refused
-      int depth = 0;
+      const int depth = max(__popcll(word) - 1, 0);
       float slope_l2 = 0.f;
-      if constexpr (VAR) {
-        depth = max(__popcll(word) - 1, 0);
+      const bool near = a.window_left >= 0 && a.window_left < kMostNodes;
+      if (near || VAR == kAlibi) {
         __syncwarp();                                       // the last segment's readers
         for (int u = lane; u < sg.s.nodes; u += 32) depths[u] = max(__popcll(word_of(u)) - 1, 0);
         __syncwarp();
-        if (a.window_left >= 0 && a.window_left < kMostNodes)
+        if (near)
           for (int u = 0; u < sg.s.nodes; ++u)
             if (depth - depths[u] > a.window_left) word &= ~(1ull << u);
-        if (a.alibi_slopes != nullptr && real) slope_l2 = a.alibi_slopes[head] * kLog2e;
       }
+      if (VAR == kAlibi && real) slope_l2 = a.alibi_slopes[head] * kLog2e;
       const int pos = sg.s.kv_len + depth;
       float m = -INFINITY, l = 0.f;
-      const float sl2 = VAR ? 1.f : p.sl2;
       for (int t = 0; t < sg.tiles; ++t) {
         const int n = n0 + t * sg.nr + r, b = n & 1;
         const int kv0 = sg.s.lo + (sg.t0 + t) * kBN;
         // Visible columns, a bit each, where some may not be.
         const bool edge = kv0 + kBN > sg.s.kv_len ||
-                          (VAR && a.window_left >= 0 && kv0 < sg.s.kv_len + kMostNodes - a.window_left);
+                          (a.window_left >= 0 && kv0 < sg.s.kv_len + kMostNodes - a.window_left);
         uint32_t vis[kBN / 32];
         if (edge) {
           const int sft = sg.s.kv_len - kv0;                // column of node 0
-          const int lo_c = (VAR && a.window_left >= 0)
-                               ? min(pos - a.window_left, sg.s.kv_len) - kv0 : 0;
+          const int lo_c =
+              a.window_left >= 0 ? min(pos - a.window_left, sg.s.kv_len) - kv0 : 0;
 #pragma unroll
           for (int c = 0; c < kBN / 32; ++c) {
             const int s = sft - 32 * c;
@@ -643,50 +693,50 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         s_phase ^= 1u << b;
         tc_fence_after();
         const uint32_t tS = tmem + b * kPitch + lane_base;
-        // ---- masks and variants, written back ----
-        if (VAR || edge) {
+        // What turns the score of column k into log2 units: x sl2 + (base + slope k).
+        float sl2 = VAR == kCap ? 1.f : p.sl2, slope = 0.f, base = 0.f;
+        if constexpr (VAR == kAlibi) {
+          slope = slope_l2;
+          base = -slope_l2 * (float)(pos - kv0);
+        }
+        // Soft-capping, masks, and ALiBi where nodes are among the keys, of 32 columns.
+        auto dress = [&](uint32_t (&x)[32], int c) {
+          if constexpr (VAR == kCap) soft_cap(x, p.cap_in, p.cap_l2);
+          if (edge) {
+            if constexpr (VAR == kAlibi) {
+              const float d0 = (float)(pos - kv0 - 32 * c);
+              const int u0 = kv0 + 32 * c - sg.s.kv_len;    // node of the first column
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float dist = u0 + k < 0 ? d0 - (float)k
+                                              : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
+                x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.sl2, -slope_l2 * dist));
+              }
+            }
+            uint32_t w = vis[0];
+#pragma unroll
+            for (int q = 1; q < kBN / 32; ++q)
+              if (c == q) w = vis[q];
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((w >> k) & 1u)) x[k] = 0xff800000u;     // -inf
+          }
+        };
+        if (VAR == kAlibi && edge) sl2 = 1.f, slope = 0.f, base = 0.f;
+        if (kBN > 64 && (VAR == kCap || edge)) {
+          // Written back, in a pass of its own.
 #pragma unroll 1
           for (int c = 0; c < kBN / 32; ++c) {
             uint32_t x[32];
             tmem_ld32(tS + c * 32, x);
             tmem_wait_ld();
-            if constexpr (VAR) {
-              if (a.softcap > 0.f) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  x[k] = __float_as_uint(p.cap_l2 * tanhf(__uint_as_float(x[k]) * p.cap_in));
-              } else {
-                const float d0 = (float)(pos - kv0 - 32 * c);
-                const int u0 = kv0 + 32 * c - sg.s.kv_len;  // node of the chunk's first column
-                if (u0 + 31 < 0) {
-                  const float far = -slope_l2 * d0;
-#pragma unroll
-                  for (int k = 0; k < 32; ++k)
-                    x[k] = __float_as_uint(
-                        fmaf(__uint_as_float(x[k]), p.sl2, fmaf(slope_l2, (float)k, far)));
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) {
-                    const float dist = u0 + k < 0 ? d0 - (float)k
-                                                  : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
-                    x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.sl2, -slope_l2 * dist));
-                  }
-                }
-              }
-            }
-            if (edge) {
-              uint32_t w = vis[0];
-#pragma unroll
-              for (int q = 1; q < kBN / 32; ++q)
-                if (c == q) w = vis[q];
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((w >> k) & 1u)) x[k] = 0xff800000u;  // -inf
-            }
+            landed(x);
+            dress(x, c);
             tmem_st32(tS + c * 32, x);
           }
           tmem_wait_st();
         }
+        const float2 sl2v = make_float2(sl2, sl2), slopev = make_float2(slope, slope);
         // ---- pass 1: the row's maximum ----
         uint32_t x[2][32];
         float mx = -INFINITY;
@@ -699,16 +749,29 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             landed(x[0]);
             landed(x[1]);
           }
-          const uint32_t (&y)[32] = x[c & 1];
+          uint32_t (&y)[32] = x[c & 1];
+          if (kBN == 64 && (VAR == kCap || edge)) dress(y, c);
           float mc[4];
+          if constexpr (VAR == kAlibi) {
+            const float2 bv = make_float2(base, base);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
-#pragma unroll
-          for (int k = 8; k < 32; k += 8)
+            for (int k = 0; k < 32; k += 2) {
+              const float2 kv = make_float2((float)(32 * c + k), (float)(32 * c + k + 1));
+              const float2 e = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
+                                    sl2v, fma2(slopev, kv, bv));
+              const int q = (k >> 1) & 3;
+              mc[q] = k < 8 ? fmaxf(e.x, e.y) : fmax3(mc[q], e.x, e.y);
+            }
+          } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
+              mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
+#pragma unroll
+            for (int k = 8; k < 32; k += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
+          }
           mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
           if (kBN > 64 && (c & 1)) {
             // The next two; after the last ones, the first two for the second pass.
@@ -717,20 +780,31 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             tmem_ld32(tS + nc * 32 + 32, x[1]);
           }
         }
+        if constexpr (VAR != kAlibi) mx *= sl2;
         // ---- the reference: raised only when some row of the warp gained 2^8 ----
-        const float m_new = fmaxf(m, mx * sl2);
-        float corr = 1.f;
-        bool rescale_o = false;
+        const float m_new = fmaxf(m, mx);
         if (m == -INFINITY) m = m_new;  // nothing seen so far: O and l are 0
         if (t > 0 && __any_sync(0xffffffffu, m_new - m > kRescaleThreshold)) {
-          corr = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
+          const float corr = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
           m = m_new;
           l *= corr;
-          rescale_o = true;
+          const int pn = n - sg.nr;                         // this row tile's last product
+          if (!mbar_wait_warp(bar(kPVDone + (pn & 1)), (pn >> 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t y[16];
+            const uint32_t at = tO + r * D + lane_base + c * 16;
+            tmem_ld16(at, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
+            tmem_st16(at, y);
+          }
         }
         const float nm = m == -INFINITY ? 0.f : -m;
         // ---- pass 2: P over S (what it overwrites has been read) ----
-        const float2 sl2v = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
+        const float2 nmv = make_float2(base + nm, base + nm);
         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < kBN / 32; ++c) {
@@ -743,8 +817,11 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
+            float2 add = nmv;
+            if constexpr (VAR == kAlibi)
+              add = fma2(slopev, make_float2((float)(32 * c + 2 * k), (float)(32 * c + 2 * k + 1)), nmv);
             const float2 e = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])),
-                                  sl2v, nmv);
+                                  sl2v, add);
             float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             rs[k & 1] = add2(rs[k & 1], pp);
             hi[k] = pack_bf16x2(pp.x, pp.y);
@@ -765,27 +842,14 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             tmem_ld32(tS + 64, x[0]);
             tmem_ld32(tS + 96, x[1]);
           }
+          if (c & 1) {                                      // 64 keys of P are there
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(kPFull + 2 * (c >> 1) + b));
+          }
         }
         const float2 rsum = add2(rs[0], rs[1]);
         l += rsum.x + rsum.y;
-        if (rescale_o) {
-          const int pn = n - sg.nr;                         // this row tile's last product
-          if (!mbar_wait_warp(bar(kPVDone + (pn & 1)), (pn >> 1) & 1, ctl)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            const uint32_t at = tO + r * D + lane_base + c * 32;
-            tmem_ld32(at, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * corr);
-            tmem_st32(at, x);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kPFull + b));
       }
       if (!ok) break;
       // ---- epilogue of the segment ----
@@ -853,66 +917,125 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// The partials of a cut item, one warp a row: O = sum w_i O_i / sum w_i with
-// w_i = exp(lse_i - max), blocks in order, so the result does not depend on which came
-// first.  blockIdx.x: the block of the first kernel where the item ended.
+// The partials of cut items: O = sum w_i O_i / sum w_i with w_i = exp(lse_i - max),
+// blocks in order (and, with many, eight running sums in order), so that the result does
+// not depend on which came first.  The first kernel's blocks leave what ended in them; every
+// block here counts through those and takes its share of the rows.  Up to kFewParts
+// partials a warp does a row; more are divided among the block's warps (one sequence of
+// 30720 tokens is cut 38 ways: 22 us with a warp a row and a grid of all possible rows).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
+constexpr int kFewParts = 8;
+constexpr int kMostBlocks = 256;  // of the first kernel's grid
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const DecodeTreeArgs a) {
+  constexpr int kV = D / 32;  // values of a lane: columns lane * kV ...
+  __shared__ int s_units[kMostBlocks + 1];  // units in front of each block's item
+  __shared__ int s_warp[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D], s_sum[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  const int c = blockIdx.x;
-  const TreeJoin j = a.joins[c];
-  const int i = blockIdx.y * kJoinWarps + warp;
-  if (j.first_block < 0 || i >= j.rows) return;
-  const int parts = c - j.first_block + 1;
-  auto at = [&](int k) {  // the first block left it at its place 1, the others at place 0
-    return ((size_t)(j.first_block + k) * 2 + (k == 0 ? 1 : 0)) * a.part_rows + i;
-  };
-  float top = -INFINITY;
-  for (int k = lane; k < parts; k += 32) top = fmax_nan(top, a.lse_part[at(k)]);
+  // Units: a row, or with few partials kJoinWarps rows.
+  {
+    const int c = threadIdx.x;
+    int units = 0;
+    if (c < a.blocks) {
+      const TreeJoin j = a.joins[c];
+      if (j.first_block >= 0)
+        units = c - j.first_block + 1 > kFewParts ? j.rows : (j.rows + kJoinWarps - 1) / kJoinWarps;
+    }
+    int incl = units;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float ref = top == -INFINITY ? 0.f : top;
-  constexpr int kV = D / 32;  // values of a lane: columns lane * kV ...
-  float acc[kV], sum = 0.f;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s_warp[w];
+    s_units[c + 1] = incl;
+    if (c == 0) s_units[0] = 0;
+    __syncthreads();
+  }
+  const int total = s_units[a.blocks];
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int c = 0;
+    for (int hi = a.blocks; hi - c > 1;) {
+      const int mid = (c + hi) >> 1;
+      if (s_units[mid] <= u) c = mid; else hi = mid;
+    }
+    const TreeJoin j = a.joins[c];
+    const int parts = c - j.first_block + 1;
+    const bool many = parts > kFewParts;
+    const int i = many ? u - s_units[c] : (u - s_units[c]) * kJoinWarps + warp;
+    const int k0 = many ? warp : 0, step = many ? kJoinWarps : 1;
+    const bool live = i < j.rows;
+    auto at = [&](int k) {  // the first block left it at its place 1, the others at place 0
+      return ((size_t)(j.first_block + k) * 2 + (k == 0 ? 1 : 0)) * a.part_rows + i;
+    };
+    float acc[kV], sum = 0.f, ref = 0.f;
 #pragma unroll
-  for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+    for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+    if (live) {
+      float top = -INFINITY;
+      for (int k = lane; k < parts; k += 32) top = fmax_nan(top, a.lse_part[at(k)]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      ref = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
-    const size_t row = at(k);
-    const float w = ex2_approx((a.lse_part[row] - ref) * kLog2e);
-    sum += w;
-    const float* src = a.o_part + row * D + lane * kV;
-    float x[kV];
-    if constexpr (kV == 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      x[0] = y.x, x[1] = y.y;
-    } else {
+      for (int k = k0; k < parts; k += step) {
+        const size_t row = at(k);
+        const float w = ex2_approx((a.lse_part[row] - ref) * kLog2e);
+        sum += w;
+        const float* src = a.o_part + row * D + lane * kV;
+        float x[kV];
+        if constexpr (kV == 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          x[0] = y.x, x[1] = y.y;
+        } else {
 #pragma unroll
-      for (int v = 0; v < kV; v += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src + v);
-        x[v] = y.x, x[v + 1] = y.y, x[v + 2] = y.z, x[v + 3] = y.w;
+          for (int v = 0; v < kV; v += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src + v);
+            x[v] = y.x, x[v + 1] = y.y, x[v + 2] = y.z, x[v + 3] = y.w;
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < kV; ++v) acc[v] = fmaf(w, x[v], acc[v]);
       }
     }
+    if (many) {
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = fmaf(w, x[v], acc[v]);
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int g = a.n_q_heads / a.n_kv_heads;
-  const int node = (j.row0 + i) / g, head = j.kvh * g + (j.row0 + i) % g;
-  const size_t orow = (size_t)(j.q0 + node) * a.n_q_heads + head;
-  if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : ref + log2f(sum) * kLn2;
-  if constexpr (WIDE) {
-    float* dst = static_cast<float*>(a.o) + orow * D + lane * kV;
+      for (int v = 0; v < kV; ++v) s_o[warp][lane * kV + v] = acc[v];
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        sum = 0.f;
+        for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) dst[v] = acc[v] * inv;
-  } else {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + orow * D + lane * kV);
+        for (int v = 0; v < kV; ++v) {
+          acc[v] = 0.f;
+          for (int w = 0; w < kJoinWarps; ++w) acc[v] += s_o[w][lane * kV + v];
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    if (!live) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int g = a.n_q_heads / a.n_kv_heads;
+    const int node = (j.row0 + i) / g, head = j.kvh * g + (j.row0 + i) % g;
+    const size_t orow = (size_t)(j.q0 + node) * a.n_q_heads + head;
+    if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : ref + log2f(sum) * kLn2;
+    if constexpr (WIDE) {
+      float* dst = static_cast<float*>(a.o) + orow * D + lane * kV;
 #pragma unroll
-    for (int v = 0; v < kV; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+      for (int v = 0; v < kV; ++v) dst[v] = acc[v] * inv;
+    } else {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + orow * D + lane * kV);
+#pragma unroll
+      for (int v = 0; v < kV; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+    }
   }
 }
 
@@ -950,7 +1073,7 @@ bool make_cache_map(CUtensorMap* m, const void* base, int D, int n_kv, int rows,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool VAR, bool WIDE>
+template <int D, int VAR, bool WIDE>
 cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   using L = TreeSmem<D, WIDE>;
   TreeKParams p;
@@ -1002,17 +1125,22 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
   if (e != cudaSuccess || a.whole) return e;
-  cfg.gridDim = dim3((unsigned)a.blocks, (unsigned)((a.part_rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3((unsigned)(4 * a.blocks));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_tree_kernel<D, WIDE>, a);
 }
 
+template <int D, bool WIDE>
+cudaError_t launch_v(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
+  if (a.softcap > 0.f) return launch_t<D, kCap, WIDE>(a, ctx);
+  if (a.alibi_slopes != nullptr) return launch_t<D, kAlibi, WIDE>(a, ctx);
+  return launch_t<D, kPlain, WIDE>(a, ctx);
+}
+
 template <int D>
 cudaError_t launch_d(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
-  const bool var = a.window_left >= 0 || a.softcap > 0.f || a.alibi_slopes != nullptr;
-  if (a.wide) return var ? launch_t<D, true, true>(a, ctx) : launch_t<D, false, true>(a, ctx);
-  return var ? launch_t<D, true, false>(a, ctx) : launch_t<D, false, false>(a, ctx);
+  return a.wide ? launch_v<D, true>(a, ctx) : launch_v<D, false>(a, ctx);
 }
 
 }  // namespace
