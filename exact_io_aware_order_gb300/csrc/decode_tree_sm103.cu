@@ -66,34 +66,31 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMostNodes = 64;
-constexpr int kMostBox = 64;
+constexpr int kMostBox = 32;
+constexpr int kBN = 64;                // keys of a tile
 
-// Row tiles of an item, keys of a tile, and the columns of an S buffer.  TMEM holds two S
-// buffers and an O of D columns a row tile: 2 x 128 + 2 x D, 2 x 64 + 256 at head_dim
-// 256, and with fp32 outputs 2 x 96 (three parts of P, 32 columns each) + 2 x D.
+// Row tiles of an item.  TMEM (512 columns): an O of D columns a row tile, and S buffers in
+// what is left, up to four: 64 columns each, or with fp32 outputs 96 (three parts of P of 32).
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
-template <int D, bool WIDE> __host__ __device__ constexpr int key_tile() {
-  return D == 256 || WIDE ? 64 : 128;
-}
-template <int D, bool WIDE> __host__ __device__ constexpr int s_pitch() {
-  return WIDE ? 96 : key_tile<D, WIDE>();
+template <bool WIDE> __host__ __device__ constexpr int s_pitch() { return WIDE ? 96 : 64; }
+template <int D, bool WIDE> __host__ __device__ constexpr int s_bufs() {
+  return ((int)kTmemCols - row_tiles<D>() * D) / s_pitch<WIDE>() >= 4 ? 4 : 2;
 }
 template <int D> __host__ __device__ constexpr int threads_of() {
   return row_tiles<D>() * kSoftmaxThreads + kProducerThreads + 64;
 }
 
-template <int D, bool WIDE>
+template <int D>
 struct TreeSmem {
-  static constexpr int kBN = key_tile<D, WIDE>();
   static constexpr int kQTileBytes = 128 * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;
   static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
   static constexpr int kChunkBytes = kBN * 128;
-  static constexpr int kMaxSlots = 8;
-  // barriers: full / empty for each slot, q_empty, s_full[row tile][2], p_full[half][2],
-  // pv_done[2], o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item
-  // of fewer rows would otherwise miss phases, and take an old one for its next.
-  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 4 + 4 + 2 + 2 + 2;
+  static constexpr int kMaxSlots = 12;
+  // barriers: full / empty for each slot, q_empty, s_full[row tile][4], p_full[4], pv_done[4],
+  // o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item of fewer
+  // rows would otherwise miss phases, and take an old one for its next.
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 8 + 4 + 4 + 2 + 2;
   static constexpr int kMiscBytes = 1024;  // barriers, then the block's share of the work
   static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
   // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
@@ -109,6 +106,7 @@ struct TreeSmem {
 
 struct TreeKParams {
   DecodeTreeArgs a;
+  int g;                // query heads of a kv head
   int q_tiles, slots;   // row tiles that an item may have here, ring slots
   int box;              // rows of a tiled copy's box; 0: no tiled copies
   float sl2;            // scale * log2(e)
@@ -129,7 +127,6 @@ struct Seq {
   bool bad_nodes, bad_len;
 };
 
-template <int BN>
 __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   const DecodeTreeArgs& a = p.a;
   Seq s;
@@ -145,9 +142,9 @@ __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   // Every node's position is kv_len or more: a window starts no earlier than this.
   s.first = a.window_left >= 0 ? max(0, s.kv_len - a.window_left) : 0;
   s.lo = s.first / kMostBox * kMostBox;
-  s.tiles = max(1, (s.end - s.lo + BN - 1) / BN);
-  const int g = a.n_q_heads / a.n_kv_heads, rows = 128 * p.q_tiles;
-  s.groups = (s.nodes * g + rows - 1) / rows;
+  s.tiles = max(1, (s.end - s.lo + kBN - 1) / kBN);
+  const int shift = 6 + p.q_tiles;  // rows of a group: 128 or 256
+  s.groups = (s.nodes * p.g + (1 << shift) - 1) >> shift;
   return s;
 }
 
@@ -161,7 +158,14 @@ __device__ __forceinline__ long long units_of(const TreeKParams& p, const Seq& s
 struct Share {
   long long u0, u1, total, base0;
   int b0;
+  Seq s0;  // sequence b0
 };
+
+// Whole-number quotients, in 32 bits where both numbers are.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
 
 // A run of key tiles of one item.
 struct Seg {
@@ -172,35 +176,32 @@ struct Seg {
   long long item_u0;           // the item's first unit
 };
 
-template <int BN>
 struct Walk {
   const TreeKParams& p;
   long long u, u1, base;
   int b;
   Seq s;
   __device__ Walk(const TreeKParams& p_, const Share& sh)
-      : p(p_), u(sh.u0), u1(sh.u1), base(sh.base0), b(sh.b0) {
-    if (u < u1) s = seq_of<BN>(p, b);
-  }
+      : p(p_), u(sh.u0), u1(sh.u1), base(sh.base0), b(sh.b0), s(sh.s0) {}
   __device__ bool next(Seg& g) {
     if (u >= u1) return false;
     long long n = units_of(p, s);
     while (u >= base + n) {
       if (b + 1 >= p.a.batch) return false;  // (lengths that changed under the call)
       base += n;
-      s = seq_of<BN>(p, ++b);
+      s = seq_of(p, ++b);
       n = units_of(p, s);
     }
     const int T = p.a.whole ? 1 : s.tiles;
     const long long local = u - base;
-    const int item = (int)(local / T), t = (int)(local - (long long)item * T);
+    const int item = (int)quotient(local, T), t = (int)(local - (long long)item * T);
     const int rows = 128 * p.q_tiles;
     const int n_units = (int)min((long long)(T - t), u1 - u);
     g.s = s;
     g.b = b;
     g.kvh = item / s.groups;
-    g.row0 = (item % s.groups) * rows;
-    g.rows = min(rows, s.nodes * (p.a.n_q_heads / p.a.n_kv_heads) - g.row0);
+    g.row0 = (item - g.kvh * s.groups) * rows;
+    g.rows = min(rows, s.nodes * p.g - g.row0);
     g.nr = (g.rows + 127) / 128;
     g.t0 = t;
     g.tiles = p.a.whole ? s.tiles : n_units;
@@ -252,6 +253,25 @@ __device__ __forceinline__ void landed(uint32_t (&r)[32]) {
                  "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31]));
+}
+
+// N x 32 bytes of a thread to consecutive addresses, a whole sector a store where the
+// address allows it (a row a thread: 16-byte stores would fill sectors by halves).
+template <int N>
+__device__ __forceinline__ void store_32B(void* dst, const uint32_t (&y)[8 * N]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                       static_cast<char*>(dst) + 32 * k),
+                   "r"(y[8 * k]), "r"(y[8 * k + 1]), "r"(y[8 * k + 2]), "r"(y[8 * k + 3]),
+                   "r"(y[8 * k + 4]), "r"(y[8 * k + 5]), "r"(y[8 * k + 6]), "r"(y[8 * k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2 * N; ++k)
+      reinterpret_cast<uint4*>(dst)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+  }
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
@@ -308,10 +328,10 @@ template <int D, int VAR, bool WIDE>
 __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ TreeKParams p) {
-  using L = TreeSmem<D, WIDE>;
-  constexpr int kBN = L::kBN, kPitch = s_pitch<D, WIDE>(), NQ = row_tiles<D>(), kThreads = threads_of<D>();
+  using L = TreeSmem<D>;
+  constexpr int kPitch = s_pitch<WIDE>(), SB = s_bufs<D, WIDE>(), NQ = row_tiles<D>(), kThreads = threads_of<D>();
   constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
-  static_assert(2 * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
+  static_assert(SB * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
   const DecodeTreeArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
-                kPFull = kSFull + 4, kPVDone = kPFull + 4, kOFull = kPVDone + 2,
+                kPFull = kSFull + 8, kPVDone = kPFull + 4, kOFull = kPVDone + 4,
                 kDrain = kOFull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
@@ -339,12 +359,13 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       mbar_init(bar(kEmpty + i), 1);
     }
     mbar_init(bar(kQEmpty), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SB; ++i) {
       mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSFull + 2 + i), 1);
+      mbar_init(bar(kSFull + 4 + i), 1);
       mbar_init(bar(kPFull + i), kSoftmaxThreads);
-      mbar_init(bar(kPFull + 2 + i), kSoftmaxThreads);
       mbar_init(bar(kPVDone + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kOFull + i), 1);
       mbar_init(bar(kDrain + i), 1);
     }
@@ -368,7 +389,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     long long mine = 0;
     bool bad_nodes = false, bad_len = false;
     for (int b = b0; b < b1; ++b) {
-      const Seq s = seq_of<kBN>(p, b);
+      const Seq s = seq_of(p, b);
       mine += units_of(p, s);
       bad_nodes |= s.bad_nodes;
       bad_len |= s.bad_len;
@@ -386,6 +407,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
     long long before = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       const long long v = warp_sums[w];
       if (w < warp) before += v;
@@ -394,7 +416,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     long long at = before + incl - mine;  // units in front of this thread's sequences
     // Blocks beyond the units get none, so that those with some are neighbours.
     const long long G = max(min((long long)gridDim.x, total), 1LL), c = blockIdx.x;
-    const long long u0 = min(c * total / G, total), u1 = min((c + 1) * total / G, total);
+    const long long u0 = c < G ? quotient(c * total, G) : total;
+    const long long u1 = c < G ? quotient((c + 1) * total, G) : total;
     if (threadIdx.x == 0) {
       share->u0 = u0;
       share->u1 = u1;
@@ -405,30 +428,38 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     __syncthreads();
     if (u0 < u1 && u0 >= at && u0 < at + mine) {
       int b = b0;
-      for (; b + 1 < b1; ++b) {
-        const long long n = units_of(p, seq_of<kBN>(p, b));
+      Seq s = seq_of(p, b);
+      while (b + 1 < b1) {
+        const long long n = units_of(p, s);
         if (u0 < at + n) break;
         at += n;
+        s = seq_of(p, ++b);
       }
       share->b0 = b;
       share->base0 = at;
+      share->s0 = s;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tO = tmem + 2 * kPitch;
+  const uint32_t tO = tmem + SB * kPitch;
   const WaitCtl ctl{abort_flag, p.err_word, p.timeout_ns};
   const Share sh = *share;
-  const int g = a.n_q_heads / a.n_kv_heads;
+  const int g = p.g;
 
+  // First key of the t-th tile that a segment visits.  ALiBi's bias grows toward the nodes:
+  // in order the maxima would rise, and O be rescaled, tile after tile, so it goes backwards.
+  auto first_key = [&](const Seg& sg, int t) {
+    return sg.s.lo + (sg.t0 + (VAR == kAlibi ? sg.tiles - 1 - t : t)) * kBN;
+  };
   // Whether a key tile is filled by tiled copies: all of its keys exist.
   auto tiled = [&](const Seg& sg, int t) {
-    const int tile0 = sg.s.lo + (sg.t0 + t) * kBN;
+    const int tile0 = first_key(sg, t);
     return p.box > 0 && tile0 >= sg.s.first && tile0 + kBN <= sg.s.end;
   };
-  // Roles walk the same segments; S products count over all of them (n: buffer n & 1),
+  // Roles walk the same segments; S products count over all of them (n: buffer n % SB),
   // and so do the ring's tiles (K and V of key tile j: 2 j and 2 j + 1).
   const uint32_t id_s = idesc_bf16_f32(128, kBN, false, false);
   const uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
@@ -441,60 +472,90 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     constexpr int kHalf = kBN / 2, kSets = kHalf / 32;     // rows of a warp, in sets of 32
     const int half = warp - kProducerWarp;
     int issued = 0, slot = 0, phase = 0, n_seg = 0;
-    Walk<kBN> walk(p, sh);
+    Walk walk(p, sh);
     Seg sg;
     bool ok = true;
     while (ok && walk.next(sg)) {
-      // The last segment's S products have to be through with Q.
-      if (n_seg > 0 && !mbar_wait_warp(bar(kQEmpty), (n_seg - 1) & 1, ctl)) break;
-      ++n_seg;
-      // Q: row i of the kv head is node i / g, head i % g; it counts as landed with the
-      // first keys, whose arrivals wait for all copies so far.
-      for (int set = half; set < 4 * sg.nr; set += 2) {
-        const int i = set * 32 + lane, row = sg.row0 + i, node = row / g;
-        const int src = i < sg.rows ? (sg.s.q0 + node) * a.n_q_heads + sg.kvh * g + (row - node * g) : -1;
-        copy_rows<D>(smem_u32(smem + (set >> 2) * L::kQTileBytes), L::kQChunkBytes, (set & 3) * 32,
-                     a.q, D, src, lane);
-      }
       const int32_t* table =
           a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
+      // Q: row i of the kv head is node i / g, head i % g.  The last segment's S products
+      // have to be through with it.  It counts as landed with the first keys, whose arrivals
+      // wait for all copies so far.
+      auto copy_q = [&]() -> bool {
+        if (n_seg > 0 && !mbar_wait_warp(bar(kQEmpty), (n_seg - 1) & 1, ctl)) return false;
+        ++n_seg;
+        for (int set = half; set < 4 * sg.nr; set += 2) {
+          const int i = set * 32 + lane, row = sg.row0 + i, node = row / g;
+          const int src =
+              i < sg.rows ? (sg.s.q0 + node) * a.n_q_heads + sg.kvh * g + (row - node * g) : -1;
+          copy_rows<D>(smem_u32(smem + (set >> 2) * L::kQTileBytes), L::kQChunkBytes,
+                       (set & 3) * 32, a.q, D, src, lane);
+        }
+        return true;
+      };
+      // Tiled copies: where box `lane` of this warp's rows lies (a look ahead, so that the
+      // block table's latency is not in the way).
+      constexpr int kSpans = D / 64, kBoxes = kHalf / 8;
+      const bool mine = lane * p.box < kHalf && p.box > 0;
+      int next_row = 0, next_plane = 0;
+      auto look = [&](int t) {
+        if (!mine || t >= sg.tiles || !tiled(sg, t)) return;
+        const int tok = first_key(sg, t) + half * kHalf + lane * p.box;
+        if (table == nullptr) {
+          next_row = tok;
+          next_plane = sg.b;
+        } else {
+          const int j = tok / a.block_size;
+          next_row = tok - j * a.block_size;
+          next_plane = table[j];
+        }
+      };
+      look(0);
       for (int t = 0; t < sg.tiles && ok; ++t) {
-        const int tile0 = sg.s.lo + (sg.t0 + t) * kBN, tok0 = tile0 + half * kHalf;
+        const int tok0 = first_key(sg, t) + half * kHalf;
         if (tiled(sg, t)) {
-          // A box and span a lane.  A bad block becomes one past the cache, which reads as
-          // zeros.
-          constexpr int kSpans = D / 64;
-          const int i = lane / kSpans, span = lane % kSpans;
-          const bool mine = i * p.box < kHalf;
-          const int tok = tok0 + i * p.box;
-          int c2 = tok, c3 = sg.b;
-          if (table != nullptr && mine) {
-            const int j = tok / a.block_size;
-            c2 = tok - j * a.block_size;
-            c3 = table[j];
-            if (c3 < 0 || c3 >= a.num_blocks) {
-              atomicOr(p.err_word, kErrBlockIndex);
-              c3 = a.num_blocks;
-            }
+          if (table != nullptr && mine && (next_plane < 0 || next_plane >= a.num_blocks)) {
+            // A bad block becomes one past the cache, which reads as zeros.
+            atomicOr(p.err_word, kErrBlockIndex);
+            next_plane = a.num_blocks;
           }
+          // One thread issues them all, from straight code: a lane each costs 140 clocks a
+          // copy, lane after lane.
+          int c2[kBoxes], c3[kBoxes];
+#pragma unroll
+          for (int i = 0; i < kBoxes; ++i) {
+            c2[i] = __shfl_sync(0xffffffffu, next_row, i);
+            c3[i] = __shfl_sync(0xffffffffu, next_plane, i);
+          }
+          look(t + 1);
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             if (issued >= slots && !mbar_wait_warp(bar(kEmpty + slot), phase ^ 1, ctl)) {
               ok = false;
               break;
             }
-            if (lane == 0) mbar_expect_tx(bar(kFull + slot), kHalf * D * 2);
+            if (lane == 0) {
+              mbar_expect_tx(bar(kFull + slot), kHalf * D * 2);
+              const CUtensorMap* map = kv ? &tm_v : &tm_k;
+              const uint32_t dst = smem_u32(ring + slot * L::kTileBytes) + half * kHalf * 128;
+#pragma unroll
+              for (int i = 0; i < kBoxes; ++i) {
+                if (i * p.box >= kHalf) break;
+#pragma unroll
+                for (int span = 0; span < kSpans; ++span)
+                  tma_load_4d(dst + span * L::kChunkBytes + i * p.box * 128, map, bar(kFull + slot),
+                              span * 64, sg.kvh, c2[i], c3[i]);
+              }
+            }
             __syncwarp();
-            if (mine)
-              tma_load_4d(smem_u32(ring + slot * L::kTileBytes + span * L::kChunkBytes) +
-                              (half * kHalf + i * p.box) * 128,
-                          kv ? &tm_v : &tm_k, bar(kFull + slot), span * 64, sg.kvh, c2, c3);
+            if (t == 0 && kv == 0 && !copy_q()) ok = false;
             cp_async_arrive(bar(kFull + slot));
             ++issued;
             if (++slot == slots) slot = 0, phase ^= 1;
           }
           continue;
         }
+        look(t + 1);
         int row[kSets];  // cache rows (a token of all kv heads); -1: none
         int blk[kSets];
 #pragma unroll
@@ -533,6 +594,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             copy_rows<D>(tile, L::kChunkBytes, half * kHalf + i * 32,
                          (kv ? a.v_cache : a.k_cache) + (size_t)sg.kvh * D,
                          (long long)a.n_kv_heads * D, row[i], lane);
+          if (t == 0 && kv == 0 && !copy_q()) ok = false;
           cp_async_arrive(bar(kFull + slot));
           ++issued;
           if (++slot == slots) slot = 0, phase ^= 1;
@@ -544,7 +606,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   } else if (warp == kSWarp) {
     // ============================ S = Q K^T issuer ============================
     if (lane == 0) {
-      Walk<kBN> walk(p, sh);
+      Walk walk(p, sh);
       Seg sg;
       bool ok = true;
       int n = 0, slot = 0, phase = 0;
@@ -556,9 +618,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           if (t == 0 || !tiled(sg, t)) fence_proxy_async_smem();
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
-            const int b = n & 1;
-            // Buffer b last held P(n - 2).
-            if (n >= 2 && !mbar_wait(bar(kPVDone + b), ((n >> 1) - 1) & 1, ctl)) { ok = false; break; }
+            const int b = n % SB;
+            // Buffer b last held P(n - SB).
+            if (n >= SB && !mbar_wait(bar(kPVDone + b), (n / SB - 1) & 1, ctl)) { ok = false; break; }
             tc_fence_after();
             const uint32_t dS = tmem + b * kPitch;
             const uint32_t q_lo = q_lo0 + (uint32_t)((r * L::kQTileBytes) >> 4);
@@ -568,7 +630,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
               const uint32_t koff = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
               mma_ss_lo(dS, q_lo + qoff, k_lo + koff, dhi, id_s, kk > 0);
             }
-            mma_commit(bar(kSFull + 2 * r + b));
+            mma_commit(bar(kSFull + 4 * r + b));
           }
           mma_commit(bar(kEmpty + slot));
           // K tiles are every other one of the ring.
@@ -586,7 +648,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   } else if (warp == kPVWarp) {
     // ============================ O += P V issuer ============================
     if (lane == 0) {
-      Walk<kBN> walk(p, sh);
+      Walk walk(p, sh);
       Seg sg;
       bool ok = true;
       int n = 0, slot = 1, phase = 0;
@@ -598,21 +660,16 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           const uint32_t v_lo =
               sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
-            const int b = n & 1;
-            // P comes in halves of 64 keys.
+            const int b = n % SB;
+            if (!mbar_wait(bar(kPFull + b), (n / SB) & 1, ctl)) { ok = false; break; }
+            tc_fence_after();
             const uint32_t aP = tmem + b * kPitch, tOr = tO + r * D;
 #pragma unroll
-            for (int h = 0; h < kBN / 64; ++h) {
-              if (!mbar_wait(bar(kPFull + 2 * h + b), (n >> 1) & 1, ctl)) { ok = false; break; }
-              tc_fence_after();
+            for (int part = 0; part < (WIDE ? 3 : 1); ++part)
 #pragma unroll
-              for (int part = 0; part < (WIDE ? 3 : 1); ++part)
-#pragma unroll
-                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                  mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
-                            id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
-            }
-            if (!ok) break;
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
+                          id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
             mma_commit(bar(kPVDone + b));
             if (t == sg.tiles - 1) mma_commit(bar(kOFull + r));
           }
@@ -633,7 +690,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int trow = (warp & 3) * 32 + lane;                // row within the tile (TMEM lane)
     int* depths = depth_tab + warp * kMostNodes;            // the nodes' depths, each warp its own
-    Walk<kBN> walk(p, sh);
+    Walk walk(p, sh);
     Seg sg;
     bool ok = true;
     int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
@@ -669,8 +726,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       const int pos = sg.s.kv_len + depth;
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < sg.tiles; ++t) {
-        const int n = n0 + t * sg.nr + r, b = n & 1;
-        const int kv0 = sg.s.lo + (sg.t0 + t) * kBN;
+        const int n = n0 + t * sg.nr + r, b = n % SB;
+        const int kv0 = first_key(sg, t);
         // Visible columns, a bit each, where some may not be.
         const bool edge = kv0 + kBN > sg.s.kv_len ||
                           (a.window_left >= 0 && kv0 < sg.s.kv_len + kMostNodes - a.window_left);
@@ -689,7 +746,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             vis[c] = w;
           }
         }
-        if (!mbar_wait_warp(bar(kSFull + 2 * r + b), (s_phase >> b) & 1u, ctl)) { ok = false; break; }
+        if (!mbar_wait_warp(bar(kSFull + 4 * r + b), (s_phase >> b) & 1u, ctl)) { ok = false; break; }
         s_phase ^= 1u << b;
         tc_fence_after();
         const uint32_t tS = tmem + b * kPitch + lane_base;
@@ -723,34 +780,19 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           }
         };
         if (VAR == kAlibi && edge) sl2 = 1.f, slope = 0.f, base = 0.f;
-        if (kBN > 64 && (VAR == kCap || edge)) {
-          // Written back, in a pass of its own.
-#pragma unroll 1
-          for (int c = 0; c < kBN / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld32(tS + c * 32, x);
-            tmem_wait_ld();
-            landed(x);
-            dress(x, c);
-            tmem_st32(tS + c * 32, x);
-          }
-          tmem_wait_st();
-        }
         const float2 sl2v = make_float2(sl2, sl2), slopev = make_float2(slope, slope);
-        // ---- pass 1: the row's maximum ----
+        // ---- the row's scores, and their maximum ----
         uint32_t x[2][32];
-        float mx = -INFINITY;
         tmem_ld32(tS, x[0]);
         tmem_ld32(tS + 32, x[1]);
+        tmem_wait_ld();
+        landed(x[0]);
+        landed(x[1]);
+        float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) {
-          if ((c & 1) == 0) {
-            tmem_wait_ld();
-            landed(x[0]);
-            landed(x[1]);
-          }
-          uint32_t (&y)[32] = x[c & 1];
-          if (kBN == 64 && (VAR == kCap || edge)) dress(y, c);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t (&y)[32] = x[c];
+          if (VAR == kCap || edge) dress(y, c);
           float mc[4];
           if constexpr (VAR == kAlibi) {
             const float2 bv = make_float2(base, base);
@@ -759,26 +801,19 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
               const float2 kv = make_float2((float)(32 * c + k), (float)(32 * c + k + 1));
               const float2 e = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
                                     sl2v, fma2(slopev, kv, bv));
-              const int q = (k >> 1) & 3;
-              mc[q] = k < 8 ? fmaxf(e.x, e.y) : fmax3(mc[q], e.x, e.y);
+              y[k] = __float_as_uint(e.x);
+              y[k + 1] = __float_as_uint(e.y);
             }
-          } else {
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
+#pragma unroll
+          for (int k = 8; k < 32; k += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
-#pragma unroll
-            for (int k = 8; k < 32; k += 8)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
-          }
+              mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
           mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-          if (kBN > 64 && (c & 1)) {
-            // The next two; after the last ones, the first two for the second pass.
-            const int nc = c + 1 < kBN / 32 ? c + 1 : 0;
-            tmem_ld32(tS + nc * 32, x[0]);
-            tmem_ld32(tS + nc * 32 + 32, x[1]);
-          }
         }
         if constexpr (VAR != kAlibi) mx *= sl2;
         // ---- the reference: raised only when some row of the warp gained 2^8 ----
@@ -789,7 +824,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           m = m_new;
           l *= corr;
           const int pn = n - sg.nr;                         // this row tile's last product
-          if (!mbar_wait_warp(bar(kPVDone + (pn & 1)), (pn >> 1) & 1, ctl)) { ok = false; break; }
+          if (!mbar_wait_warp(bar(kPVDone + pn % SB), (pn / SB) & 1, ctl)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
@@ -803,25 +838,18 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           }
         }
         const float nm = m == -INFINITY ? 0.f : -m;
-        // ---- pass 2: P over S (what it overwrites has been read) ----
-        const float2 nmv = make_float2(base + nm, base + nm);
+        // ---- P over S ----
+        const float2 nmv = make_float2(nm, nm);
         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) {
-          if (kBN > 64 && (c & 1) == 0) {
-            tmem_wait_ld();
-            landed(x[0]);
-            landed(x[1]);
-          }
-          const uint32_t (&y)[32] = x[c & 1];
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t (&y)[32] = x[c];
           uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            float2 add = nmv;
-            if constexpr (VAR == kAlibi)
-              add = fma2(slopev, make_float2((float)(32 * c + 2 * k), (float)(32 * c + 2 * k + 1)), nmv);
-            const float2 e = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])),
-                                  sl2v, add);
+            const float2 v = make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+            // (ALiBi's scores are in log2 units already)
+            const float2 e = VAR == kAlibi ? add2(v, nmv) : fma2(v, sl2v, nmv);
             float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             rs[k & 1] = add2(rs[k & 1], pp);
             hi[k] = pack_bf16x2(pp.x, pp.y);
@@ -838,16 +866,10 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             tmem_st16(tS + kBN / 2 + c * 16, mid);
             tmem_st16(tS + kBN + c * 16, lo);
           }
-          if (kBN > 64 && c == 1) {
-            tmem_ld32(tS + 64, x[0]);
-            tmem_ld32(tS + 96, x[1]);
-          }
-          if (c & 1) {                                      // 64 keys of P are there
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar(kPFull + 2 * (c >> 1) + b));
-          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + b));
         const float2 rsum = add2(rs[0], rs[1]);
         l += rsum.x + rsum.y;
       }
@@ -874,18 +896,17 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         if (!real) continue;
         auto f = [&](int k) { return __uint_as_float(x[k]) * inv; };
         if (!WIDE && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * D + c * 32);
+          uint16_t* dst = static_cast<uint16_t*>(a.o) + orow * D + c * 32;
+          uint32_t y[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack_bf16x2(f(8 * k), f(8 * k + 1)), pack_bf16x2(f(8 * k + 2), f(8 * k + 3)),
-                                pack_bf16x2(f(8 * k + 4), f(8 * k + 5)),
-                                pack_bf16x2(f(8 * k + 6), f(8 * k + 7)));
+          for (int k = 0; k < 16; ++k) y[k] = pack_bf16x2(f(2 * k), f(2 * k + 1));
+          store_32B<2>(dst, y);
         } else {
-          float4* dst = reinterpret_cast<float4*>(
-              (whole ? static_cast<float*>(a.o) + orow * D : a.o_part + prow * D) + c * 32);
+          float* dst = (whole ? static_cast<float*>(a.o) + orow * D : a.o_part + prow * D) + c * 32;
+          uint32_t y[32];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(f(4 * k), f(4 * k + 1), f(4 * k + 2), f(4 * k + 3));
+          for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(f(k));
+          store_32B<4>(dst, y);
         }
       }
       tc_fence_before();
@@ -895,7 +916,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   // ---- what the second kernel joins: the item that ends here and began before ----
   if (!a.whole && threadIdx.x == 0) {
     TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
-    Walk<kBN> walk(p, sh);
+    Walk walk(p, sh);
     Seg sg;
     if (walk.next(sg) && !sg.first && sg.last) {
       // The block that holds unit u is the last c with c total / G <= u.
@@ -1075,10 +1096,10 @@ bool make_cache_map(CUtensorMap* m, const void* base, int D, int n_kv, int rows,
 
 template <int D, int VAR, bool WIDE>
 cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
-  using L = TreeSmem<D, WIDE>;
+  using L = TreeSmem<D>;
   TreeKParams p;
   p.a = a;
-  const int g = a.n_q_heads / a.n_kv_heads;
+  const int g = p.g = a.n_q_heads / a.n_kv_heads;
   p.q_tiles = std::min(row_tiles<D>(), (std::min(a.total_nodes, kMostNodes) * g + 127) / 128);
   p.slots = L::slots(p.q_tiles);
   p.sl2 = a.scale * kLog2e;
@@ -1086,12 +1107,12 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   p.cap_l2 = a.softcap * kLog2e;
   p.err_word = ctx.err_word;
   p.timeout_ns = ctx.timeout_ns;
-  // Tiled copies where blocks are made of boxes of 8, 16, 32 or 64 rows (a box has to start at
+  // Tiled copies where blocks are made of boxes of 8, 16 or 32 rows (a box has to start at
   // a swizzle atom of 8 rows), half a key tile at most.
   CUtensorMap mk, mv;
   std::memset(&mk, 0, sizeof(mk));
   std::memset(&mv, 0, sizeof(mv));
-  p.box = L::kBN / 2;
+  p.box = kMostBox;
   if (a.block_table)
     while (p.box >= 8 && a.block_size % p.box != 0) p.box /= 2;
   if (p.box >= 8) {
