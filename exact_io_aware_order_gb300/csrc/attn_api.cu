@@ -727,7 +727,7 @@ TreePlan tree_plan(int total_nodes, int n_q_heads, int n_kv_heads, int head_dim,
                    int max_kv_len, int window_left, int num_sms) {
   TreePlan t{};
   const int g = n_q_heads / n_kv_heads;
-  t.part_rows = attn::decode_tree_part_rows(head_dim, std::min(total_nodes, kMostNodes) * g);
+  t.part_rows = attn::decode_tree_part_rows(head_dim, g, std::min(total_nodes, kMostNodes));
   t.blocks = std::min(std::max(num_sms, 1), 256);  // (what the join counts through)
   long long keys = max_kv_len;
   if (window_left >= 0) keys = std::min(keys, window_left + 1LL + kMostNodes);

@@ -280,8 +280,8 @@ cudaError_t launch_combine_fp8(const DecodeFp8Args& a, const LaunchCtx& ctx);
 int decode_fp8_max_parts(int head_dim, int num_sms);
 
 cudaError_t launch_rope(const RopeArgs& a, const LaunchCtx& ctx);
-// Rows of a partial (max_rows: the most that a kv head can have).
-int decode_tree_part_rows(int head_dim, int max_rows);
+// Rows of a partial; group: query heads of a kv head, max_nodes: the most of a sequence.
+int decode_tree_part_rows(int head_dim, int group, int max_nodes);
 cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_cache_append(const RopeArgs& a, const LaunchCtx& ctx);

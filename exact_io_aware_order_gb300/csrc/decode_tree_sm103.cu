@@ -14,6 +14,8 @@
 // path serves every size.
 //
 // Design:
+//   * a row tile holds the g rows of 128 / g nodes (so a tiled copy of queries is one box),
+//     an item two row tiles (one at head_dim 256);
 //   * persistent blocks, one an SM.  The work of all (sequence, kv head, row group)
 //     items is counted in key tiles on the device, from kv_lens and cu_nodes, and
 //     every block takes an equal run of them, across items; an item that is cut
@@ -21,29 +23,24 @@
 //     kernel joins.  A block starts at most one cut item in its run and ends at most
 //     one, so there are two places a block.  Short caches (by max_kv_len) go whole
 //     items to a block, without the second kernel;
-//   * two producer warps fill a ring of key and value tiles, 128-byte-swizzled as the MMAs
-//     read them: tiles of keys that all exist by tiled copies (TMA), a box for each run of
-//     rows inside a block; tiles that end early, or begin in front of a window, and block
-//     sizes that are no multiple of 8, by 16-byte copies (cp.async) of rows from wherever
-//     the block table says, with zeros for what is missing.  16 sequences of 1024 - 32768
-//     tokens, 32 heads: 314 us with the second way alone, where the two warps' issue rate
-//     was the limit.  Both announce themselves on the slot's barrier; the issuing threads
-//     fence what they then read against the async proxy;
+//   * a producer warp for keys (and queries) and one for values fill a ring of tiles,
+//     128-byte-swizzled as the MMAs read them: tiles of keys that all exist, in blocks of 32
+//     or more rows, by tiled copies (TMA); the others, and smaller blocks of any size, by
+//     16-byte copies (cp.async) of rows from wherever the block table says, with zeros for
+//     what is missing.  Both announce themselves on the slot's barrier; the issuing threads
+//     fence what the second kind wrote against the async proxy;
 //   * S = Q K^T and O += P V by two issuing threads, S in two TMEM buffers, P over
 //     S, one O a row tile; with two row tiles in an item they take turns, so the
 //     tensor cores work on one while the other is in the softmax;
-//   * the softmax is one row a thread, four warps a row tile, in two passes over S: the
-//     row maximum, then the exponentials (tiles of 64 keys stay in registers in between);
-//     two 32-column pieces are in registers at a time, and reading S twice costs 2 x 32
-//     clocks a warp.  ALiBi is a term of the argument, linear in the column, in both passes;
-//     masks (in tiles with nodes or a window's edge) and soft-capping are written back to S
-//     in a pass of their own, which keeps the code of the ordinary tile small: the
-//     warps run six roles, and unrolled code that is run once a tile is fetched anew each
-//     time.  P is announced in halves, so that its product begins under the second;
+//   * the softmax is one row a thread, four warps a row tile, 64 columns at a time, which
+//     stay in registers from the maximum to the exponentials (P overwrites columns that
+//     have been read).  A row's first maximum is the reference of its exponentials; it is
+//     raised, and O rescaled, only where scores outgrow it by 2^32, so that the tile after
+//     tile has neither a second look at S nor a wait for O.  P is announced in halves, so
+//     that its product begins under the second;
 //   * P is rounded to bf16 for a bf16 O (2^-8 of a weight, no more than O's own
 //     rounding), and split into three bf16 parts (2^-24) for an fp32 one;
-//   * row statistics, O and the partials are fp32; O is rescaled when a row's maximum
-//     has grown by more than 2^8 (exact: the same stale one is used for l and O);
+//   * row statistics, O and the partials are fp32;
 //   * every wait is bounded, as in the other kernels.
 #include <algorithm>
 #include <cstdint>
@@ -64,33 +61,45 @@ constexpr int kProducerThreads = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// How far (log2 units) scores may outgrow the reference of their row's exponentials before
+// it is raised and O rescaled: weights up to 2^32, and their sums, are as exact as those
+// up to 1 (floating point), and leave O room for values up to 2^60.
+constexpr float kRescaleThreshold = 32.0f;
 constexpr int kMostNodes = 64;
-constexpr int kMostBox = 32;
-constexpr int kBN = 64;                // keys of a tile
+constexpr int kMostBox = 64;
+constexpr int kLeastBox = 16;
 
-// Row tiles of an item.  TMEM (512 columns): an O of D columns a row tile, and S buffers in
-// what is left, up to four: 64 columns each, or with fp32 outputs 96 (three parts of P of 32).
+// Row tiles of an item, keys of a tile.  TMEM (512 columns): an O of D columns a row tile,
+// and S buffers in what is left: as many columns as keys, or with fp32 outputs 96 for 64 keys
+// (three parts of P of 32).  Tiles of 128 keys cost the issuing threads half the waits and
+// commits, some 100 clocks each, for a key: 16 sequences of 1024 - 32768 tokens, 32 heads, at
+// head_dim 128: 247 us against 305 with 64 and twice the buffers.
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
-template <bool WIDE> __host__ __device__ constexpr int s_pitch() { return WIDE ? 96 : 64; }
+template <int D, bool WIDE> __host__ __device__ constexpr int key_tile() {
+  return D == 256 || WIDE ? 64 : 128;
+}
+template <int D, bool WIDE> __host__ __device__ constexpr int s_pitch() {
+  return WIDE ? 96 : key_tile<D, WIDE>();
+}
 template <int D, bool WIDE> __host__ __device__ constexpr int s_bufs() {
-  return ((int)kTmemCols - row_tiles<D>() * D) / s_pitch<WIDE>() >= 4 ? 4 : 2;
+  return D == 256 && !WIDE ? 4 : D == 64 ? 3 : 2;
 }
 template <int D> __host__ __device__ constexpr int threads_of() {
   return row_tiles<D>() * kSoftmaxThreads + kProducerThreads + 64;
 }
 
-template <int D>
+template <int D, bool WIDE>
 struct TreeSmem {
+  static constexpr int kBN = key_tile<D, WIDE>();
   static constexpr int kQTileBytes = 128 * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;
   static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
   static constexpr int kChunkBytes = kBN * 128;
   static constexpr int kMaxSlots = 12;
-  // barriers: full / empty for each slot, q_empty, s_full[row tile][4], p_full[4], pv_done[4],
-  // o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item of fewer
+  // barriers: full / empty for each slot, q_empty, s_full[row tile][4], p_full[half][4],
+  // pv_done[4], o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item of fewer
   // rows would otherwise miss phases, and take an old one for its next.
-  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 8 + 4 + 4 + 2 + 2;
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 8 + 8 + 4 + 2 + 2;
   static constexpr int kMiscBytes = 1024;  // barriers, then the block's share of the work
   static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
   // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
@@ -107,7 +116,9 @@ struct TreeSmem {
 struct TreeKParams {
   DecodeTreeArgs a;
   int g;                // query heads of a kv head
+  int tile_nodes;       // nodes of a row tile: 128 / g (their g rows each)
   int q_tiles, slots;   // row tiles that an item may have here, ring slots
+  int blocks_a_tile, rest_a_tile;  // kBN tokens in blocks, and what is left
   int box;              // rows of a tiled copy's box; 0: no tiled copies
   float sl2;            // scale * log2(e)
   float cap_in, cap_l2; // soft-capping: scale / softcap, softcap * log2(e)
@@ -123,10 +134,11 @@ struct Seq {
   int first;      // first key that some node may see; keys are [first, end)
   int lo;         // where the key tiles begin, at or before `first`
   int tiles;      // key tiles, at least 1
-  int groups;     // row groups
+  int groups;     // groups of nodes, an item each
   bool bad_nodes, bad_len;
 };
 
+template <int kBN>
 __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   const DecodeTreeArgs& a = p.a;
   Seq s;
@@ -143,8 +155,8 @@ __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   s.first = a.window_left >= 0 ? max(0, s.kv_len - a.window_left) : 0;
   s.lo = s.first / kMostBox * kMostBox;
   s.tiles = max(1, (s.end - s.lo + kBN - 1) / kBN);
-  const int shift = 6 + p.q_tiles;  // rows of a group: 128 or 256
-  s.groups = (s.nodes * p.g + (1 << shift) - 1) >> shift;
+  const int group = p.tile_nodes * p.q_tiles;
+  s.groups = (s.nodes + group - 1) / group;
   return s;
 }
 
@@ -170,12 +182,13 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 // A run of key tiles of one item.
 struct Seg {
   Seq s;
-  int b, kvh, row0, rows, nr;  // rows [row0, row0 + rows) of the kv head, row tiles
+  int b, kvh, node0, nodes, nr;  // nodes [node0, node0 + nodes) of the kv head, row tiles
   int t0, tiles;               // key tiles [t0, t0 + tiles)
   bool first, last;            // whether it starts and ends its item
   long long item_u0;           // the item's first unit
 };
 
+template <int kBN>
 struct Walk {
   const TreeKParams& p;
   long long u, u1, base;
@@ -189,20 +202,20 @@ struct Walk {
     while (u >= base + n) {
       if (b + 1 >= p.a.batch) return false;  // (lengths that changed under the call)
       base += n;
-      s = seq_of(p, ++b);
+      s = seq_of<kBN>(p, ++b);
       n = units_of(p, s);
     }
     const int T = p.a.whole ? 1 : s.tiles;
     const long long local = u - base;
     const int item = (int)quotient(local, T), t = (int)(local - (long long)item * T);
-    const int rows = 128 * p.q_tiles;
+    const int group = p.tile_nodes * p.q_tiles;
     const int n_units = (int)min((long long)(T - t), u1 - u);
     g.s = s;
     g.b = b;
     g.kvh = item / s.groups;
-    g.row0 = (item - g.kvh * s.groups) * rows;
-    g.rows = min(rows, s.nodes * p.g - g.row0);
-    g.nr = (g.rows + 127) / 128;
+    g.node0 = (item - g.kvh * s.groups) * group;
+    g.nodes = min(group, s.nodes - g.node0);
+    g.nr = (g.nodes + p.tile_nodes - 1) / p.tile_nodes;
     g.t0 = t;
     g.tiles = p.a.whole ? s.tiles : n_units;
     g.first = t == 0;
@@ -225,22 +238,34 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 
 // 32 rows of D values into a tile of 128-byte-swizzled spans (rows row0 ...): lane i's
 // `row` is the place of row i in units of `pitch` values behind `base`, -1 for zeros.
-template <int D>
-__device__ __forceinline__ void copy_rows(uint32_t tile, int chunk_bytes, int row0,
-                                          const uint16_t* base, long long pitch, int row,
-                                          int lane) {
+template <int D, int kBN>
+__device__ __forceinline__ void copy_rows(uint32_t tile, int row0, const uint16_t* base,
+                                          long long pitch, int row, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a row, rows at a time
+  constexpr int kBatch = 8;  // all shuffles of a batch in front of its copies, which overlap then
   const int c = lane % kLanes, r = lane / kLanes;
-  const uint32_t dst0 = tile + (c >> 3) * chunk_bytes;
+  const uint32_t dst0 = tile + (c >> 3) * kBN * 128;
   base += c * 8;
-#pragma unroll 8
-  for (int i = 0; i < kLanes; ++i) {
-    const int k = i * kRows + r;
-    const int src = __shfl_sync(0xffffffffu, row, k);
-    const int at = row0 + k;
-    cp_async16_or_zero(dst0 + at * 128 + (((c & 7) ^ (at & 7)) << 4),
-                       base + max(src, 0) * pitch, src >= 0);
+#pragma unroll 1
+  for (int i = 0; i < kLanes; i += kBatch) {
+    int src[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) src[u] = __shfl_sync(0xffffffffu, row, (i + u) * kRows + r);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int at = row0 + (i + u) * kRows + r;
+      cp_async16_or_zero(dst0 + at * 128 + (((c & 7) ^ (at & 7)) << 4),
+                         base + max(src[u], 0) * pitch, src[u] >= 0);
+    }
   }
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
 }
 
 // Ties registers that tcgen05.ld filled to the wait in front of it: what reads them stays
@@ -276,6 +301,10 @@ __device__ __forceinline__ void store_32B(void* dst, const uint32_t (&y)[8 * N])
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n)
                : "memory");
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -326,10 +355,10 @@ __device__ __forceinline__ void soft_cap(uint32_t (&x)[32], float in, float out)
 
 template <int D, int VAR, bool WIDE>
 __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
-    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-    const __grid_constant__ TreeKParams p) {
-  using L = TreeSmem<D>;
-  constexpr int kPitch = s_pitch<WIDE>(), SB = s_bufs<D, WIDE>(), NQ = row_tiles<D>(), kThreads = threads_of<D>();
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeKParams p) {
+  using L = TreeSmem<D, WIDE>;
+  constexpr int kBN = L::kBN, kPitch = s_pitch<D, WIDE>(), SB = s_bufs<D, WIDE>(), NQ = row_tiles<D>(), kThreads = threads_of<D>();
   constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
   static_assert(SB * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
   const DecodeTreeArgs& a = p.a;
@@ -343,7 +372,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
-                kPFull = kSFull + 8, kPVDone = kPFull + 4, kOFull = kPVDone + 4,
+                kPFull = kSFull + 8, kPVDone = kPFull + 8, kOFull = kPVDone + 4,
                 kDrain = kOFull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
@@ -355,7 +384,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     for (int i = 0; i < slots; ++i) {
-      mbar_init(bar(kFull + i), kProducerThreads);
+      mbar_init(bar(kFull + i), 32);
       mbar_init(bar(kEmpty + i), 1);
     }
     mbar_init(bar(kQEmpty), 1);
@@ -363,6 +392,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kSFull + 4 + i), 1);
       mbar_init(bar(kPFull + i), kSoftmaxThreads);
+      mbar_init(bar(kPFull + 4 + i), kSoftmaxThreads);
       mbar_init(bar(kPVDone + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -371,9 +401,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     }
     fence_mbar_init();
   }
-  if (warp == kProducerWarp && lane == 0 && p.box > 0) {
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tmap(&tm_q);
+    if (p.box > 0) {
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
   }
   if (warp == kSWarp) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -389,7 +422,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     long long mine = 0;
     bool bad_nodes = false, bad_len = false;
     for (int b = b0; b < b1; ++b) {
-      const Seq s = seq_of(p, b);
+      const Seq s = seq_of<kBN>(p, b);
       mine += units_of(p, s);
       bad_nodes |= s.bad_nodes;
       bad_len |= s.bad_len;
@@ -428,12 +461,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     __syncthreads();
     if (u0 < u1 && u0 >= at && u0 < at + mine) {
       int b = b0;
-      Seq s = seq_of(p, b);
+      Seq s = seq_of<kBN>(p, b);
       while (b + 1 < b1) {
         const long long n = units_of(p, s);
         if (u0 < at + n) break;
         at += n;
-        s = seq_of(p, ++b);
+        s = seq_of<kBN>(p, ++b);
       }
       share->b0 = b;
       share->base0 = at;
@@ -467,146 +500,152 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
 
   if (warp >= kProducerWarp && warp < kSWarp) {
     // ============================ producers ============================
-    // Each warp copies half the rows of every tile.  A lane finds the place of its own rows
-    // (one look into the block table), the others get it by shuffles.
-    constexpr int kHalf = kBN / 2, kSets = kHalf / 32;     // rows of a warp, in sets of 32
-    const int half = warp - kProducerWarp;
-    int issued = 0, slot = 0, phase = 0, n_seg = 0;
-    Walk walk(p, sh);
+    // The first warp fills the keys' slots (and the queries), the second the values'.
+    const bool keys = warp == kProducerWarp;
+    const CUtensorMap* map = keys ? &tm_k : &tm_v;
+    const uint16_t* cache = keys ? a.k_cache : a.v_cache;
+    constexpr int kSpans = D / 64, kSets = kBN / 32;
+    int slot = keys ? 0 : 1, phase = 0, n_seg = 0, issued = 0;
+    bool again = false;                                    // slots have been used before
+    Walk<kBN> walk(p, sh);
     Seg sg;
     bool ok = true;
     while (ok && walk.next(sg)) {
       const int32_t* table =
           a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
-      // Q: row i of the kv head is node i / g, head i % g.  The last segment's S products
-      // have to be through with it.  It counts as landed with the first keys, whose arrivals
-      // wait for all copies so far.
-      auto copy_q = [&]() -> bool {
-        if (n_seg > 0 && !mbar_wait_warp(bar(kQEmpty), (n_seg - 1) & 1, ctl)) return false;
-        ++n_seg;
-        for (int set = half; set < 4 * sg.nr; set += 2) {
-          const int i = set * 32 + lane, row = sg.row0 + i, node = row / g;
-          const int src =
-              i < sg.rows ? (sg.s.q0 + node) * a.n_q_heads + sg.kvh * g + (row - node * g) : -1;
-          copy_rows<D>(smem_u32(smem + (set >> 2) * L::kQTileBytes), L::kQChunkBytes,
-                       (set & 3) * 32, a.q, D, src, lane);
-        }
-        return true;
-      };
-      // Tiled copies: where box `lane` of this warp's rows lies (a look ahead, so that the
-      // block table's latency is not in the way).
-      constexpr int kSpans = D / 64, kBoxes = kHalf / 8;
-      const bool mine = lane * p.box < kHalf && p.box > 0;
-      int next_row = 0, next_plane = 0;
-      auto look = [&](int t) {
-        if (!mine || t >= sg.tiles || !tiled(sg, t)) return;
-        const int tok = first_key(sg, t) + half * kHalf + lane * p.box;
-        if (table == nullptr) {
-          next_row = tok;
-          next_plane = sg.b;
-        } else {
-          const int j = tok / a.block_size;
-          next_row = tok - j * a.block_size;
-          next_plane = table[j];
-        }
-      };
-      look(0);
-      for (int t = 0; t < sg.tiles && ok; ++t) {
-        const int tok0 = first_key(sg, t) + half * kHalf;
-        if (tiled(sg, t)) {
-          if (table != nullptr && mine && (next_plane < 0 || next_plane >= a.num_blocks)) {
-            // A bad block becomes one past the cache, which reads as zeros.
-            atomicOr(p.err_word, kErrBlockIndex);
-            next_plane = a.num_blocks;
-          }
-          // One thread issues them all, from straight code: a lane each costs 140 clocks a
-          // copy, lane after lane.
-          int c2[kBoxes], c3[kBoxes];
-#pragma unroll
-          for (int i = 0; i < kBoxes; ++i) {
-            c2[i] = __shfl_sync(0xffffffffu, next_row, i);
-            c3[i] = __shfl_sync(0xffffffffu, next_plane, i);
-          }
-          look(t + 1);
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            if (issued >= slots && !mbar_wait_warp(bar(kEmpty + slot), phase ^ 1, ctl)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              mbar_expect_tx(bar(kFull + slot), kHalf * D * 2);
-              const CUtensorMap* map = kv ? &tm_v : &tm_k;
-              const uint32_t dst = smem_u32(ring + slot * L::kTileBytes) + half * kHalf * 128;
-#pragma unroll
-              for (int i = 0; i < kBoxes; ++i) {
-                if (i * p.box >= kHalf) break;
-#pragma unroll
-                for (int span = 0; span < kSpans; ++span)
-                  tma_load_4d(dst + span * L::kChunkBytes + i * p.box * 128, map, bar(kFull + slot),
-                              span * 64, sg.kvh, c2[i], c3[i]);
-              }
-            }
-            __syncwarp();
-            if (t == 0 && kv == 0 && !copy_q()) ok = false;
-            cp_async_arrive(bar(kFull + slot));
-            ++issued;
-            if (++slot == slots) slot = 0, phase ^= 1;
-          }
-          continue;
-        }
-        look(t + 1);
-        int row[kSets];  // cache rows (a token of all kv heads); -1: none
-        int blk[kSets];
+      // Where this lane's rows of a tile (lane, lane + 32, ..) lie: the block's number in the
+      // table, the row in it, and what the table says.  The table is read a tile ahead, so
+      // that its latency is not in the way.
+      int blk[kSets], row_in[kSets], entry[kSets];
+      auto look = [&](int tile0) {
 #pragma unroll
         for (int i = 0; i < kSets; ++i) {
-          const int tok = tok0 + lane + i * 32;
-          const bool real = tok >= sg.s.first && tok < sg.s.end;
-          row[i] = -1;
-          blk[i] = 0;
-          if (table == nullptr) {
-            if (real) row[i] = sg.b * a.max_kv_len + tok;
-          } else if (real) {
-            const int j = tok / a.block_size;
-            blk[i] = table[j];
-            row[i] = tok - j * a.block_size;
-          }
+          const int tok = tile0 + lane + 32 * i;
+          if (table != nullptr && tok >= sg.s.first && tok < sg.s.end) entry[i] = table[blk[i]];
         }
+      };
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        blk[i] = entry[i] = 0;
+        row_in[i] = first_key(sg, 0) + lane + 32 * i;
         if (table != nullptr) {
-#pragma unroll
-          for (int i = 0; i < kSets; ++i) {
-            if (row[i] >= 0) {
-              const bool good = blk[i] >= 0 && blk[i] < a.num_blocks;
-              if (!good) atomicOr(p.err_word, kErrBlockIndex);
-              row[i] = good ? blk[i] * a.block_size + row[i] : -1;
-            }
-          }
-        }
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          if (issued >= slots && !mbar_wait_warp(bar(kEmpty + slot), phase ^ 1, ctl)) {
-            ok = false;
-            break;
-          }
-          const uint32_t tile = smem_u32(ring + slot * L::kTileBytes);
-#pragma unroll
-          for (int i = 0; i < kSets; ++i)
-            copy_rows<D>(tile, L::kChunkBytes, half * kHalf + i * 32,
-                         (kv ? a.v_cache : a.k_cache) + (size_t)sg.kvh * D,
-                         (long long)a.n_kv_heads * D, row[i], lane);
-          if (t == 0 && kv == 0 && !copy_q()) ok = false;
-          cp_async_arrive(bar(kFull + slot));
-          ++issued;
-          if (++slot == slots) slot = 0, phase ^= 1;
+          blk[i] = row_in[i] / a.block_size;
+          row_in[i] -= blk[i] * a.block_size;
         }
       }
+      look(first_key(sg, 0));
+      for (int t = 0; t < sg.tiles && ok; ++t) {
+        const int tile0 = first_key(sg, t);
+        const uint32_t dst = smem_u32(ring + slot * L::kTileBytes), full = bar(kFull + slot);
+        // (every lane waits: a warp that one lane kept waiting copies rows ten times slower)
+        if (again && !mbar_wait_warp(bar(kEmpty + slot), phase ^ 1, ctl)) { ok = false; break; }
+        const bool q_too = keys && t == 0;
+        // The last segment's S products have to be through with Q.
+        if (q_too && n_seg > 0 && !mbar_wait_warp(bar(kQEmpty), (n_seg - 1) & 1, ctl)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0 && q_too) {
+          // Queries: tile_nodes nodes' g rows a row tile (rows past the nodes are not used).
+          mbar_expect_tx(full, (uint32_t)(sg.nr * p.tile_nodes * g) * D * 2);
+          for (int r = 0; r < sg.nr; ++r)
+            for (int span = 0; span < kSpans; ++span)
+              tma_load_3d(smem_u32(smem + r * L::kQTileBytes + span * L::kQChunkBytes), &tm_q, full,
+                          span * 64, sg.kvh * g, sg.s.q0 + sg.node0 + r * p.tile_nodes);
+        }
+        int plane[kSets];
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+          const int tok = tile0 + lane + 32 * i;
+          plane[i] = table ? entry[i] : sg.b;
+          if (table != nullptr && tok >= sg.s.first && tok < sg.s.end &&
+              (plane[i] < 0 || plane[i] >= a.num_blocks)) {
+            atomicOr(p.err_word, kErrBlockIndex);
+            plane[i] = -1;
+          }
+        }
+        if (tiled(sg, t)) {
+          // One lane issues them all.  Boxes of 32 rows or more begin where its own rows are,
+          // those of 16 also where lane 16's are.  A bad block becomes one past the cache,
+          // which reads as zeros.
+          const bool small = p.box == 16;
+          int row2[kSets], plane2[kSets];
+          if (small) {
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) {
+              row2[i] = __shfl_sync(0xffffffffu, row_in[i], 16);
+              plane2[i] = __shfl_sync(0xffffffffu, plane[i], 16);
+            }
+          }
+          if (lane == 0) {
+            mbar_expect_tx(full, kBN * D * 2);
+            auto at = [&](int plane) { return plane < 0 ? a.num_blocks : plane; };
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) {
+              if (!small && (i & (p.box / 32 - 1))) continue;
+#pragma unroll
+              for (int span = 0; span < kSpans; ++span) {
+                const uint32_t to = dst + span * L::kChunkBytes + i * 32 * 128;
+                tma_load_4d(to, map, full, span * 64, sg.kvh, row_in[i], at(plane[i]));
+                if (small)
+                  tma_load_4d(to + 16 * 128, map, full, span * 64, sg.kvh, row2[i], at(plane2[i]));
+              }
+            }
+            mbar_arrive_n(full, 32);
+          }
+          __syncwarp();
+        } else {
+          // Row by row, 16 bytes a lane, zeros for rows that are not there.
+          const int rows = table ? a.block_size : a.max_kv_len;
+#pragma unroll 1
+          for (int i = 0; i < kSets; ++i) {
+            const int tok = tile0 + lane + 32 * i;
+            int at = plane[0], in = row_in[0];
+#pragma unroll
+            for (int k = 1; k < kSets; ++k)
+              if (i == k) at = plane[k], in = row_in[k];
+            const int row = tok >= sg.s.first && tok < sg.s.end && at >= 0 ? at * rows + in : -1;
+            copy_rows<D, kBN>(dst, i * 32, cache + (size_t)sg.kvh * D, (long long)a.n_kv_heads * D, row,
+                         lane);
+          }
+          cp_async_arrive(full);
+        }
+        ++issued;
+        // The next tile of the walk.
+        const int step = VAR == kAlibi ? -1 : 1;
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+          if (table == nullptr) {
+            row_in[i] += step * kBN;
+          } else {
+            blk[i] += step * p.blocks_a_tile;
+            row_in[i] += step * p.rest_a_tile;
+            if (row_in[i] >= a.block_size) row_in[i] -= a.block_size, ++blk[i];
+            if (row_in[i] < 0) row_in[i] += a.block_size, --blk[i];
+          }
+        }
+        if (t + 1 < sg.tiles) look(first_key(sg, t + 1));
+        for (int i = 0; i < 2; ++i)
+          if (++slot == slots) slot = 0, phase ^= 1, again = true;
+      }
+      ++n_seg;
     }
     cp_async_commit();
     cp_async_wait<0>();
+    if (*abort_flag && lane == 0) {
+      // Tiled copies in flight land before the block's memory is released.
+      volatile uint32_t no_abort = 0u;
+      WaitCtl drain{&no_abort, p.err_word, p.timeout_ns};
+      for (int i = max(0, issued - (slots + 1) / 2); i < issued; ++i) {
+        const int at = 2 * i + (keys ? 0 : 1);
+        mbar_wait(bar(kFull + at % slots), (at / slots) & 1, drain);
+      }
+    }
+    __syncwarp();
   } else if (warp == kSWarp) {
     // ============================ S = Q K^T issuer ============================
     if (lane == 0) {
-      Walk walk(p, sh);
+      Walk<kBN> walk(p, sh);
       Seg sg;
       bool ok = true;
       int n = 0, slot = 0, phase = 0;
@@ -614,8 +653,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       while (ok && walk.next(sg)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
-          // The 16-byte copies' writes (Q's among them), before the MMAs that read them.
-          if (t == 0 || !tiled(sg, t)) fence_proxy_async_smem();
+          // The 16-byte copies' writes, before the MMAs that read them.
+          if (!tiled(sg, t)) fence_proxy_async_smem();
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n % SB;
@@ -648,28 +687,33 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   } else if (warp == kPVWarp) {
     // ============================ O += P V issuer ============================
     if (lane == 0) {
-      Walk walk(p, sh);
+      Walk<kBN> walk(p, sh);
       Seg sg;
       bool ok = true;
       int n = 0, slot = 1, phase = 0;
       while (ok && walk.next(sg)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
-          // The 16-byte copies' writes (Q's among them), before the MMAs that read them.
-          if (t == 0 || !tiled(sg, t)) fence_proxy_async_smem();
+          // The 16-byte copies' writes, before the MMAs that read them.
+          if (!tiled(sg, t)) fence_proxy_async_smem();
           const uint32_t v_lo =
               sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n % SB;
-            if (!mbar_wait(bar(kPFull + b), (n / SB) & 1, ctl)) { ok = false; break; }
-            tc_fence_after();
+            // P comes in halves of 64 keys.
             const uint32_t aP = tmem + b * kPitch, tOr = tO + r * D;
 #pragma unroll
-            for (int part = 0; part < (WIDE ? 3 : 1); ++part)
+            for (int h = 0; h < kBN / 64; ++h) {
+              if (!mbar_wait(bar(kPFull + 4 * h + b), (n / SB) & 1, ctl)) { ok = false; break; }
+              tc_fence_after();
 #pragma unroll
-              for (int kk = 0; kk < kBN / 16; ++kk)
-                mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
-                          id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
+              for (int part = 0; part < (WIDE ? 3 : 1); ++part)
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                  mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
+                            id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
+            }
+            if (!ok) break;
             mma_commit(bar(kPVDone + b));
             if (t == sg.tiles - 1) mma_commit(bar(kOFull + r));
           }
@@ -690,16 +734,18 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int trow = (warp & 3) * 32 + lane;                // row within the tile (TMEM lane)
     int* depths = depth_tab + warp * kMostNodes;            // the nodes' depths, each warp its own
-    Walk walk(p, sh);
+    Walk<kBN> walk(p, sh);
     Seg sg;
     bool ok = true;
     int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
     uint32_t s_phase = 0;   // s_full's phase, a bit for each buffer
     for (; ok && walk.next(sg); n0 += sg.tiles * sg.nr) {
       if (r >= sg.nr) continue;
-      const int i = r * 128 + trow;                         // row of the group
-      const bool real = i < sg.rows;
-      const int node = (sg.row0 + i) / g, head = sg.kvh * g + (sg.row0 + i) % g;
+      const int in_tile = trow / g;                         // this row's node in the row tile
+      const int node = sg.node0 + r * p.tile_nodes + in_tile;
+      const int head = sg.kvh * g + (trow - in_tile * g);
+      const bool real = in_tile < p.tile_nodes && node < sg.node0 + sg.nodes;
+      const int i = (r * p.tile_nodes + in_tile) * g + (trow - in_tile * g);  // row of the group
       // The nodes this row sees.
       const unsigned long long all =
           sg.s.nodes >= 64 ? ~0ull : (1ull << sg.s.nodes) - 1ull;
@@ -755,46 +801,57 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         if constexpr (VAR == kAlibi) {
           slope = slope_l2;
           base = -slope_l2 * (float)(pos - kv0);
+          if (edge) sl2 = 1.f, slope = 0.f, base = 0.f;
         }
-        // Soft-capping, masks, and ALiBi where nodes are among the keys, of 32 columns.
-        auto dress = [&](uint32_t (&x)[32], int c) {
-          if constexpr (VAR == kCap) soft_cap(x, p.cap_in, p.cap_l2);
-          if (edge) {
-            if constexpr (VAR == kAlibi) {
-              const float d0 = (float)(pos - kv0 - 32 * c);
-              const int u0 = kv0 + 32 * c - sg.s.kv_len;    // node of the first column
+        const bool ahead = edge || (VAR == kCap && kBN > 64);
+        if (ahead) {
+          // Soft-capping, masks, and ALiBi where nodes are among the keys: a pass of its own,
+          // written back.
+#pragma unroll 1
+          for (int c = 0; c < kBN / 32; ++c) {
+            uint32_t y[32];
+            tmem_ld32(tS + c * 32, y);
+            tmem_wait_ld();
+            landed(y);
+            if constexpr (VAR == kCap) soft_cap(y, p.cap_in, p.cap_l2);
+            if (edge) {
+              if constexpr (VAR == kAlibi) {
+                const float d0 = (float)(pos - kv0 - 32 * c);
+                const int u0 = kv0 + 32 * c - sg.s.kv_len;  // node of the first column
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float dist = u0 + k < 0 ? d0 - (float)k
-                                              : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
-                x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.sl2, -slope_l2 * dist));
+                for (int k = 0; k < 32; ++k) {
+                  const float dist = u0 + k < 0
+                                         ? d0 - (float)k
+                                         : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
+                  y[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), p.sl2, -slope_l2 * dist));
+                }
               }
+              uint32_t w = vis[0];
+#pragma unroll
+              for (int q = 1; q < kBN / 32; ++q)
+                if (c == q) w = vis[q];
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((w >> k) & 1u)) y[k] = 0xff800000u;   // -inf
             }
-            uint32_t w = vis[0];
-#pragma unroll
-            for (int q = 1; q < kBN / 32; ++q)
-              if (c == q) w = vis[q];
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((w >> k) & 1u)) x[k] = 0xff800000u;     // -inf
+            tmem_st32(tS + c * 32, y);
           }
-        };
-        if (VAR == kAlibi && edge) sl2 = 1.f, slope = 0.f, base = 0.f;
-        const float2 sl2v = make_float2(sl2, sl2), slopev = make_float2(slope, slope);
+          tmem_wait_st();
+        }
         // ---- the row's scores, and their maximum ----
-        uint32_t x[2][32];
-        tmem_ld32(tS, x[0]);
-        tmem_ld32(tS + 32, x[1]);
+        uint32_t x[kBN / 32][32];
+#pragma unroll
+        for (int c = 0; c < kBN / 32; ++c) tmem_ld32(tS + c * 32, x[c]);
         tmem_wait_ld();
-        landed(x[0]);
-        landed(x[1]);
+#pragma unroll
+        for (int c = 0; c < kBN / 32; ++c) landed(x[c]);
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kBN / 32; ++c) {
           uint32_t (&y)[32] = x[c];
-          if (VAR == kCap || edge) dress(y, c);
-          float mc[4];
+          if (VAR == kCap && !ahead) soft_cap(y, p.cap_in, p.cap_l2);
           if constexpr (VAR == kAlibi) {
+            const float2 sl2v = make_float2(sl2, sl2), slopev = make_float2(slope, slope);
             const float2 bv = make_float2(base, base);
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
@@ -805,6 +862,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
               y[k + 1] = __float_as_uint(e.y);
             }
           }
+          float mc[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
@@ -816,40 +874,43 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
         }
         if constexpr (VAR != kAlibi) mx *= sl2;
-        // ---- the reference: raised only when some row of the warp gained 2^8 ----
-        const float m_new = fmaxf(m, mx);
-        if (m == -INFINITY) m = m_new;  // nothing seen so far: O and l are 0
-        if (t > 0 && __any_sync(0xffffffffu, m_new - m > kRescaleThreshold)) {
+        // ---- the reference: the first maximum that a row sees; raised only when some row of the
+        // warp has outgrown it ----
+        if (m == -INFINITY) m = mx;                         // (O and l are 0)
+        if (__any_sync(0xffffffffu, mx - m > kRescaleThreshold)) {
+          const float m_new = fmaxf(m, mx);
           const float corr = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
           m = m_new;
           l *= corr;
-          const int pn = n - sg.nr;                         // this row tile's last product
-          if (!mbar_wait_warp(bar(kPVDone + pn % SB), (pn / SB) & 1, ctl)) { ok = false; break; }
-          tc_fence_after();
+          if (t > 0) {
+            const int pn = n - sg.nr;                       // this row tile's last product
+            if (!mbar_wait_warp(bar(kPVDone + pn % SB), (pn / SB) & 1, ctl)) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t y[16];
-            const uint32_t at = tO + r * D + lane_base + c * 16;
-            tmem_ld16(at, y);
-            tmem_wait_ld();
+            for (int c = 0; c < D / 8; ++c) {
+              uint32_t y[8];
+              const uint32_t at = tO + r * D + lane_base + c * 8;
+              tmem_ld8(at, y);
+              tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
-            tmem_st16(at, y);
+              for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
+              tmem_st8(at, y);
+            }
           }
         }
         const float nm = m == -INFINITY ? 0.f : -m;
         // ---- P over S ----
-        const float2 nmv = make_float2(nm, nm);
+        const float2 sl2w = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
         float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kBN / 32; ++c) {
           const uint32_t (&y)[32] = x[c];
           uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 v = make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
             // (ALiBi's scores are in log2 units already)
-            const float2 e = VAR == kAlibi ? add2(v, nmv) : fma2(v, sl2v, nmv);
+            const float2 e = VAR == kAlibi ? add2(v, nmv) : fma2(v, sl2w, nmv);
             float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             rs[k & 1] = add2(rs[k & 1], pp);
             hi[k] = pack_bf16x2(pp.x, pp.y);
@@ -866,10 +927,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             tmem_st16(tS + kBN / 2 + c * 16, mid);
             tmem_st16(tS + kBN + c * 16, lo);
           }
+          if (c & 1) {                                      // 64 keys of P are there
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(kPFull + 4 * (c >> 1) + b));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kPFull + b));
         const float2 rsum = add2(rs[0], rs[1]);
         l += rsum.x + rsum.y;
       }
@@ -916,15 +979,15 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   // ---- what the second kernel joins: the item that ends here and began before ----
   if (!a.whole && threadIdx.x == 0) {
     TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
-    Walk walk(p, sh);
+    Walk<kBN> walk(p, sh);
     Seg sg;
     if (walk.next(sg) && !sg.first && sg.last) {
       // The block that holds unit u is the last c with c total / G <= u.
       j.first_block =
           (int)(((sg.item_u0 + 1) * min((long long)gridDim.x, sh.total) - 1) / sh.total);
-      j.rows = sg.rows;
+      j.rows = sg.nodes * g;
       j.q0 = sg.s.q0;
-      j.row0 = sg.row0;
+      j.row0 = sg.node0 * g;
       j.kvh = sg.kvh;
     }
     a.joins[blockIdx.x] = j;
@@ -1094,28 +1157,49 @@ bool make_cache_map(CUtensorMap* m, const void* base, int D, int n_kv, int rows,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries (nodes, heads, D) bf16, boxes of 64 dims x heads x nodes.
+bool make_q_map(CUtensorMap* m, const void* base, int D, int n_q, int nodes, int box_heads,
+                int box_nodes) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)D * 2;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n_q, (cuuint64_t)nodes};
+  cuuint64_t strides[2] = {row, row * (cuuint64_t)n_q};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_nodes};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int VAR, bool WIDE>
 cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
-  using L = TreeSmem<D>;
+  using L = TreeSmem<D, WIDE>;
+  constexpr int kBN = L::kBN;
   TreeKParams p;
   p.a = a;
   const int g = p.g = a.n_q_heads / a.n_kv_heads;
-  p.q_tiles = std::min(row_tiles<D>(), (std::min(a.total_nodes, kMostNodes) * g + 127) / 128);
+  p.tile_nodes = 128 / g;
+  p.q_tiles = std::min(row_tiles<D>(), (std::min(a.total_nodes, kMostNodes) + p.tile_nodes - 1) /
+                                           p.tile_nodes);
   p.slots = L::slots(p.q_tiles);
   p.sl2 = a.scale * kLog2e;
   p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
   p.cap_l2 = a.softcap * kLog2e;
   p.err_word = ctx.err_word;
   p.timeout_ns = ctx.timeout_ns;
-  // Tiled copies where blocks are made of boxes of 8, 16 or 32 rows (a box has to start at
-  // a swizzle atom of 8 rows), half a key tile at most.
-  CUtensorMap mk, mv;
+  // Tiled copies where blocks are made of runs of 32 or 64 rows.  A tiled copy costs the SM's
+  // copy unit some 50 clocks and 2.5 for each row of 128 bytes: boxes of 16 rows come to the
+  // memory's rate only while the unit never idles, smaller ones not at all.
+  CUtensorMap mq, mk, mv;
+  if (!make_q_map(&mq, a.q, D, a.n_q_heads, a.total_nodes, g, p.tile_nodes))
+    return cudaErrorInvalidValue;
   std::memset(&mk, 0, sizeof(mk));
   std::memset(&mv, 0, sizeof(mv));
   p.box = kMostBox;
   if (a.block_table)
-    while (p.box >= 8 && a.block_size % p.box != 0) p.box /= 2;
-  if (p.box >= 8) {
+    while (p.box >= kLeastBox && a.block_size % p.box != 0) p.box /= 2;
+  if (p.box >= kLeastBox) {
     const int rows = a.block_table ? a.block_size : a.max_kv_len;
     const int planes = a.block_table ? a.num_blocks : a.batch;
     if (!make_cache_map(&mk, a.k_cache, D, a.n_kv_heads, rows, planes, p.box) ||
@@ -1124,6 +1208,8 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   } else {
     p.box = 0;
   }
+  p.blocks_a_tile = a.block_table ? kBN / a.block_size : 0;
+  p.rest_a_tile = a.block_table ? kBN % a.block_size : 0;
   auto kernel = decode_tree_kernel<D, VAR, WIDE>;
   static bool configured[64] = {};
   int dev = 0;
@@ -1144,7 +1230,7 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p);
   if (e != cudaSuccess || a.whole) return e;
   cfg.gridDim = dim3((unsigned)(4 * a.blocks));
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -1166,8 +1252,9 @@ cudaError_t launch_d(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
 
 }  // namespace
 
-int decode_tree_part_rows(int head_dim, int max_rows) {
-  return std::min(128 * (head_dim == 256 ? 1 : 2), max_rows);
+int decode_tree_part_rows(int head_dim, int group, int max_nodes) {
+  const int tile_nodes = 128 / group;
+  return std::min((head_dim == 256 ? 1 : 2) * tile_nodes, max_nodes) * group;
 }
 
 cudaError_t launch_decode_tree(const DecodeTreeArgs& a, const LaunchCtx& ctx) {

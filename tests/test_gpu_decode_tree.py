@@ -158,6 +158,27 @@ def test_long(dev, lens, nodes, block):
     attn.check_device_status()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scores_that_grow(dev, d, dtype):
+    """Maxima that rise by 30 nats every few keys, in rows' own places: the reference of the
+    exponentials is raised at tile borders and inside tiles, and O rescaled."""
+    c = Case(dev, [700, 40], [20, 64], 4, 1, d, 16, True, "any", seed=15)
+    for b, n in enumerate(c.lens):
+        k = torch.zeros_like(c.k[b])
+        step = torch.arange(len(k)) // 37
+        k[:, 0, 0] = (step.float() * 30 - 250).to(BF16)
+        k[:, 0, 1] = (-step.float() * 30).to(BF16)
+        c.k[b] = k
+        c.kc.view(-1, 1, d)[c.rows(b, len(k))] = k
+    c.q.zero_()
+    c.q[:, :, 0] = d ** 0.5
+    c.q[::3, :, 0], c.q[::3, :, 1] = 0.0, d ** 0.5            # every third row falls instead
+    c.check(*c.run(dtype))
+    c.check(*c.run(dtype, max_kv_len=800))
+    attn.check_device_status()
+
+
 def test_many_sequences(dev):
     n = 700
     lens, nodes = [(i * 37) % 300 for i in range(n)], [(i * 11) % 7 for i in range(n)]
