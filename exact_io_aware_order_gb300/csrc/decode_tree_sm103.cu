@@ -66,6 +66,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // up to 1 (floating point), and leave O room for values up to 2^60.
 constexpr float kRescaleThreshold = 32.0f;
 constexpr int kMostNodes = 64;
+constexpr int kSegSlots = 4;
 constexpr int kMostBox = 64;
 constexpr int kLeastBox = 16;
 
@@ -97,10 +98,10 @@ struct TreeSmem {
   static constexpr int kChunkBytes = kBN * 128;
   static constexpr int kMaxSlots = 12;
   // barriers: full / empty for each slot, q_empty, s_full[row tile][4], p_full[half][4],
-  // pv_done[4], o_full[2], drain[2].  s_full is a row tile's own: one that sits out an item of fewer
+  // pv_done[4], o_full[2], drain[2], full / empty for each segment slot.  s_full is a row tile's own: one that sits out an item of fewer
   // rows would otherwise miss phases, and take an old one for its next.
-  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 8 + 8 + 4 + 2 + 2;
-  static constexpr int kMiscBytes = 1024;  // barriers, then the block's share of the work
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 8 + 8 + 4 + 2 + 2 + 2 * kSegSlots;
+  static constexpr int kMiscBytes = 1024;  // barriers, then the segment slots
   static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
   // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
   static constexpr int slots(int q_tiles) {
@@ -118,6 +119,7 @@ struct TreeKParams {
   int g;                // query heads of a kv head
   int tile_nodes;       // nodes of a row tile: 128 / g (their g rows each)
   int q_tiles, slots;   // row tiles that an item may have here, ring slots
+  int unit_shift;       // a unit of work is 2^unit_shift key tiles
   int blocks_a_tile, rest_a_tile;  // kBN tokens in blocks, and what is left
   int box;              // rows of a tiled copy's box; 0: no tiled copies
   float sl2;            // scale * log2(e)
@@ -160,72 +162,24 @@ __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   return s;
 }
 
-// Units of work of a sequence: key tiles, or items where items go whole.
-__device__ __forceinline__ long long units_of(const TreeKParams& p, const Seq& s) {
-  return (long long)p.a.n_kv_heads * s.groups * (p.a.whole ? 1 : s.tiles);
+// Units of work of an item: runs of 2^unit_shift key tiles, or one where items go whole.
+__device__ __forceinline__ uint32_t item_units(const TreeKParams& p, const Seq& s) {
+  return p.a.whole ? 1u : (uint32_t)(s.tiles + (1 << p.unit_shift) - 1) >> p.unit_shift;
+}
+__device__ __forceinline__ uint32_t units_of(const TreeKParams& p, const Seq& s) {
+  return (uint32_t)(p.a.n_kv_heads * s.groups) * item_units(p, s);
 }
 
-// This block's run of units, in shared memory: [u0, u1) of total, beginning in
-// sequence b0, whose units start at base0.
-struct Share {
-  long long u0, u1, total, base0;
-  int b0;
-  Seq s0;  // sequence b0
+// A run of key tiles of one item, as the roles get it.
+struct alignas(16) Seg {
+  int b, kvh, q0, seq_nodes;   // sequence, kv head, its first packed row, its nodes
+  int kv_len, end, first, lo;  // as Seq
+  int node0, nodes, nr;        // nodes [node0, node0 + nodes) and their row tiles
+  int t0, tiles;               // key tiles [t0, t0 + tiles); none: the end
+  int place;                   // 0: a partial of an item that began before, 1: of one that begins
+                               // here, 2: a whole item
+  int pad0, pad1;
 };
-
-// Whole-number quotients, in 32 bits where both numbers are.
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-  return x / y;
-}
-
-// A run of key tiles of one item.
-struct Seg {
-  Seq s;
-  int b, kvh, node0, nodes, nr;  // nodes [node0, node0 + nodes) of the kv head, row tiles
-  int t0, tiles;               // key tiles [t0, t0 + tiles)
-  bool first, last;            // whether it starts and ends its item
-  long long item_u0;           // the item's first unit
-};
-
-template <int kBN>
-struct Walk {
-  const TreeKParams& p;
-  long long u, u1, base;
-  int b;
-  Seq s;
-  __device__ Walk(const TreeKParams& p_, const Share& sh)
-      : p(p_), u(sh.u0), u1(sh.u1), base(sh.base0), b(sh.b0), s(sh.s0) {}
-  __device__ bool next(Seg& g) {
-    if (u >= u1) return false;
-    long long n = units_of(p, s);
-    while (u >= base + n) {
-      if (b + 1 >= p.a.batch) return false;  // (lengths that changed under the call)
-      base += n;
-      s = seq_of<kBN>(p, ++b);
-      n = units_of(p, s);
-    }
-    const int T = p.a.whole ? 1 : s.tiles;
-    const long long local = u - base;
-    const int item = (int)quotient(local, T), t = (int)(local - (long long)item * T);
-    const int group = p.tile_nodes * p.q_tiles;
-    const int n_units = (int)min((long long)(T - t), u1 - u);
-    g.s = s;
-    g.b = b;
-    g.kvh = item / s.groups;
-    g.node0 = (item - g.kvh * s.groups) * group;
-    g.nodes = min(group, s.nodes - g.node0);
-    g.nr = (g.nodes + p.tile_nodes - 1) / p.tile_nodes;
-    g.t0 = t;
-    g.tiles = p.a.whole ? s.tiles : n_units;
-    g.first = t == 0;
-    g.last = t + n_units == T;
-    g.item_u0 = base + (long long)item * T;
-    u += n_units;
-    return true;
-  }
-};
-
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(real ? 16 : 0)
@@ -358,7 +312,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeKParams p) {
   using L = TreeSmem<D, WIDE>;
-  constexpr int kBN = L::kBN, kPitch = s_pitch<D, WIDE>(), SB = s_bufs<D, WIDE>(), NQ = row_tiles<D>(), kThreads = threads_of<D>();
+  constexpr int kBN = L::kBN, kPitch = s_pitch<D, WIDE>(), SB = s_bufs<D, WIDE>(), NQ = row_tiles<D>();
   constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
   static_assert(SB * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
   const DecodeTreeArgs& a = p.a;
@@ -373,12 +327,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
                 kPFull = kSFull + 8, kPVDone = kPFull + 8, kOFull = kPVDone + 4,
-                kDrain = kOFull + 2;
+                kDrain = kOFull + 2, kSegFull = kDrain + 2, kSegEmpty = kSegFull + kSegSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
-  Share* share = reinterpret_cast<Share*>(misc + L::kNumBars * 8 + 16);
-  long long* warp_sums = reinterpret_cast<long long*>(share + 1);  // one a warp
-  static_assert(L::kNumBars * 8 + 16 + sizeof(Share) + 16 * 8 <= L::kMiscBytes, "misc");
+  constexpr int kSegOffset = (L::kNumBars * 8 + 16 + 15) / 16 * 16;
+  Seg* segs = reinterpret_cast<Seg*>(misc + kSegOffset);
+  static_assert(kSegOffset + kSegSlots * sizeof(Seg) <= L::kMiscBytes, "misc");
   int* depth_tab = reinterpret_cast<int*>(misc + L::kMiscBytes);
 
   if (threadIdx.x == 0) {
@@ -399,6 +353,10 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       mbar_init(bar(kOFull + i), 1);
       mbar_init(bar(kDrain + i), 1);
     }
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(bar(kSegFull + i), 1);
+      mbar_init(bar(kSegEmpty + i), 3 + 4 * NQ);  // the values' producer, two issuers, softmax warps
+    }
     fence_mbar_init();
   }
   if (warp == kProducerWarp && lane == 0) {
@@ -415,85 +373,38 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- this block's share: each thread counts the units of a run of sequences ----
-  {
-    const int per = (a.batch + kThreads - 1) / kThreads;
-    const int b0 = min((int)threadIdx.x * per, a.batch), b1 = min(b0 + per, a.batch);
-    long long mine = 0;
-    bool bad_nodes = false, bad_len = false;
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = seq_of<kBN>(p, b);
-      mine += units_of(p, s);
-      bad_nodes |= s.bad_nodes;
-      bad_len |= s.bad_len;
-    }
-    if (blockIdx.x == 0) {
-      if (bad_nodes) atomicOr(p.err_word, kErrSeqLens);
-      if (bad_len) atomicOr(p.err_word, kErrKvLen);
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const long long v = warp_sums[w];
-      if (w < warp) before += v;
-      total += v;
-    }
-    long long at = before + incl - mine;  // units in front of this thread's sequences
-    // Blocks beyond the units get none, so that those with some are neighbours.
-    const long long G = max(min((long long)gridDim.x, total), 1LL), c = blockIdx.x;
-    const long long u0 = c < G ? quotient(c * total, G) : total;
-    const long long u1 = c < G ? quotient((c + 1) * total, G) : total;
-    if (threadIdx.x == 0) {
-      share->u0 = u0;
-      share->u1 = u1;
-      share->total = total;
-      share->b0 = 0;
-      share->base0 = 0;
-    }
-    __syncthreads();
-    if (u0 < u1 && u0 >= at && u0 < at + mine) {
-      int b = b0;
-      Seq s = seq_of<kBN>(p, b);
-      while (b + 1 < b1) {
-        const long long n = units_of(p, s);
-        if (u0 < at + n) break;
-        at += n;
-        s = seq_of<kBN>(p, ++b);
-      }
-      share->b0 = b;
-      share->base0 = at;
-      share->s0 = s;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tO = tmem + SB * kPitch;
   const WaitCtl ctl{abort_flag, p.err_word, p.timeout_ns};
-  const Share sh = *share;
   const int g = p.g;
 
   // First key of the t-th tile that a segment visits.  ALiBi's bias grows toward the nodes:
   // in order the maxima would rise, and O be rescaled, tile after tile, so it goes backwards.
   auto first_key = [&](const Seg& sg, int t) {
-    return sg.s.lo + (sg.t0 + (VAR == kAlibi ? sg.tiles - 1 - t : t)) * kBN;
+    return sg.lo + (sg.t0 + (VAR == kAlibi ? sg.tiles - 1 - t : t)) * kBN;
   };
   // Whether a key tile is filled by tiled copies: all of its keys exist.
   auto tiled = [&](const Seg& sg, int t) {
     const int tile0 = first_key(sg, t);
-    return p.box > 0 && tile0 >= sg.s.first && tile0 + kBN <= sg.s.end;
+    return p.box > 0 && tile0 >= sg.first && tile0 + kBN <= sg.end;
   };
-  // Roles walk the same segments; S products count over all of them (n: buffer n % SB),
-  // and so do the ring's tiles (K and V of key tile j: 2 j and 2 j + 1).
+  // The keys' producer plans the segments; the other roles take them from its slots, in order
+  // (`all`: by a whole warp).  S products count over all of them (n: buffer n % SB), and so
+  // do the ring's tiles (K and V of key tile j: 2 j and 2 j + 1).
+  auto take = [&](Seg& sg, int& count, bool all) -> bool {
+    const int i = count % kSegSlots;
+    const uint32_t parity = (count / kSegSlots) & 1;
+    ++count;
+    if (!(all ? mbar_wait_warp(bar(kSegFull + i), parity, ctl) : mbar_wait(bar(kSegFull + i), parity, ctl)))
+      return false;
+    sg = segs[i];
+    if (all) __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kSegEmpty + i));
+    return sg.tiles > 0;
+  };
   const uint32_t id_s = idesc_bf16_f32(128, kBN, false, false);
   const uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
   const uint32_t dhi = sw128_desc_hi(1024);
@@ -507,10 +418,109 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     constexpr int kSpans = D / 64, kSets = kBN / 32;
     int slot = keys ? 0 : 1, phase = 0, n_seg = 0, issued = 0;
     bool again = false;                                    // slots have been used before
-    Walk<kBN> walk(p, sh);
     Seg sg;
+    int count = 0;
+    // ---- the plan: this block's run of units, [u, u1) of all, from sequence b on ----
+    uint32_t u = 0, u1 = 0, base = 0;
+    int b = 0;
+    Seq s{};
+    if (keys) {
+      bool bad_nodes = false, bad_len = false;
+      uint32_t total = 0;
+#pragma unroll 4
+      for (int i = lane; i < a.batch; i += 32) {
+        const Seq x = seq_of<kBN>(p, i);
+        total += units_of(p, x);
+        bad_nodes |= x.bad_nodes;
+        bad_len |= x.bad_len;
+      }
+      if (blockIdx.x == 0) {
+        if (bad_nodes) atomicOr(p.err_word, kErrSeqLens);
+        if (bad_len) atomicOr(p.err_word, kErrKvLen);
+      }
+      total = __reduce_add_sync(0xffffffffu, total);
+      // The first `more` blocks get one unit more than the others; blocks beyond the units get
+      // none, so that those with some are neighbours.
+      const uint32_t G = min(gridDim.x, total), c = blockIdx.x;
+      const uint32_t each = G ? total / G : 0, more = G ? total - each * G : 0;
+      if (c < G) {
+        u = c * each + min(c, more);
+        u1 = u + each + (c < more ? 1 : 0);
+        for (int i0 = 0; i0 < a.batch; i0 += 32) {
+          uint32_t n = 0;
+          if (i0 + lane < a.batch) n = units_of(p, seq_of<kBN>(p, i0 + lane));
+          uint32_t incl = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, u < base + incl);
+          if (past) {
+            const int at = __ffs(past) - 1;
+            base += __shfl_sync(0xffffffffu, incl - n, at);
+            b = i0 + at;
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        s = seq_of<kBN>(p, b);
+      }
+      if (!a.whole && lane == 0) {
+        // What the second kernel joins: an item that ends here and began in another block.
+        TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
+        if (u < u1) {
+          const uint32_t T = item_units(p, s), item = (u - base) / T, at = base + item * T;
+          if (at < u && at + T <= u1) {
+            const uint32_t rich = more * (each + 1);
+            j.first_block = (int)(at < rich ? at / (each + 1) : more + (at - rich) / each);
+            j.kvh = (int)item / s.groups;
+            const int node0 = ((int)item - j.kvh * s.groups) * p.tile_nodes * p.q_tiles;
+            j.rows = min(p.tile_nodes * p.q_tiles, s.nodes - node0) * g;
+            j.q0 = s.q0;
+            j.row0 = node0 * g;
+          }
+        }
+        a.joins[blockIdx.x] = j;
+      }
+    }
+    auto plan = [&]() -> bool {
+      uint32_t n = units_of(p, s);
+      while (u < u1 && u >= base + n && b + 1 < a.batch) {
+        base += n;
+        s = seq_of<kBN>(p, ++b);
+        n = units_of(p, s);
+      }
+      sg.tiles = 0;
+      if (u < u1 && u < base + n) {  // (not: lengths that changed under the call)
+        const uint32_t T = item_units(p, s), item = (u - base) / T, t = u - base - item * T;
+        const uint32_t n_units = min(T - t, u1 - u);
+        const int group = p.tile_nodes * p.q_tiles;
+        sg.b = b, sg.q0 = s.q0, sg.seq_nodes = s.nodes;
+        sg.kv_len = s.kv_len, sg.end = s.end, sg.first = s.first, sg.lo = s.lo;
+        sg.kvh = (int)item / s.groups;
+        sg.node0 = ((int)item - sg.kvh * s.groups) * group;
+        sg.nodes = min(group, s.nodes - sg.node0);
+        sg.nr = (sg.nodes + p.tile_nodes - 1) / p.tile_nodes;
+        sg.t0 = a.whole ? 0 : (int)(t << p.unit_shift);
+        sg.tiles = a.whole ? s.tiles : min((int)(n_units << p.unit_shift), s.tiles - sg.t0);
+        sg.place = t > 0 ? 0 : n_units < T ? 1 : 2;
+        u += n_units;
+      }
+      const int i = count % kSegSlots;
+      if (count >= kSegSlots &&
+          !mbar_wait_warp(bar(kSegEmpty + i), (count / kSegSlots - 1) & 1, ctl))
+        return false;
+      ++count;
+      if (lane == 0) {
+        segs[i] = sg;
+        mbar_arrive(bar(kSegFull + i));
+      }
+      __syncwarp();
+      return sg.tiles > 0;
+    };
     bool ok = true;
-    while (ok && walk.next(sg)) {
+    while (ok && (keys ? plan() : take(sg, count, true))) {
       const int32_t* table =
           a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
       // Where this lane's rows of a tile (lane, lane + 32, ..) lie: the block's number in the
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
 #pragma unroll
         for (int i = 0; i < kSets; ++i) {
           const int tok = tile0 + lane + 32 * i;
-          if (table != nullptr && tok >= sg.s.first && tok < sg.s.end) entry[i] = table[blk[i]];
+          if (table != nullptr && tok >= sg.first && tok < sg.end) entry[i] = table[blk[i]];
         }
       };
 #pragma unroll
@@ -551,14 +561,14 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           for (int r = 0; r < sg.nr; ++r)
             for (int span = 0; span < kSpans; ++span)
               tma_load_3d(smem_u32(smem + r * L::kQTileBytes + span * L::kQChunkBytes), &tm_q, full,
-                          span * 64, sg.kvh * g, sg.s.q0 + sg.node0 + r * p.tile_nodes);
+                          span * 64, sg.kvh * g, sg.q0 + sg.node0 + r * p.tile_nodes);
         }
         int plane[kSets];
 #pragma unroll
         for (int i = 0; i < kSets; ++i) {
           const int tok = tile0 + lane + 32 * i;
           plane[i] = table ? entry[i] : sg.b;
-          if (table != nullptr && tok >= sg.s.first && tok < sg.s.end &&
+          if (table != nullptr && tok >= sg.first && tok < sg.end &&
               (plane[i] < 0 || plane[i] >= a.num_blocks)) {
             atomicOr(p.err_word, kErrBlockIndex);
             plane[i] = -1;
@@ -604,7 +614,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
 #pragma unroll
             for (int k = 1; k < kSets; ++k)
               if (i == k) at = plane[k], in = row_in[k];
-            const int row = tok >= sg.s.first && tok < sg.s.end && at >= 0 ? at * rows + in : -1;
+            const int row = tok >= sg.first && tok < sg.end && at >= 0 ? at * rows + in : -1;
             copy_rows<D, kBN>(dst, i * 32, cache + (size_t)sg.kvh * D, (long long)a.n_kv_heads * D, row,
                          lane);
           }
@@ -645,12 +655,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   } else if (warp == kSWarp) {
     // ============================ S = Q K^T issuer ============================
     if (lane == 0) {
-      Walk<kBN> walk(p, sh);
       Seg sg;
+      int count = 0;
       bool ok = true;
       int n = 0, slot = 0, phase = 0;
       const uint32_t q_lo0 = sw128_desc_lo(smem_u32(smem), 16);
-      while (ok && walk.next(sg)) {
+      while (ok && take(sg, count, false)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
           // The 16-byte copies' writes, before the MMAs that read them.
@@ -687,11 +697,11 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   } else if (warp == kPVWarp) {
     // ============================ O += P V issuer ============================
     if (lane == 0) {
-      Walk<kBN> walk(p, sh);
       Seg sg;
+      int count = 0;
       bool ok = true;
       int n = 0, slot = 1, phase = 0;
-      while (ok && walk.next(sg)) {
+      while (ok && take(sg, count, false)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
           // The 16-byte copies' writes, before the MMAs that read them.
@@ -734,12 +744,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int trow = (warp & 3) * 32 + lane;                // row within the tile (TMEM lane)
     int* depths = depth_tab + warp * kMostNodes;            // the nodes' depths, each warp its own
-    Walk<kBN> walk(p, sh);
     Seg sg;
+    int count = 0;
     bool ok = true;
     int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
     uint32_t s_phase = 0;   // s_full's phase, a bit for each buffer
-    for (; ok && walk.next(sg); n0 += sg.tiles * sg.nr) {
+    for (; ok && take(sg, count, true); n0 += sg.tiles * sg.nr) {
       if (r >= sg.nr) continue;
       const int in_tile = trow / g;                         // this row's node in the row tile
       const int node = sg.node0 + r * p.tile_nodes + in_tile;
@@ -748,40 +758,40 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       const int i = (r * p.tile_nodes + in_tile) * g + (trow - in_tile * g);  // row of the group
       // The nodes this row sees.
       const unsigned long long all =
-          sg.s.nodes >= 64 ? ~0ull : (1ull << sg.s.nodes) - 1ull;
+          sg.seq_nodes >= 64 ? ~0ull : (1ull << sg.seq_nodes) - 1ull;
       auto word_of = [&](int u) {
         const unsigned long long w = a.tree_mask
-                                         ? (unsigned long long)a.tree_mask[sg.s.q0 + u]
+                                         ? (unsigned long long)a.tree_mask[sg.q0 + u]
                                          : (2ull << u) - 1ull;
         return w & all;
       };
       unsigned long long word = real ? word_of(node) : 0ull;
-      if (sg.s.end == 0) word = 0ull;                       // a length that was refused
+      if (sg.end == 0) word = 0ull;                       // a length that was refused
       const int depth = max(__popcll(word) - 1, 0);
       float slope_l2 = 0.f;
       const bool near = a.window_left >= 0 && a.window_left < kMostNodes;
       if (near || VAR == kAlibi) {
         __syncwarp();                                       // the last segment's readers
-        for (int u = lane; u < sg.s.nodes; u += 32) depths[u] = max(__popcll(word_of(u)) - 1, 0);
+        for (int u = lane; u < sg.seq_nodes; u += 32) depths[u] = max(__popcll(word_of(u)) - 1, 0);
         __syncwarp();
         if (near)
-          for (int u = 0; u < sg.s.nodes; ++u)
+          for (int u = 0; u < sg.seq_nodes; ++u)
             if (depth - depths[u] > a.window_left) word &= ~(1ull << u);
       }
       if (VAR == kAlibi && real) slope_l2 = a.alibi_slopes[head] * kLog2e;
-      const int pos = sg.s.kv_len + depth;
+      const int pos = sg.kv_len + depth;
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < sg.tiles; ++t) {
         const int n = n0 + t * sg.nr + r, b = n % SB;
         const int kv0 = first_key(sg, t);
         // Visible columns, a bit each, where some may not be.
-        const bool edge = kv0 + kBN > sg.s.kv_len ||
-                          (a.window_left >= 0 && kv0 < sg.s.kv_len + kMostNodes - a.window_left);
+        const bool edge = kv0 + kBN > sg.kv_len ||
+                          (a.window_left >= 0 && kv0 < sg.kv_len + kMostNodes - a.window_left);
         uint32_t vis[kBN / 32];
         if (edge) {
-          const int sft = sg.s.kv_len - kv0;                // column of node 0
+          const int sft = sg.kv_len - kv0;                // column of node 0
           const int lo_c =
-              a.window_left >= 0 ? min(pos - a.window_left, sg.s.kv_len) - kv0 : 0;
+              a.window_left >= 0 ? min(pos - a.window_left, sg.kv_len) - kv0 : 0;
 #pragma unroll
           for (int c = 0; c < kBN / 32; ++c) {
             const int s = sft - 32 * c;
@@ -817,7 +827,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             if (edge) {
               if constexpr (VAR == kAlibi) {
                 const float d0 = (float)(pos - kv0 - 32 * c);
-                const int u0 = kv0 + 32 * c - sg.s.kv_len;  // node of the first column
+                const int u0 = kv0 + 32 * c - sg.kv_len;  // node of the first column
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                   const float dist = u0 + k < 0
@@ -943,10 +953,10 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       tc_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a NaN stays)
       const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      const bool whole = sg.first && sg.last;
+      const bool whole = sg.place == 2;
       // A cut item's partial: place 0 of the block for one that began before, else 1.
-      const size_t prow = ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * a.part_rows + i;
-      const size_t orow = (size_t)(sg.s.q0 + node) * a.n_q_heads + head;
+      const size_t prow = ((size_t)blockIdx.x * 2 + sg.place) * a.part_rows + i;
+      const size_t orow = (size_t)(sg.q0 + node) * a.n_q_heads + head;
       if (real) {
         if (whole) a.lse[orow] = lse;
         else a.lse_part[prow] = lse;
@@ -976,22 +986,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     }
   }
 
-  // ---- what the second kernel joins: the item that ends here and began before ----
-  if (!a.whole && threadIdx.x == 0) {
-    TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
-    Walk<kBN> walk(p, sh);
-    Seg sg;
-    if (walk.next(sg) && !sg.first && sg.last) {
-      // The block that holds unit u is the last c with c total / G <= u.
-      j.first_block =
-          (int)(((sg.item_u0 + 1) * min((long long)gridDim.x, sh.total) - 1) / sh.total);
-      j.rows = sg.nodes * g;
-      j.q0 = sg.s.q0;
-      j.row0 = sg.node0 * g;
-      j.kvh = sg.kvh;
-    }
-    a.joins[blockIdx.x] = j;
-  }
+  // ---- teardown: the TMEM readers and both MMA drains are done ----
   tc_fence_before();
   __syncthreads();
   if (warp == kSWarp) {
@@ -1183,6 +1178,18 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   p.q_tiles = std::min(row_tiles<D>(), (std::min(a.total_nodes, kMostNodes) + p.tile_nodes - 1) /
                                            p.tile_nodes);
   p.slots = L::slots(p.q_tiles);
+  {
+    // Units are counted in 31 bits: more than one tile each where the cache's capacity
+    // would allow for more.
+    const int group = p.tile_nodes * p.q_tiles;
+    const long long items = (long long)a.batch * a.n_kv_heads * ((kMostNodes + group - 1) / group);
+    const long long tiles = (a.capacity() + kBN - 1) / kBN + 1;
+    p.unit_shift = 0;
+    while (items * ((tiles >> p.unit_shift) + 1) > 0x7fffffffLL) {
+      if (tiles >> p.unit_shift == 0) return cudaErrorInvalidValue;
+      ++p.unit_shift;
+    }
+  }
   p.sl2 = a.scale * kLog2e;
   p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
   p.cap_l2 = a.softcap * kLog2e;
