@@ -137,7 +137,9 @@ def binding():
 
         B.init(*(ctypes.cast(getattr(L, name), c_void_p).value
                  for name in ("attn_cache_write_fp8", "attn_cache_read_fp8", "attn_decode_fp8",
-                              "attn_decode_fp8_workspace_bytes")))
+                              "attn_decode_fp8_workspace_bytes", "attn_rope", "attn_cache_append",
+                              "attn_decode_tree", "attn_decode_tree_workspace_bytes",
+                              "attn_verify_tree")))
         _BINDING = B
     return _BINDING
 

@@ -1,5 +1,6 @@
 """Rotary positions, and a decode step with drafted tokens, over the C ABI in
-``include/attn.h``: argument marshalling, like ``api.py``.
+``include/attn.h``: argument marshalling, like ``api.py``.  The calls go to
+csrc/binding.cpp first, which takes the plain case, and come here otherwise.
 
 A step of speculative decoding, for each sequence's nodes (its last token, node 0,
 and the drafted tokens behind it)::
@@ -18,7 +19,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import check, lib
+from ._lib import binding, check, lib
 from .api import (_BF16, _F32, _I32, _columns, _int32, _lens, _need, _need_all, _raw_stream, _rows_stride,
                   _scope)
 
@@ -100,6 +101,10 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
     the gradients of this call's inputs.  Returns (q_out, k_out), allocated with
     the inputs' layout when not given; an output may be its input.
     """
+    if stream is None:
+        r = binding().rope(q, k, inv_freq, positions, interleaved, inverse, magnitude, q_out, k_out)
+        if r is not NotImplemented:
+            return r
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dev, ndim = q.device, q.dim()
@@ -184,6 +189,11 @@ def cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor
     Returns the rotated queries, allocated with q's layout when ``q_out`` is not
     given (None without q); rows outside every sequence are left as they were.
     """
+    if stream is None:
+        r = binding().cache_append(k_new, v_new, k_cache, v_cache, kv_lens, cu_seqlens, block_table,
+                                   inv_freq, positions, q, interleaved, magnitude, q_out)
+        if r is not NotImplemented:
+            return r
     if not isinstance(k_new, torch.Tensor) or not isinstance(v_new, torch.Tensor):
         raise TypeError("k_new and v_new must be torch.Tensors")
     dev = k_new.device
@@ -283,6 +293,12 @@ def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     (uint8, allocated when not given) holds partials.  Returns (O (total, n_q, d) fp32 or
     bf16, LSE (total, n_q) fp32); rows outside every sequence are left as they were.
     """
+    if stream is None and (out_dtype is _F32 or out_dtype is _BF16):
+        r = binding().decode_tree(q, k_cache, v_cache, kv_lens, cu_nodes, tree_mask, block_table,
+                                  max_kv_len, scale, out, lse, workspace, window_left, softcap,
+                                  alibi_slopes, out_dtype is _BF16)
+        if r is not NotImplemented:
+            return r
     if not isinstance(q, torch.Tensor) or q.dtype is not _BF16 or q.dim() != 3 or \
             not q.is_cuda or not q.is_contiguous():
         _need(q, "q", _BF16, 3)
@@ -369,6 +385,11 @@ def verify_tree(target_probs: torch.Tensor, draft_tokens: torch.Tensor, parents:
     The accepted nodes' keys and values belong behind the cached tokens: with chains they
     already lie there; of a tree, append rows path[b, :n + 1] again.
     """
+    if stream is None:
+        r = binding().verify_tree(target_probs, draft_tokens, parents, cu_nodes, u_accept, u_sample,
+                                  draft_probs, num_accepted, path, next_token)
+        if r is not NotImplemented:
+            return r
     if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
         _need(target_probs, "target_probs", _F32, 2)
     dev, (total, vocab) = target_probs.device, target_probs.shape

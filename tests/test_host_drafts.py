@@ -161,3 +161,24 @@ def test_verify_validation(L, E, name, kw):
 
 def test_verify_without_drafts(L, E):
     assert verify(L, q=None, qs=0, nt=P + 2) == E["ALIGN"]
+
+
+def test_binding_takes_only_what_it_knows(L):
+    """csrc/binding.cpp on the CPU: everything is refused (NotImplemented), so drafts.py's
+    checks and messages decide."""
+    import torch
+
+    from exact_io_aware_order_gb300._lib import binding
+
+    b = binding()
+    x = torch.zeros(2, 3, 64, dtype=torch.bfloat16)
+    c = torch.zeros(2, 16, 3, 64, dtype=torch.bfloat16)
+    f, n, p = torch.ones(32, dtype=torch.float64), torch.zeros(2, dtype=torch.int32), torch.ones(2, 5)
+    u = torch.zeros(2)
+    for name, args in (("rope", (x, None, f, None, False, False, 1.0, None, None)),
+                       ("cache_append", (x, x, c, c, n, None, None, f, None, x, False, 1.0, None)),
+                       ("decode_tree", (x, c, c, n, n, None, None, None, None, None, None, None, -1, 0.0, None, False)),
+                       ("verify_tree", (p, n, n, n, u, u, None, None, None, None))):
+        call = getattr(b, name)
+        for wrong in ((), args, (None,) * len(args), (1,) * len(args), args[:-1]):
+            assert call(*wrong) is NotImplemented
