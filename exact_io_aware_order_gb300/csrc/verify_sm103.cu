@@ -7,7 +7,8 @@
 // child is left, the next token is the smallest v with w(0) + .. + w(v) > u' sum(w).
 // A drafted token so accepted, or one so drawn, is distributed as the target's.
 // Without q (drafts that are certain) a refused child only loses its weight: w(x) = 0,
-// Z less that.
+// Z less that.  After several refusals w = max(p - q (Z_1 + Z_2 + ..), 0) (what has reached
+// 0 stays there), so one product serves all of them.
 //
 // All of it in whole multiples of 2^-60: sums and products of 64-bit integers are the
 // same in any order, so the drawn index is the same however the vocabulary is divided,
@@ -36,21 +37,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMostNodes = 64;
 constexpr int kMostBlocks = 8;
+constexpr int kMostWarps = 32;
 constexpr int kUnroll = 8;
 constexpr unsigned long long kOne = 1ull << 60;
+constexpr unsigned long long kMostC = 1ull << 63;
 
 // Multiples of 2^-60 in x, rounded down; 0 for what is not in [0, 2).
 __device__ __forceinline__ unsigned long long fixed60(float x) {
-  const uint32_t b = __float_as_uint(x);
-  const int e = (int)(b >> 23);                 // a set sign makes it 256 or more
-  if (e >= 128 || e < 67) return 0ull;          // (below 2^-60: 0)
-  const unsigned long long m = (b & 0x7fffffu) | 0x800000u;
-  const int s = e - 90;
-  return s >= 0 ? m << s : m >> -s;
+  const uint32_t b = __float_as_uint(x), e = b >> 23;  // (a set sign makes it 256 or more)
+  // The 24 bits of an exponent of 127, moved down.
+  const unsigned long long top = (unsigned long long)(((b & 0x7fffffu) | 0x800000u) << 5) << 32;
+  const unsigned long long v = top >> min(127u - e, 63u);
+  return e < 128u ? v : 0ull;
 }
 // a b / 2^60, rounded down.
 __device__ __forceinline__ unsigned long long times60(unsigned long long a, unsigned long long b) {
@@ -63,17 +63,18 @@ enum Command : int { kEnd = 0, kSum = 1, kFind = 2 };
 struct Order {
   int kind;
   int node;       // whose rows (local index)
-  int levels;     // refusals so far (0 for the plain p)
+  int levels;     // with q: terms of C (0 for the plain p); without: refused tokens
   int rank;       // kFind: the block that holds the border
   unsigned long long rest;  // kFind: what of the drawn sum is left there
 };
 
 struct Shared {
   Order order;
-  unsigned long long Z[kMostNodes];      // with q: Z at each level
+  // with q: C, the sum of the Zs of the refusals so far, in terms below 8
+  unsigned long long C[kMostNodes];
   int gone[kMostNodes];                  // without q: the refused tokens
   unsigned long long totals[kMostBlocks];  // the blocks' sums (in the first block)
-  unsigned long long warp_sums[kWarps];
+  unsigned long long warp_sums[kMostWarps];
   // gathered
   int parent[kMostNodes], token[kMostNodes];
   unsigned long long p[kMostNodes], q[kMostNodes], u[kMostNodes];
@@ -81,14 +82,17 @@ struct Shared {
 
 template <bool DRAFTS>
 __device__ __forceinline__ unsigned long long weight(float pv, float qv, int v, int levels,
-                                                     const unsigned long long* Z, const int* gone) {
+                                                     unsigned long long c0,
+                                                     const unsigned long long* C, const int* gone) {
   unsigned long long w = fixed60(pv);
   if constexpr (DRAFTS) {
     if (levels > 0) {
       const unsigned long long q = fixed60(qv);
-      for (int i = 0; i < levels; ++i) {
-        const unsigned long long qz = i == 0 ? q : times60(q, Z[i]);  // Z[0] is one
-        w = w > qz ? w - qz : 0ull;
+      const unsigned long long y = c0 == kOne ? q : times60(q, c0);
+      w = w > y ? w - y : 0ull;
+      for (int i = 1; i < levels; ++i) {
+        const unsigned long long z = times60(q, C[i]);
+        w = w > z ? w - z : 0ull;
       }
     }
   } else {
@@ -98,8 +102,9 @@ __device__ __forceinline__ unsigned long long weight(float pv, float qv, int v, 
   return w;
 }
 
-template <bool DRAFTS>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+template <bool DRAFTS, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const VerifyArgs a) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
       unsigned long long w = sh.p[next], qz = Z;
       if constexpr (DRAFTS) {
         for (int i = 0; i < levels; ++i) {
-          const unsigned long long y = times60(sh.q[next], sh.Z[i]);
+          const unsigned long long y = times60(sh.q[next], sh.C[i]);
           w = w > y ? w - y : 0ull;
         }
         qz = times60(sh.q[next], Z);
@@ -200,7 +205,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         levels = 0;
         Z = kOne;
       } else if constexpr (DRAFTS) {
-        sh.Z[levels++] = Z;
+        if (levels > 0 && sh.C[levels - 1] + Z < kMostC) sh.C[levels - 1] += Z;
+        else sh.C[levels++] = Z;
         have_z = false;
       } else {
         sh.gone[levels++] = sh.token[next];
@@ -223,12 +229,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     const float* q = DRAFTS ? a.draft_probs + (size_t)(n0 + o.node) * a.q_stride : nullptr;
     if (rank != 0 && o.kind == kSum) {  // the levels, into this block's memory
       for (int i = threadIdx.x; i < o.levels; i += kThreads) {
-        if constexpr (DRAFTS) sh.Z[i] = first->Z[i];
+        if constexpr (DRAFTS) sh.C[i] = first->C[i];
         else sh.gone[i] = first->gone[i];
       }
       __syncthreads();
     }
     const bool use_q = DRAFTS && o.levels > 0;
+    const unsigned long long c0 = use_q ? sh.C[0] : 0ull;
     if (o.kind == kSum) {
       unsigned long long sum = 0ull;
       for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
@@ -241,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
-          sum += weight<DRAFTS>(x[k], y[k], v + 32 * k, o.levels, sh.Z, sh.gone);
+          sum += weight<DRAFTS>(x[k], y[k], v + 32 * k, o.levels, c0, sh.C, sh.gone);
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
           for (int k = 0; k < kUnroll; ++k) {
             if (found) break;
             const int i = v + lane + 32 * k;
-            unsigned long long s = weight<DRAFTS>(x[k], y[k], i, o.levels, sh.Z, sh.gone);
+            unsigned long long s = weight<DRAFTS>(x[k], y[k], i, o.levels, c0, sh.C, sh.gone);
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
               const unsigned long long up = __shfl_up_sync(0xffffffffu, s, d);
@@ -297,11 +304,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   cluster.sync();  // nobody leaves while its memory may be read
 }
 
-}  // namespace
-
-cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
-  // A cluster of 8 blocks from 8192 entries on.
-  const int blocks = a.vocab >= 8192 ? kMostBlocks : 1;
+template <int kThreads>
+cudaError_t launch_t(const VerifyArgs& a, int blocks, const LaunchCtx& ctx) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.batch * (unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
@@ -315,8 +319,18 @@ cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return a.draft_probs ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a)
-                       : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a);
+  return a.draft_probs ? cudaLaunchKernelEx(&cfg, verify_kernel<true, kThreads>, a)
+                       : cudaLaunchKernelEx(&cfg, verify_kernel<false, kThreads>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
+  // A cluster of 8 blocks from 8192 entries on; blocks of 1024 threads while each can have an
+  // SM, of 256 (four an SM) for larger batches.
+  const int blocks = a.vocab >= 8192 ? kMostBlocks : 1;
+  return (long long)a.batch * blocks <= ctx.num_sms ? launch_t<1024>(a, blocks, ctx)
+                                                    : launch_t<256>(a, blocks, ctx);
 }
 
 }  // namespace attn

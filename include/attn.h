@@ -918,14 +918,16 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
  *   path       : (batch, 64) int32 output: the root and the accepted nodes, by index
  *                within the sequence, then -1
  *   next_token : (batch,) int32 output
- * At the node reached last (the root at first), with its rows p and q, w = p and Z = 1.
- * Its children are tried in index order: one with token x is accepted, and becomes the
- * node reached, if floor(u_accept * q(x) Z) < w(x); otherwise w = max(w - q Z, 0) and Z =
- * sum w (without draft_probs: q(x) = 1, and a refusal sets w(x) = 0, Z = max(Z - w(x), 0)).
+ * At the node reached last (the root at first), with its rows p and q, w = p, C = 0 and Z =
+ * 1.  Its children are tried in index order: one with token x is accepted, and becomes the
+ * node reached, if floor(u_accept * q(x) Z) < w(x); otherwise C grows by Z, w = max(p - q C,
+ * 0) and Z = sum w (without draft_probs: q(x) = 1, and a refusal sets w(x) = 0, Z = max(Z -
+ * w(x), 0)).
  * With no child left, next_token is the smallest v with w(0) + .. + w(v) >
  * floor(u_sample * sum w); where sum w is 0, w = p; where no v is, vocab - 1.
- * All numbers are multiples of 2^-60: inputs and products are rounded down to them, sums
- * are exact, so the outputs do not depend on any order.
+ * All numbers are multiples of 2^-60: inputs and products are rounded down to them (q C term
+ * by term where C is 8 or more: its terms are sums of successive Zs below 8), sums are exact,
+ * so the outputs do not depend on any order.
  * A sequence without nodes gets 0, -1s and -1.  A cu_nodes that breaks its rule is clamped
  * into it and flagged; a parent that is not a smaller index, and a drafted token outside [0,
  * vocab), are flagged, and that node is never accepted.

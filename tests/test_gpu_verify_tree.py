@@ -27,7 +27,7 @@ def reference(p, q, tokens, parents, u, u_last):
         return 0, [-1] * 64, -1
     row = lambda t: [fixed(x) for x in t.tolist()]
     at, path = 0, [0]
-    w, Z, qr = row(p[0]), ONE, None if q is None else row(q[0])
+    w, Z, C, pr, qr = row(p[0]), ONE, [], row(p[0]), None if q is None else row(q[0])
     for i in range(1, n):
         if parents[i] != at or not 0 <= tokens[i] < V:
             continue
@@ -36,12 +36,16 @@ def reference(p, q, tokens, parents, u, u_last):
         if qz * fixed(u[i]) >> 60 < w[x]:
             at = i
             path.append(i)
-            w, Z, qr = row(p[i]), ONE, None if q is None else row(q[i])
+            w, Z, C, pr, qr = row(p[i]), ONE, [], row(p[i]), None if q is None else row(q[i])
         elif q is None:
             Z = max(Z - w[x], 0)
             w[x] = 0
         else:
-            w = [max(a - (b * Z >> 60), 0) for a, b in zip(w, qr)]
+            if C and C[-1] + Z < 8 * ONE:
+                C[-1] += Z
+            else:
+                C.append(Z)
+            w = [max(a - sum(b * c >> 60 for c in C), 0) for a, b in zip(pr, qr)]
             Z = sum(w)
     if sum(w) == 0:
         w = row(p[at])
@@ -118,6 +122,24 @@ def test_walks(dev, chain, drafts):
                  near=(0.0, 0.1, 1.0)[seed % 3], peak=(0.2, 2.0)[seed % 2])
         taken |= set(c.check(dev)[0])
     assert {0, 1, 2, 3} <= taken                              # the inputs reach these
+    attn.check_device_status()
+
+
+def test_many_refusals(dev):
+    """A root with 63 children that are all refused, p and q nearly apart: Z stays near 1, and C
+    passes 8 again and again."""
+    V = 300
+    c = Case([64, 64], V, True, seed=10)
+    c.parents = ([-1] + [0] * 63) * 2 + [-1] * 2
+    c.p[:, :150], c.q[:, 150:] = 1e-9, 1e-9
+    c.p /= c.p.sum(1, keepdim=True)
+    c.q /= c.q.sum(1, keepdim=True)
+    c.tokens = [i % 150 for i in range(len(c.tokens))]
+    w = c.check(dev)
+    assert w[0] == [0, 0] and min(w[2]) >= 150
+    c.p[64:] = c.q[64:] * 0.9999 + c.p[64:] * 0.0001          # and one with most of it in common
+    c.u[:] = 1 - 2.0 ** -24
+    c.check(dev)
     attn.check_device_status()
 
 
