@@ -39,7 +39,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kMostNodes = 64;
 constexpr int kMostBlocks = 8;
-constexpr int kMostWarps = 32;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 8;
 constexpr unsigned long long kOne = 1ull << 60;
 constexpr unsigned long long kMostC = 1ull << 63;
@@ -74,7 +75,7 @@ struct Shared {
   unsigned long long C[kMostNodes];
   int gone[kMostNodes];                  // without q: the refused tokens
   unsigned long long totals[kMostBlocks];  // the blocks' sums (in the first block)
-  unsigned long long warp_sums[kMostWarps];
+  unsigned long long warp_sums[kWarps];
   // gathered
   int parent[kMostNodes], token[kMostNodes];
   unsigned long long p[kMostNodes], q[kMostNodes], u[kMostNodes];
@@ -102,9 +103,8 @@ __device__ __forceinline__ unsigned long long weight(float pv, float qv, int v, 
   return w;
 }
 
-template <bool DRAFTS, int kThreads>
+template <bool DRAFTS>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const VerifyArgs a) {
-  constexpr int kWarps = kThreads / 32;
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -304,8 +304,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
   cluster.sync();  // nobody leaves while its memory may be read
 }
 
-template <int kThreads>
-cudaError_t launch_t(const VerifyArgs& a, int blocks, const LaunchCtx& ctx) {
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
+  // A cluster of 8 blocks from 8192 entries on.  Sequences differ in how many passes they
+  // need (one to four and more), so a batch is as fast as its slowest, and that as the SMs it
+  // gets to itself: 64 trees over 128257 entries with blocks of 512 threads and clusters of 8
+  // / 4: 68 / 84 us; with 256 threads 74 / 116, with 1024 97 / 82, and 116 in clusters of 2.
+  const int blocks = a.vocab >= 8192 ? kMostBlocks : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.batch * (unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
@@ -319,18 +325,8 @@ cudaError_t launch_t(const VerifyArgs& a, int blocks, const LaunchCtx& ctx) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return a.draft_probs ? cudaLaunchKernelEx(&cfg, verify_kernel<true, kThreads>, a)
-                       : cudaLaunchKernelEx(&cfg, verify_kernel<false, kThreads>, a);
-}
-
-}  // namespace
-
-cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
-  // A cluster of 8 blocks from 8192 entries on; blocks of 1024 threads while each can have an
-  // SM, of 256 (four an SM) for larger batches.
-  const int blocks = a.vocab >= 8192 ? kMostBlocks : 1;
-  return (long long)a.batch * blocks <= ctx.num_sms ? launch_t<1024>(a, blocks, ctx)
-                                                    : launch_t<256>(a, blocks, ctx);
+  return a.draft_probs ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a)
+                       : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a);
 }
 
 }  // namespace attn
