@@ -237,7 +237,7 @@ struct DecodeTreeArgs {
   int part_rows;  // rows of a partial
   TreeJoin* joins;   // (blocks,)
   float* lse_part;   // (blocks, 2, part_rows)
-  float* o_part;     // (blocks, 2, part_rows, head_dim)
+  float* o_part;     // (blocks, 2, head_dim / 8, part_rows, 8)
   __host__ __device__ long long capacity() const {
     return block_table ? (long long)max_blocks_per_seq * block_size : (long long)max_kv_len;
   }

@@ -72,26 +72,28 @@ constexpr int kLeastBox = 16;
 
 // Row tiles of an item, keys of a tile.  TMEM (512 columns): an O of D columns a row tile,
 // and S buffers in what is left: as many columns as keys, or with fp32 outputs 96 for 64 keys
-// (three parts of P of 32).  Tiles of 128 keys cost the issuing threads half the waits and
+// (three parts of P of 32).  Soft-capping and ALiBi take 64 keys too: with more scores in
+// registers they spill (ALiBi, 32 heads a kv head: 93 us, 116 with 128).  Tiles of 128 keys cost the issuing threads half the waits and
 // commits, some 100 clocks each, for a key: 16 sequences of 1024 - 32768 tokens, 32 heads, at
 // head_dim 128: 247 us against 305 with 64 and twice the buffers.
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
-template <int D, bool WIDE> __host__ __device__ constexpr int key_tile() {
-  return D == 256 || WIDE ? 64 : 128;
+enum Variant : int { kPlain = 0, kCap = 1, kAlibi = 2 };  // (a window is in all of them)
+template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int key_tile() {
+  return D == 256 || WIDE || VAR != kPlain ? 64 : 128;
 }
-template <int D, bool WIDE> __host__ __device__ constexpr int s_pitch() {
-  return WIDE ? 96 : key_tile<D, WIDE>();
+template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_pitch() {
+  return WIDE ? 96 : key_tile<D, VAR, WIDE>();
 }
-template <int D, bool WIDE> __host__ __device__ constexpr int s_bufs() {
-  return D == 256 && !WIDE ? 4 : D == 64 ? 3 : 2;
+template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_bufs() {
+  return !WIDE && (D == 256 || VAR != kPlain) ? 4 : D == 64 ? 3 : 2;
 }
 template <int D> __host__ __device__ constexpr int threads_of() {
   return row_tiles<D>() * kSoftmaxThreads + kProducerThreads + 64;
 }
 
-template <int D, bool WIDE>
+template <int D, int VAR, bool WIDE>
 struct TreeSmem {
-  static constexpr int kBN = key_tile<D, WIDE>();
+  static constexpr int kBN = key_tile<D, VAR, WIDE>();
   static constexpr int kQTileBytes = 128 * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;
   static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
@@ -162,12 +164,41 @@ __device__ __forceinline__ Seq seq_of(const TreeKParams& p, int b) {
   return s;
 }
 
-// Units of work of an item: runs of 2^unit_shift key tiles, or one where items go whole.
-__device__ __forceinline__ uint32_t item_units(const TreeKParams& p, const Seq& s) {
+// Work is counted in units: a run (2^unit_shift key tiles, or the whole item where items go
+// whole) costs kFullRun, of an item with one row tile of two kHalfRun (16 sequences of 1024 -
+// 32768 tokens, 17 - 256 rows a kv head: the copies set the pace of one, the products that
+// of two).  A block gets the runs that begin in its share of the units.
+constexpr uint32_t kFullRun = 4, kHalfRun = 3;
+__device__ __forceinline__ uint32_t runs_of(const TreeKParams& p, const Seq& s) {
   return p.a.whole ? 1u : (uint32_t)(s.tiles + (1 << p.unit_shift) - 1) >> p.unit_shift;
 }
+// Cost of a run in the last group of nodes, which may fill one row tile only.
+__device__ __forceinline__ uint32_t last_run(const TreeKParams& p, const Seq& s) {
+  const int group = p.tile_nodes * p.q_tiles;
+  return p.q_tiles > 1 && s.nodes - (s.groups - 1) * group <= p.tile_nodes ? kHalfRun : kFullRun;
+}
+__device__ __forceinline__ uint32_t head_units(const TreeKParams& p, const Seq& s) {
+  return s.groups > 0 ? runs_of(p, s) * (kFullRun * (uint32_t)(s.groups - 1) + last_run(p, s)) : 0u;
+}
 __device__ __forceinline__ uint32_t units_of(const TreeKParams& p, const Seq& s) {
-  return (uint32_t)(p.a.n_kv_heads * s.groups) * item_units(p, s);
+  return (uint32_t)p.a.n_kv_heads * head_units(p, s);
+}
+// The item that unit `local` of a sequence belongs to: its kv head and group of nodes, its
+// runs and their cost, and how many of its units lie in front.
+struct Item {
+  uint32_t kvh, group, runs, cost, off;
+};
+__device__ __forceinline__ Item item_at(const TreeKParams& p, const Seq& s, uint32_t local) {
+  Item it;
+  const uint32_t h = head_units(p, s);
+  it.kvh = local / h;
+  it.off = local - it.kvh * h;
+  it.runs = runs_of(p, s);
+  const uint32_t full = it.runs * kFullRun;
+  it.group = min(it.off / full, (uint32_t)s.groups - 1u);
+  it.off -= it.group * full;
+  it.cost = (int)it.group == s.groups - 1 ? last_run(p, s) : kFullRun;
+  return it;
 }
 
 // A run of key tiles of one item, as the roles get it.
@@ -270,9 +301,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// VAR: what happens to a score besides scale and window.  WIDE: fp32 O, P in three parts.
-enum Variant : int { kPlain = 0, kCap = 1, kAlibi = 2 };
-
 // softcap tanh(s scale / softcap) of 32 scores, in log2 units.  Up to 0.45 tanh(u) / u is
 // 1 - t/3 + 2 t^2/15 - ... in t = u^2 (its Taylor series; the first term left out is
 // 1.5e-3 t^7, 2e-8 there), six packed FMAs for two scores; a warp with a larger |u| takes
@@ -307,12 +335,13 @@ __device__ __forceinline__ void soft_cap(uint32_t (&x)[32], float in, float out)
   }
 }
 
+// VAR: what happens to a score besides scale and window.  WIDE: fp32 O, P in three parts.
 template <int D, int VAR, bool WIDE>
 __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeKParams p) {
-  using L = TreeSmem<D, WIDE>;
-  constexpr int kBN = L::kBN, kPitch = s_pitch<D, WIDE>(), SB = s_bufs<D, WIDE>(), NQ = row_tiles<D>();
+  using L = TreeSmem<D, VAR, WIDE>;
+  constexpr int kBN = L::kBN, kPitch = s_pitch<D, VAR, WIDE>(), SB = s_bufs<D, VAR, WIDE>(), NQ = row_tiles<D>();
   constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
   static_assert(SB * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
   const DecodeTreeArgs& a = p.a;
@@ -441,7 +470,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       total = __reduce_add_sync(0xffffffffu, total);
       // The first `more` blocks get one unit more than the others; blocks beyond the units get
       // none, so that those with some are neighbours.
-      const uint32_t G = min(gridDim.x, total), c = blockIdx.x;
+      const uint32_t G = total ? min(gridDim.x, max(total / kFullRun, 1u)) : 0u, c = blockIdx.x;
       const uint32_t each = G ? total / G : 0, more = G ? total - each * G : 0;
       if (c < G) {
         u = c * each + min(c, more);
@@ -470,12 +499,13 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         // What the second kernel joins: an item that ends here and began in another block.
         TreeJoin j{-1, 0, 0, 0, 0, 0, 0, 0};
         if (u < u1) {
-          const uint32_t T = item_units(p, s), item = (u - base) / T, at = base + item * T;
-          if (at < u && at + T <= u1) {
+          const Item it = item_at(p, s, u - base);
+          const uint32_t at = u - it.off, last = at + (it.runs - 1) * it.cost;
+          if (it.off > 0 && last >= u && last < u1) {
             const uint32_t rich = more * (each + 1);
             j.first_block = (int)(at < rich ? at / (each + 1) : more + (at - rich) / each);
-            j.kvh = (int)item / s.groups;
-            const int node0 = ((int)item - j.kvh * s.groups) * p.tile_nodes * p.q_tiles;
+            j.kvh = (int)it.kvh;
+            const int node0 = (int)it.group * p.tile_nodes * p.q_tiles;
             j.rows = min(p.tile_nodes * p.q_tiles, s.nodes - node0) * g;
             j.q0 = s.q0;
             j.row0 = node0 * g;
@@ -485,27 +515,32 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       }
     }
     auto plan = [&]() -> bool {
-      uint32_t n = units_of(p, s);
-      while (u < u1 && u >= base + n && b + 1 < a.batch) {
-        base += n;
-        s = seq_of<kBN>(p, ++b);
-        n = units_of(p, s);
-      }
       sg.tiles = 0;
-      if (u < u1 && u < base + n) {  // (not: lengths that changed under the call)
-        const uint32_t T = item_units(p, s), item = (u - base) / T, t = u - base - item * T;
-        const uint32_t n_units = min(T - t, u1 - u);
+      while (u < u1) {
+        uint32_t n = units_of(p, s);
+        while (u >= base + n && b + 1 < a.batch) {
+          base += n;
+          s = seq_of<kBN>(p, ++b);
+          n = units_of(p, s);
+        }
+        if (u >= base + n) break;  // (lengths that changed under the call)
+        const Item it = item_at(p, s, u - base);
+        const uint32_t n_units = min(it.runs * it.cost - it.off, u1 - u);
+        const uint32_t t = (it.off + it.cost - 1) / it.cost;
+        const uint32_t t_end = min((it.off + n_units + it.cost - 1) / it.cost, it.runs);
+        u += n_units;
+        if (t >= t_end) continue;  // (no run begins here)
         const int group = p.tile_nodes * p.q_tiles;
         sg.b = b, sg.q0 = s.q0, sg.seq_nodes = s.nodes;
         sg.kv_len = s.kv_len, sg.end = s.end, sg.first = s.first, sg.lo = s.lo;
-        sg.kvh = (int)item / s.groups;
-        sg.node0 = ((int)item - sg.kvh * s.groups) * group;
+        sg.kvh = (int)it.kvh;
+        sg.node0 = (int)it.group * group;
         sg.nodes = min(group, s.nodes - sg.node0);
         sg.nr = (sg.nodes + p.tile_nodes - 1) / p.tile_nodes;
         sg.t0 = a.whole ? 0 : (int)(t << p.unit_shift);
-        sg.tiles = a.whole ? s.tiles : min((int)(n_units << p.unit_shift), s.tiles - sg.t0);
-        sg.place = t > 0 ? 0 : n_units < T ? 1 : 2;
-        u += n_units;
+        sg.tiles = a.whole ? s.tiles : min((int)((t_end - t) << p.unit_shift), s.tiles - sg.t0);
+        sg.place = t > 0 ? 0 : t_end < it.runs ? 1 : 2;
+        break;
       }
       const int i = count % kSegSlots;
       if (count >= kSegSlots &&
@@ -813,6 +848,10 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           base = -slope_l2 * (float)(pos - kv0);
           if (edge) sl2 = 1.f, slope = 0.f, base = 0.f;
         }
+        float2 steps[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          steps[q] = make_float2(slope * (float)(2 * q), slope * (float)(2 * q + 1));
         const bool ahead = edge || (VAR == kCap && kBN > 64);
         if (ahead) {
           // Soft-capping, masks, and ALiBi where nodes are among the keys: a pass of its own,
@@ -861,13 +900,13 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           uint32_t (&y)[32] = x[c];
           if (VAR == kCap && !ahead) soft_cap(y, p.cap_in, p.cap_l2);
           if constexpr (VAR == kAlibi) {
-            const float2 sl2v = make_float2(sl2, sl2), slopev = make_float2(slope, slope);
-            const float2 bv = make_float2(base, base);
+            const float2 sl2v = make_float2(sl2, sl2);
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              const float2 kv = make_float2((float)(32 * c + k), (float)(32 * c + k + 1));
+              // slope k is that of the 8 columns' first and one of four pairs.
+              const float b8 = fmaf(slope, (float)(32 * c + (k & ~7)), base);
               const float2 e = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
-                                    sl2v, fma2(slopev, kv, bv));
+                                    sl2v, add2(make_float2(b8, b8), steps[(k >> 1) & 3]));
               y[k] = __float_as_uint(e.x);
               y[k + 1] = __float_as_uint(e.y);
             }
@@ -955,7 +994,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       const bool whole = sg.place == 2;
       // A cut item's partial: place 0 of the block for one that began before, else 1.
-      const size_t prow = ((size_t)blockIdx.x * 2 + sg.place) * a.part_rows + i;
+      const size_t pplace = (size_t)blockIdx.x * 2 + sg.place, prow = pplace * a.part_rows + i;
       const size_t orow = (size_t)(sg.q0 + node) * a.n_q_heads + head;
       if (real) {
         if (whole) a.lse[orow] = lse;
@@ -975,11 +1014,18 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           for (int k = 0; k < 16; ++k) y[k] = pack_bf16x2(f(2 * k), f(2 * k + 1));
           store_32B<2>(dst, y);
         } else {
-          float* dst = (whole ? static_cast<float*>(a.o) + orow * D : a.o_part + prow * D) + c * 32;
-          uint32_t y[32];
+          // A partial's values lie 8 columns of all rows together, so that a warp's stores are
+          // consecutive; a row of O is D values.
+          float* dst = whole ? static_cast<float*>(a.o) + orow * D + c * 32
+                             : a.o_part + (pplace * (D / 8) + c * 4) * a.part_rows * 8 + (size_t)i * 8;
+          const size_t apart = whole ? 8 : (size_t)a.part_rows * 8;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(f(k));
-          store_32B<4>(dst, y);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(f(8 * q + k));
+            store_32B<1>(dst + q * apart, y);
+          }
         }
       }
       tc_fence_before();
@@ -999,30 +1045,34 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
 // The partials of cut items: O = sum w_i O_i / sum w_i with w_i = exp(lse_i - max),
 // blocks in order (and, with many, eight running sums in order), so that the result does
 // not depend on which came first.  The first kernel's blocks leave what ended in them; every
-// block here counts through those and takes its share of the rows.  Up to kFewParts
-// partials a warp does a row; more are divided among the block's warps (one sequence of
-// 30720 tokens is cut 38 ways: 22 us with a warp a row and a grid of all possible rows).
+// block here counts through those and takes its share of the rows, four to a warp: lane l
+// has 4 values of row (l / 2) % 4 in column group l / 8 and every fourth behind it, so that
+// a load takes 128 consecutive bytes from each of four groups.  Up to kFewParts partials a
+// warp does its rows alone; more are divided among the block's warps (one sequence of 30720
+// tokens is cut 38 ways).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 4;
 constexpr int kFewParts = 8;
 constexpr int kMostBlocks = 256;  // of the first kernel's grid
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const DecodeTreeArgs a) {
-  constexpr int kV = D / 32;  // values of a lane: columns lane * kV ...
+  constexpr int kV = D / 32;  // 16-byte pieces of a lane
   __shared__ int s_units[kMostBlocks + 1];  // units in front of each block's item
   __shared__ int s_warp[kJoinWarps];
-  __shared__ float s_o[kJoinWarps][D], s_sum[kJoinWarps];
+  __shared__ float4 s_o[kJoinWarps][kV][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  // Units: a row, or with few partials kJoinWarps rows.
+  grid_dep_launch();
+  // Units: kJoinRows rows, or with few partials kJoinWarps times as many.
   {
     const int c = threadIdx.x;
     int units = 0;
     if (c < a.blocks) {
       const TreeJoin j = a.joins[c];
-      if (j.first_block >= 0)
-        units = c - j.first_block + 1 > kFewParts ? j.rows : (j.rows + kJoinWarps - 1) / kJoinWarps;
+      const int few = c - j.first_block + 1 <= kFewParts ? kJoinWarps : 1;
+      if (j.first_block >= 0) units = (j.rows + kJoinRows * few - 1) / (kJoinRows * few);
     }
     int incl = units;
 #pragma unroll
@@ -1032,7 +1082,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Decode
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += s_warp[w];
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+      if (w < warp) incl += s_warp[w];
     s_units[c + 1] = incl;
     if (c == 0) s_units[0] = 0;
     __syncthreads();
@@ -1047,73 +1099,86 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Decode
     const TreeJoin j = a.joins[c];
     const int parts = c - j.first_block + 1;
     const bool many = parts > kFewParts;
-    const int i = many ? u - s_units[c] : (u - s_units[c]) * kJoinWarps + warp;
+    const int row0 = (many ? u - s_units[c] : (u - s_units[c]) * kJoinWarps + warp) * kJoinRows;
     const int k0 = many ? warp : 0, step = many ? kJoinWarps : 1;
-    const bool live = i < j.rows;
-    auto at = [&](int k) {  // the first block left it at its place 1, the others at place 0
-      return ((size_t)(j.first_block + k) * 2 + (k == 0 ? 1 : 0)) * a.part_rows + i;
+    auto place = [&](int k) {  // the first block left it at its place 1, the others at place 0
+      return (size_t)(j.first_block + k) * 2 + (k == 0 ? 1 : 0);
     };
-    float acc[kV], sum = 0.f, ref = 0.f;
+    // Each row's largest LSE, and the sum of the weights: lane l looks at row l % 4, partials
+    // l / 4 and every eighth behind it.
+    const int mine = min(row0 + (lane & 3), j.rows - 1);
+    float top = -INFINITY, sum = 0.f;
+    if (row0 < j.rows) {
+      for (int k = lane >> 2; k < parts; k += 8)
+        top = fmax_nan(top, a.lse_part[place(k) * a.part_rows + mine]);
+    }
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+    for (int o = 16; o > 2; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref_mine = top == -INFINITY ? 0.f : top;
+    if (row0 < j.rows) {
+      for (int k = lane >> 2; k < parts; k += 8)
+        sum += ex2_approx((a.lse_part[place(k) * a.part_rows + mine] - ref_mine) * kLog2e);
+    }
+#pragma unroll
+    for (int o = 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int sub = (lane >> 1) & 3, row = row0 + sub;  // the row whose values this lane has
+    const float ref = __shfl_sync(0xffffffffu, ref_mine, sub);
+    sum = __shfl_sync(0xffffffffu, sum, sub);
+    float4 acc[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool live = row < j.rows;
     if (live) {
-      float top = -INFINITY;
-      for (int k = lane; k < parts; k += 32) top = fmax_nan(top, a.lse_part[at(k)]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      ref = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
       for (int k = k0; k < parts; k += step) {
-        const size_t row = at(k);
-        const float w = ex2_approx((a.lse_part[row] - ref) * kLog2e);
-        sum += w;
-        const float* src = a.o_part + row * D + lane * kV;
-        float x[kV];
-        if constexpr (kV == 2) {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          x[0] = y.x, x[1] = y.y;
-        } else {
+        const float w = ex2_approx((a.lse_part[place(k) * a.part_rows + row] - ref) * kLog2e);
+        const float* src =
+            a.o_part + ((place(k) * (D / 8) + (lane >> 3)) * a.part_rows + row) * 8 + (lane & 1) * 4;
 #pragma unroll
-          for (int v = 0; v < kV; v += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(src + v);
-            x[v] = y.x, x[v + 1] = y.y, x[v + 2] = y.z, x[v + 3] = y.w;
-          }
+        for (int v = 0; v < kV; ++v) {
+          const float4 x =
+              *reinterpret_cast<const float4*>(src + (size_t)v * 4 * a.part_rows * 8);
+          acc[v].x = fmaf(w, x.x, acc[v].x);
+          acc[v].y = fmaf(w, x.y, acc[v].y);
+          acc[v].z = fmaf(w, x.z, acc[v].z);
+          acc[v].w = fmaf(w, x.w, acc[v].w);
         }
-#pragma unroll
-        for (int v = 0; v < kV; ++v) acc[v] = fmaf(w, x[v], acc[v]);
       }
     }
     if (many) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v) s_o[warp][lane * kV + v] = acc[v];
-      if (lane == 0) s_sum[warp] = sum;
+      for (int v = 0; v < kV; ++v) s_o[warp][v][lane] = acc[v];
       __syncthreads();
-      if (warp == 0) {
-        sum = 0.f;
-        for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
+      // Warp w joins the pieces v = w, w + 8, ..
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          acc[v] = 0.f;
-          for (int w = 0; w < kJoinWarps; ++w) acc[v] += s_o[w][lane * kV + v];
+      for (int v = 0; v < kV; ++v) {
+        if (v % kJoinWarps != warp) continue;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kJoinWarps; ++w) {
+          const float4 x = s_o[w][v][lane];
+          t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
         }
+        acc[v] = t;
       }
       __syncthreads();
-      if (warp != 0) continue;
     }
     if (!live) continue;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int g = a.n_q_heads / a.n_kv_heads;
-    const int node = (j.row0 + i) / g, head = j.kvh * g + (j.row0 + i) % g;
+    const int node = (j.row0 + row) / g, head = j.kvh * g + (j.row0 + row) % g;
     const size_t orow = (size_t)(j.q0 + node) * a.n_q_heads + head;
-    if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : ref + log2f(sum) * kLn2;
-    if constexpr (WIDE) {
-      float* dst = static_cast<float*>(a.o) + orow * D + lane * kV;
+    if ((lane & ~6) == 0 && (!many || warp == 0))
+      a.lse[orow] = sum == 0.f ? -INFINITY : ref + log2f(sum) * kLn2;
 #pragma unroll
-      for (int v = 0; v < kV; ++v) dst[v] = acc[v] * inv;
-    } else {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + orow * D + lane * kV);
-#pragma unroll
-      for (int v = 0; v < kV; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+    for (int v = 0; v < kV; ++v) {
+      if (many && v % kJoinWarps != warp) continue;
+      const float4 x = make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+      const size_t at = orow * D + ((lane >> 3) + 4 * v) * 8 + (lane & 1) * 4;
+      if constexpr (WIDE)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = x;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + at) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     }
   }
 }
@@ -1169,7 +1234,7 @@ bool make_q_map(CUtensorMap* m, const void* base, int D, int n_q, int nodes, int
 
 template <int D, int VAR, bool WIDE>
 cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
-  using L = TreeSmem<D, WIDE>;
+  using L = TreeSmem<D, VAR, WIDE>;
   constexpr int kBN = L::kBN;
   TreeKParams p;
   p.a = a;
@@ -1185,7 +1250,7 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
     const long long items = (long long)a.batch * a.n_kv_heads * ((kMostNodes + group - 1) / group);
     const long long tiles = (a.capacity() + kBN - 1) / kBN + 1;
     p.unit_shift = 0;
-    while (items * ((tiles >> p.unit_shift) + 1) > 0x7fffffffLL) {
+    while (items * kFullRun * ((tiles >> p.unit_shift) + 1) > 0x7fffffffLL) {
       if (tiles >> p.unit_shift == 0) return cudaErrorInvalidValue;
       ++p.unit_shift;
     }
