@@ -209,7 +209,7 @@ struct alignas(16) Seg {
   int t0, tiles;               // key tiles [t0, t0 + tiles); none: the end
   int place;                   // 0: a partial of an item that began before, 1: of one that begins
                                // here, 2: a whole item
-  int pad0, pad1;
+  int full0, full1;            // of those t0 + [full0, full1) consist of keys that all exist
 };
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -221,24 +221,26 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 32 rows of D values into a tile of 128-byte-swizzled spans (rows row0 ...): lane i's
-// `row` is the place of row i in units of `pitch` values behind `base`, -1 for zeros.
+// Rows 16 k .. 16 k + 15 of a tile of 128-byte-swizzled spans, D values each: lane i has the
+// place of row i of the 32 around them in units of `pitch` values behind `base`, -1 for zeros.
 template <int D, int kBN>
-__device__ __forceinline__ void copy_rows(uint32_t tile, int row0, const uint16_t* base,
+__device__ __forceinline__ void copy_rows(uint32_t tile, int k, const uint16_t* base,
                                           long long pitch, int row, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a row, rows at a time
-  constexpr int kBatch = 8;  // all shuffles of a batch in front of its copies, which overlap then
+  constexpr int kPasses = 16 / kRows, kBatch = kPasses < 8 ? kPasses : 8;
+  // (all shuffles of a batch in front of its copies, which overlap then)
   const int c = lane % kLanes, r = lane / kLanes;
   const uint32_t dst0 = tile + (c >> 3) * kBN * 128;
   base += c * 8;
 #pragma unroll 1
-  for (int i = 0; i < kLanes; i += kBatch) {
+  for (int i = 0; i < kPasses; i += kBatch) {
     int src[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) src[u] = __shfl_sync(0xffffffffu, row, (i + u) * kRows + r);
+    for (int u = 0; u < kBatch; ++u)
+      src[u] = __shfl_sync(0xffffffffu, row, (k & 1) * 16 + (i + u) * kRows + r);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int at = row0 + (i + u) * kRows + r;
+      const int at = 16 * k + (i + u) * kRows + r;
       cp_async16_or_zero(dst0 + at * 128 + (((c & 7) ^ (at & 7)) << 4),
                          base + max(src[u], 0) * pitch, src[u] >= 0);
     }
@@ -339,7 +341,8 @@ __device__ __forceinline__ void soft_cap(uint32_t (&x)[32], float in, float out)
 template <int D, int VAR, bool WIDE>
 __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeKParams p) {
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
+    const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ TreeKParams p) {
   using L = TreeSmem<D, VAR, WIDE>;
   constexpr int kBN = L::kBN, kPitch = s_pitch<D, VAR, WIDE>(), SB = s_bufs<D, VAR, WIDE>(), NQ = row_tiles<D>();
   constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
@@ -415,10 +418,17 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   auto first_key = [&](const Seg& sg, int t) {
     return sg.lo + (sg.t0 + (VAR == kAlibi ? sg.tiles - 1 - t : t)) * kBN;
   };
-  // Whether a key tile is filled by tiled copies: all of its keys exist.
-  auto tiled = [&](const Seg& sg, int t) {
+  // Whether all keys of a tile exist (tiled copies fill it then, where blocks allow them).
+  auto full_tile = [&](const Seg& sg, int t) {
+    const int j = VAR == kAlibi ? sg.tiles - 1 - t : t;
+    return j >= sg.full0 && j < sg.full1;
+  };
+  // The steps of 16 keys of a tile that hold keys at all: what the products take, and the
+  // producers fill.
+  auto steps_of = [&](const Seg& sg, int t, int& k0, int& k1) {
     const int tile0 = first_key(sg, t);
-    return p.box > 0 && tile0 >= sg.first && tile0 + kBN <= sg.end;
+    k0 = max(sg.first - tile0, 0) >> 4;
+    k1 = max((min(sg.end - tile0, kBN) + 15) >> 4, k0);
   };
   // The keys' producer plans the segments; the other roles take them from its slots, in order
   // (`all`: by a whole warp).  S products count over all of them (n: buffer n % SB), and so
@@ -443,6 +453,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     // The first warp fills the keys' slots (and the queries), the second the values'.
     const bool keys = warp == kProducerWarp;
     const CUtensorMap* map = keys ? &tm_k : &tm_v;
+    const CUtensorMap* map16 = keys ? &tm_k16 : &tm_v16;
     const uint16_t* cache = keys ? a.k_cache : a.v_cache;
     constexpr int kSpans = D / 64, kSets = kBN / 32;
     int slot = keys ? 0 : 1, phase = 0, n_seg = 0, issued = 0;
@@ -540,6 +551,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         sg.t0 = a.whole ? 0 : (int)(t << p.unit_shift);
         sg.tiles = a.whole ? s.tiles : min((int)((t_end - t) << p.unit_shift), s.tiles - sg.t0);
         sg.place = t > 0 ? 0 : t_end < it.runs ? 1 : 2;
+        const int key0 = s.lo + sg.t0 * kBN;
+        sg.full0 = key0 < s.first ? 1 : 0;
+        sg.full1 = min(max(s.end - key0, 0) / kBN, sg.tiles);
         break;
       }
       const int i = count % kSegSlots;
@@ -609,7 +623,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             plane[i] = -1;
           }
         }
-        if (tiled(sg, t)) {
+        if (p.box > 0 && full_tile(sg, t)) {
           // One lane issues them all.  Boxes of 32 rows or more begin where its own rows are,
           // those of 16 also where lane 16's are.  A bad block becomes one past the cache,
           // which reads as zeros.
@@ -640,18 +654,46 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           }
           __syncwarp();
         } else {
-          // Row by row, 16 bytes a lane, zeros for rows that are not there.
+          // A tile that ends early or begins in front of a window, or blocks of other sizes: steps
+          // of 16 rows.  Those that are all there by a tiled copy where blocks allow it, the
+          // others row by row, 16 bytes a lane, zeros for rows that are not there (the products
+          // multiply them by weights of 0).
           const int rows = table ? a.block_size : a.max_kv_len;
-#pragma unroll 1
+          int row[kSets];
+#pragma unroll
           for (int i = 0; i < kSets; ++i) {
             const int tok = tile0 + lane + 32 * i;
-            int at = plane[0], in = row_in[0];
+            row[i] = tok >= sg.first && tok < sg.end && plane[i] >= 0 ? plane[i] * rows + row_in[i] : -1;
+          }
+          int k0, k1;
+          steps_of(sg, t, k0, k1);
+          auto whole = [&](int k) {
+            return p.box > 0 && tile0 + 16 * k >= sg.first && tile0 + 16 * k + 16 <= sg.end;
+          };
+          int n_boxes = 0;
+          for (int k = k0; k < k1; ++k) n_boxes += whole(k);
+          if (lane == 0 && n_boxes > 0) mbar_expect_tx(full, (uint32_t)(n_boxes * 16 * D * 2));
+          __syncwarp();
+#pragma unroll 1
+          for (int k = k0; k < k1; ++k) {
+            int r = row[0], in = row_in[0], pl = plane[0];
 #pragma unroll
-            for (int k = 1; k < kSets; ++k)
-              if (i == k) at = plane[k], in = row_in[k];
-            const int row = tok >= sg.first && tok < sg.end && at >= 0 ? at * rows + in : -1;
-            copy_rows<D, kBN>(dst, i * 32, cache + (size_t)sg.kvh * D, (long long)a.n_kv_heads * D, row,
-                         lane);
+            for (int i = 1; i < kSets; ++i)
+              if ((k >> 1) == i) r = row[i], in = row_in[i], pl = plane[i];
+            if (whole(k)) {
+              in = __shfl_sync(0xffffffffu, in, (k & 1) * 16);
+              pl = __shfl_sync(0xffffffffu, pl, (k & 1) * 16);
+              if (lane == 0) {
+#pragma unroll
+                for (int span = 0; span < kSpans; ++span)
+                  tma_load_4d(dst + span * L::kChunkBytes + k * 16 * 128, map16, full, span * 64,
+                              sg.kvh, in, pl < 0 ? a.num_blocks : pl);
+              }
+              __syncwarp();
+            } else {
+              copy_rows<D, kBN>(dst, k, cache + (size_t)sg.kvh * D, (long long)a.n_kv_heads * D, r,
+                                lane);
+            }
           }
           cp_async_arrive(full);
         }
@@ -699,7 +741,17 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
           // The 16-byte copies' writes, before the MMAs that read them.
-          if (!tiled(sg, t)) fence_proxy_async_smem();
+          uint32_t id = id_s;
+          bool some = true;
+          if (!full_tile(sg, t)) {
+            fence_proxy_async_smem();
+            int k0, k1;
+            steps_of(sg, t, k0, k1);
+            id = idesc_bf16_f32(128, 16 * k1, false, false);
+            some = k1 > 0;
+          } else if (p.box == 0) {
+            fence_proxy_async_smem();
+          }
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n % SB;
@@ -708,11 +760,13 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             tc_fence_after();
             const uint32_t dS = tmem + b * kPitch;
             const uint32_t q_lo = q_lo0 + (uint32_t)((r * L::kQTileBytes) >> 4);
+            if (some) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t qoff = ((kk >> 2) * L::kQChunkBytes + (kk & 3) * 32) >> 4;
-              const uint32_t koff = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-              mma_ss_lo(dS, q_lo + qoff, k_lo + koff, dhi, id_s, kk > 0);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t qoff = ((kk >> 2) * L::kQChunkBytes + (kk & 3) * 32) >> 4;
+                const uint32_t koff = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+                mma_ss_lo(dS, q_lo + qoff, k_lo + koff, dhi, id, kk > 0);
+              }
             }
             mma_commit(bar(kSFull + 4 * r + b));
           }
@@ -740,23 +794,36 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
           // The 16-byte copies' writes, before the MMAs that read them.
-          if (!tiled(sg, t)) fence_proxy_async_smem();
+          const bool full = full_tile(sg, t);
+          int k0 = 0, k1 = kBN / 16;
+          if (!full || p.box == 0) fence_proxy_async_smem();
+          if (!full) steps_of(sg, t, k0, k1);
           const uint32_t v_lo =
               sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n % SB;
             // P comes in halves of 64 keys.
             const uint32_t aP = tmem + b * kPitch, tOr = tO + r * D;
+            uint32_t onto = t > 0 ? 1u : 0u;  // (the first product of a segment overwrites O)
 #pragma unroll
             for (int h = 0; h < kBN / 64; ++h) {
               if (!mbar_wait(bar(kPFull + 4 * h + b), (n / SB) & 1, ctl)) { ok = false; break; }
               tc_fence_after();
+              auto product = [&](int part, int kk) {
+                mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
+                          id_pv, onto);
+                onto = 1u;
+              };
+              if (full) {  // (straight code: each branch between MMAs shows)
 #pragma unroll
-              for (int part = 0; part < (WIDE ? 3 : 1); ++part)
+                for (int part = 0; part < (WIDE ? 3 : 1); ++part)
 #pragma unroll
-                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                  mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
-                            id_pv, (part > 0 || kk > 0) ? 1u : (t > 0 ? 1u : 0u));
+                  for (int kk = 4 * h; kk < 4 * h + 4; ++kk) product(part, kk);
+              } else {
+#pragma unroll 1
+                for (int kk = max(k0, 4 * h); kk < min(k1, 4 * h + 4); ++kk)
+                  for (int part = 0; part < (WIDE ? 3 : 1); ++part) product(part, kk);
+              }
             }
             if (!ok) break;
             mma_commit(bar(kPVDone + b));
@@ -1006,7 +1073,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         tmem_ld32(tO + r * D + lane_base + c * 32, x);
         tmem_wait_ld();
         if (!real) continue;
-        auto f = [&](int k) { return __uint_as_float(x[k]) * inv; };
+        // (a row that has seen nothing may find anything in O)
+        auto f = [&](int k) { return l == 0.f ? 0.f : __uint_as_float(x[k]) * inv; };
         if (!WIDE && whole) {
           uint16_t* dst = static_cast<uint16_t*>(a.o) + orow * D + c * 32;
           uint32_t y[16];
@@ -1263,11 +1331,13 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   // Tiled copies where blocks are made of runs of 32 or 64 rows.  A tiled copy costs the SM's
   // copy unit some 50 clocks and 2.5 for each row of 128 bytes: boxes of 16 rows come to the
   // memory's rate only while the unit never idles, smaller ones not at all.
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mk16, mv16;
   if (!make_q_map(&mq, a.q, D, a.n_q_heads, a.total_nodes, g, p.tile_nodes))
     return cudaErrorInvalidValue;
   std::memset(&mk, 0, sizeof(mk));
   std::memset(&mv, 0, sizeof(mv));
+  std::memset(&mk16, 0, sizeof(mk16));
+  std::memset(&mv16, 0, sizeof(mv16));
   p.box = kMostBox;
   if (a.block_table)
     while (p.box >= kLeastBox && a.block_size % p.box != 0) p.box /= 2;
@@ -1275,7 +1345,9 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
     const int rows = a.block_table ? a.block_size : a.max_kv_len;
     const int planes = a.block_table ? a.num_blocks : a.batch;
     if (!make_cache_map(&mk, a.k_cache, D, a.n_kv_heads, rows, planes, p.box) ||
-        !make_cache_map(&mv, a.v_cache, D, a.n_kv_heads, rows, planes, p.box))
+        !make_cache_map(&mv, a.v_cache, D, a.n_kv_heads, rows, planes, p.box) ||
+        !make_cache_map(&mk16, a.k_cache, D, a.n_kv_heads, rows, planes, 16) ||
+        !make_cache_map(&mv16, a.v_cache, D, a.n_kv_heads, rows, planes, 16))
       p.box = 0;  // (sizes that a tensor map cannot hold)
   } else {
     p.box = 0;
@@ -1302,7 +1374,7 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mk16, mv16, p);
   if (e != cudaSuccess || a.whole) return e;
   cfg.gridDim = dim3((unsigned)(4 * a.blocks));
   cfg.blockDim = dim3(kJoinWarps * 32);
