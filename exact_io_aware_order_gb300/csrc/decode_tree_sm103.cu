@@ -99,10 +99,10 @@ struct TreeSmem {
   static constexpr int kQChunkBytes = 128 * 128;  // 128 rows of one 128-byte span
   static constexpr int kChunkBytes = kBN * 128;
   static constexpr int kMaxSlots = 12;
-  // barriers: full / empty for each slot, q_empty, s_full[row tile][4], p_full[half][4],
-  // pv_done[4], o_full[2], drain[2], full / empty for each segment slot.  s_full is a row tile's own: one that sits out an item of fewer
+  // barriers: full / empty for each slot, q_empty, s_full[row tile][half][4], p_full[half][4],
+  // half_done[4], pv_done[4], o_full[2], drain[2], full / empty for each segment slot.  s_full is a row tile's own: one that sits out an item of fewer
   // rows would otherwise miss phases, and take an old one for its next.
-  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 8 + 8 + 4 + 2 + 2 + 2 * kSegSlots;
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 16 + 8 + 4 + 4 + 2 + 2 + 2 * kSegSlots;
   static constexpr int kMiscBytes = 1024;  // barriers, then the segment slots
   static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
   // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
-                kPFull = kSFull + 8, kPVDone = kPFull + 8, kOFull = kPVDone + 4,
+                kPFull = kSFull + 16, kHalfDone = kPFull + 8, kPVDone = kHalfDone + 4, kOFull = kPVDone + 4,
                 kDrain = kOFull + 2, kSegFull = kDrain + 2, kSegEmpty = kSegFull + kSegSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     }
     mbar_init(bar(kQEmpty), 1);
     for (int i = 0; i < SB; ++i) {
-      mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kSFull + 4 + i), 1);
+      for (int j = 0; j < 16; j += 4) mbar_init(bar(kSFull + j + i), 1);
+      mbar_init(bar(kHalfDone + i), 1);
       mbar_init(bar(kPFull + i), kSoftmaxThreads);
       mbar_init(bar(kPFull + 4 + i), kSoftmaxThreads);
       mbar_init(bar(kPVDone + i), 1);
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     if (lane == 0) mbar_arrive(bar(kSegEmpty + i));
     return sg.tiles > 0;
   };
-  const uint32_t id_s = idesc_bf16_f32(128, kBN, false, false);
+  const uint32_t id_s = idesc_bf16_f32(128, 64, false, false);
   const uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
   const uint32_t dhi = sw128_desc_hi(1024);
 
@@ -741,17 +741,10 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
           // The 16-byte copies' writes, before the MMAs that read them.
-          uint32_t id = id_s;
-          bool some = true;
-          if (!full_tile(sg, t)) {
-            fence_proxy_async_smem();
-            int k0, k1;
-            steps_of(sg, t, k0, k1);
-            id = idesc_bf16_f32(128, 16 * k1, false, false);
-            some = k1 > 0;
-          } else if (p.box == 0) {
-            fence_proxy_async_smem();
-          }
+          const bool full = full_tile(sg, t);
+          int k0, k1 = kBN / 16;
+          if (!full || p.box == 0) fence_proxy_async_smem();
+          if (!full) steps_of(sg, t, k0, k1);
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n % SB;
@@ -760,15 +753,20 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             tc_fence_after();
             const uint32_t dS = tmem + b * kPitch;
             const uint32_t q_lo = q_lo0 + (uint32_t)((r * L::kQTileBytes) >> 4);
-            if (some) {
+#pragma unroll 1
+            for (int h = 0; h < kBN / 64; ++h) {            // 64 keys at a time
+              const int keys = full ? 64 : min(16 * k1 - 64 * h, 64);
+              const uint32_t id = full ? id_s : idesc_bf16_f32(128, max(keys, 16), false, false);
+              if (keys > 0) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t qoff = ((kk >> 2) * L::kQChunkBytes + (kk & 3) * 32) >> 4;
-                const uint32_t koff = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-                mma_ss_lo(dS, q_lo + qoff, k_lo + koff, dhi, id, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t qoff = ((kk >> 2) * L::kQChunkBytes + (kk & 3) * 32) >> 4;
+                  const uint32_t koff = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+                  mma_ss_lo(dS + 64 * h, q_lo + qoff, k_lo + 512 * h + koff, dhi, id, kk > 0);
+                }
               }
+              mma_commit(bar(kSFull + 8 * r + 4 * h + b));
             }
-            mma_commit(bar(kSFull + 4 * r + b));
           }
           mma_commit(bar(kEmpty + slot));
           // K tiles are every other one of the ring.
@@ -805,25 +803,26 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             // P comes in halves of 64 keys.
             const uint32_t aP = tmem + b * kPitch, tOr = tO + r * D;
             uint32_t onto = t > 0 ? 1u : 0u;  // (the first product of a segment overwrites O)
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < kBN / 64; ++h) {
               if (!mbar_wait(bar(kPFull + 4 * h + b), (n / SB) & 1, ctl)) { ok = false; break; }
               tc_fence_after();
+              const uint32_t aH = aP + 64 * h, v_h = v_lo + 512 * h;
               auto product = [&](int part, int kk) {
-                mma_ts_lo(tOr, aP + part * (kBN / 2) + kk * 8, v_lo + ((kk * 16 * 128) >> 4), dhi,
-                          id_pv, onto);
+                mma_ts_lo(tOr, aH + part * 32 + kk * 8, v_h + ((kk * 16 * 128) >> 4), dhi, id_pv, onto);
                 onto = 1u;
               };
               if (full) {  // (straight code: each branch between MMAs shows)
 #pragma unroll
                 for (int part = 0; part < (WIDE ? 3 : 1); ++part)
 #pragma unroll
-                  for (int kk = 4 * h; kk < 4 * h + 4; ++kk) product(part, kk);
+                  for (int kk = 0; kk < 4; ++kk) product(part, kk);
               } else {
 #pragma unroll 1
-                for (int kk = max(k0, 4 * h); kk < min(k1, 4 * h + 4); ++kk)
+                for (int kk = max(k0 - 4 * h, 0); kk < min(k1 - 4 * h, 4); ++kk)
                   for (int part = 0; part < (WIDE ? 3 : 1); ++part) product(part, kk);
               }
+              if (kBN > 64 && h == 0) mma_commit(bar(kHalfDone + b));
             }
             if (!ok) break;
             mma_commit(bar(kPVDone + b));
@@ -850,7 +849,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     int count = 0;
     bool ok = true;
     int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
-    uint32_t s_phase = 0;   // s_full's phase, a bit for each buffer
+    uint32_t s_phase = 0;   // s_full's phases, a bit for each half and buffer
     for (; ok && take(sg, count, true); n0 += sg.tiles * sg.nr) {
       if (r >= sg.nr) continue;
       const int in_tile = trow / g;                         // this row's node in the row tile
@@ -904,25 +903,20 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             vis[c] = w;
           }
         }
-        if (!mbar_wait_warp(bar(kSFull + 4 * r + b), (s_phase >> b) & 1u, ctl)) { ok = false; break; }
-        s_phase ^= 1u << b;
-        tc_fence_after();
         const uint32_t tS = tmem + b * kPitch + lane_base;
-        // What turns the score of column k into log2 units: x sl2 + (base + slope k).
-        float sl2 = VAR == kCap ? 1.f : p.sl2, slope = 0.f, base = 0.f;
-        if constexpr (VAR == kAlibi) {
-          slope = slope_l2;
-          base = -slope_l2 * (float)(pos - kv0);
-          if (edge) sl2 = 1.f, slope = 0.f, base = 0.f;
-        }
-        float2 steps[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          steps[q] = make_float2(slope * (float)(2 * q), slope * (float)(2 * q + 1));
+        auto wait_s = [&](int h) {
+          const int i = 4 * h + b;
+          if (!mbar_wait_warp(bar(kSFull + 8 * r + i), (s_phase >> i) & 1u, ctl)) return false;
+          s_phase ^= 1u << i;
+          tc_fence_after();
+          return true;
+        };
         const bool ahead = edge || (VAR == kCap && kBN > 64);
         if (ahead) {
           // Soft-capping, masks, and ALiBi where nodes are among the keys: a pass of its own,
           // written back.
+          for (int h = 0; h < kBN / 64 && ok; ++h) ok = wait_s(h);
+          if (!ok) break;
 #pragma unroll 1
           for (int c = 0; c < kBN / 32; ++c) {
             uint32_t y[32];
@@ -933,7 +927,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             if (edge) {
               if constexpr (VAR == kAlibi) {
                 const float d0 = (float)(pos - kv0 - 32 * c);
-                const int u0 = kv0 + 32 * c - sg.kv_len;  // node of the first column
+                const int u0 = kv0 + 32 * c - sg.kv_len;    // node of the first column
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                   const float dist = u0 + k < 0
@@ -954,103 +948,126 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           }
           tmem_wait_st();
         }
-        // ---- the row's scores, and their maximum ----
-        uint32_t x[kBN / 32][32];
-#pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) tmem_ld32(tS + c * 32, x[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) landed(x[c]);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) {
-          uint32_t (&y)[32] = x[c];
-          if (VAR == kCap && !ahead) soft_cap(y, p.cap_in, p.cap_l2);
+        // 64 keys at a time, whose scores stay in registers (one copy of the code for all: it
+        // is fetched anew for every tile, beside five other roles').
+#pragma unroll 1
+        for (int h = 0; h < kBN / 64; ++h) {
+          if (!ahead && !wait_s(h)) { ok = false; break; }
+          const uint32_t tH = tS + 64 * h;
+          // What turns the score of column k into log2 units: x sl2 + (base + slope k).
+          float sl2 = VAR == kCap ? 1.f : p.sl2, slope = 0.f, base = 0.f;
           if constexpr (VAR == kAlibi) {
-            const float2 sl2v = make_float2(sl2, sl2);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              // slope k is that of the 8 columns' first and one of four pairs.
-              const float b8 = fmaf(slope, (float)(32 * c + (k & ~7)), base);
-              const float2 e = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
-                                    sl2v, add2(make_float2(b8, b8), steps[(k >> 1) & 3]));
-              y[k] = __float_as_uint(e.x);
-              y[k + 1] = __float_as_uint(e.y);
-            }
+            slope = slope_l2;
+            base = -slope_l2 * (float)(pos - kv0 - 64 * h);
+            if (edge) sl2 = 1.f, slope = 0.f, base = 0.f;
           }
-          float mc[4];
+          uint32_t x[2][32];
+          tmem_ld32(tH, x[0]);
+          tmem_ld32(tH + 32, x[1]);
+          tmem_wait_ld();
+          landed(x[0]);
+          landed(x[1]);
+          // ---- the row's maximum ----
+          float mx = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
+          for (int c = 0; c < 2; ++c) {
+            uint32_t (&y)[32] = x[c];
+            if (VAR == kCap && !ahead) soft_cap(y, p.cap_in, p.cap_l2);
+            if constexpr (VAR == kAlibi) {
+              float2 steps[4];
 #pragma unroll
-          for (int k = 8; k < 32; k += 8)
+              for (int q = 0; q < 4; ++q)
+                steps[q] = make_float2(slope * (float)(2 * q), slope * (float)(2 * q + 1));
+              const float2 sl2v = make_float2(sl2, sl2);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                // slope k is that of the 8 columns' first and one of four pairs.
+                const float b8 = fmaf(slope, (float)(32 * c + (k & ~7)), base);
+                const float2 e = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
+                                      sl2v, add2(make_float2(b8, b8), steps[(k >> 1) & 3]));
+                y[k] = __float_as_uint(e.x);
+                y[k + 1] = __float_as_uint(e.y);
+              }
+            }
+            float mc[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
-          mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-        }
-        if constexpr (VAR != kAlibi) mx *= sl2;
-        // ---- the reference: the first maximum that a row sees; raised only when some row of the
-        // warp has outgrown it ----
-        if (m == -INFINITY) m = mx;                         // (O and l are 0)
-        if (__any_sync(0xffffffffu, mx - m > kRescaleThreshold)) {
-          const float m_new = fmaxf(m, mx);
-          const float corr = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
-          m = m_new;
-          l *= corr;
-          if (t > 0) {
-            const int pn = n - sg.nr;                       // this row tile's last product
-            if (!mbar_wait_warp(bar(kPVDone + pn % SB), (pn / SB) & 1, ctl)) { ok = false; break; }
-            tc_fence_after();
+              mc[q] = fmaxf(__uint_as_float(y[q]), __uint_as_float(y[q + 4]));
+#pragma unroll
+            for (int k = 8; k < 32; k += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mc[q] = fmax3(mc[q], __uint_as_float(y[k + q]), __uint_as_float(y[k + q + 4]));
+            mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+          }
+          if constexpr (VAR != kAlibi) mx *= sl2;
+          // ---- the reference: the first maximum that a row sees; raised only when some row of
+          // the warp has outgrown it ----
+          if (m == -INFINITY) m = mx;                       // (O and l are 0)
+          if (__any_sync(0xffffffffu, mx - m > kRescaleThreshold)) {
+            const float m_new = fmaxf(m, mx);
+            const float corr = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
+            m = m_new;
+            l *= corr;
+            if (t > 0 || h > 0) {
+              // O has to hold this row tile's products so far: the tile before's, or this one's
+              // first half.
+              const int pn = n - sg.nr;
+              if (!(h > 0 ? mbar_wait_warp(bar(kHalfDone + b), (n / SB) & 1, ctl)
+                          : mbar_wait_warp(bar(kPVDone + pn % SB), (pn / SB) & 1, ctl))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-              uint32_t y[8];
-              const uint32_t at = tO + r * D + lane_base + c * 8;
-              tmem_ld8(at, y);
-              tmem_wait_ld();
+              for (int c = 0; c < D / 8; ++c) {
+                uint32_t y[8];
+                const uint32_t at = tO + r * D + lane_base + c * 8;
+                tmem_ld8(at, y);
+                tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
-              tmem_st8(at, y);
+                for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
+                tmem_st8(at, y);
+              }
             }
           }
-        }
-        const float nm = m == -INFINITY ? 0.f : -m;
-        // ---- P over S ----
-        const float2 sl2w = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
-        float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float nm = m == -INFINITY ? 0.f : -m;
+          // ---- P over S ----
+          const float2 sl2w = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
+          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) {
-          const uint32_t (&y)[32] = x[c];
-          uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t (&y)[32] = x[c];
+            uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 v = make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
-            // (ALiBi's scores are in log2 units already)
-            const float2 e = VAR == kAlibi ? add2(v, nmv) : fma2(v, sl2w, nmv);
-            float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            rs[k & 1] = add2(rs[k & 1], pp);
-            hi[k] = pack_bf16x2(pp.x, pp.y);
+            for (int k = 0; k < 16; ++k) {
+              const float2 v = make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+              // (ALiBi's scores are in log2 units already)
+              const float2 e = VAR == kAlibi ? add2(v, nmv) : fma2(v, sl2w, nmv);
+              float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              rs[k & 1] = add2(rs[k & 1], pp);
+              hi[k] = pack_bf16x2(pp.x, pp.y);
+              if constexpr (WIDE) {
+                pp.x -= __uint_as_float(hi[k] << 16);
+                pp.y -= __uint_as_float(hi[k] & 0xffff0000u);
+                mid[k] = pack_bf16x2(pp.x, pp.y);
+                lo[k] = pack_bf16x2(pp.x - __uint_as_float(mid[k] << 16),
+                                    pp.y - __uint_as_float(mid[k] & 0xffff0000u));
+              }
+            }
+            tmem_st16(tH + c * 16, hi);
             if constexpr (WIDE) {
-              pp.x -= __uint_as_float(hi[k] << 16);
-              pp.y -= __uint_as_float(hi[k] & 0xffff0000u);
-              mid[k] = pack_bf16x2(pp.x, pp.y);
-              lo[k] = pack_bf16x2(pp.x - __uint_as_float(mid[k] << 16),
-                                  pp.y - __uint_as_float(mid[k] & 0xffff0000u));
+              tmem_st16(tH + 32 + c * 16, mid);
+              tmem_st16(tH + 64 + c * 16, lo);
             }
           }
-          tmem_st16(tS + c * 16, hi);
-          if constexpr (WIDE) {
-            tmem_st16(tS + kBN / 2 + c * 16, mid);
-            tmem_st16(tS + kBN + c * 16, lo);
-          }
-          if (c & 1) {                                      // 64 keys of P are there
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar(kPFull + 4 * (c >> 1) + b));
-          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kPFull + 4 * h + b));
+          const float2 rsum = add2(rs[0], rs[1]);
+          l += rsum.x + rsum.y;
         }
-        const float2 rsum = add2(rs[0], rs[1]);
-        l += rsum.x + rsum.y;
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- epilogue of the segment ----
