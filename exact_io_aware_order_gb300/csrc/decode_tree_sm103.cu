@@ -456,6 +456,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const CUtensorMap* map16 = keys ? &tm_k16 : &tm_v16;
     const uint16_t* cache = keys ? a.k_cache : a.v_cache;
     constexpr int kSpans = D / 64, kSets = kBN / 32;
+    const int box = lane / kSpans, span = lane % kSpans;
+    const bool mine = p.box > 0 && box * p.box < kBN;
     int slot = keys ? 0 : 1, phase = 0, n_seg = 0, issued = 0;
     bool again = false;                                    // slots have been used before
     Seg sg;
@@ -572,27 +574,17 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     while (ok && (keys ? plan() : take(sg, count, true))) {
       const int32_t* table =
           a.block_table ? a.block_table + (size_t)sg.b * a.max_blocks_per_seq : nullptr;
-      // Where this lane's rows of a tile (lane, lane + 32, ..) lie: the block's number in the
-      // table, the row in it, and what the table says.  The table is read a tile ahead, so
-      // that its latency is not in the way.
-      int blk[kSets], row_in[kSets], entry[kSets];
-      auto look = [&](int tile0) {
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-          const int tok = tile0 + lane + 32 * i;
-          if (table != nullptr && tok >= sg.first && tok < sg.end) entry[i] = table[blk[i]];
-        }
-      };
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-        blk[i] = entry[i] = 0;
-        row_in[i] = first_key(sg, 0) + lane + 32 * i;
-        if (table != nullptr) {
-          blk[i] = row_in[i] / a.block_size;
-          row_in[i] -= blk[i] * a.block_size;
-        }
+      // Tiled copies of a whole tile: a box and span a lane.  Its block's number in the table,
+      // the row in it, and what the table says, which is read a tile ahead.
+      int blk = 0, row_in = first_key(sg, 0) + box * p.box, entry = sg.b;
+      if (table != nullptr) {
+        blk = row_in / a.block_size;
+        row_in -= blk * a.block_size;
       }
-      look(first_key(sg, 0));
+      auto look = [&](int t) {
+        if (table != nullptr && mine && t < sg.tiles && full_tile(sg, t)) entry = table[blk];
+      };
+      look(0);
       for (int t = 0; t < sg.tiles && ok; ++t) {
         const int tile0 = first_key(sg, t);
         const uint32_t dst = smem_u32(ring + slot * L::kTileBytes), full = bar(kFull + slot);
@@ -608,89 +600,79 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           // Queries: tile_nodes nodes' g rows a row tile (rows past the nodes are not used).
           mbar_expect_tx(full, (uint32_t)(sg.nr * p.tile_nodes * g) * D * 2);
           for (int r = 0; r < sg.nr; ++r)
-            for (int span = 0; span < kSpans; ++span)
-              tma_load_3d(smem_u32(smem + r * L::kQTileBytes + span * L::kQChunkBytes), &tm_q, full,
-                          span * 64, sg.kvh * g, sg.q0 + sg.node0 + r * p.tile_nodes);
-        }
-        int plane[kSets];
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-          const int tok = tile0 + lane + 32 * i;
-          plane[i] = table ? entry[i] : sg.b;
-          if (table != nullptr && tok >= sg.first && tok < sg.end &&
-              (plane[i] < 0 || plane[i] >= a.num_blocks)) {
-            atomicOr(p.err_word, kErrBlockIndex);
-            plane[i] = -1;
-          }
+            for (int i = 0; i < kSpans; ++i)
+              tma_load_3d(smem_u32(smem + r * L::kQTileBytes + i * L::kQChunkBytes), &tm_q, full,
+                          i * 64, sg.kvh * g, sg.q0 + sg.node0 + r * p.tile_nodes);
         }
         if (p.box > 0 && full_tile(sg, t)) {
-          // One lane issues them all.  Boxes of 32 rows or more begin where its own rows are,
-          // those of 16 also where lane 16's are.  A bad block becomes one past the cache,
-          // which reads as zeros.
-          const bool small = p.box == 16;
-          int row2[kSets], plane2[kSets];
-          if (small) {
-#pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-              row2[i] = __shfl_sync(0xffffffffu, row_in[i], 16);
-              plane2[i] = __shfl_sync(0xffffffffu, plane[i], 16);
-            }
+          int plane = entry;
+          if (table != nullptr && mine && (plane < 0 || plane >= a.num_blocks)) {
+            // A bad block becomes one past the cache, which reads as zeros.
+            atomicOr(p.err_word, kErrBlockIndex);
+            plane = a.num_blocks;
           }
-          if (lane == 0) {
-            mbar_expect_tx(full, kBN * D * 2);
-            auto at = [&](int plane) { return plane < 0 ? a.num_blocks : plane; };
-#pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-              if (!small && (i & (p.box / 32 - 1))) continue;
-#pragma unroll
-              for (int span = 0; span < kSpans; ++span) {
-                const uint32_t to = dst + span * L::kChunkBytes + i * 32 * 128;
-                tma_load_4d(to, map, full, span * 64, sg.kvh, row_in[i], at(plane[i]));
-                if (small)
-                  tma_load_4d(to + 16 * 128, map, full, span * 64, sg.kvh, row2[i], at(plane2[i]));
-              }
-            }
-            mbar_arrive_n(full, 32);
-          }
+          if (lane == 0) mbar_expect_tx(full, kBN * D * 2);
           __syncwarp();
+          // Every lane its own: with one lane that issues them all, 16 paged sequences of up to
+          // 32768 tokens take 315 us instead of 228.
+          if (mine)
+            tma_load_4d(dst + span * L::kChunkBytes + box * p.box * 128, map, full, span * 64, sg.kvh,
+                        row_in, plane);
+          if (lane == 0) mbar_arrive_n(full, 32);
         } else {
           // A tile that ends early or begins in front of a window, or blocks of other sizes: steps
           // of 16 rows.  Those that are all there by a tiled copy where blocks allow it, the
           // others row by row, 16 bytes a lane, zeros for rows that are not there (the products
           // multiply them by weights of 0).
-          const int rows = table ? a.block_size : a.max_kv_len;
-          int row[kSets];
-#pragma unroll
-          for (int i = 0; i < kSets; ++i) {
-            const int tok = tile0 + lane + 32 * i;
-            row[i] = tok >= sg.first && tok < sg.end && plane[i] >= 0 ? plane[i] * rows + row_in[i] : -1;
-          }
           int k0, k1;
           steps_of(sg, t, k0, k1);
           auto whole = [&](int k) {
             return p.box > 0 && tile0 + 16 * k >= sg.first && tile0 + 16 * k + 16 <= sg.end;
           };
+          auto find = [&](int tok, int& in) {  // the plane of a token's row, -1 for a bad block
+            in = tok;
+            if (table == nullptr) return sg.b;
+            const int j = tok / a.block_size, x = table[j];
+            in = tok - j * a.block_size;
+            if (x >= 0 && x < a.num_blocks) return x;
+            atomicOr(p.err_word, kErrBlockIndex);
+            return -1;
+          };
           int n_boxes = 0;
           for (int k = k0; k < k1; ++k) n_boxes += whole(k);
-          if (lane == 0 && n_boxes > 0) mbar_expect_tx(full, (uint32_t)(n_boxes * 16 * D * 2));
-          __syncwarp();
-#pragma unroll 1
-          for (int k = k0; k < k1; ++k) {
-            int r = row[0], in = row_in[0], pl = plane[0];
+          if (n_boxes > 0) {
+            if (lane == 0) mbar_expect_tx(full, (uint32_t)(n_boxes * 16 * D * 2));
+            __syncwarp();
+            if (box >= k0 && box < k1 && whole(box)) {
+              int in;
+              const int plane = find(tile0 + 16 * box, in);
+              tma_load_4d(dst + span * L::kChunkBytes + box * 16 * 128, map16, full, span * 64, sg.kvh,
+                          in, plane < 0 ? a.num_blocks : plane);
+            }
+            __syncwarp();
+          }
+          if (n_boxes < k1 - k0) {
+            // The places of rows lane, lane + 32, ..
+            const int rows = table ? a.block_size : a.max_kv_len;
+            int row[kSets];
 #pragma unroll
-            for (int i = 1; i < kSets; ++i)
-              if ((k >> 1) == i) r = row[i], in = row_in[i], pl = plane[i];
-            if (whole(k)) {
-              in = __shfl_sync(0xffffffffu, in, (k & 1) * 16);
-              pl = __shfl_sync(0xffffffffu, pl, (k & 1) * 16);
-              if (lane == 0) {
-#pragma unroll
-                for (int span = 0; span < kSpans; ++span)
-                  tma_load_4d(dst + span * L::kChunkBytes + k * 16 * 128, map16, full, span * 64,
-                              sg.kvh, in, pl < 0 ? a.num_blocks : pl);
+            for (int i = 0; i < kSets; ++i) {
+              const int tok = tile0 + lane + 32 * i;
+              row[i] = -1;
+              if (tok >= sg.first && tok < sg.end && !whole(2 * i + (lane >> 4))) {
+                int in;
+                const int plane = find(tok, in);
+                if (plane >= 0) row[i] = plane * rows + in;
               }
-              __syncwarp();
-            } else {
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) {
+              if (whole(k)) continue;
+              int r = row[0];
+#pragma unroll
+              for (int i = 1; i < kSets; ++i)
+                if ((k >> 1) == i) r = row[i];
               copy_rows<D, kBN>(dst, k, cache + (size_t)sg.kvh * D, (long long)a.n_kv_heads * D, r,
                                 lane);
             }
@@ -699,19 +681,18 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         }
         ++issued;
         // The next tile of the walk.
-        const int step = VAR == kAlibi ? -1 : 1;
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-          if (table == nullptr) {
-            row_in[i] += step * kBN;
-          } else {
-            blk[i] += step * p.blocks_a_tile;
-            row_in[i] += step * p.rest_a_tile;
-            if (row_in[i] >= a.block_size) row_in[i] -= a.block_size, ++blk[i];
-            if (row_in[i] < 0) row_in[i] += a.block_size, --blk[i];
-          }
+        if (table == nullptr) {
+          row_in += VAR == kAlibi ? -kBN : kBN;
+        } else if (VAR == kAlibi) {
+          blk -= p.blocks_a_tile;
+          row_in -= p.rest_a_tile;
+          if (row_in < 0) row_in += a.block_size, --blk;
+        } else {
+          blk += p.blocks_a_tile;
+          row_in += p.rest_a_tile;
+          if (row_in >= a.block_size) row_in -= a.block_size, ++blk;
         }
-        if (t + 1 < sg.tiles) look(first_key(sg, t + 1));
+        look(t + 1);
         for (int i = 0; i < 2; ++i)
           if (++slot == slots) slot = 0, phase ^= 1, again = true;
       }
