@@ -56,7 +56,7 @@
 namespace attn {
 namespace {
 
-constexpr int kSoftmaxThreads = 128;   // of a row tile
+constexpr int kSoftmaxThreads = 128;   // a warpgroup's; two of them
 constexpr int kProducerThreads = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -88,7 +88,7 @@ template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_bufs() 
   return !WIDE && (D == 256 || VAR != kPlain) ? 4 : D == 64 ? 3 : 2;
 }
 template <int D> __host__ __device__ constexpr int threads_of() {
-  return row_tiles<D>() * kSoftmaxThreads + kProducerThreads + 64;
+  return 2 * kSoftmaxThreads + kProducerThreads + 64;
 }
 
 template <int D, int VAR, bool WIDE>
@@ -102,9 +102,11 @@ struct TreeSmem {
   // barriers: full / empty for each slot, q_empty, s_full[row tile][half][4], p_full[half][4],
   // half_done[4], pv_done[4], o_full[2], drain[2], full / empty for each segment slot.  s_full is a row tile's own: one that sits out an item of fewer
   // rows would otherwise miss phases, and take an old one for its next.
-  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 16 + 8 + 4 + 4 + 2 + 2 + 2 * kSegSlots;
+  static constexpr int kNumBars = 2 * kMaxSlots + 1 + 16 + 8 + 4 + 4 + 2 + 2 + 2 * kSegSlots + 1;
   static constexpr int kMiscBytes = 1024;  // barriers, then the segment slots
-  static constexpr int kDepthBytes = row_tiles<D>() * 4 * kMostNodes * 4;  // a table a warp
+  // A table of depths a warp; at head_dim 256 what the halves of a row tell each other.
+  static constexpr int kDepthTabBytes = 8 * kMostNodes * 4;
+  static constexpr int kDepthBytes = kDepthTabBytes + (D == 256 ? 2 * 2 * 128 * 4 : 0);
   // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
   static constexpr int slots(int q_tiles) {
     const int room = 226 * 1024 - kMiscBytes - kDepthBytes - 1024 - q_tiles * kQTileBytes;
@@ -309,32 +311,45 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 // tanhf for all of them.  ex2.approx and rcp.approx would be as fast, but their 2e-7 is an
 // absolute error of tanh, 1e-5 of a score at softcap 50.
 __device__ __forceinline__ void soft_cap(uint32_t (&x)[32], float in, float out) {
-  float top = 0.f;
+  const float2 in2 = make_float2(in, in), out2 = make_float2(out, out);
+  auto two = [](float c) { return make_float2(c, c); };
 #pragma unroll
-  for (int k = 0; k < 32; k += 2)
-    top = fmax3(top, fabsf(__uint_as_float(x[k])), fabsf(__uint_as_float(x[k + 1])));
-  if (__all_sync(0xffffffffu, top * in <= 0.45f)) {
-    const float2 in2 = make_float2(in, in), out2 = make_float2(out, out);
-    auto two = [](float c) { return make_float2(c, c); };
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      const float2 u = mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), in2);
-      const float2 t = mul2(u, u);
-      float2 y = fma2(t, two(21844.f / 6081075.f), two(-1382.f / 155925.f));
-      y = fma2(t, y, two(62.f / 2835.f));
-      y = fma2(t, y, two(-17.f / 315.f));
-      y = fma2(t, y, two(2.f / 15.f));
-      y = fma2(t, y, two(-1.f / 3.f));
-      const float2 v = mul2(u, out2);
-      y = fma2(mul2(t, y), v, v);
-      x[k] = __float_as_uint(y.x);
-      x[k + 1] = __float_as_uint(y.y);
-    }
-  } else {  // (NaN too)
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      x[k] = __float_as_uint(out * tanhf(__uint_as_float(x[k]) * in));
+  for (int k = 0; k < 32; k += 2) {
+    const float2 u = mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), in2);
+    const float2 t = mul2(u, u);
+    float2 y = fma2(t, two(21844.f / 6081075.f), two(-1382.f / 155925.f));
+    y = fma2(t, y, two(62.f / 2835.f));
+    y = fma2(t, y, two(-17.f / 315.f));
+    y = fma2(t, y, two(2.f / 15.f));
+    y = fma2(t, y, two(-1.f / 3.f));
+    const float2 v = mul2(u, out2);
+    y = fma2(mul2(t, y), v, v);
+    x[k] = __float_as_uint(y.x);
+    x[k + 1] = __float_as_uint(y.y);
   }
+}
+__device__ __forceinline__ bool small_for_cap(const uint32_t (&x)[32], float in) {
+  float top[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 32; k += 4)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      top[q] = fmax3(top[q], fabsf(__uint_as_float(x[k + 2 * q])), fabsf(__uint_as_float(x[k + 2 * q + 1])));
+  return fmaxf(top[0], top[1]) * in <= 0.45f;
+}
+// The same where a warp's scores lie in TMEM, for any |u| (NaN too): a short loop, because 32
+// copies of tanhf in a tile's way cost every tile the fetch around them.
+__device__ __forceinline__ void soft_cap_large(uint32_t at, int cols, float in, float out) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 8) {
+    uint32_t y[8];
+    tmem_ld8(at + c, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(out * tanhf(__uint_as_float(y[k]) * in));
+    tmem_st8(at + c, y);
+  }
+  tmem_wait_st();
 }
 
 // VAR: what happens to a score besides scale and window.  WIDE: fp32 O, P in three parts.
@@ -345,7 +360,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ TreeKParams p) {
   using L = TreeSmem<D, VAR, WIDE>;
   constexpr int kBN = L::kBN, kPitch = s_pitch<D, VAR, WIDE>(), SB = s_bufs<D, VAR, WIDE>(), NQ = row_tiles<D>();
-  constexpr int kProducerWarp = NQ * 4, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
+  constexpr bool kSplit = NQ == 1;  // both warpgroups work on the one row tile
+  constexpr int kProducerWarp = 8, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
   static_assert(SB * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
   const DecodeTreeArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
@@ -359,7 +375,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   constexpr int kFull = 0, kEmpty = L::kMaxSlots, kQEmpty = 2 * L::kMaxSlots, kSFull = kQEmpty + 1,
                 kPFull = kSFull + 16, kHalfDone = kPFull + 8, kPVDone = kHalfDone + 4, kOFull = kPVDone + 4,
-                kDrain = kOFull + 2, kSegFull = kDrain + 2, kSegEmpty = kSegFull + kSegSlots;
+                kDrain = kOFull + 2, kSegFull = kDrain + 2, kSegEmpty = kSegFull + kSegSlots,
+                kExchange = kSegEmpty + kSegSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L::kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
   constexpr int kSegOffset = (L::kNumBars * 8 + 16 + 15) / 16 * 16;
@@ -377,7 +394,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     for (int i = 0; i < SB; ++i) {
       for (int j = 0; j < 16; j += 4) mbar_init(bar(kSFull + j + i), 1);
       mbar_init(bar(kHalfDone + i), 1);
-      mbar_init(bar(kPFull + i), kSoftmaxThreads);
+      mbar_init(bar(kPFull + i), kSplit ? 2 * kSoftmaxThreads : kSoftmaxThreads);
       mbar_init(bar(kPFull + 4 + i), kSoftmaxThreads);
       mbar_init(bar(kPVDone + i), 1);
     }
@@ -387,8 +404,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(bar(kSegFull + i), 1);
-      mbar_init(bar(kSegEmpty + i), 3 + 4 * NQ);  // the values' producer, two issuers, softmax warps
+      mbar_init(bar(kSegEmpty + i), 3 + kProducerWarp);  // the values' producer, two issuers, softmax warps
     }
+    mbar_init(bar(kExchange), 2 * kSoftmaxThreads);
     fence_mbar_init();
   }
   if (warp == kProducerWarp && lane == 0) {
@@ -822,7 +840,11 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     __syncwarp();
   } else if (warp < kProducerWarp) {
     // ============================ softmax, epilogue ============================
-    const int r = warp >> 2;                                // row tile
+    // A warpgroup a row tile; at head_dim 256 both on the one, 32 of a tile's 64 keys each,
+    // with one reference for a row, and half of O's columns each in the end: 4 sequences of
+    // 2000 - 9000 tokens, a window of 4096, soft-capping and fp32 outputs 58 us, 70 with one.
+    const int r = kSplit ? 0 : warp >> 2;                   // row tile
+    const int part = kSplit ? warp >> 2 : 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int trow = (warp & 3) * 32 + lane;                // row within the tile (TMEM lane)
     int* depths = depth_tab + warp * kMostNodes;            // the nodes' depths, each warp its own
@@ -830,6 +852,20 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     int count = 0;
     bool ok = true;
     int n0 = 0, n_seg = 0;  // S products before the segment, segments of this row tile
+    uint32_t exchanges = 0;
+    float* told = reinterpret_cast<float*>(depth_tab + L::kDepthTabBytes / 4);
+    // What the other half of the row says (the lower half's value first).
+    auto exchange = [&](float mine, float (&both)[2]) -> bool {
+      float* at = told + (exchanges & 1) * 256 + trow;
+      at[part * 128] = mine;
+      tc_fence_before();
+      mbar_arrive(bar(kExchange));
+      if (!mbar_wait_warp(bar(kExchange), exchanges & 1, ctl)) return false;
+      ++exchanges;
+      tc_fence_after();
+      both[0] = at[0], both[1] = at[128];
+      return true;
+    };
     uint32_t s_phase = 0;   // s_full's phases, a bit for each half and buffer
     for (; ok && take(sg, count, true); n0 += sg.tiles * sg.nr) {
       if (r >= sg.nr) continue;
@@ -899,12 +935,21 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           for (int h = 0; h < kBN / 64 && ok; ++h) ok = wait_s(h);
           if (!ok) break;
 #pragma unroll 1
-          for (int c = 0; c < kBN / 32; ++c) {
+          for (int c = kSplit ? part : 0; c < (kSplit ? part + 1 : kBN / 32); ++c) {
             uint32_t y[32];
             tmem_ld32(tS + c * 32, y);
             tmem_wait_ld();
             landed(y);
-            if constexpr (VAR == kCap) soft_cap(y, p.cap_in, p.cap_l2);
+            if constexpr (VAR == kCap) {
+              if (__all_sync(0xffffffffu, small_for_cap(y, p.cap_in))) {
+                soft_cap(y, p.cap_in, p.cap_l2);
+              } else {
+                soft_cap_large(tS + c * 32, 32, p.cap_in, p.cap_l2);
+                tmem_ld32(tS + c * 32, y);
+                tmem_wait_ld();
+                landed(y);
+              }
+            }
             if (edge) {
               if constexpr (VAR == kAlibi) {
                 const float d0 = (float)(pos - kv0 - 32 * c);
@@ -934,26 +979,40 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
 #pragma unroll 1
         for (int h = 0; h < kBN / 64; ++h) {
           if (!ahead && !wait_s(h)) { ok = false; break; }
-          const uint32_t tH = tS + 64 * h;
+          const uint32_t tH = tS + 64 * h + 32 * part;
           // What turns the score of column k into log2 units: x sl2 + (base + slope k).
           float sl2 = VAR == kCap ? 1.f : p.sl2, slope = 0.f, base = 0.f;
           if constexpr (VAR == kAlibi) {
             slope = slope_l2;
-            base = -slope_l2 * (float)(pos - kv0 - 64 * h);
+            base = -slope_l2 * (float)(pos - kv0 - 64 * h - 32 * part);
             if (edge) sl2 = 1.f, slope = 0.f, base = 0.f;
           }
-          uint32_t x[2][32];
-          tmem_ld32(tH, x[0]);
-          tmem_ld32(tH + 32, x[1]);
-          tmem_wait_ld();
-          landed(x[0]);
-          landed(x[1]);
+          constexpr int kSets = kSplit ? 1 : 2;
+          uint32_t x[kSets][32];
+          auto load = [&]() {
+#pragma unroll
+            for (int c = 0; c < kSets; ++c) tmem_ld32(tH + 32 * c, x[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kSets; ++c) landed(x[c]);
+          };
+          load();
+          if (VAR == kCap && !ahead) {
+            const bool small =
+                small_for_cap(x[0], p.cap_in) && small_for_cap(x[kSets - 1], p.cap_in);
+            if (__all_sync(0xffffffffu, small)) {
+#pragma unroll
+              for (int c = 0; c < kSets; ++c) soft_cap(x[c], p.cap_in, p.cap_l2);
+            } else {
+              soft_cap_large(tH, 32 * kSets, p.cap_in, p.cap_l2);
+              load();
+            }
+          }
           // ---- the row's maximum ----
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kSets; ++c) {
             uint32_t (&y)[32] = x[c];
-            if (VAR == kCap && !ahead) soft_cap(y, p.cap_in, p.cap_l2);
             if constexpr (VAR == kAlibi) {
               float2 steps[4];
 #pragma unroll
@@ -982,6 +1041,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
           }
           if constexpr (VAR != kAlibi) mx *= sl2;
+          if constexpr (kSplit) {
+            // (both have read their scores then, which P overwrites)
+            float both[2];
+            if (!exchange(mx, both)) { ok = false; break; }
+            mx = fmaxf(both[0], both[1]);
+          }
           // ---- the reference: the first maximum that a row sees; raised only when some row of
           // the warp has outgrown it ----
           if (m == -INFINITY) m = mx;                       // (O and l are 0)
@@ -1001,7 +1066,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
               }
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 8; ++c) {
+              for (int c = part * (D / 16); c < (kSplit ? (part + 1) * (D / 16) : D / 8); ++c) {
                 uint32_t y[8];
                 const uint32_t at = tO + r * D + lane_base + c * 8;
                 tmem_ld8(at, y);
@@ -1017,7 +1082,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           const float2 sl2w = make_float2(sl2, sl2), nmv = make_float2(nm, nm);
           float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kSets; ++c) {
             const uint32_t (&y)[32] = x[c];
             uint32_t hi[16], mid[WIDE ? 16 : 1], lo[WIDE ? 16 : 1];
 #pragma unroll
@@ -1036,10 +1101,11 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
                                     pp.y - __uint_as_float(mid[k] & 0xffff0000u));
               }
             }
-            tmem_st16(tH + c * 16, hi);
+            const uint32_t tP = tS + 64 * h + (c + part) * 16;
+            tmem_st16(tP, hi);
             if constexpr (WIDE) {
-              tmem_st16(tH + 32 + c * 16, mid);
-              tmem_st16(tH + 64 + c * 16, lo);
+              tmem_st16(tP + 32, mid);
+              tmem_st16(tP + 64, lo);
             }
           }
           tmem_wait_st();
@@ -1055,18 +1121,23 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       if (!mbar_wait_warp(bar(kOFull + r), n_seg & 1, ctl)) { ok = false; break; }
       ++n_seg;
       tc_fence_after();
+      if constexpr (kSplit) {
+        float both[2];
+        if (!exchange(l, both)) { ok = false; break; }
+        l = both[0] + both[1];
+      }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a NaN stays)
       const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       const bool whole = sg.place == 2;
       // A cut item's partial: place 0 of the block for one that began before, else 1.
       const size_t pplace = (size_t)blockIdx.x * 2 + sg.place, prow = pplace * a.part_rows + i;
       const size_t orow = (size_t)(sg.q0 + node) * a.n_q_heads + head;
-      if (real) {
+      if (real && part == 0) {
         if (whole) a.lse[orow] = lse;
         else a.lse_part[prow] = lse;
       }
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = part * (D / 64); c < (kSplit ? (part + 1) * (D / 64) : D / 32); ++c) {
         uint32_t x[32];
         tmem_ld32(tO + r * D + lane_base + c * 32, x);
         tmem_wait_ld();
