@@ -68,7 +68,7 @@ constexpr float kRescaleThreshold = 32.0f;
 constexpr int kMostNodes = 64;
 constexpr int kSegSlots = 4;
 constexpr int kMostBox = 64;
-constexpr int kLeastBox = 16;
+constexpr int kLeastBox = 8;
 
 // Row tiles of an item, keys of a tile.  TMEM (512 columns): an O of D columns a row tile,
 // and S buffers in what is left: as many columns as keys, or with fp32 outputs 96 for 64 keys
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     prefetch_tmap(&tm_q);
     if (p.box > 0) {
       prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
+      if (p.box >= 16) prefetch_tmap(&tm_v);
     }
   }
   if (warp == kSWarp) {
@@ -475,7 +475,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const uint16_t* cache = keys ? a.k_cache : a.v_cache;
     constexpr int kSpans = D / 64, kSets = kBN / 32;
     const int box = lane / kSpans, span = lane % kSpans;
-    const bool mine = p.box > 0 && box * p.box < kBN;
+    // Boxes of 8 rows for keys alone (see the launch).
+    const bool tiled = p.box >= 16 || (p.box > 0 && keys);
+    const bool mine = tiled && box * p.box < kBN;
     int slot = keys ? 0 : 1, phase = 0, n_seg = 0, issued = 0;
     bool again = false;                                    // slots have been used before
     Seg sg;
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
               tma_load_3d(smem_u32(smem + r * L::kQTileBytes + i * L::kQChunkBytes), &tm_q, full,
                           i * 64, sg.kvh * g, sg.q0 + sg.node0 + r * p.tile_nodes);
         }
-        if (p.box > 0 && full_tile(sg, t)) {
+        if (tiled && full_tile(sg, t)) {
           int plane = entry;
           if (table != nullptr && mine && (plane < 0 || plane >= a.num_blocks)) {
             // A bad block becomes one past the cache, which reads as zeros.
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           int k0, k1;
           steps_of(sg, t, k0, k1);
           auto whole = [&](int k) {
-            return p.box > 0 && tile0 + 16 * k >= sg.first && tile0 + 16 * k + 16 <= sg.end;
+            return p.box >= 16 && tile0 + 16 * k >= sg.first && tile0 + 16 * k + 16 <= sg.end;
           };
           auto find = [&](int tok, int& in) {  // the plane of a token's row, -1 for a bad block
             in = tok;
@@ -793,7 +795,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           // The 16-byte copies' writes, before the MMAs that read them.
           const bool full = full_tile(sg, t);
           int k0 = 0, k1 = kBN / 16;
-          if (!full || p.box == 0) fence_proxy_async_smem();
+          if (!full || p.box < 16) fence_proxy_async_smem();
           if (!full) steps_of(sg, t, k0, k1);
           const uint32_t v_lo =
               sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), D > 64 ? L::kChunkBytes : 16);
@@ -1397,9 +1399,11 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   p.cap_l2 = a.softcap * kLog2e;
   p.err_word = ctx.err_word;
   p.timeout_ns = ctx.timeout_ns;
-  // Tiled copies where blocks are made of runs of 32 or 64 rows.  A tiled copy costs the SM's
+  // Tiled copies where blocks are made of runs of 8 to 64 rows.  A tiled copy costs the SM's
   // copy unit some 50 clocks and 2.5 for each row of 128 bytes: boxes of 16 rows come to the
-  // memory's rate only while the unit never idles, smaller ones not at all.
+  // memory's rate only while the unit never idles, those of 8 to half of it.  Copies by rows
+  // (16 bytes a lane) come to half of it too, by another way: with runs of 8 rows the keys go
+  // by the one, the values by the other.
   CUtensorMap mq, mk, mv, mk16, mv16;
   if (!make_q_map(&mq, a.q, D, a.n_q_heads, a.total_nodes, g, p.tile_nodes))
     return cudaErrorInvalidValue;
@@ -1414,9 +1418,10 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
     const int rows = a.block_table ? a.block_size : a.max_kv_len;
     const int planes = a.block_table ? a.num_blocks : a.batch;
     if (!make_cache_map(&mk, a.k_cache, D, a.n_kv_heads, rows, planes, p.box) ||
-        !make_cache_map(&mv, a.v_cache, D, a.n_kv_heads, rows, planes, p.box) ||
-        !make_cache_map(&mk16, a.k_cache, D, a.n_kv_heads, rows, planes, 16) ||
-        !make_cache_map(&mv16, a.v_cache, D, a.n_kv_heads, rows, planes, 16))
+        (p.box >= 16 &&
+         (!make_cache_map(&mv, a.v_cache, D, a.n_kv_heads, rows, planes, p.box) ||
+          !make_cache_map(&mk16, a.k_cache, D, a.n_kv_heads, rows, planes, 16) ||
+          !make_cache_map(&mv16, a.v_cache, D, a.n_kv_heads, rows, planes, 16))))
       p.box = 0;  // (sizes that a tensor map cannot hold)
   } else {
     p.box = 0;
