@@ -1,4 +1,4 @@
-// Attention of a tree of drafted tokens over a cache, sm_103a: cp.async + tcgen05 + TMEM.
+// Attention of a tree of drafted tokens over a cache, sm_103a: TMA + cp.async + tcgen05 + TMEM.
 //
 // A sequence's nodes (its last token and the drafted ones, at most 64) lie in the
 // cache behind the kv_len tokens cached before them.  Node i's query sees those
@@ -11,7 +11,9 @@
 // head_dim 128 is 64 KB, 1.5 us of an SM's share of the copy rate; a row tile of 128
 // rows takes the pipeline 0.85 us), the tensor cores and the exponentials beyond.
 // Even a few rows go through 128-row products: they hide behind the copies, and one
-// path serves every size.
+// path serves every size.  Measured (bf16 outputs, head_dim 128): 16 sequences of 1024 -
+// 32768 tokens in 16-token blocks, 1.12 GB, 229 us, 4.9 TB/s; one of 30720, 63 MB, 36 us (5
+// before the first product; the first kernel alone 32); 300 tokens 10 us.
 //
 // Design:
 //   * a row tile holds the g rows of 128 / g nodes (so a tiled copy of queries is one box),
@@ -24,20 +26,22 @@
 //     one, so there are two places a block.  Short caches (by max_kv_len) go whole
 //     items to a block, without the second kernel;
 //   * a producer warp for keys (and queries) and one for values fill a ring of tiles,
-//     128-byte-swizzled as the MMAs read them: tiles of keys that all exist, in blocks of 32
-//     or more rows, by tiled copies (TMA); the others, and smaller blocks of any size, by
+//     128-byte-swizzled as the MMAs read them: runs of rows that all exist, in blocks of
+//     whole runs, by tiled copies (TMA); the others, and blocks of any size, by
 //     16-byte copies (cp.async) of rows from wherever the block table says, with zeros for
 //     what is missing.  Both announce themselves on the slot's barrier; the issuing threads
-//     fence what the second kind wrote against the async proxy;
-//   * S = Q K^T and O += P V by two issuing threads, S in two TMEM buffers, P over
+//     fence what the second kind wrote against the async proxy.  The keys' producer plans
+//     the block's run for all the other warps;
+//   * S = Q K^T and O += P V by two issuing threads, S in two to four TMEM buffers, P over
 //     S, one O a row tile; with two row tiles in an item they take turns, so the
-//     tensor cores work on one while the other is in the softmax;
-//   * the softmax is one row a thread, four warps a row tile, 64 columns at a time, which
-//     stay in registers from the maximum to the exponentials (P overwrites columns that
-//     have been read).  A row's first maximum is the reference of its exponentials; it is
-//     raised, and O rescaled, only where scores outgrow it by 2^32, so that the tile after
-//     tile has neither a second look at S nor a wait for O.  P is announced in halves, so
-//     that its product begins under the second;
+//     tensor cores work on one while the other is in the softmax.  Tiles of 128 keys go in
+//     halves: the softmax has the first while the second is multiplied, and its P is on its
+//     way before the second's;
+//   * the softmax is one row a thread (half a row at head_dim 256), four warps a row tile, 64
+//     columns at a time, which stay in registers from the maximum to the exponentials (P
+//     overwrites columns that have been read).  A row's first maximum is the reference of its
+//     exponentials; it is raised, and O rescaled, only where scores outgrow it by 2^32, so
+//     that most tiles have neither a second look at S nor a wait for O;
 //   * P is rounded to bf16 for a bf16 O (2^-8 of a weight, no more than O's own
 //     rounding), and split into three bf16 parts (2^-24) for an fp32 one;
 //   * row statistics, O and the partials are fp32;
@@ -73,9 +77,10 @@ constexpr int kLeastBox = 8;
 // Row tiles of an item, keys of a tile.  TMEM (512 columns): an O of D columns a row tile,
 // and S buffers in what is left: as many columns as keys, or with fp32 outputs 96 for 64 keys
 // (three parts of P of 32).  Soft-capping and ALiBi take 64 keys too: with more scores in
-// registers they spill (ALiBi, 32 heads a kv head: 93 us, 116 with 128).  Tiles of 128 keys cost the issuing threads half the waits and
-// commits, some 100 clocks each, for a key: 16 sequences of 1024 - 32768 tokens, 32 heads, at
-// head_dim 128: 247 us against 305 with 64 and twice the buffers.
+// registers they spill (ALiBi, 8 sequences, 32 heads a kv head: 80 us, 116 with 128).  Tiles
+// of 128 keys cost the issuing threads half the waits and commits, some 100 clocks each, for
+// a key: 16 sequences of 1024 - 32768 tokens, 32 heads, at head_dim 128: 247 us against 305
+// with 64 and twice the buffers, when that was chosen.
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
 enum Variant : int { kPlain = 0, kCap = 1, kAlibi = 2 };  // (a window is in all of them)
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int key_tile() {
@@ -100,8 +105,9 @@ struct TreeSmem {
   static constexpr int kChunkBytes = kBN * 128;
   static constexpr int kMaxSlots = 12;
   // barriers: full / empty for each slot, q_empty, s_full[row tile][half][4], p_full[half][4],
-  // half_done[4], pv_done[4], o_full[2], drain[2], full / empty for each segment slot.  s_full is a row tile's own: one that sits out an item of fewer
-  // rows would otherwise miss phases, and take an old one for its next.
+  // half_done[4], pv_done[4], o_full[2], drain[2], full / empty for each segment slot, exchange.
+  // s_full is a row tile's own: one that sits out an item of fewer rows would otherwise miss
+  // phases, and take an old one for its next.
   static constexpr int kNumBars = 2 * kMaxSlots + 1 + 16 + 8 + 4 + 4 + 2 + 2 + 2 * kSegSlots + 1;
   static constexpr int kMiscBytes = 1024;  // barriers, then the segment slots
   // A table of depths a warp; at head_dim 256 what the halves of a row tell each other.
@@ -1403,7 +1409,8 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   // copy unit some 50 clocks and 2.5 for each row of 128 bytes: boxes of 16 rows come to the
   // memory's rate only while the unit never idles, those of 8 to half of it.  Copies by rows
   // (16 bytes a lane) come to half of it too, by another way: with runs of 8 rows the keys go
-  // by the one, the values by the other.
+  // by the one, the values by the other (16 sequences of 1024 - 32768 tokens in blocks of 24:
+  // 383 us, 414 by rows alone; of 16: 229).
   CUtensorMap mq, mk, mv, mk16, mv16;
   if (!make_q_map(&mq, a.q, D, a.n_q_heads, a.total_nodes, g, p.tile_nodes))
     return cudaErrorInvalidValue;

@@ -23,7 +23,10 @@
 // sibling behind it, and the last draw.  That thread decides for all blocks, so they meet
 // at the same barriers whatever the memory holds.
 // Bound by HBM for large batches (one row of p, and of q, a sequence), by the latency
-// of the gathers and the cluster's barriers for small ones.
+// of the gathers and the cluster's barriers for small ones.  Measured: 64 trees of 10 - 41
+// nodes over 128257 entries 68 us, of which some 9 are the rows' bytes: a sequence is a chain of
+// gathers, a pass for each refusal that has a sibling behind it, and two for the last draw;
+// a chain of 6 over 32000 entries 9 us.
 #include <algorithm>
 #include <cstdint>
 #include <cooperative_groups.h>
