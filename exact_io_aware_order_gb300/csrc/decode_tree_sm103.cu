@@ -76,21 +76,21 @@ constexpr int kLeastBox = 8;
 
 // Row tiles of an item, keys of a tile.  TMEM (512 columns): an O of D columns a row tile,
 // and S buffers in what is left: as many columns as keys, or with fp32 outputs 96 for 64 keys
-// (three parts of P of 32).  Soft-capping and ALiBi take 64 keys too: with more scores in
-// registers they spill (ALiBi, 8 sequences, 32 heads a kv head: 80 us, 116 with 128).  Tiles
-// of 128 keys cost the issuing threads half the waits and commits, some 100 clocks each, for
-// a key: 16 sequences of 1024 - 32768 tokens, 32 heads, at head_dim 128: 247 us against 305
-// with 64 and twice the buffers, when that was chosen.
+// (three parts of P of 32).  Tiles of 128 keys cost the issuing threads half the waits and
+// commits, some 100 clocks each, for a key: 16 sequences of 1024 - 32768 tokens, 32 / 8 heads, at
+// head_dim 128: soft-capped 329 us against 403 with 64 and twice the buffers, with ALiBi 266
+// against 293; at head_dim 64 184 against 207, but with ALiBi and 32 heads a kv head, whose
+// softmax is longer, 101 against 80: three buffers hold it up.
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
 enum Variant : int { kPlain = 0, kCap = 1, kAlibi = 2 };  // (a window is in all of them)
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int key_tile() {
-  return D == 256 || WIDE || VAR != kPlain ? 64 : 128;
+  return D == 256 || WIDE || (D == 64 && VAR != kPlain) ? 64 : 128;
 }
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_pitch() {
   return WIDE ? 96 : key_tile<D, VAR, WIDE>();
 }
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_bufs() {
-  return !WIDE && (D == 256 || VAR != kPlain) ? 4 : D == 64 ? 3 : 2;
+  return !WIDE && (D == 256 || (D == 64 && VAR != kPlain)) ? 4 : D == 64 ? 3 : 2;
 }
 template <int D> __host__ __device__ constexpr int threads_of() {
   return 2 * kSoftmaxThreads + kProducerThreads + 64;
@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           tc_fence_after();
           return true;
         };
-        const bool ahead = edge || (VAR == kCap && kBN > 64);
+        const bool ahead = edge;
         if (ahead) {
           // Soft-capping, masks, and ALiBi where nodes are among the keys: a pass of its own,
           // written back.
