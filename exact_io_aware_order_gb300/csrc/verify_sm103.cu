@@ -24,11 +24,12 @@
 // at the same barriers whatever the memory holds.
 // Bound by HBM for large batches (one row of p, and of q, a sequence), by the latency
 // of the gathers and the cluster's barriers for small ones.  Measured: 64 trees of 10 - 41
-// nodes over 128257 entries 68 us, of which some 9 are the rows' bytes: a sequence is a chain of
+// nodes over 128257 entries 58 us, of which some 9 are the rows' bytes: a sequence is a chain of
 // gathers, a pass for each refusal that has a sibling behind it, and two for the last draw;
 // a chain of 6 over 32000 entries 9 us.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -42,8 +43,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kMostNodes = 64;
 constexpr int kMostBlocks = 8;
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMostWarps = 16;
 constexpr int kUnroll = 8;
 constexpr unsigned long long kOne = 1ull << 60;
 constexpr unsigned long long kMostC = 1ull << 63;
@@ -53,8 +53,7 @@ __device__ __forceinline__ unsigned long long fixed60(float x) {
   const uint32_t b = __float_as_uint(x), e = b >> 23;  // (a set sign makes it 256 or more)
   // The 24 bits of an exponent of 127, moved down.
   const unsigned long long top = (unsigned long long)(((b & 0x7fffffu) | 0x800000u) << 5) << 32;
-  const unsigned long long v = top >> min(127u - e, 63u);
-  return e < 128u ? v : 0ull;
+  return top >> min(127u - e, 63u);  // (top is below 2^61: an e of 128 or more wraps, and leaves 0)
 }
 // a b / 2^60, rounded down.
 __device__ __forceinline__ unsigned long long times60(unsigned long long a, unsigned long long b) {
@@ -78,36 +77,47 @@ struct Shared {
   unsigned long long C[kMostNodes];
   int gone[kMostNodes];                  // without q: the refused tokens
   unsigned long long totals[kMostBlocks];  // the blocks' sums (in the first block)
-  unsigned long long warp_sums[kWarps];
+  unsigned long long warp_sums[kMostWarps];
   // gathered
   int parent[kMostNodes], token[kMostNodes];
   unsigned long long p[kMostNodes], q[kMostNodes], u[kMostNodes];
 };
 
-template <bool DRAFTS>
+// What a pass over the vocabulary computes for an entry, chosen once a pass so that its loops
+// have no branches inside (with them 64 trees over 128257 entries take 67 us instead of 58).
+enum Form : int {
+  kPlain = 0,  // p
+  kLess = 1,   // max(p - q, 0): after the first refusal
+  kTerm = 2,   // max(p - q C, 0)
+  kAny = 3     // several terms of C, or tokens that are gone
+};
+
+template <bool DRAFTS, int FORM>
 __device__ __forceinline__ unsigned long long weight(float pv, float qv, int v, int levels,
                                                      unsigned long long c0,
                                                      const unsigned long long* C, const int* gone) {
   unsigned long long w = fixed60(pv);
-  if constexpr (DRAFTS) {
-    if (levels > 0) {
-      const unsigned long long q = fixed60(qv);
-      const unsigned long long y = c0 == kOne ? q : times60(q, c0);
-      w = w > y ? w - y : 0ull;
+  if constexpr (DRAFTS && FORM != kPlain) {
+    const unsigned long long q = fixed60(qv);
+    const unsigned long long y = FORM == kLess ? q : times60(q, c0);
+    w = w > y ? w - y : 0ull;
+    if constexpr (FORM == kAny) {
       for (int i = 1; i < levels; ++i) {
         const unsigned long long z = times60(q, C[i]);
         w = w > z ? w - z : 0ull;
       }
     }
-  } else {
+  } else if constexpr (FORM == kAny) {
     for (int i = 0; i < levels; ++i)
       if (gone[i] == v) w = 0ull;
   }
   return w;
 }
 
-template <bool DRAFTS>
+template <bool DRAFTS, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const VerifyArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps <= kMostWarps, "warp_sums");
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -241,17 +251,29 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
     const unsigned long long c0 = use_q ? sh.C[0] : 0ull;
     if (o.kind == kSum) {
       unsigned long long sum = 0ull;
-      for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
-        float x[kUnroll], y[kUnroll];
+      auto add = [&](auto form) {
+        constexpr int FORM = decltype(form)::value;
+        for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
+          float x[kUnroll], y[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          const int i = v + 32 * k;
-          x[k] = i < v1 ? p[i] : 0.f;
-          y[k] = use_q && i < v1 ? q[i] : 0.f;
+          for (int k = 0; k < kUnroll; ++k) {
+            const int i = v + 32 * k;
+            x[k] = i < v1 ? p[i] : 0.f;
+            y[k] = DRAFTS && FORM != kPlain && i < v1 ? q[i] : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < kUnroll; ++k)
+            sum += weight<DRAFTS, FORM>(x[k], y[k], v + 32 * k, o.levels, c0, sh.C, sh.gone);
         }
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-          sum += weight<DRAFTS>(x[k], y[k], v + 32 * k, o.levels, c0, sh.C, sh.gone);
+      };
+      if (o.levels == 0) {
+        add(std::integral_constant<int, kPlain>{});
+      } else if constexpr (!DRAFTS) {
+        add(std::integral_constant<int, kAny>{});
+      } else {
+        if (o.levels > 1) add(std::integral_constant<int, kAny>{});
+        else if (c0 == kOne) add(std::integral_constant<int, kLess>{});
+        else add(std::integral_constant<int, kTerm>{});
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
@@ -283,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
           for (int k = 0; k < kUnroll; ++k) {
             if (found) break;
             const int i = v + lane + 32 * k;
-            unsigned long long s = weight<DRAFTS>(x[k], y[k], i, o.levels, c0, sh.C, sh.gone);
+            unsigned long long s =
+                weight<DRAFTS, kAny>(x[k], y[k], i, o.levels, c0, sh.C, sh.gone);
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
               const unsigned long long up = __shfl_up_sync(0xffffffffu, s, d);
@@ -310,14 +333,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
-  // A cluster of 8 blocks from 8192 entries on.  Sequences differ in how many passes they
-  // need (one to four and more), so a batch is as fast as its slowest, and that as the SMs it
-  // gets to itself: 64 trees over 128257 entries with blocks of 512 threads and clusters of 8
-  // / 4: 68 / 84 us; with 256 threads 74 / 116, with 1024 97 / 82, and 116 in clusters of 2.
+  // A cluster of 8 blocks from 8192 entries on.  Sequences differ in how many passes they need
+  // (one to four and more), so a batch that the GPU holds at once (two blocks of 512 threads
+  // an SM, in clusters) is as fast as its slowest, and that as the SMs it gets to itself; of
+  // larger ones more run side by side with blocks of 256.  128257 entries, blocks of 512 / 256
+  // threads: 8 trees 26 / 29 us, 64 trees 59 / 59, 200 trees 147 / 118 (clusters of 4 with 512:
+  // 36, 68, 132).
   const int blocks = a.vocab >= 8192 ? kMostBlocks : 1;
+  const int threads = (long long)a.batch * blocks > 4LL * ctx.num_sms ? 256 : 512;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.batch * (unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = ctx.stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -328,8 +354,9 @@ cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtx& ctx) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return a.draft_probs ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a)
-                       : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a);
+  auto* kernel = threads == 512 ? (a.draft_probs ? verify_kernel<true, 512> : verify_kernel<false, 512>)
+                                : (a.draft_probs ? verify_kernel<true, 256> : verify_kernel<false, 256>);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace attn

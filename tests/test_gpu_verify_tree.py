@@ -125,6 +125,15 @@ def test_walks(dev, chain, drafts):
     attn.check_device_status()
 
 
+@pytest.mark.parametrize("drafts", [False, True])
+@pytest.mark.parametrize("batch,V", [(80, 8200), (640, 9)])
+def test_large_batches(dev, batch, V, drafts):
+    """More sequences than are on the GPU at once."""
+    c = Case([1 + i % 4 for i in range(batch)], V, drafts, seed=batch, near=0.3)
+    c.check(dev)
+    attn.check_device_status()
+
+
 def test_many_refusals(dev):
     """A root with 63 children that are all refused, p and q nearly apart: Z stays near 1, and C
     passes 8 again and again."""
