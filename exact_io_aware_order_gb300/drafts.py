@@ -245,8 +245,8 @@ def cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor
 def tree_mask(parents: torch.Tensor, cu_nodes: torch.Tensor) -> torch.Tensor:
     """The mask words of :func:`decode_tree` for trees: each node's ancestors and
     itself.  parents: (total,) int32, a node's parent by its index within its sequence
-    (smaller than the node's), the root's -1; cu_nodes: (B + 1,) int32.  Returns
-    (total,) int64 on parents' device; of rows outside every sequence, 0."""
+    (smaller than the node's, any other counts as none), the root's -1; cu_nodes: (B + 1,)
+    int32.  Returns (total,) int64 on parents' device; of rows outside every sequence, 0."""
     t = torch.arange(parents.shape[0], dtype=_I64, device=parents.device)
     cu = cu_nodes.to(_I64)
     seq = torch.searchsorted(cu[1:].contiguous(), t, right=True)
@@ -256,7 +256,7 @@ def tree_mask(parents: torch.Tensor, cu_nodes: torch.Tensor) -> torch.Tensor:
     one = torch.ones_like(t)
     word = torch.where(real, one << i, 0)
     # The ancestor 1, 2, 4, ... generations up, itself for none.
-    up = torch.where(real & (parents >= 0), first + parents, -1)
+    up = torch.where(real & (parents >= 0) & (parents < t - first), first + parents, -1)
     for _ in range(6):
         at = up.clamp(min=0)
         word = torch.where(up >= 0, word | word[at], word)

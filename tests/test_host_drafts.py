@@ -182,3 +182,15 @@ def test_binding_takes_only_what_it_knows(L):
         call = getattr(b, name)
         for wrong in ((), args, (None,) * len(args), (1,) * len(args), args[:-1]):
             assert call(*wrong) is NotImplemented
+
+
+def test_tree_masks_of_parents_that_are_none():
+    """A parent that is not a smaller index of the sequence is none, and reads nothing outside."""
+    import torch
+
+    import exact_io_aware_order_gb300 as attn
+
+    big = 2**31 - 1
+    parents = torch.tensor([-1, 1, 0, big, 3, -9, -1, 5, 0, 0], dtype=torch.int32)
+    w = attn.tree_mask(parents, torch.tensor([0, 6, 9], dtype=torch.int32))
+    assert w.tolist() == [1, 2, 5, 8, 24, 32, 1, 2, 5, 0]
