@@ -12,7 +12,7 @@
 // rows takes the pipeline 0.85 us), the tensor cores and the exponentials beyond.
 // Even a few rows go through 128-row products: they hide behind the copies, and one
 // path serves every size.  Measured (bf16 outputs, head_dim 128): 16 sequences of 1024 -
-// 32768 tokens in 16-token blocks, 1.12 GB, 229 us, 4.9 TB/s; one of 30720, 63 MB, 36 us (5
+// 32768 tokens in 16-token blocks, 1.12 GB, 205 us, 5.5 TB/s; one of 30720, 63 MB, 35 us (5
 // before the first product; the first kernel alone 32); 300 tokens 10 us.
 //
 // Design:
@@ -34,9 +34,8 @@
 //     the block's run for all the other warps;
 //   * S = Q K^T and O += P V by two issuing threads, S in two to four TMEM buffers, P over
 //     S, one O a row tile; with two row tiles in an item they take turns, so the
-//     tensor cores work on one while the other is in the softmax.  Tiles of 128 keys go in
-//     halves: the softmax has the first while the second is multiplied, and its P is on its
-//     way before the second's;
+//     tensor cores work on one while the other is in the softmax.  P comes in halves of a tile
+//     of 128 keys: the first is multiplied while the second is in the softmax;
 //   * the softmax is one row a thread (half a row at head_dim 256), four warps a row tile, 64
 //     columns at a time, which stay in registers from the maximum to the exponentials (P
 //     overwrites columns that have been read).  A row's first maximum is the reference of its
@@ -366,6 +365,12 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ TreeKParams p) {
   using L = TreeSmem<D, VAR, WIDE>;
   constexpr int kBN = L::kBN, kPitch = s_pitch<D, VAR, WIDE>(), SB = s_bufs<D, VAR, WIDE>(), NQ = row_tiles<D>();
+  // Keys of an S product.  An issuing thread pays some 59 clocks an MMA and 100 a wait or commit,
+  // whatever the MMA's size, so a whole tile at once is cheaper for it (16 sequences of 1024 -
+  // 32768 tokens, 32 / 8 heads: 205 us against 228 with halves, with ALiBi 238 against 265); with
+  // soft-capping the softmax takes long, and starts sooner with halves (311 against 329 when
+  // both wait for all of the last P).
+  constexpr int kSKeys = VAR == kCap ? 64 : kBN;
   constexpr bool kSplit = NQ == 1;  // both warpgroups work on the one row tile
   constexpr int kProducerWarp = 8, kSWarp = kProducerWarp + 2, kPVWarp = kSWarp + 1;
   static_assert(SB * kPitch + NQ * D <= (int)kTmemCols, "TMEM budget");
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     if (lane == 0) mbar_arrive(bar(kSegEmpty + i));
     return sg.tiles > 0;
   };
-  const uint32_t id_s = idesc_bf16_f32(128, 64, false, false);
+  const uint32_t id_s = idesc_bf16_f32(128, kSKeys, false, false);
   const uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
   const uint32_t dhi = sw128_desc_hi(1024);
 
@@ -755,14 +760,15 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           const uint32_t k_lo = sw128_desc_lo(smem_u32(ring + slot * L::kTileBytes), 16);
           for (int r = 0; r < sg.nr; ++r, ++n) {
             const int b = n % SB;
-            // Buffer b last held P(n - SB).
-            if (n >= SB && !mbar_wait(bar(kPVDone + b), (n / SB - 1) & 1, ctl)) { ok = false; break; }
-            tc_fence_after();
             const uint32_t dS = tmem + b * kPitch;
             const uint32_t q_lo = q_lo0 + (uint32_t)((r * L::kQTileBytes) >> 4);
 #pragma unroll 1
-            for (int h = 0; h < kBN / 64; ++h) {            // 64 keys at a time
-              const int keys = full ? 64 : min(16 * k1 - 64 * h, 64);
+            for (int h = 0; h < kBN / kSKeys; ++h) {
+              // Buffer b last held P(n - SB), whose halves are done one after the other.
+              const uint32_t held = bar((kSKeys < kBN && h == 0 ? kHalfDone : kPVDone) + b);
+              if (n >= SB && !mbar_wait(held, (n / SB - 1) & 1, ctl)) { ok = false; break; }
+              tc_fence_after();
+              const int keys = full ? kSKeys : min(16 * k1 - kSKeys * h, kSKeys);
               const uint32_t id = full ? id_s : idesc_bf16_f32(128, max(keys, 16), false, false);
               if (keys > 0) {
 #pragma unroll
@@ -774,6 +780,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
               }
               mma_commit(bar(kSFull + 8 * r + 4 * h + b));
             }
+            if (!ok) break;
           }
           mma_commit(bar(kEmpty + slot));
           // K tiles are every other one of the ring.
@@ -930,6 +937,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         }
         const uint32_t tS = tmem + b * kPitch + lane_base;
         auto wait_s = [&](int h) {
+          if (h >= kBN / kSKeys) return true;               // (it came with the first half)
           const int i = 4 * h + b;
           if (!mbar_wait_warp(bar(kSFull + 8 * r + i), (s_phase >> i) & 1u, ctl)) return false;
           s_phase ^= 1u << i;
