@@ -78,18 +78,19 @@ constexpr int kLeastBox = 8;
 // (three parts of P of 32).  Tiles of 128 keys cost the issuing threads half the waits and
 // commits, some 100 clocks each, for a key: 16 sequences of 1024 - 32768 tokens, 32 / 8 heads, at
 // head_dim 128: soft-capped 329 us against 403 with 64 and twice the buffers, with ALiBi 266
-// against 293; at head_dim 64 184 against 207, but with ALiBi and 32 heads a kv head, whose
-// softmax is longer, 101 against 80: three buffers hold it up.
+// against 293; at head_dim 64 184 against 207, soft-capped 284 against 302.  With ALiBi at
+// head_dim 64 it is 224 against 240 there, but 100 against 80 for 8 sequences of 100 - 16000
+// tokens and 32 heads a kv head, whose many ends cost a whole tile's pass each.
 template <int D> __host__ __device__ constexpr int row_tiles() { return D == 256 ? 1 : 2; }
 enum Variant : int { kPlain = 0, kCap = 1, kAlibi = 2 };  // (a window is in all of them)
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int key_tile() {
-  return D == 256 || WIDE || (D == 64 && VAR != kPlain) ? 64 : 128;
+  return D == 256 || WIDE || (D == 64 && VAR == kAlibi) ? 64 : 128;
 }
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_pitch() {
   return WIDE ? 96 : key_tile<D, VAR, WIDE>();
 }
 template <int D, int VAR, bool WIDE> __host__ __device__ constexpr int s_bufs() {
-  return !WIDE && (D == 256 || (D == 64 && VAR != kPlain)) ? 4 : D == 64 ? 3 : 2;
+  return !WIDE && (D == 256 || (D == 64 && VAR == kAlibi)) ? 4 : D == 64 ? 3 : 2;
 }
 template <int D> __host__ __device__ constexpr int threads_of() {
   return 2 * kSoftmaxThreads + kProducerThreads + 64;
@@ -1418,7 +1419,7 @@ cudaError_t launch_t(const DecodeTreeArgs& a, const LaunchCtx& ctx) {
   // memory's rate only while the unit never idles, those of 8 to half of it.  Copies by rows
   // (16 bytes a lane) come to half of it too, by another way: with runs of 8 rows the keys go
   // by the one, the values by the other (16 sequences of 1024 - 32768 tokens in blocks of 24:
-  // 383 us, 414 by rows alone; of 16: 229).
+  // 383 us, 414 by rows alone).
   CUtensorMap mq, mk, mv, mk16, mv16;
   if (!make_q_map(&mq, a.q, D, a.n_q_heads, a.total_nodes, g, p.tile_nodes))
     return cudaErrorInvalidValue;
