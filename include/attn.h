@@ -16,6 +16,8 @@
  *   - the merge of partial results by their LSE weights (section "The online
  *     softmax ...", combining partial results, and the merge rule in section
  *     "Minimal implementation").
+ * Beside it: the cache held in 8 bits, rotary positions, and a decode step with
+ * drafted tokens (append, attention of a tree, verification).
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is a DEVICE pointer, allocated and owned by the
@@ -24,7 +26,8 @@
  *     on the caller's stream (`stream` is a cudaStream_t; NULL = the legacy
  *     default stream).
  *   - bf16 tensors are passed as `const attn_bf16*` (the raw 16-bit pattern).
- *   - All arrays are dense and row-major in the order their shape is written.
+ *   - All arrays are dense and row-major in the order their shape is written,
+ *     but for those that are passed with strides.
  *   - LSE values are natural logarithms of sums of exp(scaled score); an
  *     empty key set yields LSE = -inf and O = 0.
  *   - Arguments are validated before anything is launched; on any error the
