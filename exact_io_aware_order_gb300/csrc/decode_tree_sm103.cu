@@ -341,7 +341,7 @@ __device__ __forceinline__ bool small_for_cap(const uint32_t (&x)[32], float in)
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       top[q] = fmax3(top[q], fabsf(__uint_as_float(x[k + 2 * q])), fabsf(__uint_as_float(x[k + 2 * q + 1])));
-  return fmaxf(top[0], top[1]) * in <= 0.45f;
+  return !(fmaxf(top[0], top[1]) * in > 0.45f);
 }
 // The same where a warp's scores lie in TMEM, for any |u| (NaN too): a short loop, because 32
 // copies of tanhf in a tile's way cost every tile the fetch around them.
@@ -356,6 +356,23 @@ __device__ __forceinline__ void soft_cap_large(uint32_t at, int cols, float in, 
     tmem_st8(at + c, y);
   }
   tmem_wait_st();
+}
+
+// Whether 32 scores in TMEM are that small, without those whose bits in w are clear: what masked
+// columns hold must not decide how the others are computed.  A short loop too: with the masks
+// written out over the 32 registers, 16 sequences of 1024 - 32768 tokens take 345 us, not 314.
+__device__ __forceinline__ bool small_where(uint32_t at, uint32_t w, float in) {
+  float top = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 8, w >>= 8) {
+    uint32_t y[8];
+    tmem_ld8(at + c, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if ((w >> k) & 1u) top = fmaxf(top, fabsf(__uint_as_float(y[k])));
+  }
+  return !(top * in > 0.45f);
 }
 
 // VAR: what happens to a score besides scale and window.  WIDE: fp32 O, P in three parts.
@@ -914,6 +931,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       }
       if (VAR == kAlibi && real) slope_l2 = a.alibi_slopes[head] * kLog2e;
       const int pos = sg.kv_len + depth;
+      // Rows of no node hold what the queries' tile held before, or other sequences' queries:
+      // nothing in them may decide how the other rows of their warp are computed.
+      const float vote = real ? p.cap_in : 0.f;
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < sg.tiles; ++t) {
         const int n = n0 + t * sg.nr + r, b = n % SB;
@@ -945,20 +965,23 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           tc_fence_after();
           return true;
         };
-        const bool ahead = edge;
-        if (ahead) {
+        if (edge) {
           // Soft-capping, masks, and ALiBi where nodes are among the keys: a pass of its own,
           // written back.
           for (int h = 0; h < kBN / 64 && ok; ++h) ok = wait_s(h);
           if (!ok) break;
 #pragma unroll 1
           for (int c = kSplit ? part : 0; c < (kSplit ? part + 1 : kBN / 32); ++c) {
+            uint32_t w = vis[0];
+#pragma unroll
+            for (int q = 1; q < kBN / 32; ++q)
+              if (c == q) w = vis[q];
             uint32_t y[32];
             tmem_ld32(tS + c * 32, y);
             tmem_wait_ld();
             landed(y);
             if constexpr (VAR == kCap) {
-              if (__all_sync(0xffffffffu, small_for_cap(y, p.cap_in))) {
+              if (__all_sync(0xffffffffu, small_where(tS + c * 32, w, vote))) {
                 soft_cap(y, p.cap_in, p.cap_l2);
               } else {
                 soft_cap_large(tS + c * 32, 32, p.cap_in, p.cap_l2);
@@ -967,26 +990,20 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
                 landed(y);
               }
             }
-            if (edge) {
-              if constexpr (VAR == kAlibi) {
-                const float d0 = (float)(pos - kv0 - 32 * c);
-                const int u0 = kv0 + 32 * c - sg.kv_len;    // node of the first column
+            if constexpr (VAR == kAlibi) {
+              const float d0 = (float)(pos - kv0 - 32 * c);
+              const int u0 = kv0 + 32 * c - sg.kv_len;      // node of the first column
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const float dist = u0 + k < 0
-                                         ? d0 - (float)k
-                                         : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
-                  y[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), p.sl2, -slope_l2 * dist));
-                }
+              for (int k = 0; k < 32; ++k) {
+                const float dist = u0 + k < 0
+                                       ? d0 - (float)k
+                                       : (float)(depth - depths[min(u0 + k, kMostNodes - 1)]);
+                y[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), p.sl2, -slope_l2 * dist));
               }
-              uint32_t w = vis[0];
-#pragma unroll
-              for (int q = 1; q < kBN / 32; ++q)
-                if (c == q) w = vis[q];
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((w >> k) & 1u)) y[k] = 0xff800000u;   // -inf
             }
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((w >> k) & 1u)) y[k] = 0xff800000u;     // -inf
             tmem_st32(tS + c * 32, y);
           }
           tmem_wait_st();
@@ -995,7 +1012,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
         // is fetched anew for every tile, beside five other roles').
 #pragma unroll 1
         for (int h = 0; h < kBN / 64; ++h) {
-          if (!ahead && !wait_s(h)) { ok = false; break; }
+          if (!edge && !wait_s(h)) { ok = false; break; }
           const uint32_t tH = tS + 64 * h + 32 * part;
           // What turns the score of column k into log2 units: x sl2 + (base + slope k).
           float sl2 = VAR == kCap ? 1.f : p.sl2, slope = 0.f, base = 0.f;
@@ -1014,9 +1031,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             for (int c = 0; c < kSets; ++c) landed(x[c]);
           };
           load();
-          if (VAR == kCap && !ahead) {
-            const bool small =
-                small_for_cap(x[0], p.cap_in) && small_for_cap(x[kSets - 1], p.cap_in);
+          if (VAR == kCap && !edge) {
+            const bool small = small_for_cap(x[0], vote) && small_for_cap(x[kSets - 1], vote);
             if (__all_sync(0xffffffffu, small)) {
 #pragma unroll
               for (int c = 0; c < kSets; ++c) soft_cap(x[c], p.cap_in, p.cap_l2);
@@ -1058,6 +1074,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             mx = fmax3(mx, fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
           }
           if constexpr (VAR != kAlibi) mx *= sl2;
+          if (!real) mx = -INFINITY;                        // (no vote on the reference)
           if constexpr (kSplit) {
             // (both have read their scores then, which P overwrites)
             float both[2];

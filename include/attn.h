@@ -884,7 +884,8 @@ size_t attn_decode_tree_workspace_bytes(int batch, int total_nodes, int n_q_head
  * into it (more than 64 nodes: to the first 64) and flagged; a sequence with a negative
  * kv_lens, or whose nodes do not fit the capacity, is flagged and its rows are O = 0 and
  * LSE = -inf; a block-table entry outside [0, num_blocks) is flagged and its tokens are
- * taken as zeros.  Results do not depend on timing: cut items are joined in order.
+ * taken as zeros.  Results do not depend on timing (cut items are joined in order), nor a
+ * sequence's on the other sequences' queries, keys and values.
  * Limits: those of attn_decode_splitkv; total_nodes <= 2^24; max_kv_len <= 2^30; the cache's
  *   slots (num_blocks * block_size, batch * max_kv_len) and total_nodes * n_q_heads < 2^31.
  * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _GQA, _ALIGN, _SCRATCH, _ARCH, _LAUNCH.
