@@ -14,7 +14,9 @@
 // same in any order, so the drawn index is the same however the vocabulary is divided,
 // and two probabilities that differ are never taken for equal by rounding (an fp32
 // running sum over 128k entries moves a border by 1e-6, the size of many entries).
-// 64-bit integer additions are two instructions; fp64 ones would run at 1/64 rate.
+// 64-bit integer additions are two instructions; fp64 ones would run at 1/64 rate.  Sums end
+// at 8 - 2^-60 (what probabilities never reach): such a sum is the same in any order too, and
+// its products with numbers below 2 fit 64 bits.
 //
 // Work split: a cluster of blocks a sequence, the vocabulary in equal runs, a run a
 // warp.  The walk itself is scalar: one thread of the first block does it on numbers that
@@ -47,6 +49,7 @@ constexpr int kMostWarps = 16;
 constexpr int kUnroll = 8;
 constexpr unsigned long long kOne = 1ull << 60;
 constexpr unsigned long long kMostC = 1ull << 63;
+constexpr unsigned long long kMostSum = kMostC - 1;
 
 // Multiples of 2^-60 in x, rounded down; 0 for what is not in [0, 2).
 __device__ __forceinline__ unsigned long long fixed60(float x) {
@@ -58,6 +61,17 @@ __device__ __forceinline__ unsigned long long fixed60(float x) {
 // a b / 2^60, rounded down.
 __device__ __forceinline__ unsigned long long times60(unsigned long long a, unsigned long long b) {
   return (__umul64hi(a, b) << 4) | ((a * b) >> 60);
+}
+
+// The sum of a warp's numbers, each at most kMostSum and so the sum, in pieces of 21 bits (whose
+// sums take 26).
+__device__ __forceinline__ unsigned long long warp_sum60(unsigned long long x) {
+  constexpr uint32_t kPiece = (1u << 21) - 1u;
+  const uint32_t s0 = __reduce_add_sync(0xffffffffu, (uint32_t)x & kPiece);
+  const uint32_t s1 = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 21) & kPiece) + (s0 >> 21);
+  const uint32_t s2 = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 42)) + (s1 >> 21);
+  if (s2 > kPiece) return kMostSum;
+  return (unsigned long long)s2 << 42 | (unsigned long long)(s1 & kPiece) << 21 | (s0 & kPiece);
 }
 
 enum Command : int { kEnd = 0, kSum = 1, kFind = 2 };
@@ -167,9 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
   unsigned long long Z = kOne;
   bool have_z = true, drawing = false;
   auto sum_of_totals = [&] {
-    unsigned long long t = 0ull;
-    for (int r = 0; r < blocks; ++r) t += sh.totals[r];
-    return t;
+    unsigned long long hi = 0ull, lo = 0ull;
+    for (int r = 0; r < blocks; ++r) {
+      const unsigned long long t = sh.totals[r];
+      hi += t >> 32;
+      lo += (uint32_t)t;
+    }
+    hi += lo >> 32;
+    return hi >> 31 ? kMostSum : hi << 32 | (uint32_t)lo;
   };
   auto decide = [&]() -> Order {
     if (n == 0) {
@@ -189,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         a.next_token[b] = a.vocab - 1;
         return Order{kEnd, 0, 0, 0, 0ull};
       }
-      unsigned long long c = 0ull;
+      unsigned long long c = 0ull;  // (T is below the largest sum: none that stays at or below it ended)
       int r = 0;
       while (r + 1 < blocks && c + sh.totals[r] <= T) c += sh.totals[r++];
       return Order{kFind, at, levels, r, T - c};
@@ -251,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
     const unsigned long long c0 = use_q ? sh.C[0] : 0ull;
     if (o.kind == kSum) {
       unsigned long long sum = 0ull;
+      bool carries = false;
       auto add = [&](auto form) {
         constexpr int FORM = decltype(form)::value;
         for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
@@ -261,9 +281,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
             x[k] = i < v1 ? p[i] : 0.f;
             y[k] = DRAFTS && FORM != kPlain && i < v1 ? q[i] : 0.f;
           }
+          unsigned long long some = 0ull;
+          static_assert(kUnroll <= 8, "weights are below 2^61");
 #pragma unroll
           for (int k = 0; k < kUnroll; ++k)
-            sum += weight<DRAFTS, FORM>(x[k], y[k], v + 32 * k, o.levels, c0, sh.C, sh.gone);
+            some += weight<DRAFTS, FORM>(x[k], y[k], v + 32 * k, o.levels, c0, sh.C, sh.gone);
+          sum += some;
+          carries |= sum < some;
         }
       };
       if (o.levels == 0) {
@@ -275,14 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         else if (c0 == kOne) add(std::integral_constant<int, kLess>{});
         else add(std::integral_constant<int, kTerm>{});
       }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      sum = warp_sum60(carries ? kMostSum : min(sum, kMostSum));
       if (lane == 0) sh.warp_sums[warp] = sum;
       __syncthreads();
-      if (threadIdx.x == 0) {
-        unsigned long long t = 0ull;
-        for (int w = 0; w < kWarps; ++w) t += sh.warp_sums[w];
-        first->totals[rank] = t;
+      if (warp == 0) {
+        sum = warp_sum60(lane < kWarps ? sh.warp_sums[lane] : 0ull);
+        if (lane == 0) first->totals[rank] = sum;
       }
       cluster.sync();
     } else if (rank == o.rank) {  // kFind: the warp, then the entry
@@ -312,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
               const unsigned long long up = __shfl_up_sync(0xffffffffu, s, d);
               if (lane >= d) s += up;
             }
+            // (up to the entry looked for sums are below T + 2: nothing wraps)
             const uint32_t over = __ballot_sync(0xffffffffu, base + s > T);
             if (over != 0u) {
               found = true;

@@ -909,7 +909,7 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
  *
  *   target_probs: (total_nodes, vocab) fp32, node t's row at t * target_stride (>= vocab):
  *                the target's probabilities of the token after node t.  What is not in
- *                [0, 2) counts as 0.
+ *                [0, 2) counts as 0; sums of a row end at 8 - 2^-60.
  *   draft_probs: the same for the draft: row t is what the children of node t were drawn
  *                from; or NULL: the drafted tokens are certain (the draft's most likely
  *                ones, for example)
@@ -931,8 +931,8 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
  * With no child left, next_token is the smallest v with w(0) + .. + w(v) >
  * floor(u_sample * sum w); where sum w is 0, w = p; where no v is, vocab - 1.
  * All numbers are multiples of 2^-60: inputs and products are rounded down to them (q C term
- * by term where C is 8 or more: its terms are sums of successive Zs below 8), sums are exact,
- * so the outputs do not depend on any order.
+ * by term where C is 8 or more: its terms are sums of successive Zs below 8), sums of entries
+ * are exact (those that would reach 8 are 8 - 2^-60), so the outputs do not depend on any order.
  * A sequence without nodes gets 0, -1s and -1.  A cu_nodes that breaks its rule is clamped
  * into it and flagged; a parent that is not a smaller index, and a drafted token outside [0,
  * vocab), are flagged, and that node is never accepted.
