@@ -11,6 +11,7 @@ constexpr uint32_t kErrTimeout = 1u;     // a bounded wait gave up
 constexpr uint32_t kErrBlockIndex = 2u;  // a block-table entry outside [0, num_blocks)
 constexpr uint32_t kErrKvLen = 4u;       // a kv_len outside [0, capacity]
 constexpr uint32_t kErrSeqLens = 8u;     // cu_seqlens not increasing within [0, total]
+constexpr uint32_t kErrProbs = 16u;      // a row of probabilities that are not numbers
 
 struct LaunchCtx {
   cudaStream_t stream;

@@ -74,7 +74,7 @@ __device__ __forceinline__ unsigned long long warp_sum60(unsigned long long x) {
   return (unsigned long long)s2 << 42 | (unsigned long long)(s1 & kPiece) << 21 | (s0 & kPiece);
 }
 
-enum Command : int { kEnd = 0, kSum = 1, kFind = 2 };
+enum Command : int { kEnd = 0, kSum = 1, kFind = 2, kLook = 3 };
 
 // What the first block tells the others.
 struct Order {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
       const unsigned long long T = times60(total, fixed60(a.u_sample[b]));
       if (T >= total) {
         a.next_token[b] = a.vocab - 1;
-        return Order{kEnd, 0, 0, 0, 0ull};
+        return Order{total == 0ull ? kLook : kEnd, at, 0, 0, 0ull};
       }
       unsigned long long c = 0ull;  // (T is below the largest sum: none that stays at or below it ended)
       int r = 0;
@@ -307,6 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         if (lane == 0) first->totals[rank] = sum;
       }
       cluster.sync();
+    } else if (o.kind == kLook) {  // a row without weight: flagged where it holds no numbers
+      bool bad = false;
+      for (int v = v0 + lane; v < v1; v += 32) bad |= !(p[v] >= 0.f && p[v] < 2.f);
+      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err_word, kErrProbs);
     } else if (rank == o.rank) {  // kFind: the warp, then the entry
       unsigned long long c = 0ull;
       int w = 0;
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         if (!found && lane == 0) a.next_token[b] = v1 - 1;
       }
     }
-    if (o.kind == kFind) break;
+    if (o.kind != kSum) break;
   }
   cluster.sync();  // nobody leaves while its memory may be read
 }
