@@ -8,10 +8,12 @@
 //
 // The angle.  p * inv_freq in fp32 is off by 2^-24 of itself: 0.06 rad at a
 // million.  Here a frequency is a whole number of 2^-64 turns, made once a block
-// in 64 bits; the product with the position modulo 2^64 is the fraction of a turn
-// exactly (integers wrap as turns do), and its upper 32 bits, as a signed number
-// of half turns in [-1, 1), go to sincospif: the angle is good to 2^-24 half turns
-// at any position.
+// from 128 bits of 1 / (2 pi) (an fp64 product would be off by 2^-53 of the frequency's
+// turns: 0.2 rad at position 2^31 for a million radians a position); the product with the
+// position modulo 2^64 is the fraction of a turn to a unit for each position (integers
+// wrap as turns do), and its upper 32 bits, as a signed number of half turns in [-1, 1),
+// go to sincospif: the angle is good to 2^-24 half turns at any position, for frequencies
+// up to 2^53.
 //
 // Work split: a lane owns 2 x 8 values of a token's rows, the pieces that hold
 // eight pairs, and keeps their 8 sines and cosines in registers while it walks
@@ -43,6 +45,21 @@ struct RopeKParams {
   long long token_groups;
   uint32_t* err_word;
 };
+
+// Turns a position, without whole ones, in units of 2^-64: the 53 bits of f times those of
+// 1 / (2 pi) at f's exponent, in whole numbers (a few multiplications; fp64 takes longer here).
+__device__ __forceinline__ unsigned long long turns64(double f) {
+  // 2^128 / (2 pi), rounded down.
+  constexpr unsigned __int128 kTurn = ((unsigned __int128)0x28be60db9391054aull << 64) | 0x7f09d5f47d4d3770ull;
+  const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
+  const unsigned long long m = (bits & ((1ull << 52) - 1)) | (1ull << 52);
+  const int down = 1075 - (int)((bits >> 52) & 0x7ff);  // f = m 2^-down
+  unsigned __int128 w = 0;
+  if (down >= 0 && down < 128) w = kTurn >> down;
+  if (down < 0 && down > -128) w = kTurn << -down;
+  const unsigned long long t = (unsigned long long)((w * m) >> 64);
+  return bits >> 63 ? 0ull - t : t;
+}
 
 // Turns eight pairs: pieces a and b of 8 bf16 each.  Half layout: pair j is
 // (a[j], b[j]); neighbouring pairs: (a[2j], a[2j + 1]) for j < 4, b's behind them.
@@ -99,11 +116,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeKParams p) {
   const int lc = lane % kLanes, lt = lane / kLanes;
   grid_dep_wait();
   const int half = a.rotary_dim / 2;
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    // Turns a position, without whole ones, in units of 2^-64.
-    const double f = a.inv_freq[i] * 0.15915494309189533577;
-    s_step[i] = (unsigned long long)((f - floor(f)) * 18446744073709551616.0);
-  }
+  for (int i = threadIdx.x; i < half; i += kThreads) s_step[i] = turns64(a.inv_freq[i]);
   if (APPEND && a.cu_seqlens != nullptr && blockIdx.x == 0) {
     bool bad = false;
     for (int i = threadIdx.x; i < a.batch; i += kThreads) {

@@ -779,8 +779,8 @@ int attn_decode_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16*
  *            (magnitude kept) the gradient of this call with respect to its inputs
  *   magnitude: finite; multiplies cosines and sines (so rotated columns only)
  * y1 = magnitude (x1 cos a - x2 sin a), y2 = magnitude (x2 cos a + x1 sin a) in
- * fp32, rounded to bf16 once.  The angle is exact to 2^-24 half turns at any position
- * (it is kept modulo a turn in 64-bit whole numbers).
+ * fp32, rounded to bf16 once.  The angle is exact to 2^-24 half turns at any position, for
+ * |inv_freq| up to 2^53 (it is kept modulo a turn in 64-bit whole numbers).
  * Limits: head_dim in {64, 128, 256}; batch * seqlen <= 2^30; heads <= 65535.
  * Errors: ATTN_ERR_NULL, _SHAPE, _HEADDIM, _ALIGN, _ARCH, _LAUNCH.
  */
