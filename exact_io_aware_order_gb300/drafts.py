@@ -3,10 +3,13 @@
 csrc/binding.cpp first, which takes the plain case, and come here otherwise.
 
 A step of speculative decoding, for each sequence's nodes (its last token, node 0,
-and the drafted tokens behind it)::
+and the drafted tokens behind it), q, k and v tokens first as projections leave them
+((total, heads, d); the cache's calls take heads first, decode_tree tokens first and
+contiguous)::
 
-    q = cache_append(k, v, k_cache, v_cache, kv_lens, cu, table, inv_freq, positions, q=q)
-    o, lse = decode_tree(q.transpose(0, 1), k_cache, v_cache, kv_lens, cu, mask, table)
+    t = lambda x: x.transpose(0, 1)
+    q = t(cache_append(t(k), t(v), k_cache, v_cache, kv_lens, cu, table, inv_freq, positions, q=t(q)))
+    o, lse = decode_tree(q.contiguous(), k_cache, v_cache, kv_lens, cu, mask, table)
     ...                                             # the rest of the model, its probabilities
     n, path, token = verify_tree(probs, tokens, parents, cu, u, u_last, draft_probs)
 """
