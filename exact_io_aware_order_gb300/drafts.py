@@ -101,7 +101,9 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
     tokens first, seen through ``transpose``).  inv_freq: (rotary_dim / 2,) float64
     (:func:`rope_inv_freq`); positions: int32 (B, N) or (N,), packed (total,), None:
     the row's index.  ``inverse`` rotates back; with gradients for q and k it gives
-    the gradients of this call's inputs.  Returns (q_out, k_out), allocated with
+    the gradients of this call's inputs.  Autograd does not record this call, as none of
+    this package's: outputs are detached, and a model that is trained through it wraps both
+    directions in a ``torch.autograd.Function``.  Returns (q_out, k_out), allocated with
     the inputs' layout when not given; an output may be its input.
     """
     if stream is None:
@@ -382,7 +384,9 @@ def verify_tree(target_probs: torch.Tensor, draft_tokens: torch.Tensor, parents:
     node; draft_probs: those that each node's children were drawn from, None: drafts that
     are certain; draft_tokens, parents: (total,) int32; cu_nodes: (B + 1,) int32; u_accept:
     (total,) and u_sample: (B,) fp32 random numbers in [0, 1).  Children of a node are
-    tried in index order.  Returns (num_accepted (B,), path (B, 64): the root and the accepted
+    tried in index order; those of one node are independent draws from its draft_probs row
+    (drawn without replacement, the outputs would not be distributed as the target's).
+    Returns (num_accepted (B,), path (B, 64): the root and the accepted
     nodes by index within the sequence, then -1; next_token (B,)), int32.
 
     The accepted nodes' keys and values belong behind the cached tokens: with chains they

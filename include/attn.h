@@ -910,9 +910,11 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
  *   target_probs: (total_nodes, vocab) fp32, node t's row at t * target_stride (>= vocab):
  *                the target's probabilities of the token after node t.  What is not in
  *                [0, 2) counts as 0; sums of a row end at 8 - 2^-60.
- *   draft_probs: the same for the draft: row t is what the children of node t were drawn
- *                from; or NULL: the drafted tokens are certain (the draft's most likely
- *                ones, for example)
+ *   draft_probs: the same for the draft: row t is what each of the children of node t was
+ *                drawn from, independently of its siblings (of children that are drawn
+ *                without replacement the outputs are not distributed as the target's); or
+ *                NULL: the drafted tokens are certain (the draft's most likely ones, for
+ *                example)
  *   draft_tokens: (total_nodes,) int32 each node's token (a root's is not read)
  *   parents    : (total_nodes,) int32 each node's parent, by its index within the
  *                sequence, smaller than the node's own; the root's (node 0) is -1
