@@ -23,7 +23,7 @@ def printed_step():
 
 
 @pytest.mark.parametrize("n_q,n_kv,nodes,sliced", [(6, 2, [12, 1, 9], False), (22, 2, [12, 1, 9], True),
-                                                   (8, 1, [64, 30], True)])
+                                                   (8, 1, [64, 30], True), (4, 4, [7, 0, 5], True)])
 def test_printed_step(dev, n_q, n_kv, nodes, sliced):
     """With as many nodes as heads too, where axes that are exchanged have the right sizes."""
     d, V, block = 128, 260, 16
@@ -31,7 +31,7 @@ def test_printed_step(dev, n_q, n_kv, nodes, sliced):
     total, B = sum(nodes), len(nodes)
     cu = [sum(nodes[:i]) for i in range(B + 1)]
     lens = [0, 37, 500][:B]
-    trees = [tree(n, 10 * b + 1) for b, n in enumerate(nodes)]
+    trees = [tree(n, 10 * b + 1) if n else [] for b, n in enumerate(nodes)]
     qkv = torch.randn(total, n_q + 2 * n_kv, d, generator=g).to(BF16)
     logits = torch.randn(total, V, generator=g)
     p = torch.softmax(logits, 1)
@@ -55,6 +55,9 @@ def test_printed_step(dev, n_q, n_kv, nodes, sliced):
     got_q, o, token = (names[x].cpu() for x in ("q", "o", "token"))
     n_new = names["kv_lens"].tolist()
     for b, n in enumerate(nodes):
+        if n == 0:
+            assert int(token[b]) == -1 and n_new[b] == lens[b]
+            continue
         sl, words = slice(cu[b], cu[b] + n), words_of(trees[b])
         pos = torch.tensor([lens[b] + bin(w).count("1") - 1 for w in words])
         want, err = turned(qkv[sl, :n_q].transpose(0, 1), pos, f.cpu())
