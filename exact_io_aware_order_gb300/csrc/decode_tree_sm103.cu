@@ -25,7 +25,7 @@
 //     kernel joins.  A block starts at most one cut item in its run and ends at most
 //     one, so there are two places a block.  Short caches (by max_kv_len) go whole
 //     items to a block, without the second kernel;
-//   * a producer warp for keys (and queries) and one for values fill a ring of tiles,
+//   * a producer warp for keys (and queries) and one for values fill a ring of tiles each,
 //     128-byte-swizzled as the MMAs read them: runs of rows that all exist, in blocks of
 //     whole runs, by tiled copies (TMA); the others, and blocks of any size, by
 //     16-byte copies (cp.async) of rows from wherever the block table says, with zeros for
@@ -113,7 +113,7 @@ struct TreeSmem {
   // A table of depths a warp; at head_dim 256 what the halves of a row tell each other.
   static constexpr int kDepthTabBytes = 8 * kMostNodes * 4;
   static constexpr int kDepthBytes = kDepthTabBytes + (D == 256 ? 2 * 2 * 128 * 4 : 0);
-  // The ring takes what the query tiles leave of 226 KB, up to kMaxSlots tiles.
+  // The rings take what the query tiles leave of 226 KB, up to kMaxSlots tiles.
   static constexpr int slots(int q_tiles) {
     const int room = 226 * 1024 - kMiscBytes - kDepthBytes - 1024 - q_tiles * kQTileBytes;
     const int n = room / kTileBytes;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slots = p.slots;
+  const int slots = p.slots, k_slots = (slots + 1) / 2;  // (the keys' slots are the first ones)
   uint8_t* ring = smem + p.q_tiles * L::kQTileBytes;
   uint8_t* misc = ring + slots * L::kTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
@@ -486,7 +486,11 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
   };
   // The keys' producer plans the segments; the other roles take them from its slots, in order
   // (`all`: by a whole warp).  S products count over all of them (n: buffer n % SB), and so
-  // do the ring's tiles (K and V of key tile j: 2 j and 2 j + 1).
+  // do the tiles of keys and of values, each in slots of their own: a slot's releases all come
+  // from one issuer, in order, so that a producer that has waited for one release knows of all
+  // before it.  In one ring of an odd number of slots, keys and values would take turns in each,
+  // and with 5 slots the values' producer could take a release by the S issuer for the one that
+  // the P V issuer still owed (phases are told apart by their parity alone).
   auto take = [&](Seg& sg, int& count, bool all) -> bool {
     const int i = count % kSegSlots;
     const uint32_t parity = (count / kSegSlots) & 1;
@@ -514,7 +518,8 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
     // Boxes of 8 rows for keys alone (see the launch).
     const bool tiled = p.box >= 16 || (p.box > 0 && keys);
     const bool mine = tiled && box * p.box < kBN;
-    int slot = keys ? 0 : 1, phase = 0, n_seg = 0, issued = 0;
+    const int slot0 = keys ? 0 : k_slots, slot1 = keys ? k_slots : slots;
+    int slot = slot0, phase = 0, n_seg = 0, issued = 0;
     bool again = false;                                    // slots have been used before
     Seg sg;
     int count = 0;
@@ -749,8 +754,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
           if (row_in >= a.block_size) row_in -= a.block_size, ++blk;
         }
         look(t + 1);
-        for (int i = 0; i < 2; ++i)
-          if (++slot == slots) slot = 0, phase ^= 1, again = true;
+        if (++slot == slot1) slot = slot0, phase ^= 1, again = true;
       }
       ++n_seg;
     }
@@ -760,10 +764,9 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       // Tiled copies in flight land before the block's memory is released.
       volatile uint32_t no_abort = 0u;
       WaitCtl drain{&no_abort, p.err_word, p.timeout_ns};
-      for (int i = max(0, issued - (slots + 1) / 2); i < issued; ++i) {
-        const int at = 2 * i + (keys ? 0 : 1);
-        mbar_wait(bar(kFull + at % slots), (at / slots) & 1, drain);
-      }
+      const int n = slot1 - slot0;
+      for (int i = max(0, issued - n); i < issued; ++i)
+        mbar_wait(bar(kFull + slot0 + i % n), (i / n) & 1, drain);
     }
     __syncwarp();
   } else if (warp == kSWarp) {
@@ -808,9 +811,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             if (!ok) break;
           }
           mma_commit(bar(kEmpty + slot));
-          // K tiles are every other one of the ring.
-          for (int i = 0; i < 2; ++i)
-            if (++slot == slots) slot = 0, phase ^= 1;
+          if (++slot == k_slots) slot = 0, phase ^= 1;
         }
         mma_commit(bar(kQEmpty));
       }
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
       Seg sg;
       int count = 0;
       bool ok = true;
-      int n = 0, slot = 1, phase = 0;
+      int n = 0, slot = k_slots, phase = 0;
       while (ok && take(sg, count, false)) {
         for (int t = 0; t < sg.tiles && ok; ++t) {
           if (!mbar_wait(bar(kFull + slot), phase, ctl)) { ok = false; break; }
@@ -868,8 +869,7 @@ __global__ void __launch_bounds__(threads_of<D>(), 1) decode_tree_kernel(
             if (t == sg.tiles - 1) mma_commit(bar(kOFull + r));
           }
           mma_commit(bar(kEmpty + slot));
-          for (int i = 0; i < 2; ++i)
-            if (++slot == slots) slot = 0, phase ^= 1;
+          if (++slot == slots) slot = k_slots, phase ^= 1;
         }
       }
       mma_commit(bar(kDrain + 1));
