@@ -265,8 +265,12 @@ cudaError_t launch_t(const RopeArgs& a, const LaunchCtx& ctx) {
   const long long tokens = APPEND ? a.tokens : (long long)a.batch * a.tokens;
   p.token_groups = (tokens + kTokens - 1) / kTokens;
   const int heads = a.n_q_heads + (APPEND ? 2 : 1) * a.n_kv_heads;
-  // Heads of a warp: as many as leave the GPU 16 warps an SM, up to 8.
-  const long long want = 16LL * std::max(ctx.num_sms, 1);
+  // Heads of a warp, which share its sines and cosines: as many as leave the GPU 8 warps an SM,
+  // up to 8.  With 16 warps, and so fewer heads each: a prompt of 512 with 28 + 4 heads 5.4 us
+  // (3.9), of 2048 9.6 (8.5), 16 trees of 64 nodes into the cache 10.3 (8.9); from 4096 rows on
+  // and up to 256 the same.  With 4 warps: 3.6, 8.7, 8.8.  Up to 4 heads: 8192 rows 26.0 (24.7),
+  // 16 prompts into the cache 163 (142); up to 16: 26.2, 134.
+  const long long want = 8LL * std::max(ctx.num_sms, 1);
   int hpg = 8;
   while (hpg > 1 && p.token_groups * ((heads + hpg - 1) / hpg) < want) hpg /= 2;
   p.heads_per_group = hpg;
