@@ -12,7 +12,7 @@
 // rows takes the pipeline 0.85 us), the tensor cores and the exponentials beyond.
 // Even a few rows go through 128-row products: they hide behind the copies, and one
 // path serves every size.  Measured (bf16 outputs, head_dim 128): 16 sequences of 1024 -
-// 32768 tokens in 16-token blocks, 1.12 GB, 205 us, 5.5 TB/s; one of 30720, 63 MB, 35 us (5
+// 32768 tokens in 16-token blocks, 1.12 GB, 203 us, 5.5 TB/s; one of 30720, 63 MB, 35 us (5
 // before the first product; the first kernel alone 30); 300 tokens 10 us.
 //
 // Design:

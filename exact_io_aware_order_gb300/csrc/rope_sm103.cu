@@ -21,9 +21,9 @@
 // neighbouring tokens, so heads-first tensors are read in runs of 1 KB / 2, and
 // tokens-first ones row by row.  Heads are split over warps only as far as the GPU
 // needs warps.  Bound by HBM: 4 bytes a value; the arithmetic takes half of the issue slots.
-// Measured: 28 + 4 heads of 128 over 8192 tokens, 134 MB, 25.0 us (5.4 TB/s, the reads from
+// Measured: 28 + 4 heads of 128 over 8192 tokens, 134 MB, 24.8 us (5.4 TB/s, the reads from
 // HBM, the writes still partly in L2); gradients of 710 MB 108 us (6.6 TB/s); an append of
-// 16 prompts, 855 MB, 143 us (6.0 TB/s); of one token to each of 16 sequences 3 us.
+// 16 prompts, 855 MB, 142 us (6.0 TB/s); of one token to each of 16 sequences 2.8 us.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -26,7 +26,7 @@
 // at the same barriers whatever the memory holds.
 // Bound by HBM for large batches (one row of p, and of q, a sequence), by the latency
 // of the gathers and the cluster's barriers for small ones.  Measured: 64 trees of 10 - 41
-// nodes over 128257 entries 58 us, of which some 9 are the rows' bytes: a sequence is a chain of
+// nodes over 128257 entries 60 us, of which some 9 are the rows' bytes: a sequence is a chain of
 // gathers, a pass for each refusal that has a sibling behind it, and two for the last draw;
 // a chain of 6 over 32000 entries 9 us.
 #include <algorithm>
@@ -98,7 +98,7 @@ struct Shared {
 };
 
 // What a pass over the vocabulary computes for an entry, chosen once a pass so that its loops
-// have no branches inside (with them 64 trees over 128257 entries take 67 us instead of 58).
+// have no branches inside (with them 64 trees over 128257 entries took 67 us instead of 58).
 enum Form : int {
   kPlain = 0,  // p
   kLess = 1,   // max(p - q, 0): after the first refusal

@@ -878,7 +878,8 @@ size_t attn_decode_tree_workspace_bytes(int batch, int total_nodes, int n_q_head
  * A row that sees nothing (no cached token, no bit) has O = 0 and LSE = -inf.  With
  * fp32 outputs the softmax weights enter the product with V in three bf16 parts (good to
  * 2^-24 of each), with bf16 outputs in one (2^-8), as in attn_prefill; all else is fp32, the
- * exponential itself good to 2^-22.  Keys that a
+ * exponential itself good to 2^-22, the tensor core's sums cut off instead of rounded (some 2^-26
+ * of O for each part of 16 keys, toward zero: fp32 outputs are good to a few 1e-6).  Keys that a
  * node does not see may hold anything; values have to be finite unless no node of the
  * sequence sees them and they lie behind its nodes or in front of every window.
  * Rows outside every sequence are not written.  A cu_nodes that breaks its rule is clamped
