@@ -932,8 +932,8 @@ int attn_decode_tree(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf
  * 0) and Z = sum w (without draft_probs: q(x) = 1, and a refusal sets w(x) = 0, Z = max(Z -
  * w(x), 0)).
  * With no child left, next_token is the smallest v with w(0) + .. + w(v) >
- * floor(u_sample * sum w); where sum w is 0, w = p; where no v is, vocab - 1, and flagged if
- * p has an entry that is not in [0, 2) (a NaN).
+ * floor(u_sample * sum w); where sum w is 0, w = p; where no v is, vocab - 1 (flagged if p
+ * sums to 0 and has an entry that is not in [0, 2), a NaN for example).
  * All numbers are multiples of 2^-60: inputs and products are rounded down to them (q C term
  * by term where C is 8 or more: its terms are sums of successive Zs below 8), sums of entries
  * are exact (those that would reach 8 are 8 - 2^-60), so the outputs do not depend on any order.
